@@ -48,6 +48,11 @@ _SIGS = {
                                _c_p, _c_p, _c_p, _c_int, _c_p, _c_sz, _c_p]),
     "cq_moe_route": (_c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_int, _c_p, _c_p, _c_p]),
     "cq_moe_layout": (_c_int, [_c_p, _c_i64, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p]),
+    "cq_kv8_write": (_c_int, [_c_p, _c_p, _c_p, _c_int, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p]),
+    "cq_kv8_read": (_c_int, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_int, _c_i64, _c_i64, _c_i64, _c_p]),
+    "cq_attn_kv8_workspace_bytes": (_c_sz, [_c_i64] * 6),
+    "cq_attn_kv8": (_c_int, [_c_p, _c_int, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_i64, ctypes.c_float, _c_int,
+                             _c_i64, _c_p, _c_int, _c_i64, _c_p, _c_p, _c_sz, _c_p]),
     "cq_dequant_q4": (_c_int, [_c_p, _c_p, _c_i64, _c_i64, _c_p, _c_p]),
     "cq_dequant_q8row": (_c_int, [_c_p, _c_p, _c_i64, _c_i64, _c_p, _c_p]),
     "cq_get_device_error": (_c_int, [_c_p]),
@@ -251,6 +256,112 @@ def cq_moe_route(logits, topk, idx, w, shared=False, stream=None):
 
 def cq_moe_layout(ws, T, H, I, E, topk, perm_out, seg_out, stream=None):
     _check(lib().cq_moe_layout(_ptr(ws), T, H, I, E, topk, _ptr(perm_out), _ptr(seg_out), _stream(stream)))
+
+
+# ---- 8-bit key/value cache (include/cq_kv8.h) ---------------------------
+
+class _kv8_desc(ctypes.Structure):
+    _fields_ = [("Kq", _c_p), ("Ks", _c_p), ("Vq", _c_p), ("Vs", _c_p), ("pages", _c_i64), ("Hkv", _c_i64),
+                ("page", _c_i64), ("D", _c_i64), ("table", _c_p), ("ldt", _c_i64), ("B", _c_i64)]
+
+
+class cq_kv8_cache:
+    """One layer's 8-bit cache: Kq, Vq int8 [pages][Hkv][page][D], Ks, Vs f32
+    [pages][Hkv][page / 32], table int32 [B][ldt].  Holds the tensors (which
+    must be dense; a table's rows may be a slice of a wider one) and the C
+    descriptor of the same name."""
+
+    def __init__(self, Kq, Ks, Vq, Vs, table):
+        import torch
+        pages, Hkv, page, D = Kq.shape
+        for t, dt, shape in ((Kq, torch.int8, (pages, Hkv, page, D)), (Vq, torch.int8, (pages, Hkv, page, D)),
+                             (Ks, torch.float32, (pages, Hkv, page // 32)), (Vs, torch.float32, (pages, Hkv, page // 32))):
+            if t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous():
+                raise ValueError(f"a dense {dt} tensor of shape {shape} is needed, got {t.dtype} {tuple(t.shape)}")
+        if table.dtype != torch.int32 or table.dim() != 2 or table.stride(1) != 1:
+            raise ValueError("the table must be int32 [B][ldt]")
+        self.Kq, self.Ks, self.Vq, self.Vs, self.table = Kq, Ks, Vq, Vs, table
+        ldt = table.stride(0) if table.shape[0] > 1 else table.shape[1]
+        self.desc = _kv8_desc(Kq.data_ptr(), Ks.data_ptr(), Vq.data_ptr(), Vs.data_ptr(), pages, Hkv, page, D,
+                              table.data_ptr(), ldt, table.shape[0])
+
+    @staticmethod
+    def empty(pages, Hkv, page, D, table, device="cuda"):
+        """A cache of zeroed pools over `table`."""
+        import torch
+        q = lambda: torch.zeros(pages, Hkv, page, D, dtype=torch.int8, device=device)
+        s = lambda: torch.zeros(pages, Hkv, page // 32, dtype=torch.float32, device=device)
+        return cq_kv8_cache(q(), s(), q(), s(), table)
+
+
+def _kv8_rows(t, what, heads, D):
+    """Row pitch of a [T][heads][D] tensor whose rows are dense."""
+    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, D) or t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
+        raise ValueError(f"{what} must be [T][{heads}][{D}] with dense rows, got shape {tuple(t.shape)}, strides {t.stride()}")
+    return t.stride(0) if t.shape[0] > 1 else heads * D
+
+
+def _kv8_index(t, what, n):
+    import torch
+    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be a dense int32 tensor of {n} entries, got {t.dtype} {tuple(t.shape)}")
+    return _ptr(t)
+
+
+def cq_kv8_write(cache, K, V, q_start, lens, stream=None, raise_on_error=True):
+    """The rows of K, V ([T][Hkv][D], fp16/bf16/f32; rows q_start[b] .. q_start[b+1]
+    - 1 of sequence b) become the last tokens of their sequences, which hold
+    lens[b] tokens afterwards."""
+    c = cache.desc
+    ldk, ldv = _kv8_rows(K, "K", c.Hkv, c.D), _kv8_rows(V, "V", c.Hkv, c.D)
+    if V.dtype != K.dtype or V.shape != K.shape:
+        raise ValueError("K and V must have one type and shape")
+    st = lib().cq_kv8_write(ctypes.byref(c), _ptr(K), _ptr(V), _xt(K), K.shape[0], ldk, ldv,
+                            _kv8_index(q_start, "q_start", c.B + 1), _kv8_index(lens, "lens", c.B), _stream(stream))
+    if raise_on_error:
+        _check(st)
+    return st
+
+
+def cq_kv8_read(cache, first, out_start, K, V, stream=None, raise_on_error=True):
+    """Rows out_start[b] .. out_start[b+1] - 1 of K, V ([T][Hkv][D], fp16/bf16/f32)
+    become the values of tokens first[b] .. of sequence b (first None: from 0)."""
+    c = cache.desc
+    ldk, ldv = _kv8_rows(K, "K", c.Hkv, c.D), _kv8_rows(V, "V", c.Hkv, c.D)
+    if V.dtype != K.dtype or V.shape != K.shape:
+        raise ValueError("K and V must have one type and shape")
+    st = lib().cq_kv8_read(ctypes.byref(c), None if first is None else _kv8_index(first, "first", c.B),
+                           _kv8_index(out_start, "out_start", c.B + 1), _ptr(K), _ptr(V), _xt(K), K.shape[0], ldk, ldv,
+                           _stream(stream))
+    if raise_on_error:
+        _check(st)
+    return st
+
+
+def cq_attn_kv8_workspace_bytes(T, Hq, Hkv, D, B, max_q) -> int:
+    return lib().cq_attn_kv8_workspace_bytes(T, Hq, Hkv, D, B, max_q)
+
+
+def cq_attn_kv8(Q, cache, q_start, lens, max_q, O, ws, scale=None, causal=True, window=0, lse=None, stream=None,
+                raise_on_error=True):
+    """O[T][Hq][D] = softmax attention of Q [T][Hq][D] (fp16/bf16) over the cache;
+    the rows of sequence b are the last of its lens[b] tokens.  scale None:
+    1 / sqrt(D).  lse (f32 [T][Hq]) takes each row's log of the sum of exponentials."""
+    import torch
+    c = cache.desc
+    Hq = Q.shape[1]
+    ldq, ldo = _kv8_rows(Q, "Q", Hq, c.D), _kv8_rows(O, "O", Hq, c.D)
+    if O.shape != Q.shape:
+        raise ValueError("O must have the shape of Q")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != tuple(Q.shape[:2]) or not lse.is_contiguous()):
+        raise ValueError("lse must be a dense f32 tensor [T][Hq]")
+    st = lib().cq_attn_kv8(_ptr(Q), _xt(Q), Q.shape[0], Hq, ldq, ctypes.byref(c), _kv8_index(q_start, "q_start", c.B + 1),
+                           _kv8_index(lens, "lens", c.B), max_q, c.D ** -0.5 if scale is None else scale,
+                           1 if causal else 0, window, _ptr(O), _xt(O), ldo, _ptr(lse), _ptr(ws),
+                           0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+    if raise_on_error:
+        _check(st)
+    return st
 
 
 def cq_dequant_q4(Wq, Ws, W, stream=None):

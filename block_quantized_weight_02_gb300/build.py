@@ -11,8 +11,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libcq.so")
-SOURCES = ["cq_api.cu", "k_aux.cu", "k_skinny.cu", "k_tc.cu", "k_tc_ffn.cu", "k_tc_q4a.cu", "k_tc_q8b.cu", "k_rows.cu", "cq_noalloc.cu"]
-HEADERS = ["cq_internal.h", "cq_ptx.cuh", "k_tc.cuh"]
+SOURCES = ["cq_api.cu", "k_aux.cu", "k_skinny.cu", "k_tc.cu", "k_tc_ffn.cu", "k_tc_q4a.cu", "k_tc_q8b.cu", "k_rows.cu", "cq_noalloc.cu",
+           "kv8/kv8_api.cu", "kv8/kv8_store.cu", "kv8/kv8_attn.cu"]
+HEADERS = ["cq_internal.h", "cq_ptx.cuh", "k_tc.cuh", "kv8/kv8.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(HERE, "..", "include")]
@@ -34,12 +35,12 @@ def _stale(target: str, deps) -> bool:
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
-    hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(HERE, "..", "include", "cq.h")]
+    hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(HERE, "..", "include", h) for h in ("cq.h", "cq_kv8.h")]
     procs = []
     objs = []
     for src in SOURCES:
         s = os.path.join(CSRC, src)
-        o = os.path.join(OUT_DIR, src.replace(".cu", ".o"))
+        o = os.path.join(OUT_DIR, os.path.basename(src).replace(".cu", ".o"))
         objs.append(o)
         if force or _stale(o, [s] + hdrs):
             cmd = [nvcc(), *ARCH, *FLAGS, *extra, "-c", s, "-o", o]
