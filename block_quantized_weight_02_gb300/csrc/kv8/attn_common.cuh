@@ -1,0 +1,64 @@
+// What the attention kernels share: queries to fp16, codes to fp16, outputs.
+#pragma once
+#include "kv8.cuh"
+
+namespace cq {
+namespace kv8 {
+
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+// Exponent of a scale (a power of two of at least 2^-64, or NaN).
+__device__ __forceinline__ int exp_of(float s) { return (int)(__float_as_uint(s) >> 23) - 127; }
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+// Two codes (bytes of w ^ 0x80808080 picked by sel) -> fp16 exactly: with 0x64 as the high byte
+// u = code + 128 reads as 1024 + u, and minus 1152 is the code.
+__device__ __forceinline__ uint32_t codes_f16(uint32_t u, uint32_t sel) {
+    return sub_f16x2(prmt(u, 0x64646464u, sel), 0x64806480u);
+}
+
+// bf16 queries reach fp16 behind a power of two per row that puts the row's largest
+// magnitude in [2^13, 2^14): exact for values within 2^27 of it.  Returns the shift.
+__device__ __forceinline__ int guard_of(float amax) {
+    const int e = (int)(__float_as_uint(amax) >> 23) - 127;
+    return amax == 0.f || e == 128 ? 0 : min(max(13 - e, -114), 126);
+}
+
+__device__ __forceinline__ void store_out(void* p, int64_t i, int t, float v) {
+    if (t == CQ_F32) static_cast<float*>(p)[i] = v;
+    else if (t == CQ_F16) static_cast<__half*>(p)[i] = __float2half_rn(v);
+    else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
+// Four neighbouring outputs (i a multiple of four).
+__device__ __forceinline__ void store_out4(void* p, int64_t i, int t, float a, float b, float c, float d) {
+    if (t == CQ_F32) {
+        *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = make_float4(a, b, c, d);
+    } else if (t == CQ_F16) {
+        *reinterpret_cast<uint2*>(static_cast<__half*>(p) + i) = make_uint2(pack_f16(a, b), pack_f16(c, d));
+    } else {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(a, b), y = __floats2bfloat162_rn(c, d);
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + i) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+    }
+}
+
+// The tokens [lo, hi) that row i of a sequence with n rows and L tokens sees.
+__device__ __forceinline__ int row_hi(int i, int n, int L, int causal) { return causal ? max(L - n + i + 1, 0) : L; }
+__device__ __forceinline__ int row_lo(int i, int n, int L, int64_t window) {
+    return window ? (int)max((int64_t)0, (int64_t)(L - n + i) - window + 1) : 0;
+}
+
+}  // namespace kv8
+}  // namespace cq

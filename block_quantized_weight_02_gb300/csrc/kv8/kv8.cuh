@@ -51,6 +51,9 @@ cudaError_t launch_write(const Cache& c, const Batch& b, int D, const void* K, c
 cudaError_t launch_read(const Cache& c, const Batch& b, int D, void* K, void* V, int yt, int64_t ldk, int64_t ldv,
                         cudaStream_t s);
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s);
+bool decode_serves(int64_t rows);                     // rows: query rows of a sequence that share a KV head
+size_t decode_workspace(int64_t D);
+cudaError_t launch_decode(const AttnArgs& a, cudaStream_t s);
 size_t attn_workspace(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q);
 
 template <class... KArgs, class... Args>

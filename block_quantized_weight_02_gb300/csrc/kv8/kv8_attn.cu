@@ -81,9 +81,13 @@ __global__ void __launch_bounds__(128) k_attn_rows(const AttnArgs a) {
 
 }  // namespace
 
-size_t attn_workspace(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) { return 256; }
+size_t attn_workspace(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t, int64_t max_q) {
+    if (decode_serves(std::min(max_q, T) * (Hq / Hkv))) return decode_workspace(D);
+    return 256;
+}
 
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s) {
+    if (decode_serves((int64_t)a.max_q * (a.Hq / a.c.Hkv))) return launch_decode(a, s);
     const dim3 grid((unsigned)(((int64_t)a.b.T * a.Hq + 3) / 4));
     if (a.D == 128) return launch_pdl(k_attn_rows<128>, grid, dim3(128), 0, s, a);
     return launch_pdl(k_attn_rows<64>, grid, dim3(128), 0, s, a);
