@@ -9,13 +9,15 @@
 // next without any barrier.  Each warp owns a ring of blocks that TMA fills ahead of it
 // across those borders.
 //
-// One block: S = Q K^T as m16n8k16 products (rows x tokens), the running maximum and
-// sum in f32 registers, then O += P V with the score fragments as the first operand,
-// so nothing of the softmax leaves registers.  The codes become fp16 in registers,
-// exactly.  The operands' inner order is free as long as both sides agree: a lane takes 4
-// neighbouring codes of its token as one k16 step's part (keys), and 16 neighbouring
-// channels of its tokens as the 16 output tiles (values), so every shared-memory load is
-// 16 bytes, without bank conflicts under the copies' swizzle.
+// One block: S^T = K Q^T as m16n8k16 products (tokens x rows), the running maximum and
+// sum in f32 registers, then O^T += V^T P^T; an 8 x 8 transpose in registers turns the
+// score fragments into the second operand.  With the rows as the narrow side a group of
+// up to 8 rows takes half the products that rows x tokens would (they pad rows to 16).
+// The codes become fp16 in registers, exactly.  The operands' inner order is free as long
+// as both sides agree: a lane takes 4 neighbouring codes of its token as one k16 step's
+// part (keys), and D/8 neighbouring channels of its tokens as the output tiles (values),
+// so every shared-memory load is 16 bytes (values at D = 64: 8), without bank conflicts
+// under the copies' swizzle.
 //
 // A key block's scale multiplies the scores in f32.  A value block's scale 2^lv joins the
 // exponent, w = 2^(s - m + 15 + lv - ref) with ref the largest lv so far, so the weights
@@ -31,33 +33,37 @@ namespace cq {
 namespace kv8 {
 namespace {
 
-constexpr int NW = 8;                 // warps per CTA
 constexpr int ROWS = 16;
 constexpr int MAX_CTAS = 256;         // workspace bound
+constexpr int MAX_NW = 12;
 constexpr int P_EXP = 15;             // weights carry 2^15
+constexpr int JOIN = 8;               // partials in flight while joining
 
 struct Maps {
     CUtensorMap t[2];                 // keys, values: {D, pages * Hkv * page}, box {D, 32}
 };
 
-// Workspace: per-warp partials [MAX_CTAS * NW][2], per-CTA partials [MAX_CTAS][2], then each CTA's two segments.
 template <int D>
 struct Part {
     float o[ROWS][D];
     float m[ROWS], l[ROWS];
 };
+// Workspace: partials of segments that end inside a warp's share, partials of the CTAs, the CTAs' two segments.
 template <int D>
 struct Space {
-    Part<D> warp[MAX_CTAS * NW][2];
+    Part<D> warp[MAX_CTAS * MAX_NW];
     Part<D> cta[MAX_CTAS][2];
     int seg[MAX_CTAS][2];             // segment of cta[i][0] (began earlier) and cta[i][1] (began here, goes on), or -1
 };
 
-template <int D>
+// NT: n8 tiles of rows.  One tile fits 12 warps with two blocks each (registers), two tiles 8 warps with three.
+template <int D, int NT>
 struct Ring {
-    static constexpr int ST = D == 128 ? 3 : 6;           // blocks in the ring of a warp: 192 KB a CTA
-    static constexpr int TILE = BLK * D;                  // bytes of a block's keys or values
+    static constexpr int NW = NT == 1 ? 12 : 8;
+    static constexpr int ST = (NT == 1 ? 2 : 3) * (128 / D);   // blocks in the ring of a warp: 192 KB a CTA
+    static constexpr int TILE = BLK * D;                       // bytes of a block's keys or values
     static constexpr int BYTES = NW * ST * 2 * TILE;
+    static_assert(ST * 2 * TILE >= (int)sizeof(Part<D>) && NW <= MAX_NW, "a partial fits the ring of its warp");
 };
 
 struct Seq {
@@ -99,33 +105,44 @@ __device__ __forceinline__ uint2 lds64(uint32_t p) {
     return v;
 }
 
-// The 16 x D result of a warp: lane (g, t) holds rows g and g + 8, channels t * D/4 ...
-template <int D>
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+// 4 bytes to shared memory; `bar` gets this thread's arrival when they are there.
+__device__ __forceinline__ void copy4_async(uint32_t dst, const void* src, uint32_t bar) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;\n\tcp.async.mbarrier.arrive.noinc.shared::cta.b64 [%2];"
+                 ::"r"(dst), "l"(src), "r"(bar) : "memory");
+}
+
+// The result of a warp: lane (g, t) holds rows 8 n + 2 t, + 1 and channels g D/8 .. + D/8 - 1.
+template <int D, int NT>
 struct Acc {
-    static constexpr int DL = D / 4;   // channels of a lane
-    float o[D / 8][4];                 // output tile nn: rows g, g, g + 8, g + 8; channels t DL + nn, t DL + DL/2 + nn
-    float m[2], l[2];
-    __device__ __forceinline__ float ch(int row, int i) const {   // channel t DL + i of row g + 8 row
-        return o[i % (DL / 2)][2 * row + i / (DL / 2)];
-    }
+    static constexpr int DL = D / 8;   // channels of a lane
+    float o[NT][D / 16][4];            // tile i: channel 2 i of rows 2 t, 2 t + 1, channel 2 i + 1 of the same
+    float m[NT][2], l[NT][2];
+    __device__ __forceinline__ float ch(int n, int k, int c) const { return o[n][c / 2][2 * (c & 1) + k]; }
 };
 
-template <int D>
-__device__ __forceinline__ void write_part(Part<D>* p, const Acc<D>& c, int rows) {
+template <int D, int NT>
+__device__ __forceinline__ void write_part(Part<D>* p, const Acc<D, NT>& c, int rows) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int r = g + 8 * k;
-        if (r >= rows) continue;
-        float4* o = reinterpret_cast<float4*>(&p->o[r][t * Acc<D>::DL]);
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < Acc<D>::DL / 4; ++i)
-            o[i] = make_float4(c.ch(k, 4 * i), c.ch(k, 4 * i + 1), c.ch(k, 4 * i + 2), c.ch(k, 4 * i + 3));
-        if (t == 0) {
-            p->m[r] = c.m[k];
-            p->l[r] = c.l[k];
+        for (int k = 0; k < 2; ++k) {
+            const int r = 8 * n + 2 * t + k;
+            if (r >= rows) continue;
+            float4* o = reinterpret_cast<float4*>(&p->o[r][g * Acc<D, NT>::DL]);
+#pragma unroll
+            for (int i = 0; i < Acc<D, NT>::DL / 4; ++i)
+                o[i] = make_float4(c.ch(n, k, 4 * i), c.ch(n, k, 4 * i + 1), c.ch(n, k, 4 * i + 2), c.ch(n, k, 4 * i + 3));
+            if (g == 0) {
+                p->m[r] = c.m[n][k];
+                p->l[r] = c.l[n][k];
+            }
         }
-    }
 }
 
 __device__ __forceinline__ float inv_sum(float l) { return l == 0.f ? 0.f : 1.0f / l; }
@@ -133,81 +150,110 @@ __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
 }
 
-template <int D>
-__device__ __forceinline__ void write_out(const AttnArgs& a, const Acc<D>& c, const Seq& s, int h) {
+template <int D, int NT>
+__device__ __forceinline__ void write_out(const AttnArgs& a, const Acc<D, NT>& c, const Seq& s, int h) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, G = a.Hq / a.c.Hkv;
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const int r = g + 8 * k;
-        if (r >= s.n * G) continue;
-        const int row = s.q0 + r / G, head = h * G + r % G;
-        const float f = inv_sum(c.l[k]);
-        const int64_t at = row * a.ldo + (int64_t)head * D + t * Acc<D>::DL;
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < Acc<D>::DL / 4; ++i)
-            store_out4(a.O, at + 4 * i, a.yt, c.ch(k, 4 * i) * f, c.ch(k, 4 * i + 1) * f, c.ch(k, 4 * i + 2) * f,
-                       c.ch(k, 4 * i + 3) * f);
-        if (a.lse && t == 0) a.lse[(int64_t)row * a.Hq + head] = lse_of(c.m[k], c.l[k]);
-    }
+        for (int k = 0; k < 2; ++k) {
+            const int r = 8 * n + 2 * t + k;
+            if (r >= s.n * G) continue;
+            const int row = s.q0 + r / G, head = h * G + r % G;
+            const float f = inv_sum(c.l[n][k]);
+            const int64_t at = row * a.ldo + (int64_t)head * D + g * Acc<D, NT>::DL;
+#pragma unroll
+            for (int i = 0; i < Acc<D, NT>::DL / 4; ++i)
+                store_out4(a.O, at + 4 * i, a.yt, c.ch(n, k, 4 * i) * f, c.ch(n, k, 4 * i + 1) * f,
+                           c.ch(n, k, 4 * i + 2) * f, c.ch(n, k, 4 * i + 3) * f);
+            if (a.lse && g == 0) a.lse[(int64_t)row * a.Hq + head] = lse_of(c.m[n][k], c.l[n][k]);
+        }
 }
 
-// Joins partials part(0) .. part(cnt - 1) of one segment: into `out` (nullable), else the output rows.
-// All threads of the CTA.
-template <int D, class F>
-__device__ __forceinline__ void join(const AttnArgs& a, const Seq& s, int h, int cnt, F part, Part<D>* out) {
-    const int G = a.Hq / a.c.Hkv, rows = s.n * G;
-    for (int k = threadIdx.x; k < rows * (D / 4); k += NW * 32) {
-        const int r = k / (D / 4), d = k % (D / 4) * 4;
-        float m = -INFINITY;
-        for (int j = 0; j < cnt; ++j) m = fmaxf(m, __ldcg(&part(j)->m[r]));
-        float l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int j = 0; j < cnt; ++j) {
-            const Part<D>* p = part(j);
-            const float pm = __ldcg(&p->m[r]), w = pm == -INFINITY ? 0.f : ex2(pm - m);
-            const float pl = __ldcg(&p->l[r]);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(&p->o[r][d]));
-            if (pm == -INFINITY && pl == 0.f) continue;    // saw nothing
-            l += pl * w;
-            o.x += v.x * w;
-            o.y += v.y * w;
-            o.z += v.z * w;
-            o.w += v.w * w;
-        }
-        if (out) {
-            *reinterpret_cast<float4*>(&out->o[r][d]) = o;
-            if (d == 0) {
-                out->m[r] = m;
-                out->l[r] = l;
+// Joins the partials part(0) .. part(cnt - 1) of one segment at row r, channels d .. d + 3: into `out`
+// (nullable), else the output row.  JOIN partials are read at a time; FAR ones come from other CTAs.
+template <bool FAR, class T>
+__device__ __forceinline__ T part_ld(const T* p) { return FAR ? __ldcg(p) : *p; }
+template <bool FAR, int D, class F>
+__device__ __forceinline__ void join(const AttnArgs& a, const Seq& s, int h, int r, int d, int cnt, F part, Part<D>* out) {
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = 0; j0 < cnt; j0 += JOIN) {
+        float pm[JOIN], pl[JOIN];
+        float4 v[JOIN];
+#pragma unroll
+        for (int j = 0; j < JOIN; ++j) {
+            pm[j] = -INFINITY;
+            pl[j] = 0.f;
+            v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (j0 + j < cnt) {
+                const Part<D>* p = part(j0 + j);
+                pm[j] = part_ld<FAR>(&p->m[r]);
+                pl[j] = part_ld<FAR>(&p->l[r]);
+                v[j] = part_ld<FAR>(reinterpret_cast<const float4*>(&p->o[r][d]));
             }
-        } else {
-            const int row = s.q0 + r / G, head = h * G + r % G;
-            const float f = inv_sum(l);
-            store_out4(a.O, row * a.ldo + (int64_t)head * D + d, a.yt, o.x * f, o.y * f, o.z * f, o.w * f);
-            if (a.lse && d == 0) a.lse[(int64_t)row * a.Hq + head] = lse_of(m, l);
         }
+        float top = m;
+#pragma unroll
+        for (int j = 0; j < JOIN; ++j) top = fmaxf(top, pm[j]);
+        const float keep = m == -INFINITY ? 0.f : ex2(m - top);
+        l *= keep;
+        o.x *= keep;
+        o.y *= keep;
+        o.z *= keep;
+        o.w *= keep;
+#pragma unroll
+        for (int j = 0; j < JOIN; ++j) {
+            if (pm[j] == -INFINITY && pl[j] == 0.f) continue;    // saw nothing
+            const float w = pm[j] == -INFINITY ? 1.f : ex2(pm[j] - top);   // -inf with a sum: NaN scores
+            l = fmaf(pl[j], w, l);
+            o.x = fmaf(v[j].x, w, o.x);
+            o.y = fmaf(v[j].y, w, o.y);
+            o.z = fmaf(v[j].z, w, o.z);
+            o.w = fmaf(v[j].w, w, o.w);
+        }
+        m = top;
+    }
+    if (out) {
+        *reinterpret_cast<float4*>(&out->o[r][d]) = o;
+        if (d == 0) {
+            out->m[r] = m;
+            out->l[r] = l;
+        }
+    } else {
+        const int G = a.Hq / a.c.Hkv, row = s.q0 + r / G, head = h * G + r % G;
+        const float f = inv_sum(l);
+        store_out4(a.O, row * a.ldo + (int64_t)head * D + d, a.yt, o.x * f, o.y * f, o.z * f, o.w * f);
+        if (a.lse && d == 0) a.lse[(int64_t)row * a.Hq + head] = lse_of(m, l);
     }
 }
 
 // PT: fp16 terms that carry a weight (one for 16-bit outputs, two for f32).
-template <int D, int PT>
-__global__ void __launch_bounds__(NW * 32, 1) k_attn_decode(const __grid_constant__ Maps maps, const AttnArgs a,
-                                                            uint64_t wait_ns) {
-    using R = Ring<D>;
-    constexpr int KS = D / 16;           // k16 steps of a score
+template <int D, int NT, int PT>
+__global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const __grid_constant__ Maps maps,
+                                                                         const AttnArgs a, uint64_t wait_ns) {
+    using R = Ring<D, NT>;
+    constexpr int NW = R::NW, KS = D / 16;   // k16 steps of a score
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t bars[NW][R::ST];
     __shared__ float2 scales[NW][R::ST]; // the staged blocks' key scale and value scale
     __shared__ int64_t pre[NW * 32 + 1]; // units before each thread's sequences
     __shared__ int64_t wsum[NW];
-    __shared__ int wseg[NW][2];          // segment of each warp's two partials, or -1
+    __shared__ int wseg[NW * 2];         // segment of each warp's two partials, or -1
+    __shared__ bool wfrom[NW * 2];       // that partial has its segment's first unit
+    __shared__ bool wend[NW * 2];        // and its last
+    __shared__ uint32_t runs[NW * 2];    // the CTA's runs of partials of one segment
+    __shared__ int nruns;
     __shared__ int stop;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const uint32_t ring0 = ((smem_u32(raw) + 1023u) & ~1023u) + warp * (R::ST * 2 * R::TILE);
+    uint8_t* ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    const uint32_t ring0 = smem_u32(ring) + warp * (R::ST * 2 * R::TILE);
+    // a warp's partial of the segment that its share ends in goes to its ring, which is done by then
+    auto last_part = [&](int w) { return reinterpret_cast<Part<D>*>(ring + w * (R::ST * 2 * R::TILE)); };
     Space<D>* sp = static_cast<Space<D>*>(a.ws);
     if (lane == 0)
-        for (int i = 0; i < R::ST; ++i) mbar_init(smem_u32(&bars[warp][i]), 1);
+        for (int i = 0; i < R::ST; ++i) mbar_init(smem_u32(&bars[warp][i]), 3);   // the copies' bytes, two scales
     if (threadIdx.x == 0) stop = 0;
     fence_mbar_init();
     pdl_launch_dependents();
@@ -246,8 +292,8 @@ __global__ void __launch_bounds__(NW * 32, 1) k_attn_decode(const __grid_constan
     __syncthreads();
     // Shares: of the CTAs, at least NW units each while there are few; of its warps.
     const int64_t ctas = min((int64_t)gridDim.x, (total + NW - 1) / NW);
-    const bool busy = blockIdx.x < ctas;
-    const int64_t c0 = busy ? total * blockIdx.x / ctas : 0, c1 = busy ? total * (blockIdx.x + 1) / ctas : 0;
+    const int64_t c0 = blockIdx.x < ctas ? total * blockIdx.x / ctas : 0;
+    const int64_t c1 = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : 0;
     const int64_t u0 = c0 + (c1 - c0) * warp / NW, u1 = c0 + (c1 - c0) * (warp + 1) / NW;
 
     auto seek = [&](int64_t u, Cursor& c) {      // u < total
@@ -269,16 +315,15 @@ __global__ void __launch_bounds__(NW * 32, 1) k_attn_decode(const __grid_constan
         c.i = (int)(at % c.s.units);
     };
 
-    if (lane < 2) wseg[warp][lane] = -1;
+    if (lane < 2) wseg[warp * 2 + lane] = -1;
     if (u0 < u1) {
         Cursor cons, prod;
         seek(u0, cons);
         prod = cons;
         int64_t pu = u0;                         // next unit to load
         int pstage = 0;
-        // 32 blocks' pages and scales at a time, one per lane
+        // 32 blocks' places in the pools at a time, one per lane
         int have = 0, used = 0, row = 0;
-        float2 sc = make_float2(0.f, 0.f);
 
         auto produce = [&]() {
             if (pu >= u1) return;
@@ -294,14 +339,13 @@ __global__ void __launch_bounds__(NW * 32, 1) k_attn_decode(const __grid_constan
                             pid = 0;
                         }
                         row = (pid * a.c.Hkv + prod.h) * a.c.page + tok % a.c.page;
-                        sc = make_float2(__ldg(a.c.s[0] + row / BLK), __ldg(a.c.s[1] + row / BLK));
                     }
                 }
                 const int r = __shfl_sync(0xffffffffu, row, used);
-                if (lane == used) scales[warp][pstage] = sc;
-                __syncwarp();                     // lane 0's arrival publishes it
+                const uint32_t bar = smem_u32(&bars[warp][pstage]);
+                if (lane < 2) copy4_async(smem_u32(&scales[warp][pstage]) + 4 * lane, a.c.s[lane] + r / BLK, bar);
                 if (lane == 0) {
-                    const uint32_t bar = smem_u32(&bars[warp][pstage]), dst = ring0 + pstage * 2 * R::TILE;
+                    const uint32_t dst = ring0 + pstage * 2 * R::TILE;
                     mbar_arrive_expect_tx(bar, 2 * R::TILE);
                     tma_load_2d(dst, &maps.t[0], bar, 0, r);
                     tma_load_2d(dst + R::TILE, &maps.t[1], bar, 0, r);
@@ -327,21 +371,19 @@ __global__ void __launch_bounds__(NW * 32, 1) k_attn_decode(const __grid_constan
             const Seq s = cons.s;
             const int h = cons.h, from = cons.i;
             const int until = (int)min((int64_t)s.units, from + (u1 - u));
-            uint32_t q[KS][4];
-            float qf[2];                          // score to log2 units, without the block's scale
-            int rlo[2], rhi[2];
+            uint32_t q[NT][KS][2];
+            float qf[NT][2];                      // score to log2 units, without the block's scale
+            int rlo[NT][2], rhi[NT][2];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int r = g + 8 * k;
+            for (int n = 0; n < NT; ++n) {
+                const int r = 8 * n + g;          // this lane holds row r of Q
                 const bool in = r < s.n * G;
-                const int i = r / G, head = h * G + r % G;
-                rhi[k] = in ? row_hi(i, s.n, s.L, a.causal) : 0;
-                rlo[k] = in ? row_lo(i, s.n, s.L, a.window) : 0;
+                const char* src = static_cast<const char*>(a.Q) +
+                                  2 * ((s.q0 + r / G) * a.ldq + (int64_t)(h * G + r % G) * D + t * (D / 4));
                 uint4 w[KS / 2];
-                const char* src = static_cast<const char*>(a.Q) + 2 * ((s.q0 + i) * a.ldq + (int64_t)head * D + t * (D / 4));
 #pragma unroll
                 for (int j = 0; j < KS / 2; ++j) w[j] = in ? __ldg(reinterpret_cast<const uint4*>(src) + j) : make_uint4(0, 0, 0, 0);
-                float f = 1.f;
+                float f = a.scale * LOG2E;
                 uint32_t v[KS * 2];
 #pragma unroll
                 for (int j = 0; j < KS / 2; ++j) {
@@ -357,134 +399,148 @@ __global__ void __launch_bounds__(NW * 32, 1) k_attn_decode(const __grid_constan
                     mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                     mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                     const int sh = guard_of(__uint_as_float(mx));
-                    f = pow2i(-sh);
+                    f *= pow2i(-sh);
                     const float up = pow2i(sh);
 #pragma unroll
                     for (int j = 0; j < KS * 2; ++j)
                         v[j] = pack_f16(__uint_as_float(v[j] << 16) * up, __uint_as_float(v[j] & 0xFFFF0000u) * up);
                 }
-                qf[k] = a.scale * LOG2E * f;
 #pragma unroll
                 for (int j = 0; j < KS; ++j) {
-                    q[j][k] = v[2 * j];
-                    q[j][2 + k] = v[2 * j + 1];
+                    q[n][j][0] = v[2 * j];
+                    q[n][j][1] = v[2 * j + 1];
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {     // and its scores and outputs are of rows 2 t, 2 t + 1
+                    qf[n][k] = __shfl_sync(0xffffffffu, f, (2 * t + k) * 4);
+                    const int rr = 8 * n + 2 * t + k, i = rr / G;
+                    rhi[n][k] = rr < s.n * G ? row_hi(i, s.n, s.L, a.causal) : 0;
+                    rlo[n][k] = rr < s.n * G ? row_lo(i, s.n, s.L, a.window) : 0;
                 }
             }
             // blocks in [free_lo, free_hi) tokens need no mask
             const int free_hi = row_hi(0, s.n, s.L, a.causal), free_lo = row_lo(s.n - 1, s.n, s.L, a.window);
-            Acc<D> acc;
+            Acc<D, NT> acc;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) acc.o[i][0] = acc.o[i][1] = acc.o[i][2] = acc.o[i][3] = 0.f;
-            acc.m[0] = acc.m[1] = -INFINITY;
-            acc.l[0] = acc.l[1] = 0.f;
+            for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) acc.o[n][i][0] = acc.o[n][i][1] = acc.o[n][i][2] = acc.o[n][i][3] = 0.f;
+                acc.m[n][0] = acc.m[n][1] = -INFINITY;
+                acc.l[n][0] = acc.l[n][1] = 0.f;
+            }
             int ref = -64;                        // largest value-scale exponent so far
 
             for (int i = from; i < until && s.L > 0; ++i) {
-                const uint32_t bar = smem_u32(&bars[warp][stage]);
-                if (!mbar_wait_spin(bar, parity, wait_ns, &stop)) {
+                if (!mbar_wait_spin(smem_u32(&bars[warp][stage]), parity, wait_ns, &stop)) {
                     alive = false;
                     break;
                 }
                 const uint32_t kt = ring0 + stage * 2 * R::TILE, vt = kt + R::TILE;
                 const float2 bs = scales[warp][stage];
                 const int tok0 = (s.first + i) * BLK;
-                float x[4][4];
+                float x[NT][2][4];                // tokens 16 mt + g (rows 2 t, 2 t + 1), + 8 (the same)
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    const int r = 8 * nt + g;
-                    uint32_t w[KS];
-                    if constexpr (D == 128) {
-                        const uint4 p = lds128(kt + r * 128 + (((2 * t) ^ (r & 7)) << 4));
-                        const uint4 p2 = lds128(kt + r * 128 + (((2 * t + 1) ^ (r & 7)) << 4));
-                        w[0] = p.x, w[1] = p.y, w[2] = p.z, w[3] = p.w;
-                        w[4] = p2.x, w[5] = p2.y, w[6] = p2.z, w[7] = p2.w;
-                    } else {
-                        const uint4 p = lds128(kt + r * 64 + ((t ^ ((r >> 1) & 3)) << 4));
-                        w[0] = p.x, w[1] = p.y, w[2] = p.z, w[3] = p.w;
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int mt = 0; mt < 2; ++mt) x[n][mt][0] = x[n][mt][1] = x[n][mt][2] = x[n][mt][3] = 0.f;
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    uint32_t w[2][KS];            // tokens 16 mt + g, + 8
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = 16 * mt + 8 * e + g;
+#pragma unroll
+                        for (int c = 0; c < D / 64; ++c) {
+                            const uint32_t at = D == 128 ? kt + r * 128 + (((2 * t + c) ^ (r & 7)) << 4)
+                                                         : kt + r * 64 + ((t ^ ((r >> 1) & 3)) << 4);
+                            const uint4 y = lds128(at);
+                            w[e][4 * c] = y.x ^ 0x80808080u;
+                            w[e][4 * c + 1] = y.y ^ 0x80808080u;
+                            w[e][4 * c + 2] = y.z ^ 0x80808080u;
+                            w[e][4 * c + 3] = y.w ^ 0x80808080u;
+                        }
                     }
-                    x[nt][0] = x[nt][1] = x[nt][2] = x[nt][3] = 0.f;
 #pragma unroll
                     for (int j = 0; j < KS; ++j) {
-                        const uint32_t v = w[j] ^ 0x80808080u;
-                        mma_16816_f16(x[nt], q[j], codes_f16(v, 0x4140u), codes_f16(v, 0x4342u));
+                        const uint32_t ka[4] = {codes_f16(w[0][j], 0x4140u), codes_f16(w[1][j], 0x4140u),
+                                                codes_f16(w[0][j], 0x4342u), codes_f16(w[1][j], 0x4342u)};
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma_16816_f16(x[n][mt], ka, q[n][j][0], q[n][j][1]);
                     }
                 }
                 // scores in log2 units; a value scale of NaN spoils them like a key scale of NaN
                 const float ks = bs.y == bs.y ? bs.x : bs.y;
-                const float f0 = qf[0] * ks, f1 = qf[1] * ks;
+                float mx[NT][2];
+                bool grows = false;
 #pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    x[nt][0] *= f0;
-                    x[nt][1] *= f0;
-                    x[nt][2] *= f1;
-                    x[nt][3] *= f1;
-                }
-                if (tok0 < free_lo || tok0 + BLK > free_hi) {
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int nt = 0; nt < 4; ++nt)
+                    for (int k = 0; k < 2; ++k) {
+                        const float f = qf[n][k] * ks;
+                        float m = acc.m[n][k];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int tok = tok0 + 8 * nt + 2 * t + (e & 1);
-                            if (tok < rlo[e >> 1] || tok >= rhi[e >> 1]) x[nt][e] = -INFINITY;
+                            float& y = x[n][e >> 1][2 * (e & 1) + k];
+                            y *= f;
+                            if (tok0 < free_lo || tok0 + BLK > free_hi) {
+                                const int tok = tok0 + 8 * e + g;
+                                if (tok < rlo[n][k] || tok >= rhi[n][k]) y = -INFINITY;
+                            }
+                            m = fmaxf(m, y);
                         }
-                }
-                float mx0 = acc.m[0], mx1 = acc.m[1];
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    mx0 = fmaxf(mx0, fmaxf(x[nt][0], x[nt][1]));
-                    mx1 = fmaxf(mx1, fmaxf(x[nt][2], x[nt][3]));
-                }
-                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                        mx[n][k] = m;
+                        grows |= m > acc.m[n][k];
+                    }
                 const int lv0 = bs.y == bs.y ? exp_of(bs.y) : ref;
-                if (__any_sync(0xffffffffu, mx0 > acc.m[0] || mx1 > acc.m[1]) || lv0 > ref) {
+                if (__any_sync(0xffffffffu, grows) || lv0 > ref) {
                     const int nref = max(ref, lv0);
-                    const float a0 = mx0 > acc.m[0] ? ex2(acc.m[0] - mx0) : 1.f;
-                    const float a1 = mx1 > acc.m[1] ? ex2(acc.m[1] - mx1) : 1.f;
                     const float rf = pow2i(max(ref - nref, -126));
                     ref = nref;
-                    acc.m[0] = mx0;
-                    acc.m[1] = mx1;
-                    acc.l[0] *= a0;
-                    acc.l[1] *= a1;
 #pragma unroll
-                    for (int n = 0; n < D / 8; ++n) {
-                        acc.o[n][0] *= a0 * rf;
-                        acc.o[n][1] *= a0 * rf;
-                        acc.o[n][2] *= a1 * rf;
-                        acc.o[n][3] *= a1 * rf;
-                    }
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float f = mx[n][k] > acc.m[n][k] ? ex2(acc.m[n][k] - mx[n][k]) : 1.f;
+                            acc.m[n][k] = mx[n][k];
+                            acc.l[n][k] *= f;
+#pragma unroll
+                            for (int i2 = 0; i2 < D / 16; ++i2) {
+                                acc.o[n][i2][k] *= f * rf;
+                                acc.o[n][i2][2 + k] *= f * rf;
+                            }
+                        }
                 }
                 const int lv = max(lv0, ref - 64);
-                const float s0 = (float)(P_EXP + lv - ref) - (acc.m[0] == -INFINITY ? 0.f : acc.m[0]);
-                const float s1 = (float)(P_EXP + lv - ref) - (acc.m[1] == -INFINITY ? 0.f : acc.m[1]);
-                float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-                for (int nt = 0; nt < 4; ++nt) {
-                    x[nt][0] = ex2(x[nt][0] + s0);
-                    x[nt][1] = ex2(x[nt][1] + s0);
-                    x[nt][2] = ex2(x[nt][2] + s1);
-                    x[nt][3] = ex2(x[nt][3] + s1);
-                    sum0 += x[nt][0] + x[nt][1];
-                    sum1 += x[nt][2] + x[nt][3];
-                }
                 const float back = pow2i(ref - lv - P_EXP);
-                acc.l[0] = fmaf(sum0, back, acc.l[0]);
-                acc.l[1] = fmaf(sum1, back, acc.l[1]);
-                uint32_t p[2][4], p2[2][4];
+                uint32_t p[NT][PT][4];            // weights of tokens 8 e + 2 t, + 1, row g
 #pragma unroll
-                for (int kk = 0; kk < 2; ++kk)
+                for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float sub = (float)(P_EXP + lv - ref) - (acc.m[n][k] == -INFINITY ? 0.f : acc.m[n][k]);
+                        float sum = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float& y = x[n][e >> 1][2 * (e & 1) + k];
+                            y = ex2(y + sub);
+                            sum += y;
+                        }
+                        acc.l[n][k] = fmaf(sum, back, acc.l[n][k]);
+                    }
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float lo = x[2 * kk + (e >> 1)][2 * (e & 1)], hi = x[2 * kk + (e >> 1)][2 * (e & 1) + 1];
-                        p[kk][e] = pack_f16(lo, hi);
+                        const float y0 = x[n][e >> 1][2 * (e & 1)], y1 = x[n][e >> 1][2 * (e & 1) + 1];
+                        const uint32_t hi = pack_f16(y0, y1);
+                        p[n][0][e] = transpose8(hi);
                         if (PT == 2) {
-                            const float2 r = unpack_f16(p[kk][e]);
-                            p2[kk][e] = pack_f16(lo - r.x, hi - r.y);
+                            const float2 r = unpack_f16(hi);
+                            p[n][PT - 1][e] = transpose8(pack_f16(y0 - r.x, y1 - r.y));
                         }
                     }
+                }
 #pragma unroll
                 for (int kk = 0; kk < 2; ++kk) {
                     // tokens 16 kk + 2 t, + 1, + 8, + 9: D/8 neighbouring channels each
@@ -507,15 +563,17 @@ __global__ void __launch_bounds__(NW * 32, 1) k_attn_decode(const __grid_constan
                         for (int e = 0; e < 4; ++e) v[e][j] ^= 0x80808080u;
                         const uint32_t a01 = prmt(v[0][j], v[1][j], 0x5140u), a23 = prmt(v[0][j], v[1][j], 0x7362u);
                         const uint32_t b01 = prmt(v[2][j], v[3][j], 0x5140u), b23 = prmt(v[2][j], v[3][j], 0x7362u);
-                        const uint32_t b[4][2] = {{codes_f16(a01, 0x4140u), codes_f16(b01, 0x4140u)},
-                                                  {codes_f16(a01, 0x4342u), codes_f16(b01, 0x4342u)},
-                                                  {codes_f16(a23, 0x4140u), codes_f16(b23, 0x4140u)},
-                                                  {codes_f16(a23, 0x4342u), codes_f16(b23, 0x4342u)}};
+                        const uint32_t va[2][4] = {{codes_f16(a01, 0x4140u), codes_f16(a01, 0x4342u), codes_f16(b01, 0x4140u),
+                                                    codes_f16(b01, 0x4342u)},
+                                                   {codes_f16(a23, 0x4140u), codes_f16(a23, 0x4342u), codes_f16(b23, 0x4140u),
+                                                    codes_f16(b23, 0x4342u)}};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            mma_16816_f16(acc.o[4 * j + e], p[kk], b[e][0], b[e][1]);
-                            if (PT == 2) mma_16816_f16(acc.o[4 * j + e], p2[kk], b[e][0], b[e][1]);
-                        }
+                        for (int e = 0; e < 2; ++e)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int z = 0; z < PT; ++z)
+                                    mma_16816_f16(acc.o[n][2 * j + e], va[e], p[n][z][2 * kk], p[n][z][2 * kk + 1]);
                     }
                 }
                 __syncwarp();                     // the stage is free
@@ -529,20 +587,28 @@ __global__ void __launch_bounds__(NW * 32, 1) k_attn_decode(const __grid_constan
             u += until - from;
             const float un = pow2i(ref - P_EXP);
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n)
+            for (int n = 0; n < NT; ++n) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc.o[n][e] *= un;
+                for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                acc.l[k] += __shfl_xor_sync(0xffffffffu, acc.l[k], 1);
-                acc.l[k] += __shfl_xor_sync(0xffffffffu, acc.l[k], 2);
+                    for (int e = 0; e < 4; ++e) acc.o[n][i][e] *= un;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    acc.l[n][k] += __shfl_xor_sync(0xffffffffu, acc.l[n][k], 4);
+                    acc.l[n][k] += __shfl_xor_sync(0xffffffffu, acc.l[n][k], 8);
+                    acc.l[n][k] += __shfl_xor_sync(0xffffffffu, acc.l[n][k], 16);
+                }
             }
             if (from == 0 && until == s.units) {
-                write_out<D>(a, acc, s, h);
+                write_out<D, NT>(a, acc, s, h);
             } else {
-                const int slot = from == 0 ? 1 : 0;   // began here and goes on, or began earlier
-                write_part<D>(&sp->warp[blockIdx.x * NW + warp][slot], acc, s.n * G);
-                if (lane == 0) wseg[warp][slot] = s.b * a.c.Hkv + h;
+                const int slot = u == u1 ? 1 : 0;     // the share's last segment, or one that began before it
+                write_part<D, NT>(slot ? last_part(warp) : &sp->warp[blockIdx.x * NW + warp], acc, s.n * G);
+                if (lane == 0) {
+                    wseg[warp * 2 + slot] = s.b * a.c.Hkv + h;
+                    wend[warp * 2 + slot] = until == s.units;
+                    wfrom[warp * 2 + slot] = from == 0;
+                }
             }
             cons.i = until - 1;
             if (u < u1) cons.next(a);
@@ -562,55 +628,65 @@ __global__ void __launch_bounds__(NW * 32, 1) k_attn_decode(const __grid_constan
         }
     }
     __syncthreads();
-    // ---- the CTA's partials, in order: runs of one segment are joined
-    if (threadIdx.x == 0) sp->seg[blockIdx.x][0] = sp->seg[blockIdx.x][1] = -1;
-    if (stop || !busy) return;
-    for (int i = 0; i < 2 * NW;) {
-        const int seg = wseg[i >> 1][i & 1];
-        if (seg < 0) {
-            ++i;
-            continue;
+    // ---- the CTA's partials, in order: runs of one segment are joined, all at once
+    if (warp == 0) {
+        const int seg = lane < 2 * NW ? wseg[lane] : -1;
+        const uint32_t same = __match_any_sync(0xffffffffu, seg);
+        const bool first = seg >= 0 && (same & ((1u << lane) - 1)) == 0;
+        const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+        if (first) runs[__popc(firsts & ((1u << lane) - 1))] = same;
+        if (lane == 0) {
+            nruns = __popc(firsts);
+            sp->seg[blockIdx.x][0] = sp->seg[blockIdx.x][1] = -1;
         }
-        int e = i, cnt = 0;
-        for (; e < 2 * NW && (wseg[e >> 1][e & 1] == seg || wseg[e >> 1][e & 1] < 0); ++e) cnt += wseg[e >> 1][e & 1] == seg;
+    }
+    __syncthreads();
+    if (stop) return;
+    const int quads = a.max_q * (a.Hq / a.c.Hkv) * (D / 4);    // of a run, at most
+    for (int k = threadIdx.x; k < nruns * quads; k += NW * 32) {
+        const uint32_t run = runs[k / quads];
+        const int i = __ffs(run) - 1, seg = wseg[i], h = seg % a.c.Hkv;
         const Seq s = seq_of(a, seg / a.c.Hkv);
-        const int h = seg % a.c.Hkv;
-        // the segment's first unit is here iff its first partial began its segment
-        const bool begins = (i & 1) == 1;
-        bool ends = true;                 // its last unit is here iff the next unit of the CTA is another segment's
-        if (e == 2 * NW && c1 < total) {
-            Cursor c;
-            seek(c1, c);
-            ends = c.i == 0;
-        }
-        auto part = [&](int j) {
-            for (int k = i; k < e; ++k)
-                if (wseg[k >> 1][k & 1] == seg && j-- == 0) return (const Part<D>*)&sp->warp[blockIdx.x * NW + (k >> 1)][k & 1];
-            return (const Part<D>*)nullptr;
+        const int r = k % quads / (D / 4), d = k % (D / 4) * 4;
+        if (r >= s.n * (a.Hq / a.c.Hkv)) continue;
+        const bool begins = wfrom[i], ends = wend[31 - __clz(run)];
+        uint32_t left = run;
+        auto part = [&](int) {               // called in order
+            const int w = __ffs(left) - 1;
+            left &= left - 1;
+            return (const Part<D>*)(w & 1 ? last_part(w >> 1) : &sp->warp[blockIdx.x * NW + (w >> 1)]);
         };
-        Part<D>* out = begins && ends ? nullptr : &sp->cta[blockIdx.x][begins ? 1 : 0];
-        join<D>(a, s, h, cnt, part, out);
-        if (out && threadIdx.x == 0) sp->seg[blockIdx.x][begins ? 1 : 0] = seg;
-        i = e;
+        join<false, D>(a, s, h, r, d, __popc(run), part, begins && ends ? nullptr : &sp->cta[blockIdx.x][begins ? 1 : 0]);
+        if (!(begins && ends) && r == 0 && d == 0) sp->seg[blockIdx.x][begins ? 1 : 0] = seg;
     }
 }
 
 // Joins the segments that lie across CTAs: CTA i takes the one that began in share i.
+constexpr int JOIN_THREADS = 256;
 template <int D>
-__global__ void __launch_bounds__(NW * 32) k_attn_join(const AttnArgs a) {
+__global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(const AttnArgs a) {
     pdl_launch_dependents();
     pdl_wait();
     const Space<D>* sp = static_cast<const Space<D>*>(a.ws);
-    const int i = blockIdx.x, seg = __ldcg(&sp->seg[i][1]);
-    if (seg < 0) return;
+    const int i = blockIdx.x, lane = threadIdx.x & 31, seg = __ldcg(&sp->seg[i][1]);
     int cnt = 1;
-    while (i + cnt < (int)gridDim.x && __ldcg(&sp->seg[i + cnt][0]) == seg) ++cnt;
+    while (true) {                     // the shares after it that go on with the segment
+        const int j = i + cnt + lane;
+        const bool more = j < (int)gridDim.x && __ldcg(&sp->seg[j][0]) == seg;
+        const int k = __ffs(~__ballot_sync(0xffffffffu, more));
+        cnt += k ? k - 1 : 32;
+        if (k) break;
+    }
+    if (seg < 0) return;
     const Seq s = seq_of(a, seg / a.c.Hkv);
-    join<D>(a, s, seg % a.c.Hkv, cnt, [&](int j) { return j == 0 ? &sp->cta[i][1] : &sp->cta[i + j][0]; }, nullptr);
+    for (int k = threadIdx.x; k < s.n * (a.Hq / a.c.Hkv) * (D / 4); k += JOIN_THREADS)
+        join<true, D>(a, s, seg % a.c.Hkv, k / (D / 4), k % (D / 4) * 4, cnt,
+                [&](int j) { return j == 0 ? &sp->cta[i][1] : &sp->cta[i + j][0]; }, (Part<D>*)nullptr);
 }
 
-template <int D, int PT>
+template <int D, int NT, int PT>
 cudaError_t run(const AttnArgs& a, cudaStream_t s) {
+    using R = Ring<D, NT>;
     Maps maps;
     const uint64_t dims[2] = {(uint64_t)D, (uint64_t)a.c.pages * a.c.Hkv * a.c.page}, strides[1] = {(uint64_t)D};
     const uint32_t box[2] = {(uint32_t)D, (uint32_t)BLK};
@@ -618,13 +694,22 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
         if (!encode_tiled(&maps.t[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.c.q[i], dims, strides, box,
                           D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
             return cudaErrorInvalidValue;
-    constexpr size_t smem = Ring<D>::BYTES + 1024;
-    cudaError_t e = cudaFuncSetAttribute(k_attn_decode<D, PT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    constexpr size_t smem = R::BYTES + 1024;
+    cudaError_t e = cudaFuncSetAttribute(k_attn_decode<D, NT, PT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const unsigned ctas = (unsigned)std::min(num_sms(), MAX_CTAS);
-    e = launch_pdl(k_attn_decode<D, PT>, dim3(ctas), dim3(NW * 32), smem, s, maps, a, (uint64_t)options().wait_ns.load());
+    e = launch_pdl(k_attn_decode<D, NT, PT>, dim3(ctas), dim3(R::NW * 32), smem, s, maps, a, (uint64_t)options().wait_ns.load());
     if (e != cudaSuccess) return e;
-    return launch_pdl(k_attn_join<D>, dim3(ctas), dim3(NW * 32), 0, s, a);
+    return launch_pdl(k_attn_join<D>, dim3(ctas), dim3(JOIN_THREADS), 0, s, a);
+}
+
+template <int D, int NT>
+cudaError_t run_as(const AttnArgs& a, cudaStream_t s) {
+    return a.yt == CQ_F32 ? run<D, NT, 2>(a, s) : run<D, NT, 1>(a, s);
+}
+template <int D>
+cudaError_t run_d(const AttnArgs& a, cudaStream_t s) {
+    return a.max_q * (a.Hq / a.c.Hkv) <= 8 ? run_as<D, 1>(a, s) : run_as<D, 2>(a, s);
 }
 
 }  // namespace
@@ -632,10 +717,7 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
 bool decode_serves(int64_t rows) { return rows <= ROWS; }
 size_t decode_workspace(int64_t D) { return D == 128 ? sizeof(Space<128>) : sizeof(Space<64>); }
 
-cudaError_t launch_decode(const AttnArgs& a, cudaStream_t s) {
-    if (a.D == 128) return a.yt == CQ_F32 ? run<128, 2>(a, s) : run<128, 1>(a, s);
-    return a.yt == CQ_F32 ? run<64, 2>(a, s) : run<64, 1>(a, s);
-}
+cudaError_t launch_decode(const AttnArgs& a, cudaStream_t s) { return a.D == 128 ? run_d<128>(a, s) : run_d<64>(a, s); }
 
 }  // namespace kv8
 }  // namespace cq
