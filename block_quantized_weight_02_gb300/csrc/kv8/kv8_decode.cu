@@ -37,17 +37,13 @@ constexpr int ROWS = 16;
 constexpr int MAX_CTAS = 256;         // workspace bound
 constexpr int MAX_NW = 12;
 constexpr int P_EXP = 15;             // weights carry 2^15
-constexpr int JOIN = 8;               // partials in flight while joining
 
 struct Maps {
     CUtensorMap t[2];                 // keys, values: {D, pages * Hkv * page}, box {D, 32}
 };
 
 template <int D>
-struct Part {
-    float o[ROWS][D];
-    float m[ROWS], l[ROWS];
-};
+using Part = PartOf<D, ROWS>;
 // Workspace: partials of segments that end inside a warp's share, partials of the CTAs, the CTAs' two segments.
 template <int D>
 struct Space {
@@ -145,11 +141,6 @@ __device__ __forceinline__ void write_part(Part<D>* p, const Acc<D, NT>& c, int 
         }
 }
 
-__device__ __forceinline__ float inv_sum(float l) { return l == 0.f ? 0.f : 1.0f / l; }
-__device__ __forceinline__ float lse_of(float m, float l) {
-    return l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
-}
-
 template <int D, int NT>
 __device__ __forceinline__ void write_out(const AttnArgs& a, const Acc<D, NT>& c, const Seq& s, int h) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, G = a.Hq / a.c.Hkv;
@@ -168,64 +159,6 @@ __device__ __forceinline__ void write_out(const AttnArgs& a, const Acc<D, NT>& c
                            c.ch(n, k, 4 * i + 2) * f, c.ch(n, k, 4 * i + 3) * f);
             if (a.lse && g == 0) a.lse[(int64_t)row * a.Hq + head] = lse_of(c.m[n][k], c.l[n][k]);
         }
-}
-
-// Joins the partials part(0) .. part(cnt - 1) of one segment at row r, channels d .. d + 3: into `out`
-// (nullable), else the output row.  JOIN partials are read at a time; FAR ones come from other CTAs.
-template <bool FAR, class T>
-__device__ __forceinline__ T part_ld(const T* p) { return FAR ? __ldcg(p) : *p; }
-template <bool FAR, int D, class F>
-__device__ __forceinline__ void join(const AttnArgs& a, const Seq& s, int h, int r, int d, int cnt, F part, Part<D>* out) {
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j0 = 0; j0 < cnt; j0 += JOIN) {
-        float pm[JOIN], pl[JOIN];
-        float4 v[JOIN];
-#pragma unroll
-        for (int j = 0; j < JOIN; ++j) {
-            pm[j] = -INFINITY;
-            pl[j] = 0.f;
-            v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (j0 + j < cnt) {
-                const Part<D>* p = part(j0 + j);
-                pm[j] = part_ld<FAR>(&p->m[r]);
-                pl[j] = part_ld<FAR>(&p->l[r]);
-                v[j] = part_ld<FAR>(reinterpret_cast<const float4*>(&p->o[r][d]));
-            }
-        }
-        float top = m;
-#pragma unroll
-        for (int j = 0; j < JOIN; ++j) top = fmaxf(top, pm[j]);
-        const float keep = m == -INFINITY ? 0.f : ex2(m - top);
-        l *= keep;
-        o.x *= keep;
-        o.y *= keep;
-        o.z *= keep;
-        o.w *= keep;
-#pragma unroll
-        for (int j = 0; j < JOIN; ++j) {
-            if (pm[j] == -INFINITY && pl[j] == 0.f) continue;    // saw nothing
-            const float w = pm[j] == -INFINITY ? 1.f : ex2(pm[j] - top);   // -inf with a sum: NaN scores
-            l = fmaf(pl[j], w, l);
-            o.x = fmaf(v[j].x, w, o.x);
-            o.y = fmaf(v[j].y, w, o.y);
-            o.z = fmaf(v[j].z, w, o.z);
-            o.w = fmaf(v[j].w, w, o.w);
-        }
-        m = top;
-    }
-    if (out) {
-        *reinterpret_cast<float4*>(&out->o[r][d]) = o;
-        if (d == 0) {
-            out->m[r] = m;
-            out->l[r] = l;
-        }
-    } else {
-        const int G = a.Hq / a.c.Hkv, row = s.q0 + r / G, head = h * G + r % G;
-        const float f = inv_sum(l);
-        store_out4(a.O, row * a.ldo + (int64_t)head * D + d, a.yt, o.x * f, o.y * f, o.z * f, o.w * f);
-        if (a.lse && d == 0) a.lse[(int64_t)row * a.Hq + head] = lse_of(m, l);
-    }
 }
 
 // PT: fp16 terms that carry a weight (one for 16-bit outputs, two for f32).
@@ -656,7 +589,7 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
             left &= left - 1;
             return (const Part<D>*)(w & 1 ? last_part(w >> 1) : &sp->warp[blockIdx.x * NW + (w >> 1)]);
         };
-        join<false, D>(a, s, h, r, d, __popc(run), part, begins && ends ? nullptr : &sp->cta[blockIdx.x][begins ? 1 : 0]);
+        join<false, D>(a, s.q0, h, r, r, d, __popc(run), part, begins && ends ? nullptr : &sp->cta[blockIdx.x][begins ? 1 : 0]);
         if (!(begins && ends) && r == 0 && d == 0) sp->seg[blockIdx.x][begins ? 1 : 0] = seg;
     }
 }
@@ -680,7 +613,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(const AttnArgs a) {
     if (seg < 0) return;
     const Seq s = seq_of(a, seg / a.c.Hkv);
     for (int k = threadIdx.x; k < s.n * (a.Hq / a.c.Hkv) * (D / 4); k += JOIN_THREADS)
-        join<true, D>(a, s, seg % a.c.Hkv, k / (D / 4), k % (D / 4) * 4, cnt,
+        join<true, D>(a, s.q0, seg % a.c.Hkv, k / (D / 4), k / (D / 4), k % (D / 4) * 4, cnt,
                 [&](int j) { return j == 0 ? &sp->cta[i][1] : &sp->cta[i + j][0]; }, (Part<D>*)nullptr);
 }
 

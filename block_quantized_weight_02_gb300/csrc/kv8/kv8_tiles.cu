@@ -1,0 +1,658 @@
+// Attention over the 8-bit cache for many query rows: tiles of 256 rows x 128 tokens on
+// the 5th-generation tensor cores.
+//
+// A row is a (token, head of the group) pair, so the heads that share a KV head share its
+// tiles.  Per 128 tokens a CTA does S = Q K^T (Q and K in shared memory, S in tensor
+// memory) and O += P V (P in tensor memory over S, V in shared memory token-major) for two
+// 128-row tiles A and B in turn: while one's softmax runs, the tensor cores have the other.
+//   warps 0-3, 4-7  softmax of A and B, one row a thread: maximum, weights, sum; queries in, outputs out
+//   warps 8-11      codes -> fp16 (exactly), into the 128-byte-swizzled operand tiles
+//   warp 12         issues the products
+//   warp 13         TMA loads of the codes by page, 32 tokens a box, and their scales
+// A key block's scale joins the scores in f32, a value block's scale 2^lv the exponent:
+// w = 2^(s - m + 10 + lv - ref), with m at most 5 below the row's maximum (O is only rescaled
+// when the maximum has grown by more) and ref the largest lv so far; the normaliser takes
+// w 2^(ref - lv).  For f32 outputs P goes in two fp16 terms, two products each.
+//
+// The work is the list of all (row tile, KV head, 128 tokens), cut into one equal share per
+// SM.  A first small kernel lays the list out (only the device knows the lengths), a third
+// joins the tiles that lie across shares, in share order.
+#include "attn_common.cuh"
+
+namespace cq {
+namespace kv8 {
+namespace {
+
+constexpr int TM = 128;                // rows of a tensor-core tile
+constexpr int ROWS = 2 * TM;           // rows of a work item
+constexpr int TN = 128;                // tokens of a step
+constexpr int NB = TN / BLK;           // blocks of a step
+constexpr int MAX_CTAS = 256;          // workspace bound
+constexpr int THREADS = 448;
+constexpr int CONV_WARP = 8, MMA_WARP = 12, LOAD_WARP = 13;
+constexpr int PLAN_THREADS = 1024;
+constexpr float W_EXP = 10.f, GROW = 5.f;
+constexpr int HS = 4;                  // fp16 operand tiles in the ring (keys and values alternate)
+constexpr int SS = 8;                  // steps whose scales are kept
+
+struct Maps {
+    CUtensorMap t[2];
+};
+
+template <int D>
+using Part = PartOf<D, ROWS>;
+struct alignas(16) Item {
+    int b, f0, tok0, steps;            // sequence, first row, first token, steps of TN tokens (none visible: 1)
+};
+struct Start {
+    int slot, h, step;                 // where a CTA's share begins
+};
+// Workspace: partials, the CTAs' segments and starts, the list.
+template <int D>
+struct Space {
+    Part<D> cta[MAX_CTAS][2];
+    int seg[MAX_CTAS][2];              // (slot * Hkv + h) of cta[i][0] (began earlier) and cta[i][1] (began here, goes on)
+    Start start[MAX_CTAS];
+    int total, ok;
+    Item item[1];                      // [slots]
+};
+
+int64_t slots_of(int64_t T, int64_t G, int64_t B) { return T * G / ROWS + B; }
+
+// ---- the list ------------------------------------------------------------------------------------------------------
+// Sequence b owns the slots floor(q_start[b] G / ROWS) + b .., since n rows make at most floor(n G / ROWS) + 1 tiles.
+template <int D>
+__global__ void __launch_bounds__(PLAN_THREADS) k_tiles_plan(const AttnArgs a, int slots, int ctas) {
+    pdl_launch_dependents();
+    pdl_wait();
+    __shared__ int64_t wsum[PLAN_THREADS / 32];
+    Space<D>* sp = static_cast<Space<D>*>(a.ws);
+    const int G = a.Hq / a.c.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    bool bad = false;
+    for (int b = threadIdx.x; b < a.c.B; b += PLAN_THREADS) {
+        const int L = __ldg(a.b.lens + b);
+        if (!rows_ok(__ldg(a.b.q_start + b), __ldg(a.b.q_start + b + 1), a.b.T, a.max_q) || L < 0 || L > a.c.ldt * a.c.page) bad = true;
+    }
+    for (int i = threadIdx.x; i < MAX_CTAS; i += PLAN_THREADS) sp->seg[i][0] = sp->seg[i][1] = -1;
+    if (__syncthreads_or(bad)) {
+        if (threadIdx.x == 0) {
+            set_err(a.b.err, DEV_INDEX);
+            sp->total = 0;
+        }
+        return;
+    }
+    const int per = (slots + PLAN_THREADS - 1) / PLAN_THREADS;      // neighbouring slots of a thread
+    const int s0 = min(threadIdx.x * per, slots), s1 = min(s0 + per, slots);
+    auto key = [&](int b) { return (int64_t)__ldg(a.b.q_start + b) * G / ROWS + b; };
+    int64_t mine = 0;
+    int b = 0, n = a.c.B;
+    if (s0 < s1)
+        while (n > 1) {                                            // the largest b whose slots start at or before s0
+            const int half = n / 2;
+            if (key(b + half) <= s0) b += half, n -= half; else n = half;
+        }
+    for (int s = s0; s < s1; ++s) {
+        while (b + 1 < a.c.B && key(b + 1) <= s) ++b;
+        Item it = {b, 0, 0, 0};
+        const int q0 = __ldg(a.b.q_start + b), nq = __ldg(a.b.q_start + b + 1) - q0, L = __ldg(a.b.lens + b);
+        const int64_t f0 = (s - key(b)) * ROWS, rows = (int64_t)nq * G;
+        if (f0 >= 0 && f0 < rows) {
+            const int first = (int)(f0 / G), last = (int)((min(f0 + ROWS, rows) - 1) / G);
+            const int lo = row_lo(first, nq, L, a.window) / BLK * BLK, hi = row_hi(last, nq, L, a.causal);
+            it.f0 = (int)f0;
+            it.tok0 = lo;
+            it.steps = hi > lo ? (hi - lo + TN - 1) / TN : 1;
+        }
+        sp->item[s] = it;
+        mine += (int64_t)it.steps * a.c.Hkv;
+    }
+    int64_t inc = mine;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int64_t at = inc - mine, total = 0;
+    for (int i = 0; i < PLAN_THREADS / 32; ++i) {
+        if (i < warp) at += wsum[i];
+        total += wsum[i];
+    }
+    if (total > INT32_MAX) {
+        if (threadIdx.x == 0) {
+            set_err(a.b.err, DEV_INDEX);
+            sp->total = 0;
+        }
+        return;
+    }
+    if (threadIdx.x == 0) sp->total = (int)total;
+    // the shares that begin in this thread's slots
+    const int q = (int)(total / ctas), rem = (int)(total % ctas);
+    for (int s = s0; s < s1; ++s) {
+        const int steps = sp->item[s].steps;
+        const int64_t end = at + (int64_t)steps * a.c.Hkv;
+        if (steps) {
+            int i = q ? (int)min((int64_t)ctas, max((int64_t)0, at / (q + 1))) : (int)min((int64_t)ctas, at);
+            for (; i < ctas; ++i) {
+                const int64_t u = (int64_t)i * q + min(i, rem);
+                if (u >= end) break;
+                if (u >= at) sp->start[i] = {s, (int)((u - at) / steps), (int)((u - at) % steps)};
+            }
+        }
+        at = end;
+    }
+}
+
+// ---- shared memory -------------------------------------------------------------------------------------------------
+template <int D>
+struct Smem {
+    static constexpr int QT = TM * D * 2;         // a query tile: D/64 chunks of [128 rows][128 B], swizzled
+    static constexpr int HT = TN * D * 2;         // an fp16 operand tile, the same
+    static constexpr int RT = TN * D;             // codes
+    static constexpr int Q = 0, H = 2 * QT, R = H + HS * HT, MISC = R + 2 * RT;
+    static constexpr int NBAR = 4 + 2 * HS + SS + 8;
+    static constexpr int SC = MISC + NBAR * 8;    // float2 [SS][NB]
+    static constexpr int END = SC + SS * NB * 8 + 16;
+};
+
+// MN-major operand (rows of 64 16-bit elements along N, one row per k; 128-byte swizzle): 8-row
+// groups 1024 bytes apart, the next 64 elements of N `lbo` bytes on.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t lbo) {
+    return (smem_desc_sw128(saddr) & ~(0x3FFFull << 16)) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16);
+}
+
+// The parts of items that a CTA's share is made of, in order; every role walks the same list.
+struct Walk {
+    int slot, h, step, left;
+    Item it;
+    int from, until;      // steps of the current part
+    template <int D>
+    __device__ __forceinline__ bool next(const AttnArgs& a, const Space<D>* sp, bool first) {
+        if (!first) {
+            step = until;
+            if (step == it.steps) {
+                step = 0;
+                if (++h == a.c.Hkv) {
+                    h = 0;
+                    ++slot;
+                }
+            }
+        }
+        if (left == 0) return false;
+        const int4* p = reinterpret_cast<const int4*>(&sp->item[slot]);
+        int4 v = __ldcg(p);
+        while (v.w == 0) {
+            ++slot;
+            v = __ldcg(++p);
+        }
+        it = {v.x, v.y, v.z, v.w};
+        from = step;
+        until = min(it.steps, step + left);
+        left -= until - from;
+        return true;
+    }
+};
+
+template <int D, int PT>
+__global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Maps maps, const AttnArgs a, uint64_t wait_ns) {
+    using M = Smem<D>;
+    extern __shared__ __align__(1024) uint8_t raw[];
+    uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    const uint32_t sb = smem_u32(smem), bar0 = sb + M::MISC;
+    const uint32_t raw_full = bar0, raw_empty = bar0 + 16, h_full = bar0 + 32, h_empty = h_full + 8 * HS,
+                   sc_full = h_empty + 8 * HS, q_ready = sc_full + 8 * SS, s_full = q_ready + 16, p_ready = s_full + 16,
+                   o_full = p_ready + 16;
+    float2* scales = reinterpret_cast<float2*>(smem + M::SC);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + M::SC + SS * NB * 8);
+    volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    const volatile int* never = reinterpret_cast<const volatile int*>(tmem_slot + 2);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(raw_full + 8 * i, 1);
+            mbar_init(raw_empty + 8 * i, 4);
+            mbar_init(q_ready + 8 * i, 4);
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(p_ready + 8 * i, 4);
+            mbar_init(o_full + 8 * i, 1);
+        }
+        for (int i = 0; i < HS; ++i) {
+            mbar_init(h_full + 8 * i, 4);
+            mbar_init(h_empty + 8 * i, 1);
+        }
+        for (int i = 0; i < SS; ++i) mbar_init(sc_full + 8 * i, 1);
+        tmem_slot[1] = tmem_slot[2] = 0;
+        fence_mbar_init();
+    }
+    if (warp == MMA_WARP) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    auto tm_s = [&](int x) { return tmem + x * TN; };            // scores, then weights
+    auto tm_o = [&](int x) { return tmem + 2 * TN + x * D; };
+    pdl_launch_dependents();
+    pdl_wait();
+
+    Space<D>* sp = static_cast<Space<D>*>(a.ws);
+    const int total = __ldcg(&sp->total), G = a.Hq / a.c.Hkv;
+    Walk w;
+    {
+        const int q = total / (int)gridDim.x, rem = total % (int)gridDim.x;
+        w.left = q + ((int)blockIdx.x < rem);
+        if (w.left) {
+            w.slot = __ldcg(&sp->start[blockIdx.x].slot);
+            w.h = __ldcg(&sp->start[blockIdx.x].h);
+            w.step = __ldcg(&sp->start[blockIdx.x].step);
+        }
+    }
+    // Every wait is bounded; the first to give up stops the CTA.
+    bool alive = true;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (alive && !mbar_wait_spin(bar, parity, wait_ns, stop)) {
+            alive = false;
+            *stop = 1;
+            set_err(a.b.err, DEV_TIMEOUT);
+        }
+        return alive;
+    };
+    auto wait_warp = [&](uint32_t bar, uint32_t parity) {     // the same answer for all lanes
+        wait(bar, parity);
+        return alive = __all_sync(0xffffffffu, alive);
+    };
+    auto nq_of = [&](const Item& it) {       // 128-row tiles of an item
+        const int n = __ldg(a.b.q_start + it.b + 1) - __ldg(a.b.q_start + it.b);
+        return (int64_t)n * G - it.f0 > TM ? 2 : 1;
+    };
+
+    if (warp < CONV_WARP) {
+        // ---- softmax: thread = row of tile x
+        const int x = warp >> 2, row = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;        // tensor-memory lane of the warp's first row
+        uint32_t parts = 0, steps = 0, tile = 0;                  // of this tile: parts, steps; of the CTA: steps
+        for (bool first = true; alive && w.next<D>(a, sp, first); first = false) {
+            const int n = w.until - w.from;
+            const int q0 = __ldg(a.b.q_start + w.it.b), nq = __ldg(a.b.q_start + w.it.b + 1) - q0, L = __ldg(a.b.lens + w.it.b);
+            const int64_t rows = (int64_t)nq * G - w.it.f0;
+            if (rows <= x * TM) {
+                tile += n;
+                continue;
+            }
+            const int r = x * TM + row, f = w.it.f0 + r;
+            const bool in = r < rows;
+            const int i = f / G, head = w.h * G + f % G;
+            float qf = a.scale * LOG2E;
+            {
+                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.Q) + (q0 + i) * a.ldq + (int64_t)head * D);
+                uint4 v[D / 8];
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) v[c] = in ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                if (a.xt == CQ_BF16) {
+                    uint32_t mx = 0;
+                    auto top = [&](uint32_t y) { mx = max(mx, max((y << 16) & 0x7FFFFFFFu, y & 0x7FFF0000u)); };
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) top(v[c].x), top(v[c].y), top(v[c].z), top(v[c].w);
+                    const int sh = guard_of(__uint_as_float(mx));
+                    const float up = pow2i(sh);
+                    qf *= pow2i(-sh);
+                    auto cv = [&](uint32_t y) { return pack_f16(__uint_as_float(y << 16) * up, __uint_as_float(y & 0xFFFF0000u) * up); };
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) v[c] = make_uint4(cv(v[c].x), cv(v[c].y), cv(v[c].z), cv(v[c].w));
+                }
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c)
+                    *reinterpret_cast<uint4*>(smem + M::Q + x * M::QT + (c >> 3) * (TM * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[c];
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_ready + 8 * x);
+
+            const int rhi = in ? row_hi(i, nq, L, a.causal) : 0, rlo = in ? row_lo(i, nq, L, a.window) : 0;
+            // steps inside [free_lo, free_hi) need no mask in this warp
+            const int wf = w.it.f0 + x * TM + (warp & 3) * 32, wl = (int)min((int64_t)wf + 31, w.it.f0 + rows - 1);
+            const int free_hi = wf < w.it.f0 + rows ? row_hi(wf / G, nq, L, a.causal) : 0;
+            const int free_lo = wf < w.it.f0 + rows ? row_lo(wl / G, nq, L, a.window) : INT32_MAX;
+            float m = -INFINITY, l = 0.f;
+            int ref = -64;
+            for (int j = 0; j < n; ++j, ++steps, ++tile) {
+                if (!wait_warp(s_full + 8 * x, steps & 1) || !wait_warp(sc_full + 8 * (tile % SS), tile / SS & 1)) break;
+                tc_fence_after();
+                const int t0 = w.it.tok0 + (w.from + j) * TN;
+                const bool masked = t0 < free_lo || t0 + TN > free_hi;
+                float km[NB];
+                int lv[NB], nref = ref;
+#pragma unroll
+                for (int c = 0; c < NB; ++c) {
+                    const float2 s = scales[tile % SS * NB + c];
+                    const bool nan = s.y != s.y;
+                    km[c] = qf * (nan ? s.y : s.x);
+                    lv[c] = nan ? -64 : exp_of(s.y);
+                    nref = max(nref, lv[c]);
+                }
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < NB; ++c) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(tm_s(x) + lanes + 32 * c, v);
+                    tmem_ld_wait();
+                    float mx = -INFINITY;
+                    if (masked) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const int tok = t0 + 32 * c + e;
+                            mx = fmaxf(mx, tok >= rlo && tok < rhi ? __uint_as_float(v[e]) : -INFINITY);
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[e]));
+                    }
+                    top = fmaxf(top, mx * km[c]);
+                }
+                const bool grow = top > m + GROW || (m == -INFINITY && top > m);
+                if (__any_sync(0xffffffffu, grow) || nref > ref) {
+                    const float nm = grow ? top : m;
+                    const float fm = grow ? ex2(m - nm) : 1.f, fo = fm * pow2i(max(ref - nref, -126));
+                    m = nm;
+                    l *= fm;
+                    ref = nref;
+                    if (j > 0) {
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t v[32];
+                            tmem_ld_32x32b_x32(tm_o(x) + lanes + 32 * c, v);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * fo);
+                            tmem_st_32x32b_x32(tm_o(x) + lanes + 32 * c, v);
+                        }
+                    }
+                }
+                // Scores of 2^20 and more are rounded before m is taken off, as they were for m: a fused step
+                // would leave their own rounding, which is then no longer small.
+                const bool big = __any_sync(0xffffffffu, fabsf(m) > 1048576.f && m != -INFINITY);
+                uint32_t low[PT == 2 ? 2 : 1][16];      // second terms that wait for their columns to be read
+#pragma unroll
+                for (int c = 0; c < NB; ++c) {
+                    const int lc = max(lv[c], ref - 64);
+                    const float sub = W_EXP + (float)(lc - ref) - (m == -INFINITY ? 0.f : m);
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(tm_s(x) + lanes + 32 * c, v);
+                    tmem_ld_wait();
+                    float kc = km[c];
+                    if (big) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * kc);
+                        kc = 1.f;
+                    }
+                    float sum = 0.f;
+                    uint32_t p[16], p2[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float y0 = ex2(fmaf(__uint_as_float(v[2 * e]), kc, sub));
+                        float y1 = ex2(fmaf(__uint_as_float(v[2 * e + 1]), kc, sub));
+                        if (masked) {
+                            const int tok = t0 + 32 * c + 2 * e;
+                            y0 = tok >= rlo && tok < rhi ? y0 : 0.f;
+                            y1 = tok + 1 >= rlo && tok + 1 < rhi ? y1 : 0.f;
+                        }
+                        sum += y0 + y1;
+                        p[e] = pack_f16(y0, y1);
+                        if (PT == 2) {
+                            const float2 h = unpack_f16(p[e]);
+                            p2[e] = pack_f16(y0 - h.x, y1 - h.y);
+                        }
+                    }
+                    l = fmaf(sum, pow2i(ref - lc - (int)W_EXP), l);
+                    tmem_st_32x32b_x16(tm_s(x) + lanes + 16 * c, p);
+                    if (PT == 2) {
+                        // columns 64 + 16 c lie over the scores of block 2 + c / 2
+                        if (c == 2) {
+                            tmem_st_32x32b_x16(tm_s(x) + lanes + 64, low[0]);
+                            tmem_st_32x32b_x16(tm_s(x) + lanes + 80, low[PT - 1]);
+                        }
+                        if (c == 3) {
+                            tmem_st_32x32b_x16(tm_s(x) + lanes + 96, low[0]);
+                            tmem_st_32x32b_x16(tm_s(x) + lanes + 112, p2);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) low[c == 1 ? PT - 1 : 0][e] = p2[e];
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_ready + 8 * x);
+            }
+            if (!wait_warp(o_full + 8 * x, parts & 1)) break;
+            ++parts;
+            tc_fence_after();
+            const bool begins = w.from == 0, ends = w.until == w.it.steps;
+            const float un = pow2i(ref - (int)W_EXP), inv = begins && ends ? un * inv_sum(l) : un;
+            Part<D>* part = &sp->cta[blockIdx.x][begins ? 1 : 0];
+            const int64_t at = (q0 + i) * a.ldo + (int64_t)head * D;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(tm_o(x) + lanes + 32 * c, v);
+                tmem_ld_wait();
+                if (in) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float y0 = __uint_as_float(v[e]) * inv, y1 = __uint_as_float(v[e + 1]) * inv;
+                        const float y2 = __uint_as_float(v[e + 2]) * inv, y3 = __uint_as_float(v[e + 3]) * inv;
+                        if (begins && ends) store_out4(a.O, at + 32 * c + e, a.yt, y0, y1, y2, y3);
+                        else *reinterpret_cast<float4*>(&part->o[r][32 * c + e]) = make_float4(y0, y1, y2, y3);
+                    }
+                }
+            }
+            tc_fence_before();
+            if (in) {
+                if (begins && ends) {
+                    if (a.lse) a.lse[(int64_t)(q0 + i) * a.Hq + head] = lse_of(m, l);
+                } else {
+                    part->m[r] = m;
+                    part->l[r] = l;
+                }
+            }
+            if (!(begins && ends) && threadIdx.x == 0) sp->seg[blockIdx.x][begins ? 1 : 0] = w.slot * a.c.Hkv + w.h;
+        }
+    } else if (warp < MMA_WARP) {
+        // ---- codes -> fp16: thread = token; keys and values of a step alternate
+        const int tok = threadIdx.x - CONV_WARP * 32;
+        uint32_t k = 0;                          // operand tiles so far
+        for (bool first = true; alive && w.next<D>(a, sp, first); first = false) {
+            for (int j = 0; j < 2 * (w.until - w.from) && alive; ++j, ++k) {
+                const uint32_t rs = k & 1, hs = k % HS;
+                if (!wait_warp(raw_full + 8 * rs, k / 2 & 1) || !wait_warp(h_empty + 8 * hs, (k / HS & 1) ^ 1)) break;
+                const uint8_t* src = smem + M::R + rs * M::RT + tok * D;
+                uint8_t* dst = smem + M::H + hs * M::HT + tok * 128;
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c) {
+                    const int at = D == 128 ? (c ^ (tok & 7)) : (c ^ ((tok >> 1) & 3));
+                    const uint4 v = *reinterpret_cast<const uint4*>(src + at * 16);
+                    const uint32_t u[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int ch = (2 * c + e) & 7;       // 16-byte chunk of the 64-channel row
+                        *reinterpret_cast<uint4*>(dst + (c >> 2) * (TN * 128) + ((ch ^ (tok & 7)) << 4)) =
+                            make_uint4(codes_f16(u[2 * e], 0x4140u), codes_f16(u[2 * e], 0x4342u),
+                                       codes_f16(u[2 * e + 1], 0x4140u), codes_f16(u[2 * e + 1], 0x4342u));
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(raw_empty + 8 * rs);
+                    mbar_arrive(h_full + 8 * hs);
+                }
+            }
+        }
+    } else if (warp == MMA_WARP) {
+        // ---- products, from one thread
+        if (lane == 0) {
+            constexpr uint32_t id_qk = idesc_f16(TM, TN, 0), id_pv = idesc_f16(TM, D, 0) | (1u << 16);
+            uint32_t k = 0, parts[2] = {0, 0}, steps[2] = {0, 0};
+            auto qk = [&](int x, uint32_t kt) {
+                const uint32_t qa = sb + M::Q + x * M::QT, ka = sb + M::H + (kt % HS) * M::HT;
+#pragma unroll
+                for (int s = 0; s < D / 16; ++s) {
+                    const uint32_t off = (s >> 2) * (TM * 128) + (s & 3) * 32;
+                    tc_mma_f16(tm_s(x), smem_desc_sw128(qa + off), smem_desc_sw128(ka + off), id_qk, s > 0);
+                }
+            };
+            auto pv = [&](int x, uint32_t vt, bool acc) {
+                const uint32_t va = sb + M::H + (vt % HS) * M::HT;
+#pragma unroll
+                for (int z = 0; z < PT; ++z)
+#pragma unroll
+                    for (int s = 0; s < TN / 16; ++s)
+                        tc_mma_f16_ts(tm_o(x), tm_s(x) + z * (TN / 2) + s * 8, smem_desc_mn_sw128(va + s * 2048, TN * 128), id_pv,
+                                      acc || s > 0 || z > 0);
+            };
+            auto h_wait = [&](uint32_t kt) { return wait(h_full + 8 * (kt % HS), kt / HS & 1); };
+            for (bool first = true; alive && w.next<D>(a, sp, first); first = false) {
+                const int n = w.until - w.from, nq = nq_of(w.it);
+                if (!h_wait(k)) break;
+                for (int x = 0; x < nq; ++x) {
+                    if (!wait(q_ready + 8 * x, parts[x]++ & 1)) break;
+                    tc_fence_after();
+                    qk(x, k);
+                    tc_commit(s_full + 8 * x);
+                }
+                if (!alive) break;
+                tc_commit(h_empty + 8 * (k % HS));
+                for (int j = 0; j < n && alive; ++j, k += 2) {
+                    if (!h_wait(k + 1)) break;
+                    const bool more = j + 1 < n;
+                    for (int x = 0; x < nq; ++x) {
+                        if (!wait(p_ready + 8 * x, steps[x]++ & 1)) break;
+                        tc_fence_after();
+                        pv(x, k + 1, j > 0);
+                        if (more) {
+                            if (x == 0 && !h_wait(k + 2)) break;
+                            tc_fence_after();
+                            qk(x, k + 2);
+                            tc_commit(s_full + 8 * x);
+                        } else {
+                            tc_commit(o_full + 8 * x);
+                        }
+                    }
+                    if (!alive) break;
+                    tc_commit(h_empty + 8 * ((k + 1) % HS));
+                    if (more) tc_commit(h_empty + 8 * ((k + 2) % HS));
+                }
+            }
+            if (!alive) {      // let the products in flight end before the tensor memory goes (the barrier is not waited for again)
+                tc_commit(q_ready);
+                mbar_wait(q_ready, parts[0] & 1, 10000000, never);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---- loads: lane c < NB has block c of the step
+        uint32_t k = 0, tile = 0;
+        for (bool first = true; alive && w.next<D>(a, sp, first); first = false) {
+            const int L = __ldg(a.b.lens + w.it.b);
+            for (int j = w.from; j < w.until && alive; ++j, ++tile) {
+                const int tok = w.it.tok0 + j * TN + lane * BLK;
+                const bool have = lane < NB && tok < L;
+                int row = 0;
+                float2 s = make_float2(1.f, pow2i(-64));
+                if (have) {
+                    int pid = __ldg(a.c.table + w.it.b * a.c.ldt + tok / a.c.page);
+                    if (pid < 0 || pid >= a.c.pages) {       // read some page instead: the result is void
+                        set_err(a.b.err, DEV_INDEX);
+                        pid = 0;
+                    }
+                    row = (pid * a.c.Hkv + w.h) * a.c.page + tok % a.c.page;
+                    s = make_float2(__ldg(a.c.s[0] + row / BLK), __ldg(a.c.s[1] + row / BLK));
+                }
+                const uint32_t blocks = __popc(__ballot_sync(0xffffffffu, have));
+                for (int z = 0; z < 2 && alive; ++z, ++k) {
+                    if (!wait_warp(raw_empty + 8 * z, (k / 2 & 1) ^ 1)) break;
+                    const uint32_t bar = raw_full + 8 * z;
+                    if (lane == 0) mbar_arrive_expect_tx(bar, blocks * BLK * D);
+                    __syncwarp();
+                    if (have) tma_load_2d(sb + M::R + z * M::RT + lane * BLK * D, &maps.t[z], bar, 0, row);
+                    if (z == 0) {
+                        if (lane < NB) scales[tile % SS * NB + lane] = s;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(sc_full + 8 * (tile % SS));
+                    }
+                }
+            }
+        }
+        if (!alive) {          // copies in flight land in memory that must still be this CTA's
+            for (int z = 0; z < 2; ++z)
+                for (uint32_t par = 0; par < 2; ++par) mbar_wait(raw_full + 8 * z, par, 10000000, never);
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == MMA_WARP) tmem_dealloc(tmem, 512);
+}
+
+// Joins the items that lie across shares: CTA (i, y) takes rows 32 y .. of the one that began in share i.
+template <int D>
+__global__ void __launch_bounds__(256) k_tiles_join(const AttnArgs a, int ctas) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const Space<D>* sp = static_cast<const Space<D>*>(a.ws);
+    const int i = blockIdx.x, lane = threadIdx.x & 31, seg = __ldcg(&sp->seg[i][1]);
+    int cnt = 1;
+    while (true) {
+        const int j = i + cnt + lane;
+        const bool more = j < ctas && __ldcg(&sp->seg[j][0]) == seg;
+        const int k = __ffs(~__ballot_sync(0xffffffffu, more));
+        cnt += k ? k - 1 : 32;
+        if (k) break;
+    }
+    if (seg < 0) return;
+    const int4 it = __ldcg(reinterpret_cast<const int4*>(&sp->item[seg / a.c.Hkv]));
+    const int q0 = __ldg(a.b.q_start + it.x), n = __ldg(a.b.q_start + it.x + 1) - q0;
+    const int rows = (int)min((int64_t)ROWS, (int64_t)n * (a.Hq / a.c.Hkv) - it.y);
+    for (int k = threadIdx.x; k < 32 * (D / 4); k += 256) {
+        const int r = blockIdx.y * 32 + k / (D / 4);
+        if (r < rows)
+            join<true, D>(a, q0, seg % a.c.Hkv, it.y + r, r, k % (D / 4) * 4, cnt,
+                          [&](int j) { return j == 0 ? &sp->cta[i][1] : &sp->cta[i + j][0]; }, (Part<D>*)nullptr);
+    }
+}
+
+template <int D, int PT>
+cudaError_t run(const AttnArgs& a, cudaStream_t s) {
+    Maps maps;
+    const uint64_t dims[2] = {(uint64_t)D, (uint64_t)a.c.pages * a.c.Hkv * a.c.page}, strides[1] = {(uint64_t)D};
+    const uint32_t box[2] = {(uint32_t)D, (uint32_t)BLK};
+    for (int i = 0; i < 2; ++i)
+        if (!encode_tiled(&maps.t[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.c.q[i], dims, strides, box,
+                          D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+            return cudaErrorInvalidValue;
+    constexpr size_t smem = Smem<D>::END + 1024;
+    static_assert(smem <= 232448, "shared memory");
+    cudaError_t e = cudaFuncSetAttribute(k_tiles<D, PT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int ctas = std::min(num_sms(), MAX_CTAS), G = a.Hq / a.c.Hkv;
+    e = launch_pdl(k_tiles_plan<D>, dim3(1), dim3(PLAN_THREADS), 0, s, a, (int)slots_of(a.b.T, G, a.c.B), ctas);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(k_tiles<D, PT>, dim3(ctas), dim3(THREADS), smem, s, maps, a, (uint64_t)options().wait_ns.load());
+    if (e != cudaSuccess) return e;
+    return launch_pdl(k_tiles_join<D>, dim3(ctas, (unsigned)((std::min<int64_t>(ROWS, (int64_t)a.max_q * G) + 31) / 32)), dim3(256), 0, s, a, ctas);
+}
+
+}  // namespace
+
+size_t tiles_workspace(int64_t T, int64_t G, int64_t D, int64_t B) {
+    return (D == 128 ? sizeof(Space<128>) : sizeof(Space<64>)) + slots_of(T, G, B) * sizeof(Item);
+}
+cudaError_t launch_tiles(const AttnArgs& a, cudaStream_t s) {
+    if (a.D == 128) return a.yt == CQ_F32 ? run<128, 2>(a, s) : run<128, 1>(a, s);
+    return a.yt == CQ_F32 ? run<64, 2>(a, s) : run<64, 1>(a, s);
+}
+
+}  // namespace kv8
+}  // namespace cq
