@@ -6,7 +6,8 @@ namespace kv8 {
 
 size_t attn_workspace(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q) {
     const int64_t G = Hq / Hkv;
-    return decode_serves(std::min(max_q, T) * G) ? decode_workspace(D) : tiles_workspace(T, G, D, B);
+    max_q = std::min(max_q, T);
+    return decode_serves(max_q * G) ? decode_workspace(D) : tiles_workspace(T, G, D, B, max_q);
 }
 
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s) {

@@ -1,22 +1,24 @@
-// Attention over the 8-bit cache for many query rows: tiles of 256 rows x 128 tokens on
-// the 5th-generation tensor cores.
+// Attention over the 8-bit cache for many query rows: 128-row x 128-token tiles on the
+// 5th-generation tensor cores.
 //
 // A row is a (token, head of the group) pair, so the heads that share a KV head share its
-// tiles.  Per 128 tokens a CTA does S = Q K^T (Q and K in shared memory, S in tensor
-// memory) and O += P V (P in tensor memory over S, V in shared memory token-major) for two
-// 128-row tiles A and B in turn: while one's softmax runs, the tensor cores have the other.
-//   warps 0-3, 4-7  softmax of A and B, one row a thread: maximum, weights, sum; queries in, outputs out
-//   warps 8-11      codes -> fp16 (exactly), into the 128-byte-swizzled operand tiles
-//   warp 12         issues the products
-//   warp 13         TMA loads of the codes by page, 32 tokens a box, and their scales
+// tiles.  Per 128 tokens (a step) and tile S = Q K^T (Q and K in shared memory, S in tensor
+// memory) and O += P V (P in tensor memory over S, V in shared memory token-major).  A CTA
+// keeps two tiles going, so that the tensor cores have one while the other's softmax runs:
+// two row tiles (TILES 2, items of 256 rows), or, where no sequence has more than 128 rows,
+// the even and the odd steps of one row tile (TILES 1), whose two results are joined at the end.
+//   warp 0          issues the products
+//   warp 1          TMA loads of the codes by page, 32 tokens a box, and their scales
+//   warps 4-7, 8-11 softmax of the two tiles, one row a thread; queries in, outputs out
+//   warps 12-15     codes -> fp16 (exactly), into the 128-byte-swizzled operand tiles
 // A key block's scale joins the scores in f32, a value block's scale 2^lv the exponent:
 // w = 2^(s - m + 10 + lv - ref), with m at most 5 below the row's maximum (O is only rescaled
 // when the maximum has grown by more) and ref the largest lv so far; the normaliser takes
 // w 2^(ref - lv).  For f32 outputs P goes in two fp16 terms, two products each.
 //
-// The work is the list of all (row tile, KV head, 128 tokens), cut into one equal share per
-// SM.  A first small kernel lays the list out (only the device knows the lengths), a third
-// joins the tiles that lie across shares, in share order.
+// The work is the list of all (row tile, KV head, step), cut into one equal share per SM.  A
+// first small kernel lays the list out (only the device knows the lengths), a third joins the
+// row tiles that lie across shares, in share order.
 #include "attn_common.cuh"
 
 namespace cq {
@@ -24,49 +26,53 @@ namespace kv8 {
 namespace {
 
 constexpr int TM = 128;                // rows of a tensor-core tile
-constexpr int ROWS = 2 * TM;           // rows of a work item
 constexpr int TN = 128;                // tokens of a step
 constexpr int NB = TN / BLK;           // blocks of a step
 constexpr int MAX_CTAS = 256;          // workspace bound
-constexpr int THREADS = 448;
-constexpr int CONV_WARP = 8, MMA_WARP = 12, LOAD_WARP = 13;
+constexpr int THREADS = 512;           // four warpgroups of 128 registers a thread at launch
+constexpr int MMA_WARP = 0, LOAD_WARP = 1, SOFT_WARP = 4, CONV_WARP = 12;
+constexpr int REGS_SOFTMAX = 184, REGS_CONV = 72, REGS_ISSUE = 72;
+static_assert(2 * REGS_SOFTMAX + REGS_CONV + REGS_ISSUE <= 4 * 128, "what the launch has");
 constexpr int PLAN_THREADS = 1024;
 constexpr float W_EXP = 10.f, GROW = 5.f;
 constexpr int HS = 4;                  // fp16 operand tiles in the ring (keys and values alternate)
 constexpr int SS = 8;                  // steps whose scales are kept
+constexpr int LB = 32 / NB;            // steps that the loading warp looks up at a time
 
 struct Maps {
     CUtensorMap t[2];
 };
 
-template <int D>
-using Part = PartOf<D, ROWS>;
+template <int D, int TILES>
+using Part = PartOf<D, TILES * TM>;
 struct alignas(16) Item {
-    int b, f0, tok0, steps;            // sequence, first row, first token, steps of TN tokens (none visible: 1)
+    int b, f0, tok0, steps;            // sequence, first row, first token, steps (none visible: 1)
 };
 struct Start {
     int slot, h, step;                 // where a CTA's share begins
 };
 // Workspace: partials, the CTAs' segments and starts, the list.
-template <int D>
+template <int D, int TILES>
 struct Space {
-    Part<D> cta[MAX_CTAS][2];
+    Part<D, TILES> cta[MAX_CTAS][2];
+    Part<D, TILES> odd[TILES == 1 ? MAX_CTAS : 1];   // TILES 1: the odd steps' result
     int seg[MAX_CTAS][2];              // (slot * Hkv + h) of cta[i][0] (began earlier) and cta[i][1] (began here, goes on)
     Start start[MAX_CTAS];
-    int total, ok;
+    int total, pad;
     Item item[1];                      // [slots]
 };
 
-int64_t slots_of(int64_t T, int64_t G, int64_t B) { return T * G / ROWS + B; }
+int64_t slots_of(int64_t T, int64_t G, int64_t B, int rows) { return T * G / rows + B; }
 
 // ---- the list ------------------------------------------------------------------------------------------------------
-// Sequence b owns the slots floor(q_start[b] G / ROWS) + b .., since n rows make at most floor(n G / ROWS) + 1 tiles.
-template <int D>
+// Sequence b owns the slots floor(q_start[b] G / ROWS) + b .., since n tokens make at most floor(n G / ROWS) + 1 items.
+template <int D, int TILES>
 __global__ void __launch_bounds__(PLAN_THREADS) k_tiles_plan(const AttnArgs a, int slots, int ctas) {
     pdl_launch_dependents();
     pdl_wait();
+    constexpr int ROWS = TILES * TM;
     __shared__ int64_t wsum[PLAN_THREADS / 32];
-    Space<D>* sp = static_cast<Space<D>*>(a.ws);
+    Space<D, TILES>* sp = static_cast<Space<D, TILES>*>(a.ws);
     const int G = a.Hq / a.c.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     bool bad = false;
     for (int b = threadIdx.x; b < a.c.B; b += PLAN_THREADS) {
@@ -144,13 +150,14 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tiles_plan(const AttnArgs a, i
 }
 
 // ---- shared memory -------------------------------------------------------------------------------------------------
-template <int D>
+template <int D, int TILES>
 struct Smem {
+    static constexpr int RS = TILES == 1 ? 4 : 2; // code tiles in the ring (keys and values alternate)
     static constexpr int QT = TM * D * 2;         // a query tile: D/64 chunks of [128 rows][128 B], swizzled
     static constexpr int HT = TN * D * 2;         // an fp16 operand tile, the same
     static constexpr int RT = TN * D;             // codes
-    static constexpr int Q = 0, H = 2 * QT, R = H + HS * HT, MISC = R + 2 * RT;
-    static constexpr int NBAR = 4 + 2 * HS + SS + 8;
+    static constexpr int Q = 0, H = TILES * QT, R = H + HS * HT, MISC = R + RS * RT;
+    static constexpr int NBAR = 2 * RS + 2 * HS + SS + 9;
     static constexpr int SC = MISC + NBAR * 8;    // float2 [SS][NB]
     static constexpr int END = SC + SS * NB * 8 + 16;
 };
@@ -166,8 +173,8 @@ struct Walk {
     int slot, h, step, left;
     Item it;
     int from, until;      // steps of the current part
-    template <int D>
-    __device__ __forceinline__ bool next(const AttnArgs& a, const Space<D>* sp, bool first) {
+    template <class S>
+    __device__ __forceinline__ bool next(const AttnArgs& a, const S* sp, bool first) {
         if (!first) {
             step = until;
             if (step == it.steps) {
@@ -193,15 +200,61 @@ struct Walk {
     }
 };
 
-template <int D, int PT>
+// A block's factor from products to scores in log2 units (NaN if either scale is) and its value exponent.
+struct Scale {
+    float k;
+    int lv;
+};
+__device__ __forceinline__ Scale scale_of(float2 s, float qf) {
+    const bool nan = s.y != s.y;
+    return {qf * (nan ? s.y : s.x), nan ? -64 : exp_of(s.y)};
+}
+// Two floats in one register pair: one instruction for both.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(x));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// Two weights join the sum and become one (or two) fp16 terms.
+template <int PT>
+__device__ __forceinline__ void weights(float y0, float y1, uint64_t& sum, uint32_t& p, uint32_t& p2) {
+    sum = add2(sum, pair(y0, y1));
+    p = pack_f16(y0, y1);
+    if (PT == 2) {
+        const float2 h = unpack_f16(p);
+        p2 = pack_f16(y0 - h.x, y1 - h.y);
+    }
+}
+// Registers of a warpgroup from here on (a multiple of 8; the groups' shares add up to the launch's).
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+template <int D, int PT, int TILES>
 __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Maps maps, const AttnArgs a, uint64_t wait_ns) {
-    using M = Smem<D>;
+    using M = Smem<D, TILES>;
     extern __shared__ __align__(1024) uint8_t raw[];
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    const uint32_t sb = smem_u32(smem), bar0 = sb + M::MISC;
-    const uint32_t raw_full = bar0, raw_empty = bar0 + 16, h_full = bar0 + 32, h_empty = h_full + 8 * HS,
-                   sc_full = h_empty + 8 * HS, q_ready = sc_full + 8 * SS, s_full = q_ready + 16, p_ready = s_full + 16,
-                   o_full = p_ready + 16;
+    const uint32_t sb = smem_u32(smem), raw_full = sb + M::MISC, raw_empty = raw_full + 8 * M::RS,
+                   h_full = raw_empty + 8 * M::RS, h_empty = h_full + 8 * HS, sc_full = h_empty + 8 * HS,
+                   q_ready = sc_full + 8 * SS, s_full = q_ready + 16, p_ready = s_full + 16, o_full = p_ready + 16,
+                   odd_full = o_full + 16;
     float2* scales = reinterpret_cast<float2*>(smem + M::SC);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + M::SC + SS * NB * 8);
     volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -210,12 +263,15 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(raw_full + 8 * i, 1);
-            mbar_init(raw_empty + 8 * i, 4);
             mbar_init(q_ready + 8 * i, 4);
             mbar_init(s_full + 8 * i, 1);
             mbar_init(p_ready + 8 * i, 4);
             mbar_init(o_full + 8 * i, 1);
+        }
+        mbar_init(odd_full, 4);
+        for (int i = 0; i < M::RS; ++i) {
+            mbar_init(raw_full + 8 * i, 1);
+            mbar_init(raw_empty + 8 * i, 4);
         }
         for (int i = 0; i < HS; ++i) {
             mbar_init(h_full + 8 * i, 4);
@@ -225,6 +281,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
         tmem_slot[1] = tmem_slot[2] = 0;
         fence_mbar_init();
     }
+    __syncwarp();
     if (warp == MMA_WARP) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
@@ -233,12 +290,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    auto tm_s = [&](int x) { return tmem + x * TN; };            // scores, then weights
+    auto tm_s = [&](int x) { return tmem + x * TN; };            // scores; block c's weights over its own columns
     auto tm_o = [&](int x) { return tmem + 2 * TN + x * D; };
     pdl_launch_dependents();
     pdl_wait();
 
-    Space<D>* sp = static_cast<Space<D>*>(a.ws);
+    Space<D, TILES>* sp = static_cast<Space<D, TILES>*>(a.ws);
     const int total = __ldcg(&sp->total), G = a.Hq / a.c.Hkv;
     Walk w;
     {
@@ -264,210 +321,23 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
         wait(bar, parity);
         return alive = __all_sync(0xffffffffu, alive);
     };
-    auto nq_of = [&](const Item& it) {       // 128-row tiles of an item
-        const int n = __ldg(a.b.q_start + it.b + 1) - __ldg(a.b.q_start + it.b);
-        return (int64_t)n * G - it.f0 > TM ? 2 : 1;
+    // Steps of a part that tile x takes (TILES 2: whether it has rows), out of n.
+    auto steps_of = [&](const Item& it, int n, int x) {
+        if (TILES == 1) return (n + 1 - x) / 2;
+        const int nq = __ldg(a.b.q_start + it.b + 1) - __ldg(a.b.q_start + it.b);
+        return (int64_t)nq * G - it.f0 > x * TM ? n : 0;
     };
+    constexpr int EACH = TILES == 1 ? 2 : 1;      // tile x takes steps x0, x0 + EACH, ..
 
-    if (warp < CONV_WARP) {
-        // ---- softmax: thread = row of tile x
-        const int x = warp >> 2, row = threadIdx.x & 127;
-        const uint32_t lanes = (uint32_t)(warp & 3) << 21;        // tensor-memory lane of the warp's first row
-        uint32_t parts = 0, steps = 0, tile = 0;                  // of this tile: parts, steps; of the CTA: steps
-        for (bool first = true; alive && w.next<D>(a, sp, first); first = false) {
-            const int n = w.until - w.from;
-            const int q0 = __ldg(a.b.q_start + w.it.b), nq = __ldg(a.b.q_start + w.it.b + 1) - q0, L = __ldg(a.b.lens + w.it.b);
-            const int64_t rows = (int64_t)nq * G - w.it.f0;
-            if (rows <= x * TM) {
-                tile += n;
-                continue;
-            }
-            const int r = x * TM + row, f = w.it.f0 + r;
-            const bool in = r < rows;
-            const int i = f / G, head = w.h * G + f % G;
-            float qf = a.scale * LOG2E;
-            {
-                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.Q) + (q0 + i) * a.ldq + (int64_t)head * D);
-                uint4 v[D / 8];
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) v[c] = in ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-                if (a.xt == CQ_BF16) {
-                    uint32_t mx = 0;
-                    auto top = [&](uint32_t y) { mx = max(mx, max((y << 16) & 0x7FFFFFFFu, y & 0x7FFF0000u)); };
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c) top(v[c].x), top(v[c].y), top(v[c].z), top(v[c].w);
-                    const int sh = guard_of(__uint_as_float(mx));
-                    const float up = pow2i(sh);
-                    qf *= pow2i(-sh);
-                    auto cv = [&](uint32_t y) { return pack_f16(__uint_as_float(y << 16) * up, __uint_as_float(y & 0xFFFF0000u) * up); };
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c) v[c] = make_uint4(cv(v[c].x), cv(v[c].y), cv(v[c].z), cv(v[c].w));
-                }
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c)
-                    *reinterpret_cast<uint4*>(smem + M::Q + x * M::QT + (c >> 3) * (TM * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[c];
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_ready + 8 * x);
-
-            const int rhi = in ? row_hi(i, nq, L, a.causal) : 0, rlo = in ? row_lo(i, nq, L, a.window) : 0;
-            // steps inside [free_lo, free_hi) need no mask in this warp
-            const int wf = w.it.f0 + x * TM + (warp & 3) * 32, wl = (int)min((int64_t)wf + 31, w.it.f0 + rows - 1);
-            const int free_hi = wf < w.it.f0 + rows ? row_hi(wf / G, nq, L, a.causal) : 0;
-            const int free_lo = wf < w.it.f0 + rows ? row_lo(wl / G, nq, L, a.window) : INT32_MAX;
-            float m = -INFINITY, l = 0.f;
-            int ref = -64;
-            for (int j = 0; j < n; ++j, ++steps, ++tile) {
-                if (!wait_warp(s_full + 8 * x, steps & 1) || !wait_warp(sc_full + 8 * (tile % SS), tile / SS & 1)) break;
-                tc_fence_after();
-                const int t0 = w.it.tok0 + (w.from + j) * TN;
-                const bool masked = t0 < free_lo || t0 + TN > free_hi;
-                float km[NB];
-                int lv[NB], nref = ref;
-#pragma unroll
-                for (int c = 0; c < NB; ++c) {
-                    const float2 s = scales[tile % SS * NB + c];
-                    const bool nan = s.y != s.y;
-                    km[c] = qf * (nan ? s.y : s.x);
-                    lv[c] = nan ? -64 : exp_of(s.y);
-                    nref = max(nref, lv[c]);
-                }
-                float top = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < NB; ++c) {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(tm_s(x) + lanes + 32 * c, v);
-                    tmem_ld_wait();
-                    float mx = -INFINITY;
-                    if (masked) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const int tok = t0 + 32 * c + e;
-                            mx = fmaxf(mx, tok >= rlo && tok < rhi ? __uint_as_float(v[e]) : -INFINITY);
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[e]));
-                    }
-                    top = fmaxf(top, mx * km[c]);
-                }
-                const bool grow = top > m + GROW || (m == -INFINITY && top > m);
-                if (__any_sync(0xffffffffu, grow) || nref > ref) {
-                    const float nm = grow ? top : m;
-                    const float fm = grow ? ex2(m - nm) : 1.f, fo = fm * pow2i(max(ref - nref, -126));
-                    m = nm;
-                    l *= fm;
-                    ref = nref;
-                    if (j > 0) {
-#pragma unroll
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t v[32];
-                            tmem_ld_32x32b_x32(tm_o(x) + lanes + 32 * c, v);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * fo);
-                            tmem_st_32x32b_x32(tm_o(x) + lanes + 32 * c, v);
-                        }
-                    }
-                }
-                // Scores of 2^20 and more are rounded before m is taken off, as they were for m: a fused step
-                // would leave their own rounding, which is then no longer small.
-                const bool big = __any_sync(0xffffffffu, fabsf(m) > 1048576.f && m != -INFINITY);
-                uint32_t low[PT == 2 ? 2 : 1][16];      // second terms that wait for their columns to be read
-#pragma unroll
-                for (int c = 0; c < NB; ++c) {
-                    const int lc = max(lv[c], ref - 64);
-                    const float sub = W_EXP + (float)(lc - ref) - (m == -INFINITY ? 0.f : m);
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(tm_s(x) + lanes + 32 * c, v);
-                    tmem_ld_wait();
-                    float kc = km[c];
-                    if (big) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * kc);
-                        kc = 1.f;
-                    }
-                    float sum = 0.f;
-                    uint32_t p[16], p2[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float y0 = ex2(fmaf(__uint_as_float(v[2 * e]), kc, sub));
-                        float y1 = ex2(fmaf(__uint_as_float(v[2 * e + 1]), kc, sub));
-                        if (masked) {
-                            const int tok = t0 + 32 * c + 2 * e;
-                            y0 = tok >= rlo && tok < rhi ? y0 : 0.f;
-                            y1 = tok + 1 >= rlo && tok + 1 < rhi ? y1 : 0.f;
-                        }
-                        sum += y0 + y1;
-                        p[e] = pack_f16(y0, y1);
-                        if (PT == 2) {
-                            const float2 h = unpack_f16(p[e]);
-                            p2[e] = pack_f16(y0 - h.x, y1 - h.y);
-                        }
-                    }
-                    l = fmaf(sum, pow2i(ref - lc - (int)W_EXP), l);
-                    tmem_st_32x32b_x16(tm_s(x) + lanes + 16 * c, p);
-                    if (PT == 2) {
-                        // columns 64 + 16 c lie over the scores of block 2 + c / 2
-                        if (c == 2) {
-                            tmem_st_32x32b_x16(tm_s(x) + lanes + 64, low[0]);
-                            tmem_st_32x32b_x16(tm_s(x) + lanes + 80, low[PT - 1]);
-                        }
-                        if (c == 3) {
-                            tmem_st_32x32b_x16(tm_s(x) + lanes + 96, low[0]);
-                            tmem_st_32x32b_x16(tm_s(x) + lanes + 112, p2);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) low[c == 1 ? PT - 1 : 0][e] = p2[e];
-                    }
-                }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_ready + 8 * x);
-            }
-            if (!wait_warp(o_full + 8 * x, parts & 1)) break;
-            ++parts;
-            tc_fence_after();
-            const bool begins = w.from == 0, ends = w.until == w.it.steps;
-            const float un = pow2i(ref - (int)W_EXP), inv = begins && ends ? un * inv_sum(l) : un;
-            Part<D>* part = &sp->cta[blockIdx.x][begins ? 1 : 0];
-            const int64_t at = (q0 + i) * a.ldo + (int64_t)head * D;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(tm_o(x) + lanes + 32 * c, v);
-                tmem_ld_wait();
-                if (in) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        const float y0 = __uint_as_float(v[e]) * inv, y1 = __uint_as_float(v[e + 1]) * inv;
-                        const float y2 = __uint_as_float(v[e + 2]) * inv, y3 = __uint_as_float(v[e + 3]) * inv;
-                        if (begins && ends) store_out4(a.O, at + 32 * c + e, a.yt, y0, y1, y2, y3);
-                        else *reinterpret_cast<float4*>(&part->o[r][32 * c + e]) = make_float4(y0, y1, y2, y3);
-                    }
-                }
-            }
-            tc_fence_before();
-            if (in) {
-                if (begins && ends) {
-                    if (a.lse) a.lse[(int64_t)(q0 + i) * a.Hq + head] = lse_of(m, l);
-                } else {
-                    part->m[r] = m;
-                    part->l[r] = l;
-                }
-            }
-            if (!(begins && ends) && threadIdx.x == 0) sp->seg[blockIdx.x][begins ? 1 : 0] = w.slot * a.c.Hkv + w.h;
-        }
-    } else if (warp < MMA_WARP) {
+    if (warp >= CONV_WARP) {
+        regs_down<REGS_CONV>();
         // ---- codes -> fp16: thread = token; keys and values of a step alternate
         const int tok = threadIdx.x - CONV_WARP * 32;
         uint32_t k = 0;                          // operand tiles so far
-        for (bool first = true; alive && w.next<D>(a, sp, first); first = false) {
+        for (bool first = true; alive && w.next(a, sp, first); first = false) {
             for (int j = 0; j < 2 * (w.until - w.from) && alive; ++j, ++k) {
-                const uint32_t rs = k & 1, hs = k % HS;
-                if (!wait_warp(raw_full + 8 * rs, k / 2 & 1) || !wait_warp(h_empty + 8 * hs, (k / HS & 1) ^ 1)) break;
+                const uint32_t rs = k % M::RS, hs = k % HS;
+                if (!wait_warp(raw_full + 8 * rs, k / M::RS & 1) || !wait_warp(h_empty + 8 * hs, (k / HS & 1) ^ 1)) break;
                 const uint8_t* src = smem + M::R + rs * M::RT + tok * D;
                 uint8_t* dst = smem + M::H + hs * M::HT + tok * 128;
 #pragma unroll
@@ -491,104 +361,373 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                 }
             }
         }
-    } else if (warp == MMA_WARP) {
-        // ---- products, from one thread
-        if (lane == 0) {
-            constexpr uint32_t id_qk = idesc_f16(TM, TN, 0), id_pv = idesc_f16(TM, D, 0) | (1u << 16);
-            uint32_t k = 0, parts[2] = {0, 0}, steps[2] = {0, 0};
-            auto qk = [&](int x, uint32_t kt) {
-                const uint32_t qa = sb + M::Q + x * M::QT, ka = sb + M::H + (kt % HS) * M::HT;
+    } else if (warp >= SOFT_WARP) {
+        regs_up<REGS_SOFTMAX>();
+        // ---- softmax: thread = row of tile x
+        const int x = (warp - SOFT_WARP) >> 2, row = threadIdx.x & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;        // tensor-memory lane of the warp's first row
+        uint32_t parts = 0, steps = 0, odds = 0, tile0 = 0;       // of this tile: parts, steps, joined parts; of the CTA: steps
+        for (bool first = true; alive && w.next(a, sp, first); first = false) {
+            const int n = w.until - w.from, mine = steps_of(w.it, n, x);
+            const uint32_t tile1 = tile0 + n;
+            const int q0 = __ldg(a.b.q_start + w.it.b), nq = __ldg(a.b.q_start + w.it.b + 1) - q0, L = __ldg(a.b.lens + w.it.b);
+            const int64_t rows = (int64_t)nq * G - w.it.f0;
+            if (mine == 0) {
+                tile0 = tile1;
+                continue;
+            }
+            const int r = (TILES == 1 ? 0 : x * TM) + row, f = w.it.f0 + r;
+            const bool in = r < rows;
+            const int i = f / G, head = w.h * G + f % G;
+            float qf = a.scale * LOG2E;
+            {
+                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.Q) + (q0 + i) * a.ldq + (int64_t)head * D);
+                uint4 v[D / 8];
 #pragma unroll
-                for (int s = 0; s < D / 16; ++s) {
-                    const uint32_t off = (s >> 2) * (TM * 128) + (s & 3) * 32;
-                    tc_mma_f16(tm_s(x), smem_desc_sw128(qa + off), smem_desc_sw128(ka + off), id_qk, s > 0);
+                for (int c = 0; c < D / 8; ++c) v[c] = in ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                if (a.xt == CQ_BF16) {
+                    uint32_t mx = 0;
+                    auto top = [&](uint32_t y) { mx = max(mx, max((y << 16) & 0x7FFFFFFFu, y & 0x7FFF0000u)); };
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) top(v[c].x), top(v[c].y), top(v[c].z), top(v[c].w);
+                    const int sh = guard_of(__uint_as_float(mx));
+                    const float up = pow2i(sh);
+                    qf *= pow2i(-sh);
+                    auto cv = [&](uint32_t y) { return pack_f16(__uint_as_float(y << 16) * up, __uint_as_float(y & 0xFFFF0000u) * up); };
+#pragma unroll
+                    for (int c = 0; c < D / 8; ++c) v[c] = make_uint4(cv(v[c].x), cv(v[c].y), cv(v[c].z), cv(v[c].w));
                 }
-            };
-            auto pv = [&](int x, uint32_t vt, bool acc) {
-                const uint32_t va = sb + M::H + (vt % HS) * M::HT;
+                if (TILES == 2 || x == 0) {
 #pragma unroll
-                for (int z = 0; z < PT; ++z)
-#pragma unroll
-                    for (int s = 0; s < TN / 16; ++s)
-                        tc_mma_f16_ts(tm_o(x), tm_s(x) + z * (TN / 2) + s * 8, smem_desc_mn_sw128(va + s * 2048, TN * 128), id_pv,
-                                      acc || s > 0 || z > 0);
-            };
-            auto h_wait = [&](uint32_t kt) { return wait(h_full + 8 * (kt % HS), kt / HS & 1); };
-            for (bool first = true; alive && w.next<D>(a, sp, first); first = false) {
-                const int n = w.until - w.from, nq = nq_of(w.it);
-                if (!h_wait(k)) break;
-                for (int x = 0; x < nq; ++x) {
-                    if (!wait(q_ready + 8 * x, parts[x]++ & 1)) break;
-                    tc_fence_after();
-                    qk(x, k);
-                    tc_commit(s_full + 8 * x);
+                    for (int c = 0; c < D / 8; ++c)
+                        *reinterpret_cast<uint4*>(smem + M::Q + x * M::QT + (c >> 3) * (TM * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[c];
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(q_ready + 8 * x);
                 }
-                if (!alive) break;
-                tc_commit(h_empty + 8 * (k % HS));
-                for (int j = 0; j < n && alive; ++j, k += 2) {
-                    if (!h_wait(k + 1)) break;
-                    const bool more = j + 1 < n;
-                    for (int x = 0; x < nq; ++x) {
-                        if (!wait(p_ready + 8 * x, steps[x]++ & 1)) break;
-                        tc_fence_after();
-                        pv(x, k + 1, j > 0);
-                        if (more) {
-                            if (x == 0 && !h_wait(k + 2)) break;
-                            tc_fence_after();
-                            qk(x, k + 2);
-                            tc_commit(s_full + 8 * x);
-                        } else {
-                            tc_commit(o_full + 8 * x);
+            }
+
+            const int rhi = in ? row_hi(i, nq, L, a.causal) : 0, rlo = in ? row_lo(i, nq, L, a.window) : 0;
+            // steps inside [free_lo, free_hi) need no mask in this warp (rows past the item's take no part)
+            const int wf = f - lane, wl = (int)min((int64_t)wf + 31, w.it.f0 + rows - 1);
+            const int free_hi = wf <= wl ? row_hi(wf / G, nq, L, a.causal) : INT32_MAX;
+            const int free_lo = wf <= wl ? row_lo(wl / G, nq, L, a.window) : 0;
+            float m = -INFINITY, l = 0.f;
+            int ref = -64;
+            for (int j = 0; j < mine; ++j, ++steps) {
+                const uint32_t tile = tile0 + j * EACH + (TILES == 1 ? x : 0);
+                if (!wait_warp(s_full + 8 * x, steps & 1) || !wait_warp(sc_full + 8 * (tile % SS), tile / SS & 1)) break;
+                tc_fence_after();
+                const int t0 = w.it.tok0 + (w.from + (int)(tile - tile0)) * TN;
+                const bool masked = t0 < free_lo || t0 + TN > free_hi;
+                const float2* sc = scales + tile % SS * NB;
+                int nref = ref;
+#pragma unroll
+                for (int c = 0; c < NB; ++c) nref = max(nref, scale_of(sc[c], qf).lv);
+                // Scores: held in registers where no row of the warp has a mask, else read again by block.
+                float top = -INFINITY;
+                uint32_t v[TN];
+                if (!masked) {
+#pragma unroll
+                    for (int c = 0; c < NB; ++c)
+                        tmem_ld_32x32b_x32(tm_s(x) + lanes + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int c = 0; c < NB; ++c) {
+                        float mx = -INFINITY;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[32 * c + e]));
+                        top = fmaxf(top, mx * scale_of(sc[c], qf).k);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < NB; ++c) {
+                        uint32_t u[32];
+                        tmem_ld_32x32b_x32(tm_s(x) + lanes + 32 * c, u);
+                        tmem_ld_wait();
+                        float mx = -INFINITY;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const int tok = t0 + 32 * c + e;
+                            mx = fmaxf(mx, tok >= rlo && tok < rhi ? __uint_as_float(u[e]) : -INFINITY);
+                        }
+                        top = fmaxf(top, mx * scale_of(sc[c], qf).k);
+                    }
+                }
+                const bool grow = top > m + GROW;
+                if (__any_sync(0xffffffffu, grow) || nref > ref) {
+                    const float nm = grow ? top : m;
+                    const float fm = grow ? ex2(m - nm) : 1.f, fo = fm * pow2i(max(ref - nref, -126));
+                    m = nm;
+                    l *= fm;
+                    ref = nref;
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t u[32];
+                            tmem_ld_32x32b_x32(tm_o(x) + lanes + 32 * c, u);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * fo);
+                            tmem_st_32x32b_x32(tm_o(x) + lanes + 32 * c, u);
                         }
                     }
-                    if (!alive) break;
-                    tc_commit(h_empty + 8 * ((k + 1) % HS));
-                    if (more) tc_commit(h_empty + 8 * ((k + 2) % HS));
                 }
-            }
-            if (!alive) {      // let the products in flight end before the tensor memory goes (the barrier is not waited for again)
-                tc_commit(q_ready);
-                mbar_wait(q_ready, parts[0] & 1, 10000000, never);
-            }
-        }
-        __syncwarp();
-    } else {
-        // ---- loads: lane c < NB has block c of the step
-        uint32_t k = 0, tile = 0;
-        for (bool first = true; alive && w.next<D>(a, sp, first); first = false) {
-            const int L = __ldg(a.b.lens + w.it.b);
-            for (int j = w.from; j < w.until && alive; ++j, ++tile) {
-                const int tok = w.it.tok0 + j * TN + lane * BLK;
-                const bool have = lane < NB && tok < L;
-                int row = 0;
-                float2 s = make_float2(1.f, pow2i(-64));
-                if (have) {
-                    int pid = __ldg(a.c.table + w.it.b * a.c.ldt + tok / a.c.page);
-                    if (pid < 0 || pid >= a.c.pages) {       // read some page instead: the result is void
-                        set_err(a.b.err, DEV_INDEX);
-                        pid = 0;
+                // Scores of 2^20 and more are rounded before m is taken off, as they were for m: a fused step
+                // would leave their own rounding, which is then no longer small.
+                const float m0 = m == -INFINITY ? 0.f : m;
+                const bool big = __any_sync(0xffffffffu, fabsf(m0) > 1048576.f);
+                if (!masked && !big) {
+#pragma unroll
+                    for (int c = 0; c < NB; ++c) {
+                        const Scale k = scale_of(sc[c], qf);
+                        const int lc = max(k.lv, ref - 64);
+                        const float sub = W_EXP + (float)(lc - ref) - m0;
+                        const uint64_t k2 = pair(k.k, k.k), sub2 = pair(sub, sub);
+                        uint64_t sum = 0;
+                        uint32_t p[16], p2[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 y = unpair(fma2(pair(__uint_as_float(v[32 * c + 2 * e]), __uint_as_float(v[32 * c + 2 * e + 1])), k2, sub2));
+                            weights<PT>(ex2(y.x), ex2(y.y), sum, p[e], p2[e]);
+                        }
+                        const float2 t = unpair(sum);
+                        l = fmaf(t.x + t.y, pow2i(ref - lc - (int)W_EXP), l);
+                        tmem_st_32x32b_x16(tm_s(x) + lanes + 32 * c, p);
+                        if (PT == 2) tmem_st_32x32b_x16(tm_s(x) + lanes + 32 * c + 16, p2);
                     }
-                    row = (pid * a.c.Hkv + w.h) * a.c.page + tok % a.c.page;
-                    s = make_float2(__ldg(a.c.s[0] + row / BLK), __ldg(a.c.s[1] + row / BLK));
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < NB; ++c) {
+                        const Scale k = scale_of(sc[c], qf);
+                        const int lc = max(k.lv, ref - 64);
+                        const float sub = W_EXP + (float)(lc - ref) - m0;
+                        uint32_t u[32], p[16], p2[16];
+                        tmem_ld_32x32b_x32(tm_s(x) + lanes + 32 * c, u);
+                        tmem_ld_wait();
+                        uint64_t sum = 0;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const int tok = t0 + 32 * c + 2 * e;
+                            const float y0 = __fadd_rn(__fmul_rn(__uint_as_float(u[2 * e]), k.k), sub);
+                            const float y1 = __fadd_rn(__fmul_rn(__uint_as_float(u[2 * e + 1]), k.k), sub);
+                            weights<PT>(tok >= rlo && tok < rhi ? ex2(y0) : 0.f, tok + 1 >= rlo && tok + 1 < rhi ? ex2(y1) : 0.f,
+                                        sum, p[e], p2[e]);
+                        }
+                        const float2 t = unpair(sum);
+                        l = fmaf(t.x + t.y, pow2i(ref - lc - (int)W_EXP), l);
+                        tmem_st_32x32b_x16(tm_s(x) + lanes + 32 * c, p);
+                        if (PT == 2) tmem_st_32x32b_x16(tm_s(x) + lanes + 32 * c + 16, p2);
+                    }
                 }
-                const uint32_t blocks = __popc(__ballot_sync(0xffffffffu, have));
-                for (int z = 0; z < 2 && alive; ++z, ++k) {
-                    if (!wait_warp(raw_empty + 8 * z, (k / 2 & 1) ^ 1)) break;
-                    const uint32_t bar = raw_full + 8 * z;
-                    if (lane == 0) mbar_arrive_expect_tx(bar, blocks * BLK * D);
-                    __syncwarp();
-                    if (have) tma_load_2d(sb + M::R + z * M::RT + lane * BLK * D, &maps.t[z], bar, 0, row);
-                    if (z == 0) {
-                        if (lane < NB) scales[tile % SS * NB + lane] = s;
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_ready + 8 * x);
+            }
+            if (!wait_warp(o_full + 8 * x, parts & 1)) break;
+            ++parts;
+            tile0 = tile1;
+            tc_fence_after();
+            const bool begins = w.from == 0, ends = w.until == w.it.steps, whole = begins && ends;
+            const float un = pow2i(ref - (int)W_EXP);
+            // TILES 1: the odd steps' result goes to the even steps' threads
+            Part<D, TILES>* odd = &sp->odd[TILES == 1 ? blockIdx.x : 0];
+            const bool both = TILES == 1 && n > 1;
+            float w0 = un, w1 = 0.f;
+            if (both && x == 0) {
+                if (!wait_warp(odd_full, odds++ & 1)) break;
+                if (in) {
+                    const float m1 = odd->m[r], l1 = odd->l[r], top = fmaxf(m, m1);
+                    const float e0 = m == -INFINITY ? 1.f : ex2(m - top), e1 = m1 == -INFINITY ? 1.f : ex2(m1 - top);
+                    w0 = un * e0;
+                    w1 = e1;
+                    l = l * e0 + l1 * e1;
+                    m = top;
+                }
+            }
+            Part<D, TILES>* part = both && x == 1 ? odd : &sp->cta[blockIdx.x][begins ? 1 : 0];
+            const bool direct = whole && !(both && x == 1);
+            if (direct) {
+                const float inv = inv_sum(l);
+                w0 *= inv;
+                w1 *= inv;
+            }
+            const int64_t at = (q0 + i) * a.ldo + (int64_t)head * D;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(tm_o(x) + lanes + 32 * c, v);
+                tmem_ld_wait();
+                if (in) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        float4 y = make_float4(__uint_as_float(v[e]) * w0, __uint_as_float(v[e + 1]) * w0,
+                                               __uint_as_float(v[e + 2]) * w0, __uint_as_float(v[e + 3]) * w0);
+                        if (both && x == 0) {
+                            const float4 z = *reinterpret_cast<const float4*>(&odd->o[r][32 * c + e]);
+                            y = make_float4(fmaf(z.x, w1, y.x), fmaf(z.y, w1, y.y), fmaf(z.z, w1, y.z), fmaf(z.w, w1, y.w));
+                        }
+                        if (direct) store_out4(a.O, at + 32 * c + e, a.yt, y.x, y.y, y.z, y.w);
+                        else *reinterpret_cast<float4*>(&part->o[r][32 * c + e]) = y;
+                    }
+                }
+            }
+            tc_fence_before();
+            if (in) {
+                if (direct) {
+                    if (a.lse) a.lse[(int64_t)(q0 + i) * a.Hq + head] = lse_of(m, l);
+                } else {
+                    part->m[r] = m;
+                    part->l[r] = l;
+                }
+            }
+            if (both && x == 1) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(odd_full);
+            }
+            if (!whole && x == 0 && row == 0) sp->seg[blockIdx.x][begins ? 1 : 0] = w.slot * a.c.Hkv + w.h;
+        }
+    } else {
+        regs_down<REGS_ISSUE>();
+        if (warp == MMA_WARP) {
+            // ---- products, from one thread
+            if (lane == 0) {
+                constexpr uint32_t id_qk = idesc_f16(TM, TN, 0), id_pv = idesc_f16(TM, D, 0) | (1u << 16);
+                uint32_t k = 0, parts[2] = {0, 0}, steps[2] = {0, 0};
+                auto qk = [&](int x, uint32_t kt) {
+                    const uint64_t qa = smem_desc_sw128(sb + M::Q + (TILES == 1 ? 0 : x) * M::QT);
+                    const uint64_t ka = smem_desc_sw128(sb + M::H + (kt % HS) * M::HT);
+#pragma unroll
+                    for (int s = 0; s < D / 16; ++s) {
+                        const uint32_t off = ((s >> 2) * (TM * 128) + (s & 3) * 32) >> 4;
+                        tc_mma_f16(tm_s(x), qa + off, ka + off, id_qk, s > 0);
+                    }
+                    tc_commit(s_full + 8 * x);
+                };
+                auto pv = [&](int x, uint32_t vt, bool acc) {
+                    const uint64_t va = smem_desc_mn_sw128(sb + M::H + (vt % HS) * M::HT, TN * 128);
+#pragma unroll
+                    for (int z = 0; z < PT; ++z)
+#pragma unroll
+                        for (int s = 0; s < TN / 16; ++s)
+                            tc_mma_f16_ts(tm_o(x), tm_s(x) + (s >> 1) * 32 + (s & 1) * 8 + z * 16, va + s * (2048 >> 4), id_pv,
+                                          acc || s > 0 || z > 0);
+                };
+                auto h_wait = [&](uint32_t kt) { return wait(h_full + 8 * (kt % HS), kt / HS & 1); };
+                for (bool first = true; alive && w.next(a, sp, first); first = false) {
+                    const int n = w.until - w.from;
+                    if (TILES == 1) {
+                        // steps j take tile j % 2; step j + 2's scores follow step j's output
+                        if (!wait(q_ready, parts[0]++ & 1)) break;
+                        for (int j = 0; j < min(n, 2); ++j) {
+                            if (!h_wait(k + 2 * j)) break;
+                            tc_fence_after();
+                            qk(j, k + 2 * j);
+                            tc_commit(h_empty + 8 * ((k + 2 * j) % HS));
+                        }
+                        for (int j = 0; j < n && alive; ++j) {
+                            const int x = j & 1;
+                            const uint32_t kt = k + 2 * j;
+                            if (!wait(p_ready + 8 * x, steps[x]++ & 1) || !h_wait(kt + 1)) break;
+                            tc_fence_after();
+                            pv(x, kt + 1, j >= 2);
+                            if (j + 2 < n) {
+                                tc_commit(h_empty + 8 * ((kt + 1) % HS));
+                                if (!h_wait(kt + 4)) break;
+                                tc_fence_after();
+                                qk(x, kt + 4);
+                                tc_commit(h_empty + 8 * ((kt + 4) % HS));
+                            } else {
+                                tc_commit(o_full + 8 * x);
+                                tc_commit(h_empty + 8 * ((kt + 1) % HS));
+                            }
+                        }
+                        k += 2 * n;
+                    } else {
+                        const int nx = steps_of(w.it, n, 1) ? 2 : 1;
+                        if (!h_wait(k)) break;
+                        for (int x = 0; x < nx; ++x) {
+                            if (!wait(q_ready + 8 * x, parts[x]++ & 1)) break;
+                            tc_fence_after();
+                            qk(x, k);
+                        }
+                        if (!alive) break;
+                        tc_commit(h_empty + 8 * (k % HS));
+                        for (int j = 0; j < n && alive; ++j, k += 2) {
+                            if (!h_wait(k + 1)) break;
+                            const bool more = j + 1 < n;
+                            for (int x = 0; x < nx; ++x) {
+                                if (!wait(p_ready + 8 * x, steps[x]++ & 1)) break;
+                                tc_fence_after();
+                                pv(x, k + 1, j > 0);
+                                if (more) {
+                                    if (x == 0 && !h_wait(k + 2)) break;
+                                    tc_fence_after();
+                                    qk(x, k + 2);
+                                } else {
+                                    tc_commit(o_full + 8 * x);
+                                }
+                            }
+                            if (!alive) break;
+                            tc_commit(h_empty + 8 * ((k + 1) % HS));
+                            if (more) tc_commit(h_empty + 8 * ((k + 2) % HS));
+                        }
+                    }
+                }
+                if (!alive) {  // let the products in flight end before the tensor memory goes: nothing else waits for this
+                    tc_commit(q_ready);
+                    mbar_wait(q_ready, parts[0] & 1, 10000000, never);
+                }
+            }
+            __syncwarp();
+        } else if (warp == LOAD_WARP) {
+            // ---- loads: lane NB i + c has block c of step i of a batch of LB steps
+            uint32_t k = 0, tile = 0;
+            for (bool first = true; alive && w.next(a, sp, first); first = false) {
+                const int L = __ldg(a.b.lens + w.it.b);
+                int row1 = 0;
+                float2 s1;
+                auto look_up = [&](int j) {       // of the batch that begins at step j
+                    const int tok = w.it.tok0 + j * TN + lane * BLK;
+                    row1 = -1;
+                    s1 = make_float2(1.f, pow2i(-64));
+                    if (j + lane / NB < w.until && tok < L) {
+                        int pid = __ldg(a.c.table + w.it.b * a.c.ldt + tok / a.c.page);
+                        if (pid < 0 || pid >= a.c.pages) {       // read some page instead: the result is void
+                            set_err(a.b.err, DEV_INDEX);
+                            pid = 0;
+                        }
+                        row1 = (pid * a.c.Hkv + w.h) * a.c.page + tok % a.c.page;
+                        s1 = make_float2(__ldg(a.c.s[0] + row1 / BLK), __ldg(a.c.s[1] + row1 / BLK));
+                    }
+                };
+                look_up(w.from);
+                for (int j0 = w.from; j0 < w.until && alive; j0 += LB) {
+                    const int row = row1;
+                    const float2 s = s1;
+                    if (j0 + LB < w.until) look_up(j0 + LB);
+                    for (int i = 0; i < min(LB, w.until - j0) && alive; ++i, ++tile) {
+                        const bool me = lane / NB == i, have = me && row >= 0;
+                        const uint32_t blocks = __popc(__ballot_sync(0xffffffffu, have));
+                        for (int z = 0; z < 2 && alive; ++z, ++k) {
+                            const uint32_t rs = k % M::RS, bar = raw_full + 8 * rs;
+                            if (!wait_warp(raw_empty + 8 * rs, (k / M::RS & 1) ^ 1)) break;
+                            if (lane == 0) mbar_arrive_expect_tx(bar, blocks * BLK * D);
+                            __syncwarp();
+                            if (have) tma_load_2d(sb + M::R + rs * M::RT + lane % NB * BLK * D, &maps.t[z], bar, 0, row);
+                        }
+                        if (!alive) break;
+                        if (me) scales[tile % SS * NB + lane % NB] = s;
                         __syncwarp();
                         if (lane == 0) mbar_arrive(sc_full + 8 * (tile % SS));
                     }
                 }
             }
-        }
-        if (!alive) {          // copies in flight land in memory that must still be this CTA's
-            for (int z = 0; z < 2; ++z)
-                for (uint32_t par = 0; par < 2; ++par) mbar_wait(raw_full + 8 * z, par, 10000000, never);
+            if (!alive) {      // copies in flight land in memory that must still be this CTA's
+                for (int i = 0; i < M::RS; ++i)
+                    for (uint32_t par = 0; par < 2; ++par) mbar_wait(raw_full + 8 * i, par, 10000000, never);
+            }
         }
     }
     tc_fence_before();
@@ -597,11 +736,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
 }
 
 // Joins the items that lie across shares: CTA (i, y) takes rows 32 y .. of the one that began in share i.
-template <int D>
+template <int D, int TILES>
 __global__ void __launch_bounds__(256) k_tiles_join(const AttnArgs a, int ctas) {
     pdl_launch_dependents();
     pdl_wait();
-    const Space<D>* sp = static_cast<const Space<D>*>(a.ws);
+    const Space<D, TILES>* sp = static_cast<const Space<D, TILES>*>(a.ws);
     const int i = blockIdx.x, lane = threadIdx.x & 31, seg = __ldcg(&sp->seg[i][1]);
     int cnt = 1;
     while (true) {
@@ -614,16 +753,16 @@ __global__ void __launch_bounds__(256) k_tiles_join(const AttnArgs a, int ctas) 
     if (seg < 0) return;
     const int4 it = __ldcg(reinterpret_cast<const int4*>(&sp->item[seg / a.c.Hkv]));
     const int q0 = __ldg(a.b.q_start + it.x), n = __ldg(a.b.q_start + it.x + 1) - q0;
-    const int rows = (int)min((int64_t)ROWS, (int64_t)n * (a.Hq / a.c.Hkv) - it.y);
+    const int rows = (int)min((int64_t)TILES * TM, (int64_t)n * (a.Hq / a.c.Hkv) - it.y);
     for (int k = threadIdx.x; k < 32 * (D / 4); k += 256) {
         const int r = blockIdx.y * 32 + k / (D / 4);
         if (r < rows)
             join<true, D>(a, q0, seg % a.c.Hkv, it.y + r, r, k % (D / 4) * 4, cnt,
-                          [&](int j) { return j == 0 ? &sp->cta[i][1] : &sp->cta[i + j][0]; }, (Part<D>*)nullptr);
+                          [&](int j) { return j == 0 ? &sp->cta[i][1] : &sp->cta[i + j][0]; }, (Part<D, TILES>*)nullptr);
     }
 }
 
-template <int D, int PT>
+template <int D, int PT, int TILES>
 cudaError_t run(const AttnArgs& a, cudaStream_t s) {
     Maps maps;
     const uint64_t dims[2] = {(uint64_t)D, (uint64_t)a.c.pages * a.c.Hkv * a.c.page}, strides[1] = {(uint64_t)D};
@@ -632,27 +771,39 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
         if (!encode_tiled(&maps.t[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.c.q[i], dims, strides, box,
                           D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
             return cudaErrorInvalidValue;
-    constexpr size_t smem = Smem<D>::END + 1024;
+    constexpr size_t smem = Smem<D, TILES>::END + 1024;
     static_assert(smem <= 232448, "shared memory");
-    cudaError_t e = cudaFuncSetAttribute(k_tiles<D, PT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(k_tiles<D, PT, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const int ctas = std::min(num_sms(), MAX_CTAS), G = a.Hq / a.c.Hkv;
-    e = launch_pdl(k_tiles_plan<D>, dim3(1), dim3(PLAN_THREADS), 0, s, a, (int)slots_of(a.b.T, G, a.c.B), ctas);
+    const int ctas = std::min(num_sms(), MAX_CTAS), G = a.Hq / a.c.Hkv, rows = TILES * TM;
+    e = launch_pdl(k_tiles_plan<D, TILES>, dim3(1), dim3(PLAN_THREADS), 0, s, a, (int)slots_of(a.b.T, G, a.c.B, rows), ctas);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(k_tiles<D, PT>, dim3(ctas), dim3(THREADS), smem, s, maps, a, (uint64_t)options().wait_ns.load());
+    e = launch_pdl(k_tiles<D, PT, TILES>, dim3(ctas), dim3(THREADS), smem, s, maps, a, (uint64_t)options().wait_ns.load());
     if (e != cudaSuccess) return e;
-    return launch_pdl(k_tiles_join<D>, dim3(ctas, (unsigned)((std::min<int64_t>(ROWS, (int64_t)a.max_q * G) + 31) / 32)), dim3(256), 0, s, a, ctas);
+    const unsigned y = (unsigned)((std::min<int64_t>(rows, (int64_t)a.max_q * G) + 31) / 32);
+    return launch_pdl(k_tiles_join<D, TILES>, dim3(ctas, y), dim3(256), 0, s, a, ctas);
+}
+
+template <int D, int TILES>
+cudaError_t run_as(const AttnArgs& a, cudaStream_t s) {
+    return a.yt == CQ_F32 ? run<D, 2, TILES>(a, s) : run<D, 1, TILES>(a, s);
+}
+template <int D>
+cudaError_t run_d(const AttnArgs& a, cudaStream_t s) {
+    return (int64_t)a.max_q * (a.Hq / a.c.Hkv) <= TM ? run_as<D, 1>(a, s) : run_as<D, 2>(a, s);
+}
+template <int D>
+size_t space_bytes(int64_t T, int64_t G, int64_t B, int64_t max_q) {
+    return max_q * G <= TM ? sizeof(Space<D, 1>) + slots_of(T, G, B, TM) * sizeof(Item)
+                           : sizeof(Space<D, 2>) + slots_of(T, G, B, 2 * TM) * sizeof(Item);
 }
 
 }  // namespace
 
-size_t tiles_workspace(int64_t T, int64_t G, int64_t D, int64_t B) {
-    return (D == 128 ? sizeof(Space<128>) : sizeof(Space<64>)) + slots_of(T, G, B) * sizeof(Item);
+size_t tiles_workspace(int64_t T, int64_t G, int64_t D, int64_t B, int64_t max_q) {
+    return D == 128 ? space_bytes<128>(T, G, B, max_q) : space_bytes<64>(T, G, B, max_q);
 }
-cudaError_t launch_tiles(const AttnArgs& a, cudaStream_t s) {
-    if (a.D == 128) return a.yt == CQ_F32 ? run<128, 2>(a, s) : run<128, 1>(a, s);
-    return a.yt == CQ_F32 ? run<64, 2>(a, s) : run<64, 1>(a, s);
-}
+cudaError_t launch_tiles(const AttnArgs& a, cudaStream_t s) { return a.D == 128 ? run_d<128>(a, s) : run_d<64>(a, s); }
 
 }  // namespace kv8
 }  // namespace cq
