@@ -20,6 +20,10 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
 __device__ __forceinline__ float2 unpack_f16(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
@@ -36,11 +40,6 @@ __device__ __forceinline__ int guard_of(float amax) {
     return amax == 0.f || e == 128 ? 0 : min(max(13 - e, -114), 126);
 }
 
-__device__ __forceinline__ void store_out(void* p, int64_t i, int t, float v) {
-    if (t == CQ_F32) static_cast<float*>(p)[i] = v;
-    else if (t == CQ_F16) static_cast<__half*>(p)[i] = __float2half_rn(v);
-    else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-}
 // Four neighbouring outputs (i a multiple of four).
 __device__ __forceinline__ void store_out4(void* p, int64_t i, int t, float a, float b, float c, float d) {
     if (t == CQ_F32) {
@@ -48,9 +47,7 @@ __device__ __forceinline__ void store_out4(void* p, int64_t i, int t, float a, f
     } else if (t == CQ_F16) {
         *reinterpret_cast<uint2*>(static_cast<__half*>(p) + i) = make_uint2(pack_f16(a, b), pack_f16(c, d));
     } else {
-        const __nv_bfloat162 x = __floats2bfloat162_rn(a, b), y = __floats2bfloat162_rn(c, d);
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + i) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p) + i) = make_uint2(pack_bf16(a, b), pack_bf16(c, d));
     }
 }
 
@@ -65,6 +62,7 @@ template <int D, int R>
 struct PartOf {
     float o[R][D];
     float m[R], l[R];
+    __device__ __forceinline__ const float4* quad(int r, int d) const { return reinterpret_cast<const float4*>(&o[r][d]); }
 };
 constexpr int JOIN = 8;   // partials in flight while joining
 
@@ -93,7 +91,7 @@ __device__ __forceinline__ void join(const AttnArgs& a, int q0, int h, int f, in
                 const P* p = part(j0 + j);
                 pm[j] = part_ld<FAR>(&p->m[r]);
                 pl[j] = part_ld<FAR>(&p->l[r]);
-                v[j] = part_ld<FAR>(reinterpret_cast<const float4*>(&p->o[r][d]));
+                v[j] = part_ld<FAR>(p->quad(r, d));
             }
         }
         float top = m;
@@ -118,7 +116,7 @@ __device__ __forceinline__ void join(const AttnArgs& a, int q0, int h, int f, in
         m = top;
     }
     if (out) {
-        *reinterpret_cast<float4*>(&out->o[r][d]) = o;
+        *const_cast<float4*>(out->quad(r, d)) = o;
         if (d == 0) {
             out->m[r] = m;
             out->l[r] = l;

@@ -43,8 +43,13 @@ struct Maps {
     CUtensorMap t[2];
 };
 
+// An unfinished result, channels in fours with the rows side by side, as the threads hold them.
 template <int D, int TILES>
-using Part = PartOf<D, TILES * TM>;
+struct Part {
+    float4 o[D / 4][TILES * TM];
+    float m[TILES * TM], l[TILES * TM];
+    __device__ __forceinline__ const float4* quad(int r, int d) const { return &o[d / 4][r]; }
+};
 struct alignas(16) Item {
     int b, f0, tok0, steps;            // sequence, first row, first token, steps (none visible: 1)
 };
@@ -379,37 +384,54 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
             const int r = (TILES == 1 ? 0 : x * TM) + row, f = w.it.f0 + r;
             const bool in = r < rows;
             const int i = f / G, head = w.h * G + f % G;
+            const int wf = f - lane, wl = (int)min((int64_t)wf + 31, w.it.f0 + rows - 1);   // the warp's rows (none: wl < wf)
             float qf = a.scale * LOG2E;
-            {
-                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.Q) + (q0 + i) * a.ldq + (int64_t)head * D);
-                uint4 v[D / 8];
+            auto guard = [&](const uint4 (&v)[D / 8]) {               // bf16: the row's shift
+                uint32_t mx = 0;
+                auto top = [&](uint32_t y) { mx = max(mx, max((y << 16) & 0x7FFFFFFFu, y & 0x7FFF0000u)); };
 #pragma unroll
-                for (int c = 0; c < D / 8; ++c) v[c] = in ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                for (int c = 0; c < D / 8; ++c) top(v[c].x), top(v[c].y), top(v[c].z), top(v[c].w);
+                const int sh = guard_of(__uint_as_float(mx));
+                qf *= pow2i(-sh);
+                return pow2i(sh);
+            };
+            uint4 v[D / 8];
+            if (TILES == 2 || x == 0) {
+                // neighbouring lanes read neighbouring chunks of a row; each row's own thread then sees to its guard
+                uint8_t* q = smem + M::Q + x * M::QT;
+                auto chunk = [&](int rr, int c) { return reinterpret_cast<uint4*>(q + (c >> 3) * (TM * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)); };
+                constexpr int LPR = D / 8, RPI = 32 / LPR;            // lanes a row, rows a load
+#pragma unroll
+                for (int k = 0; k < 32 / RPI; ++k) {
+                    const int ff = wf + k * RPI + lane / LPR;
+                    v[k] = make_uint4(0, 0, 0, 0);
+                    if (ff <= wl)
+                        v[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.Q) + (q0 + ff / G) * a.ldq +
+                                                                    (int64_t)(w.h * G + ff % G) * D) + lane % LPR);
+                }
+#pragma unroll
+                for (int k = 0; k < 32 / RPI; ++k) *chunk((row & 96) + k * RPI + lane / LPR, lane % LPR) = v[k];
+                __syncwarp();
                 if (a.xt == CQ_BF16) {
-                    uint32_t mx = 0;
-                    auto top = [&](uint32_t y) { mx = max(mx, max((y << 16) & 0x7FFFFFFFu, y & 0x7FFF0000u)); };
 #pragma unroll
-                    for (int c = 0; c < D / 8; ++c) top(v[c].x), top(v[c].y), top(v[c].z), top(v[c].w);
-                    const int sh = guard_of(__uint_as_float(mx));
-                    const float up = pow2i(sh);
-                    qf *= pow2i(-sh);
+                    for (int c = 0; c < D / 8; ++c) v[c] = *chunk(row, c);
+                    const float up = guard(v);
                     auto cv = [&](uint32_t y) { return pack_f16(__uint_as_float(y << 16) * up, __uint_as_float(y & 0xFFFF0000u) * up); };
 #pragma unroll
-                    for (int c = 0; c < D / 8; ++c) v[c] = make_uint4(cv(v[c].x), cv(v[c].y), cv(v[c].z), cv(v[c].w));
+                    for (int c = 0; c < D / 8; ++c) *chunk(row, c) = make_uint4(cv(v[c].x), cv(v[c].y), cv(v[c].z), cv(v[c].w));
                 }
-                if (TILES == 2 || x == 0) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(q_ready + 8 * x);
+            } else if (a.xt == CQ_BF16) {
+                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.Q) + (q0 + i) * a.ldq + (int64_t)head * D);
 #pragma unroll
-                    for (int c = 0; c < D / 8; ++c)
-                        *reinterpret_cast<uint4*>(smem + M::Q + x * M::QT + (c >> 3) * (TM * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = v[c];
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(q_ready + 8 * x);
-                }
+                for (int c = 0; c < D / 8; ++c) v[c] = in ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                guard(v);
             }
 
             const int rhi = in ? row_hi(i, nq, L, a.causal) : 0, rlo = in ? row_lo(i, nq, L, a.window) : 0;
             // steps inside [free_lo, free_hi) need no mask in this warp (rows past the item's take no part)
-            const int wf = f - lane, wl = (int)min((int64_t)wf + 31, w.it.f0 + rows - 1);
             const int free_hi = wf <= wl ? row_hi(wf / G, nq, L, a.causal) : INT32_MAX;
             const int free_lo = wf <= wl ? row_lo(wl / G, nq, L, a.window) : 0;
             float m = -INFINITY, l = 0.f;
@@ -417,6 +439,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
             for (int j = 0; j < mine; ++j, ++steps) {
                 const uint32_t tile = tile0 + j * EACH + (TILES == 1 ? x : 0);
                 if (!wait_warp(s_full + 8 * x, steps & 1) || !wait_warp(sc_full + 8 * (tile % SS), tile / SS & 1)) break;
+                if (wl < wf) {                                        // no rows: whatever lies there as weights only meets its own rows
+                    if (lane == 0) mbar_arrive(p_ready + 8 * x);
+                    continue;
+                }
                 tc_fence_after();
                 const int t0 = w.it.tok0 + (w.from + (int)(tile - tile0)) * TN;
                 const bool masked = t0 < free_lo || t0 + TN > free_hi;
@@ -424,36 +450,65 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                 int nref = ref;
 #pragma unroll
                 for (int c = 0; c < NB; ++c) nref = max(nref, scale_of(sc[c], qf).lv);
-                // Scores: held in registers where no row of the warp has a mask, else read again by block.
-                float top = -INFINITY;
-                uint32_t v[TN];
-                if (!masked) {
-#pragma unroll
-                    for (int c = 0; c < NB; ++c)
-                        tmem_ld_32x32b_x32(tm_s(x) + lanes + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
-                    tmem_ld_wait();
+                // One pass where no row of the warp has a mask and the maximum may stay as it is (all but a few
+                // steps): weights against the m so far, kept in registers until the step's maximum is known.  It is
+                // not for scores of 2^20 and more, which have to be rounded before m is taken off, as they were for
+                // m: the fused step would leave their own rounding, which is then no longer small.
+                bool done = false;
+                if (PT == 1 && !masked && nref == ref && !__any_sync(0xffffffffu, !(fabsf(m) <= 1048576.f))) {
+                    float top = -INFINITY, more = 0.f;
+                    uint32_t v[2][32], p[NB][16], unused;
+                    tmem_ld_32x32b_x32(tm_s(x) + lanes, v[0]);
 #pragma unroll
                     for (int c = 0; c < NB; ++c) {
+                        tmem_ld_wait();
+                        if (c + 1 < NB) tmem_ld_32x32b_x32(tm_s(x) + lanes + 32 * (c + 1), v[(c + 1) & 1]);
+                        const Scale k = scale_of(sc[c], qf);
+                        const int lc = max(k.lv, ref - 64);
+                        const float sub = W_EXP + (float)(lc - ref) - m;
+                        const uint64_t k2 = pair(k.k, k.k), sub2 = pair(sub, sub);
+                        const uint32_t(&u)[32] = v[c & 1];
+                        uint64_t sum = 0;
                         float mx = -INFINITY;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(v[32 * c + e]));
-                        top = fmaxf(top, mx * scale_of(sc[c], qf).k);
+                        for (int e = 0; e < 16; ++e) {
+                            const float a0 = __uint_as_float(u[2 * e]), a1 = __uint_as_float(u[2 * e + 1]);
+                            mx = fmaxf(mx, fmaxf(a0, a1));
+                            const float2 y = unpair(fma2(pair(a0, a1), k2, sub2));
+                            weights<1>(ex2(y.x), ex2(y.y), sum, p[c][e], unused);
+                        }
+                        top = fmaxf(top, mx * k.k);
+                        const float2 t = unpair(sum);
+                        more = fmaf(t.x + t.y, pow2i(ref - lc - (int)W_EXP), more);
                     }
-                } else {
+                    if (!__any_sync(0xffffffffu, top > m + GROW)) {
+                        l += more;
+#pragma unroll
+                        for (int c = 0; c < NB; ++c) tmem_st_32x32b_x16(tm_s(x) + lanes + 32 * c, p[c]);
+                        done = true;
+                    }
+                }
+                if (!done) {
+                    // Two passes by block: the maximum, then the weights.
+                    float top = -INFINITY;
 #pragma unroll 1
                     for (int c = 0; c < NB; ++c) {
                         uint32_t u[32];
                         tmem_ld_32x32b_x32(tm_s(x) + lanes + 32 * c, u);
                         tmem_ld_wait();
                         float mx = -INFINITY;
+                        if (masked) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const int tok = t0 + 32 * c + e;
-                            mx = fmaxf(mx, tok >= rlo && tok < rhi ? __uint_as_float(u[e]) : -INFINITY);
+                            for (int e = 0; e < 32; ++e) {
+                                const int tok = t0 + 32 * c + e;
+                                mx = fmaxf(mx, tok >= rlo && tok < rhi ? __uint_as_float(u[e]) : -INFINITY);
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(u[e]));
                         }
                         top = fmaxf(top, mx * scale_of(sc[c], qf).k);
                     }
-                }
                 const bool grow = top > m + GROW;
                 if (__any_sync(0xffffffffu, grow) || nref > ref) {
                     const float nm = grow ? top : m;
@@ -473,30 +528,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                         }
                     }
                 }
-                // Scores of 2^20 and more are rounded before m is taken off, as they were for m: a fused step
-                // would leave their own rounding, which is then no longer small.
                 const float m0 = m == -INFINITY ? 0.f : m;
-                const bool big = __any_sync(0xffffffffu, fabsf(m0) > 1048576.f);
-                if (!masked && !big) {
-#pragma unroll
-                    for (int c = 0; c < NB; ++c) {
-                        const Scale k = scale_of(sc[c], qf);
-                        const int lc = max(k.lv, ref - 64);
-                        const float sub = W_EXP + (float)(lc - ref) - m0;
-                        const uint64_t k2 = pair(k.k, k.k), sub2 = pair(sub, sub);
-                        uint64_t sum = 0;
-                        uint32_t p[16], p2[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float2 y = unpair(fma2(pair(__uint_as_float(v[32 * c + 2 * e]), __uint_as_float(v[32 * c + 2 * e + 1])), k2, sub2));
-                            weights<PT>(ex2(y.x), ex2(y.y), sum, p[e], p2[e]);
-                        }
-                        const float2 t = unpair(sum);
-                        l = fmaf(t.x + t.y, pow2i(ref - lc - (int)W_EXP), l);
-                        tmem_st_32x32b_x16(tm_s(x) + lanes + 32 * c, p);
-                        if (PT == 2) tmem_st_32x32b_x16(tm_s(x) + lanes + 32 * c + 16, p2);
-                    }
-                } else {
+                const bool plain = !masked && !__any_sync(0xffffffffu, fabsf(m0) > 1048576.f);
+                {
 #pragma unroll 1
                     for (int c = 0; c < NB; ++c) {
                         const Scale k = scale_of(sc[c], qf);
@@ -508,17 +542,23 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                         uint64_t sum = 0;
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const int tok = t0 + 32 * c + 2 * e;
-                            const float y0 = __fadd_rn(__fmul_rn(__uint_as_float(u[2 * e]), k.k), sub);
-                            const float y1 = __fadd_rn(__fmul_rn(__uint_as_float(u[2 * e + 1]), k.k), sub);
-                            weights<PT>(tok >= rlo && tok < rhi ? ex2(y0) : 0.f, tok + 1 >= rlo && tok + 1 < rhi ? ex2(y1) : 0.f,
-                                        sum, p[e], p2[e]);
+                            const float a0 = __uint_as_float(u[2 * e]), a1 = __uint_as_float(u[2 * e + 1]);
+                            if (plain) {
+                                const float2 y = unpair(fma2(pair(a0, a1), pair(k.k, k.k), pair(sub, sub)));
+                                weights<PT>(ex2(y.x), ex2(y.y), sum, p[e], p2[e]);
+                            } else {
+                                const int tok = t0 + 32 * c + 2 * e;
+                                const float y0 = ex2(__fadd_rn(__fmul_rn(a0, k.k), sub)), y1 = ex2(__fadd_rn(__fmul_rn(a1, k.k), sub));
+                                weights<PT>(tok >= rlo && tok < rhi ? y0 : 0.f, tok + 1 >= rlo && tok + 1 < rhi ? y1 : 0.f, sum,
+                                            p[e], p2[e]);
+                            }
                         }
                         const float2 t = unpair(sum);
                         l = fmaf(t.x + t.y, pow2i(ref - lc - (int)W_EXP), l);
                         tmem_st_32x32b_x16(tm_s(x) + lanes + 32 * c, p);
                         if (PT == 2) tmem_st_32x32b_x16(tm_s(x) + lanes + 32 * c + 16, p2);
                     }
+                }
                 }
                 tmem_st_wait();
                 tc_fence_before();
@@ -553,24 +593,57 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                 w0 *= inv;
                 w1 *= inv;
             }
-            const int64_t at = (q0 + i) * a.ldo + (int64_t)head * D;
+            // Outputs go through the query tile (its products are done), so that neighbouring lanes store
+            // neighbouring chunks of a row: 16-bit rows whole, f32 rows half at a time.
+            constexpr int RB = 2 * D, LPR = RB / 16, RPI = 32 / LPR;  // staged bytes and chunks of a row, rows a store
+            uint8_t* stage = smem + M::Q + (TILES == 1 ? 0 : x) * M::QT;
+            auto chunk = [&](int rr, int c) { return reinterpret_cast<uint4*>(stage + rr * RB + ((c ^ (rr & 7)) << 4)); };
+            const int es = a.yt == CQ_F32 ? 4 : 2;
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t v[32];
                 tmem_ld_32x32b_x32(tm_o(x) + lanes + 32 * c, v);
                 tmem_ld_wait();
-                if (in) {
+                float y[32];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
-                        float4 y = make_float4(__uint_as_float(v[e]) * w0, __uint_as_float(v[e + 1]) * w0,
-                                               __uint_as_float(v[e + 2]) * w0, __uint_as_float(v[e + 3]) * w0);
-                        if (both && x == 0) {
-                            const float4 z = *reinterpret_cast<const float4*>(&odd->o[r][32 * c + e]);
-                            y = make_float4(fmaf(z.x, w1, y.x), fmaf(z.y, w1, y.y), fmaf(z.z, w1, y.z), fmaf(z.w, w1, y.w));
-                        }
-                        if (direct) store_out4(a.O, at + 32 * c + e, a.yt, y.x, y.y, y.z, y.w);
-                        else *reinterpret_cast<float4*>(&part->o[r][32 * c + e]) = y;
+                for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(v[e]) * w0;
+                if (both && x == 0 && in) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float4 z = odd->o[8 * c + e][r];
+                        y[4 * e] = fmaf(z.x, w1, y[4 * e]);
+                        y[4 * e + 1] = fmaf(z.y, w1, y[4 * e + 1]);
+                        y[4 * e + 2] = fmaf(z.z, w1, y[4 * e + 2]);
+                        y[4 * e + 3] = fmaf(z.w, w1, y[4 * e + 3]);
                     }
+                }
+                if (!direct) {
+                    if (in)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) part->o[8 * c + e][r] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+                    continue;
+                }
+                if (a.yt == CQ_F32) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        *reinterpret_cast<float4*>(chunk(row, c % (D / 64) * 8 + e)) = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+                } else {
+                    uint32_t h[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) h[e] = a.yt == CQ_F16 ? pack_f16(y[2 * e], y[2 * e + 1]) : pack_bf16(y[2 * e], y[2 * e + 1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) *chunk(row, 4 * c + e) = make_uint4(h[4 * e], h[4 * e + 1], h[4 * e + 2], h[4 * e + 3]);
+                }
+                const int done = (c + 1) * 32 * es;                   // bytes of the row so far
+                if (done % RB == 0) {
+                    __syncwarp();
+                    for (int k = 0; k < 32 / RPI; ++k) {
+                        const int rr = k * RPI + lane / LPR, ff = wf + rr;
+                        if (ff <= wl)
+                            reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.O) + ((q0 + ff / G) * a.ldo + (int64_t)(w.h * G + ff % G) * D) * es +
+                                                     done - RB)[lane % LPR] = *chunk((row & 96) + rr, lane % LPR);
+                    }
+                    __syncwarp();
                 }
             }
             tc_fence_before();
@@ -755,9 +828,9 @@ __global__ void __launch_bounds__(256) k_tiles_join(const AttnArgs a, int ctas) 
     const int q0 = __ldg(a.b.q_start + it.x), n = __ldg(a.b.q_start + it.x + 1) - q0;
     const int rows = (int)min((int64_t)TILES * TM, (int64_t)n * (a.Hq / a.c.Hkv) - it.y);
     for (int k = threadIdx.x; k < 32 * (D / 4); k += 256) {
-        const int r = blockIdx.y * 32 + k / (D / 4);
+        const int r = blockIdx.y * 32 + k % 32;
         if (r < rows)
-            join<true, D>(a, q0, seg % a.c.Hkv, it.y + r, r, k % (D / 4) * 4, cnt,
+            join<true, D>(a, q0, seg % a.c.Hkv, it.y + r, r, k / 32 * 4, cnt,
                           [&](int j) { return j == 0 ? &sp->cta[i][1] : &sp->cta[i + j][0]; }, (Part<D, TILES>*)nullptr);
     }
 }
