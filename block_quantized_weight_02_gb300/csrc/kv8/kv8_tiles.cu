@@ -7,7 +7,8 @@
 // keeps two tiles going, so that the tensor cores have one while the other's softmax runs:
 // two row tiles (TILES 2, items of 256 rows), or, where no sequence has more than 128 rows,
 // the even and the odd steps of one row tile (TILES 1), whose two results are joined at the end.
-//   warp 0          issues the products
+//   warps 0, 2      issue the products of the two tiles (one thread each: a wait or a commit costs a
+//                   thread about 100 cycles, which the other's products cover)
 //   warp 1          TMA loads of the codes by page, 32 tokens a box, and their scales
 //   warps 4-7, 8-11 softmax of the two tiles, one row a thread; queries in, outputs out
 //   warps 12-15     codes -> fp16 (exactly), into the 128-byte-swizzled operand tiles
@@ -30,10 +31,11 @@ constexpr int TN = 128;                // tokens of a step
 constexpr int NB = TN / BLK;           // blocks of a step
 constexpr int MAX_CTAS = 256;          // workspace bound
 constexpr int THREADS = 512;           // four warpgroups of 128 registers a thread at launch
-constexpr int MMA_WARP = 0, LOAD_WARP = 1, SOFT_WARP = 4, CONV_WARP = 12;
+constexpr int MMA_WARP = 0, LOAD_WARP = 1, MMA_WARP2 = 2, SOFT_WARP = 4, CONV_WARP = 12;
 constexpr int REGS_SOFTMAX = 184, REGS_CONV = 72, REGS_ISSUE = 72;
 static_assert(2 * REGS_SOFTMAX + REGS_CONV + REGS_ISSUE <= 4 * 128, "what the launch has");
 constexpr int PLAN_THREADS = 1024;
+constexpr int ITEM_COST = 3;           // of beginning and ending an item, in steps
 constexpr float W_EXP = 10.f, GROW = 5.f;
 constexpr int HS = 4;                  // fp16 operand tiles in the ring (keys and values alternate)
 constexpr int SS = 8;                  // steps whose scales are kept
@@ -62,8 +64,8 @@ struct Space {
     Part<D, TILES> cta[MAX_CTAS][2];
     Part<D, TILES> odd[TILES == 1 ? MAX_CTAS : 1];   // TILES 1: the odd steps' result
     int seg[MAX_CTAS][2];              // (slot * Hkv + h) of cta[i][0] (began earlier) and cta[i][1] (began here, goes on)
-    Start start[MAX_CTAS];
-    int total, pad;
+    Start start[MAX_CTAS + 1];
+    int ok, pad[3];                    // the list stands
     Item item[1];                      // [slots]
 };
 
@@ -88,7 +90,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tiles_plan(const AttnArgs a, i
     if (__syncthreads_or(bad)) {
         if (threadIdx.x == 0) {
             set_err(a.b.err, DEV_INDEX);
-            sp->total = 0;
+            sp->ok = 0;
         }
         return;
     }
@@ -115,7 +117,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tiles_plan(const AttnArgs a, i
             it.steps = hi > lo ? (hi - lo + TN - 1) / TN : 1;
         }
         sp->item[s] = it;
-        mine += (int64_t)it.steps * a.c.Hkv;
+        if (it.steps) mine += (int64_t)(it.steps + ITEM_COST) * a.c.Hkv;
     }
     int64_t inc = mine;
     for (int o = 1; o < 32; o <<= 1) {
@@ -129,29 +131,26 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tiles_plan(const AttnArgs a, i
         if (i < warp) at += wsum[i];
         total += wsum[i];
     }
-    if (total > INT32_MAX) {
-        if (threadIdx.x == 0) {
-            set_err(a.b.err, DEV_INDEX);
-            sp->total = 0;
-        }
-        return;
+    if (threadIdx.x == 0) {
+        sp->ok = 1;
+        sp->start[ctas] = {slots, 0, 0};
     }
-    if (threadIdx.x == 0) sp->total = (int)total;
-    // the shares that begin in this thread's slots
-    const int q = (int)(total / ctas), rem = (int)(total % ctas);
+    // the shares that begin in this thread's slots: share i at cost i q + min(i, rem)
+    const int64_t q = total / ctas, rem = total % ctas;
     for (int s = s0; s < s1; ++s) {
-        const int steps = sp->item[s].steps;
-        const int64_t end = at + (int64_t)steps * a.c.Hkv;
-        if (steps) {
-            int i = q ? (int)min((int64_t)ctas, max((int64_t)0, at / (q + 1))) : (int)min((int64_t)ctas, at);
-            for (; i < ctas; ++i) {
-                const int64_t u = (int64_t)i * q + min(i, rem);
-                if (u >= end) break;
-                if (u >= at) sp->start[i] = {s, (int)((u - at) / steps), (int)((u - at) % steps)};
-            }
+        const int cost = sp->item[s].steps + ITEM_COST;
+        if (cost == ITEM_COST) continue;
+        const int64_t end = at + (int64_t)cost * a.c.Hkv;
+        for (int64_t i = at / (q + 1); i < ctas; ++i) {
+            const int64_t u = i * q + min(i, rem);
+            if (u >= end) break;
+            if (u >= at) sp->start[i] = {s, (int)((u - at) / cost), max((int)((u - at) % cost) - ITEM_COST, 0)};
         }
         at = end;
     }
+    // shares past the list (there are more CTAs than cost)
+    for (int64_t i = threadIdx.x; i < ctas; i += PLAN_THREADS)
+        if (i * q + min(i, rem) >= total) sp->start[i] = {slots, 0, 0};
 }
 
 // ---- shared memory -------------------------------------------------------------------------------------------------
@@ -175,33 +174,33 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t 
 
 // The parts of items that a CTA's share is made of, in order; every role walks the same list.
 struct Walk {
-    int slot, h, step, left;
+    Start at, end;
     Item it;
     int from, until;      // steps of the current part
     template <class S>
     __device__ __forceinline__ bool next(const AttnArgs& a, const S* sp, bool first) {
         if (!first) {
-            step = until;
-            if (step == it.steps) {
-                step = 0;
-                if (++h == a.c.Hkv) {
-                    h = 0;
-                    ++slot;
+            at.step = until;
+            if (until == it.steps) {
+                at.step = 0;
+                if (++at.h == a.c.Hkv) {
+                    at.h = 0;
+                    ++at.slot;
                 }
             }
         }
-        if (left == 0) return false;
-        const int4* p = reinterpret_cast<const int4*>(&sp->item[slot]);
-        int4 v = __ldcg(p);
-        while (v.w == 0) {
-            ++slot;
-            v = __ldcg(++p);
+        while (true) {
+            const bool last = at.slot == end.slot && at.h == end.h;
+            if (at.slot > end.slot || (at.slot == end.slot && at.h > end.h) || (last && at.step >= end.step)) return false;
+            const int4 v = __ldcg(reinterpret_cast<const int4*>(&sp->item[at.slot]));
+            if (v.w != 0) {
+                it = {v.x, v.y, v.z, v.w};
+                from = at.step;
+                until = last ? end.step : v.w;
+                return true;
+            }
+            ++at.slot;
         }
-        it = {v.x, v.y, v.z, v.w};
-        from = step;
-        until = min(it.steps, step + left);
-        left -= until - from;
-        return true;
     }
 };
 
@@ -280,7 +279,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
         }
         for (int i = 0; i < HS; ++i) {
             mbar_init(h_full + 8 * i, 4);
-            mbar_init(h_empty + 8 * i, 1);
+            mbar_init(h_empty + 8 * i, TILES);                    // TILES 1: a step belongs to one tile
         }
         for (int i = 0; i < SS; ++i) mbar_init(sc_full + 8 * i, 1);
         tmem_slot[1] = tmem_slot[2] = 0;
@@ -301,16 +300,16 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
     pdl_wait();
 
     Space<D, TILES>* sp = static_cast<Space<D, TILES>*>(a.ws);
-    const int total = __ldcg(&sp->total), G = a.Hq / a.c.Hkv;
+    const int G = a.Hq / a.c.Hkv;
     Walk w;
-    {
-        const int q = total / (int)gridDim.x, rem = total % (int)gridDim.x;
-        w.left = q + ((int)blockIdx.x < rem);
-        if (w.left) {
-            w.slot = __ldcg(&sp->start[blockIdx.x].slot);
-            w.h = __ldcg(&sp->start[blockIdx.x].h);
-            w.step = __ldcg(&sp->start[blockIdx.x].step);
-        }
+    w.at = w.end = {0, 0, 0};
+    if (__ldcg(&sp->ok)) {
+        auto get = [&](int i) {
+            const Start* p = &sp->start[i];
+            return Start{__ldcg(&p->slot), __ldcg(&p->h), __ldcg(&p->step)};
+        };
+        w.at = get(blockIdx.x);
+        w.end = get(blockIdx.x + 1);
     }
     // Every wait is bounded; the first to give up stops the CTA.
     bool alive = true;
@@ -371,22 +370,58 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
         // ---- softmax: thread = row of tile x
         const int x = (warp - SOFT_WARP) >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;        // tensor-memory lane of the warp's first row
-        uint32_t parts = 0, steps = 0, odds = 0, tile0 = 0;       // of this tile: parts, steps, joined parts; of the CTA: steps
-        for (bool first = true; alive && w.next(a, sp, first); first = false) {
-            const int n = w.until - w.from, mine = steps_of(w.it, n, x);
-            const uint32_t tile1 = tile0 + n;
-            const int q0 = __ldg(a.b.q_start + w.it.b), nq = __ldg(a.b.q_start + w.it.b + 1) - q0, L = __ldg(a.b.lens + w.it.b);
-            const int64_t rows = (int64_t)nq * G - w.it.f0;
-            if (mine == 0) {
-                tile0 = tile1;
-                continue;
+        uint32_t steps = 0, odds = 0, parts = 0, tile0 = 0;       // of this tile: steps, joined parts, parts; of the CTA: steps
+        // A part's place in the batch; its queries are on their way to registers while the part before it ends.
+        struct Rows {
+            int q0, nq, L, r, f, wf, wl;     // the sequence; this thread's row; the warp's rows (none: wl < wf)
+            int64_t rows;                    // of the item
+            bool in;
+        } t;
+        constexpr int QLPR = D / 8, QRPI = 32 / QLPR;             // lanes a row of queries, rows a load
+        uint4 v[D / 8];
+        auto enter = [&]() {
+            t.q0 = __ldg(a.b.q_start + w.it.b);
+            t.nq = __ldg(a.b.q_start + w.it.b + 1) - t.q0;
+            t.L = __ldg(a.b.lens + w.it.b);
+            t.rows = (int64_t)t.nq * G - w.it.f0;
+            t.r = (TILES == 1 ? 0 : x * TM) + row;
+            t.f = w.it.f0 + t.r;
+            t.in = t.r < t.rows;
+            t.wf = t.f - lane;
+            t.wl = (int)min((int64_t)t.wf + 31, w.it.f0 + t.rows - 1);
+            const uint16_t* Q = static_cast<const uint16_t*>(a.Q) + (int64_t)w.at.h * G * D;
+            if (TILES == 2 || x == 0) {      // neighbouring lanes read neighbouring chunks of a row
+                int ff = t.wf + lane / QLPR, tok = ff / G, g = ff % G;
+#pragma unroll
+                for (int k = 0; k < 32 / QRPI; ++k) {
+                    v[k] = make_uint4(0, 0, 0, 0);
+                    if (ff <= t.wl) v[k] = __ldg(reinterpret_cast<const uint4*>(Q + (t.q0 + tok) * a.ldq + g * D) + lane % QLPR);
+                    ff += QRPI;
+                    for (g += QRPI; g >= G; g -= G) ++tok;
+                }
+            } else if (a.xt == CQ_BF16) {    // the row's own chunks, for its guard
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c) {
+                    v[c] = make_uint4(0, 0, 0, 0);
+                    if (t.in) v[c] = __ldg(reinterpret_cast<const uint4*>(Q + (t.q0 + t.f / G) * a.ldq + t.f % G * D) + c);
+                }
             }
-            const int r = (TILES == 1 ? 0 : x * TM) + row, f = w.it.f0 + r;
-            const bool in = r < rows;
-            const int i = f / G, head = w.h * G + f % G;
-            const int wf = f - lane, wl = (int)min((int64_t)wf + 31, w.it.f0 + rows - 1);   // the warp's rows (none: wl < wf)
+        };
+        // The next part that this tile has steps of.
+        auto advance = [&](bool first) {
+            while (w.next(a, sp, first)) {
+                if (steps_of(w.it, w.until - w.from, x)) return true;
+                tile0 += w.until - w.from;
+                first = false;
+            }
+            return false;
+        };
+        bool more = advance(true);
+        if (more) enter();
+        while (more && alive) {
+            const int n = w.until - w.from, mine = steps_of(w.it, n, x);
             float qf = a.scale * LOG2E;
-            auto guard = [&](const uint4 (&v)[D / 8]) {               // bf16: the row's shift
+            auto guard = [&]() {             // bf16: the row's shift, from its chunks in v
                 uint32_t mx = 0;
                 auto top = [&](uint32_t y) { mx = max(mx, max((y << 16) & 0x7FFFFFFFu, y & 0x7FFF0000u)); };
 #pragma unroll
@@ -395,181 +430,177 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                 qf *= pow2i(-sh);
                 return pow2i(sh);
             };
-            uint4 v[D / 8];
             if (TILES == 2 || x == 0) {
-                // neighbouring lanes read neighbouring chunks of a row; each row's own thread then sees to its guard
                 uint8_t* q = smem + M::Q + x * M::QT;
                 auto chunk = [&](int rr, int c) { return reinterpret_cast<uint4*>(q + (c >> 3) * (TM * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)); };
-                constexpr int LPR = D / 8, RPI = 32 / LPR;            // lanes a row, rows a load
 #pragma unroll
-                for (int k = 0; k < 32 / RPI; ++k) {
-                    const int ff = wf + k * RPI + lane / LPR;
-                    v[k] = make_uint4(0, 0, 0, 0);
-                    if (ff <= wl)
-                        v[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.Q) + (q0 + ff / G) * a.ldq +
-                                                                    (int64_t)(w.h * G + ff % G) * D) + lane % LPR);
-                }
-#pragma unroll
-                for (int k = 0; k < 32 / RPI; ++k) *chunk((row & 96) + k * RPI + lane / LPR, lane % LPR) = v[k];
+                for (int k = 0; k < 32 / QRPI; ++k) *chunk((row & 96) + k * QRPI + lane / QLPR, lane % QLPR) = v[k];
                 __syncwarp();
-                if (a.xt == CQ_BF16) {
+                if (a.xt == CQ_BF16) {       // each row's own thread sees to its guard
 #pragma unroll
                     for (int c = 0; c < D / 8; ++c) v[c] = *chunk(row, c);
-                    const float up = guard(v);
+                    const float up = guard();
                     auto cv = [&](uint32_t y) { return pack_f16(__uint_as_float(y << 16) * up, __uint_as_float(y & 0xFFFF0000u) * up); };
 #pragma unroll
                     for (int c = 0; c < D / 8; ++c) *chunk(row, c) = make_uint4(cv(v[c].x), cv(v[c].y), cv(v[c].z), cv(v[c].w));
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(q_ready + 8 * x);
+                if (lane == 0) {
+                    mbar_arrive(q_ready + 8 * x);
+                    if (TILES == 1 && n > 1) mbar_arrive(q_ready + 8);
+                }
             } else if (a.xt == CQ_BF16) {
-                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.Q) + (q0 + i) * a.ldq + (int64_t)head * D);
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c) v[c] = in ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-                guard(v);
+                guard();
             }
 
-            const int rhi = in ? row_hi(i, nq, L, a.causal) : 0, rlo = in ? row_lo(i, nq, L, a.window) : 0;
+            const Rows u0 = t;               // of this part; t goes on to the next
+            const int i = u0.f / G;
+            const int rhi = u0.in ? row_hi(i, u0.nq, u0.L, a.causal) : 0, rlo = u0.in ? row_lo(i, u0.nq, u0.L, a.window) : 0;
             // steps inside [free_lo, free_hi) need no mask in this warp (rows past the item's take no part)
-            const int free_hi = wf <= wl ? row_hi(wf / G, nq, L, a.causal) : INT32_MAX;
-            const int free_lo = wf <= wl ? row_lo(wl / G, nq, L, a.window) : 0;
+            const int free_hi = u0.wf <= u0.wl ? row_hi(u0.wf / G, u0.nq, u0.L, a.causal) : INT32_MAX;
+            const int free_lo = u0.wf <= u0.wl ? row_lo(u0.wl / G, u0.nq, u0.L, a.window) : 0;
             float m = -INFINITY, l = 0.f;
             int ref = -64;
             for (int j = 0; j < mine; ++j, ++steps) {
                 const uint32_t tile = tile0 + j * EACH + (TILES == 1 ? x : 0);
                 if (!wait_warp(s_full + 8 * x, steps & 1) || !wait_warp(sc_full + 8 * (tile % SS), tile / SS & 1)) break;
-                if (wl < wf) {                                        // no rows: whatever lies there as weights only meets its own rows
+                if (u0.wl < u0.wf) {         // no rows: whatever lies there as weights only meets its own rows
                     if (lane == 0) mbar_arrive(p_ready + 8 * x);
                     continue;
                 }
                 tc_fence_after();
                 const int t0 = w.it.tok0 + (w.from + (int)(tile - tile0)) * TN;
-                const bool masked = t0 < free_lo || t0 + TN > free_hi;
                 const float2* sc = scales + tile % SS * NB;
                 int nref = ref;
+                uint32_t odd_k = 0;          // blocks whose factor is no positive number: their scores are taken in full below
 #pragma unroll
-                for (int c = 0; c < NB; ++c) nref = max(nref, scale_of(sc[c], qf).lv);
-                // One pass where no row of the warp has a mask and the maximum may stay as it is (all but a few
-                // steps): weights against the m so far, kept in registers until the step's maximum is known.  It is
-                // not for scores of 2^20 and more, which have to be rounded before m is taken off, as they were for
-                // m: the fused step would leave their own rounding, which is then no longer small.
-                bool done = false;
-                if (PT == 1 && !masked && nref == ref && !__any_sync(0xffffffffu, !(fabsf(m) <= 1048576.f))) {
-                    float top = -INFINITY, more = 0.f;
-                    uint32_t v[2][32], p[NB][16], unused;
-                    tmem_ld_32x32b_x32(tm_s(x) + lanes, v[0]);
-#pragma unroll
-                    for (int c = 0; c < NB; ++c) {
-                        tmem_ld_wait();
-                        if (c + 1 < NB) tmem_ld_32x32b_x32(tm_s(x) + lanes + 32 * (c + 1), v[(c + 1) & 1]);
-                        const Scale k = scale_of(sc[c], qf);
-                        const int lc = max(k.lv, ref - 64);
-                        const float sub = W_EXP + (float)(lc - ref) - m;
-                        const uint64_t k2 = pair(k.k, k.k), sub2 = pair(sub, sub);
-                        const uint32_t(&u)[32] = v[c & 1];
-                        uint64_t sum = 0;
-                        float mx = -INFINITY;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float a0 = __uint_as_float(u[2 * e]), a1 = __uint_as_float(u[2 * e + 1]);
-                            mx = fmaxf(mx, fmaxf(a0, a1));
-                            const float2 y = unpair(fma2(pair(a0, a1), k2, sub2));
-                            weights<1>(ex2(y.x), ex2(y.y), sum, p[c][e], unused);
-                        }
-                        top = fmaxf(top, mx * k.k);
-                        const float2 t = unpair(sum);
-                        more = fmaf(t.x + t.y, pow2i(ref - lc - (int)W_EXP), more);
-                    }
-                    if (!__any_sync(0xffffffffu, top > m + GROW)) {
-                        l += more;
-#pragma unroll
-                        for (int c = 0; c < NB; ++c) tmem_st_32x32b_x16(tm_s(x) + lanes + 32 * c, p[c]);
-                        done = true;
-                    }
+                for (int c = 0; c < NB; ++c) {
+                    const Scale k = scale_of(sc[c], qf);
+                    nref = max(nref, k.lv);
+                    if (!(k.k > 0.f && k.k < INFINITY)) odd_k |= 1u << c;
                 }
-                if (!done) {
-                    // Two passes by block: the maximum, then the weights.
-                    float top = -INFINITY;
+                // Scores that a row does not see become -inf.  Blocks with an odd factor are multiplied here.
+                auto prepare = [&](uint32_t full) {
 #pragma unroll 1
-                    for (int c = 0; c < NB; ++c) {
-                        uint32_t u[32];
-                        tmem_ld_32x32b_x32(tm_s(x) + lanes + 32 * c, u);
+                    for (int c = 0; c < TN / 16; ++c) {
+                        uint32_t y[16];
+                        tmem_ld_32x32b_x16(tm_s(x) + lanes + 16 * c, y);
                         tmem_ld_wait();
-                        float mx = -INFINITY;
-                        if (masked) {
+                        const float k = full >> (c >> 1) & 1 ? scale_of(sc[c >> 1], qf).k : 1.f;
+                        const int lo = rlo - t0 - 16 * c, hi = rhi - t0 - 16 * c;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                const int tok = t0 + 32 * c + e;
-                                mx = fmaxf(mx, tok >= rlo && tok < rhi ? __uint_as_float(u[e]) : -INFINITY);
-                            }
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(u[e]));
-                        }
-                        top = fmaxf(top, mx * scale_of(sc[c], qf).k);
+                        for (int e = 0; e < 16; ++e)
+                            y[e] = e >= lo && e < hi ? __float_as_uint(__uint_as_float(y[e]) * k) : 0xFF800000u;
+                        tmem_st_32x32b_x16(tm_s(x) + lanes + 16 * c, y);
                     }
-                const bool grow = top > m + GROW;
-                if (__any_sync(0xffffffffu, grow) || nref > ref) {
-                    const float nm = grow ? top : m;
-                    const float fm = grow ? ex2(m - nm) : 1.f, fo = fm * pow2i(max(ref - nref, -126));
-                    m = nm;
-                    l *= fm;
-                    ref = nref;
-                    if (j > 0) {
+                    tmem_st_wait();
+                };
+                uint32_t full = 0;
+                if (__any_sync(0xffffffffu, t0 < free_lo || t0 + TN > free_hi || odd_k != 0)) {
+                    // one choice of blocks for the warp: a factor that is odd in one row is taken in full in all
+                    full = __reduce_or_sync(0xffffffffu, odd_k);
+                    prepare(full);
+                }
+                // One pass: weights against the m so far, kept in registers until the step's maximum is known.  Where
+                // that has grown by more than GROW (and at first) the maximum comes before them.  f32 outputs
+                // (whose weights take twice the registers) always take the maximum first.
+                bool again = PT == 2 || nref != ref || __any_sync(0xffffffffu, !(fabsf(m) <= 1048576.f));
+                while (true) {
+                    if (again) {
+                        float top = -INFINITY;
 #pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t u[32];
-                            tmem_ld_32x32b_x32(tm_o(x) + lanes + 32 * c, u);
+                        for (int c = 0; c < NB; ++c) {
+                            uint32_t y[32];
+                            tmem_ld_32x32b_x32(tm_s(x) + lanes + 32 * c, y);
                             tmem_ld_wait();
+                            float mx = -INFINITY;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * fo);
-                            tmem_st_32x32b_x32(tm_o(x) + lanes + 32 * c, u);
+                            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(y[e]));
+                            top = fmaxf(top, full >> c & 1 ? mx : mx * scale_of(sc[c], qf).k);
+                        }
+                        const bool grow = top > m + GROW;
+                        if (__any_sync(0xffffffffu, grow) || nref > ref) {
+                            const float nm = grow ? top : m;
+                            const float fm = grow ? ex2(m - nm) : 1.f, fo = fm * pow2i(max(ref - nref, -126));
+                            m = nm;
+                            l *= fm;
+                            ref = nref;
+                            if (j > 0) {
+#pragma unroll 1
+                                for (int c = 0; c < D / 32; ++c) {
+                                    uint32_t y[32];
+                                    tmem_ld_32x32b_x32(tm_o(x) + lanes + 32 * c, y);
+                                    tmem_ld_wait();
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * fo);
+                                    tmem_st_32x32b_x32(tm_o(x) + lanes + 32 * c, y);
+                                }
+                            }
+                        }
+                        // Scores of 2^20 and more are rounded before m is taken off, as they were for m: a fused step
+                        // would leave their own rounding, which is then no longer small.
+                        if (full != (1u << NB) - 1 && __any_sync(0xffffffffu, fabsf(m) > 1048576.f && m != -INFINITY)) {
+                            prepare(~full & ((1u << NB) - 1));
+                            full = (1u << NB) - 1;
                         }
                     }
-                }
-                const float m0 = m == -INFINITY ? 0.f : m;
-                const bool plain = !masked && !__any_sync(0xffffffffu, fabsf(m0) > 1048576.f);
-                {
-#pragma unroll 1
+                    const float m0 = m == -INFINITY ? 0.f : m;
+                    float top = -INFINITY, add = 0.f;
+                    uint32_t s[2][32], p[PT == 1 ? NB : 1][16], p2[16];
+                    tmem_ld_32x32b_x32(tm_s(x) + lanes, s[0]);
+#pragma unroll
                     for (int c = 0; c < NB; ++c) {
+                        tmem_ld_wait();
+                        if (c + 1 < NB) tmem_ld_32x32b_x32(tm_s(x) + lanes + 32 * (c + 1), s[(c + 1) & 1]);
                         const Scale k = scale_of(sc[c], qf);
+                        const float kc = full >> c & 1 ? 1.f : k.k;
                         const int lc = max(k.lv, ref - 64);
                         const float sub = W_EXP + (float)(lc - ref) - m0;
-                        uint32_t u[32], p[16], p2[16];
-                        tmem_ld_32x32b_x32(tm_s(x) + lanes + 32 * c, u);
-                        tmem_ld_wait();
+                        const uint64_t k2 = pair(kc, kc), sub2 = pair(sub, sub);
+                        const uint32_t(&y)[32] = s[c & 1];
+                        uint32_t(&pc)[16] = p[PT == 1 ? c : 0];
                         uint64_t sum = 0;
+                        float mx = -INFINITY;
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const float a0 = __uint_as_float(u[2 * e]), a1 = __uint_as_float(u[2 * e + 1]);
-                            if (plain) {
-                                const float2 y = unpair(fma2(pair(a0, a1), pair(k.k, k.k), pair(sub, sub)));
-                                weights<PT>(ex2(y.x), ex2(y.y), sum, p[e], p2[e]);
-                            } else {
-                                const int tok = t0 + 32 * c + 2 * e;
-                                const float y0 = ex2(__fadd_rn(__fmul_rn(a0, k.k), sub)), y1 = ex2(__fadd_rn(__fmul_rn(a1, k.k), sub));
-                                weights<PT>(tok >= rlo && tok < rhi ? y0 : 0.f, tok + 1 >= rlo && tok + 1 < rhi ? y1 : 0.f, sum,
-                                            p[e], p2[e]);
-                            }
+                            const float a0 = __uint_as_float(y[2 * e]), a1 = __uint_as_float(y[2 * e + 1]);
+                            if (PT == 1) mx = fmaxf(mx, fmaxf(a0, a1));
+                            const float2 z = unpair(fma2(pair(a0, a1), k2, sub2));
+                            weights<PT>(ex2(z.x), ex2(z.y), sum, pc[e], p2[e]);
                         }
-                        const float2 t = unpair(sum);
-                        l = fmaf(t.x + t.y, pow2i(ref - lc - (int)W_EXP), l);
-                        tmem_st_32x32b_x16(tm_s(x) + lanes + 32 * c, p);
-                        if (PT == 2) tmem_st_32x32b_x16(tm_s(x) + lanes + 32 * c + 16, p2);
+                        top = fmaxf(top, mx * kc);
+                        const float2 z = unpair(sum);
+                        add = fmaf(z.x + z.y, pow2i(ref - lc - (int)W_EXP), add);
+                        if (PT == 2) {
+                            tmem_st_32x32b_x16(tm_s(x) + lanes + 32 * c, pc);
+                            tmem_st_32x32b_x16(tm_s(x) + lanes + 32 * c + 16, p2);
+                        }
                     }
-                }
+                    if (PT == 1 && !again && __any_sync(0xffffffffu, top > m + GROW)) {
+                        again = true;
+                        continue;
+                    }
+                    l += add;
+                    if (PT == 1) {
+#pragma unroll
+                        for (int c = 0; c < NB; ++c) tmem_st_32x32b_x16(tm_s(x) + lanes + 32 * c, p[PT == 1 ? c : 0]);
+                    }
+                    break;
                 }
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_ready + 8 * x);
             }
+            const Walk cur = w;              // this part; w goes on to the next
+            tile0 += n;
+            more = alive && advance(false);
+            if (more) enter();
             if (!wait_warp(o_full + 8 * x, parts & 1)) break;
             ++parts;
-            tile0 = tile1;
             tc_fence_after();
-            const bool begins = w.from == 0, ends = w.until == w.it.steps, whole = begins && ends;
+            const bool begins = cur.from == 0, ends = cur.until == cur.it.steps, whole = begins && ends;
             const float un = pow2i(ref - (int)W_EXP);
             // TILES 1: the odd steps' result goes to the even steps' threads
             Part<D, TILES>* odd = &sp->odd[TILES == 1 ? blockIdx.x : 0];
@@ -577,8 +608,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
             float w0 = un, w1 = 0.f;
             if (both && x == 0) {
                 if (!wait_warp(odd_full, odds++ & 1)) break;
-                if (in) {
-                    const float m1 = odd->m[r], l1 = odd->l[r], top = fmaxf(m, m1);
+                if (u0.in) {
+                    const float m1 = odd->m[u0.r], l1 = odd->l[u0.r], top = fmaxf(m, m1);
                     const float e0 = m == -INFINITY ? 1.f : ex2(m - top), e1 = m1 == -INFINITY ? 1.f : ex2(m1 - top);
                     w0 = un * e0;
                     w1 = e1;
@@ -607,10 +638,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                 float y[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(v[e]) * w0;
-                if (both && x == 0 && in) {
+                if (both && x == 0 && u0.in) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        const float4 z = odd->o[8 * c + e][r];
+                        const float4 z = odd->o[8 * c + e][u0.r];
                         y[4 * e] = fmaf(z.x, w1, y[4 * e]);
                         y[4 * e + 1] = fmaf(z.y, w1, y[4 * e + 1]);
                         y[4 * e + 2] = fmaf(z.z, w1, y[4 * e + 2]);
@@ -618,9 +649,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                     }
                 }
                 if (!direct) {
-                    if (in)
+                    if (u0.in)
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) part->o[8 * c + e][r] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+                        for (int e = 0; e < 8; ++e) part->o[8 * c + e][u0.r] = make_float4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
                     continue;
                 }
                 if (a.yt == CQ_F32) {
@@ -637,40 +668,46 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                 const int done = (c + 1) * 32 * es;                   // bytes of the row so far
                 if (done % RB == 0) {
                     __syncwarp();
+                    int ff = u0.wf + lane / LPR, tok = ff / G, g = ff % G;
+                    char* out = static_cast<char*>(a.O) + (int64_t)cur.at.h * G * D * es + (done - RB) + lane % LPR * 16;
+#pragma unroll 4
                     for (int k = 0; k < 32 / RPI; ++k) {
-                        const int rr = k * RPI + lane / LPR, ff = wf + rr;
-                        if (ff <= wl)
-                            reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.O) + ((q0 + ff / G) * a.ldo + (int64_t)(w.h * G + ff % G) * D) * es +
-                                                     done - RB)[lane % LPR] = *chunk((row & 96) + rr, lane % LPR);
+                        if (ff <= u0.wl)
+                            *reinterpret_cast<uint4*>(out + ((u0.q0 + tok) * a.ldo + g * D) * es) = *chunk((row & 96) + k * RPI + lane / LPR, lane % LPR);
+                        ff += RPI;
+                        for (g += RPI; g >= G; g -= G) ++tok;
                     }
                     __syncwarp();
                 }
             }
             tc_fence_before();
-            if (in) {
+            if (u0.in) {
                 if (direct) {
-                    if (a.lse) a.lse[(int64_t)(q0 + i) * a.Hq + head] = lse_of(m, l);
+                    if (a.lse) a.lse[(int64_t)(u0.q0 + i) * a.Hq + cur.at.h * G + u0.f % G] = lse_of(m, l);
                 } else {
-                    part->m[r] = m;
-                    part->l[r] = l;
+                    part->m[u0.r] = m;
+                    part->l[u0.r] = l;
                 }
             }
             if (both && x == 1) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(odd_full);
             }
-            if (!whole && x == 0 && row == 0) sp->seg[blockIdx.x][begins ? 1 : 0] = w.slot * a.c.Hkv + w.h;
+            if (!whole && x == 0 && row == 0) sp->seg[blockIdx.x][begins ? 1 : 0] = cur.at.slot * a.c.Hkv + cur.at.h;
         }
     } else {
         regs_down<REGS_ISSUE>();
-        if (warp == MMA_WARP) {
-            // ---- products, from one thread
+        if (warp == MMA_WARP || warp == MMA_WARP2) {
+            // ---- products of tile x, from one thread
             if (lane == 0) {
                 constexpr uint32_t id_qk = idesc_f16(TM, TN, 0), id_pv = idesc_f16(TM, D, 0) | (1u << 16);
-                uint32_t k = 0, parts[2] = {0, 0}, steps[2] = {0, 0};
-                auto qk = [&](int x, uint32_t kt) {
+                const int x = warp == MMA_WARP2;
+                uint32_t k0 = 0, parts = 0, steps = 0;            // k0: operand tiles before the part
+                auto h_wait = [&](uint32_t kt) { return wait(h_full + 8 * (kt % HS), kt / HS & 1); };
+                auto qk = [&](uint32_t kt) {
                     const uint64_t qa = smem_desc_sw128(sb + M::Q + (TILES == 1 ? 0 : x) * M::QT);
                     const uint64_t ka = smem_desc_sw128(sb + M::H + (kt % HS) * M::HT);
+                    tc_fence_after();
 #pragma unroll
                     for (int s = 0; s < D / 16; ++s) {
                         const uint32_t off = ((s >> 2) * (TM * 128) + (s & 3) * 32) >> 4;
@@ -678,8 +715,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                     }
                     tc_commit(s_full + 8 * x);
                 };
-                auto pv = [&](int x, uint32_t vt, bool acc) {
+                auto pv = [&](uint32_t vt, bool acc) {
                     const uint64_t va = smem_desc_mn_sw128(sb + M::H + (vt % HS) * M::HT, TN * 128);
+                    tc_fence_after();
 #pragma unroll
                     for (int z = 0; z < PT; ++z)
 #pragma unroll
@@ -687,70 +725,38 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                             tc_mma_f16_ts(tm_o(x), tm_s(x) + (s >> 1) * 32 + (s & 1) * 8 + z * 16, va + s * (2048 >> 4), id_pv,
                                           acc || s > 0 || z > 0);
                 };
-                auto h_wait = [&](uint32_t kt) { return wait(h_full + 8 * (kt % HS), kt / HS & 1); };
                 for (bool first = true; alive && w.next(a, sp, first); first = false) {
-                    const int n = w.until - w.from;
-                    if (TILES == 1) {
-                        // steps j take tile j % 2; step j + 2's scores follow step j's output
-                        if (!wait(q_ready, parts[0]++ & 1)) break;
-                        for (int j = 0; j < min(n, 2); ++j) {
-                            if (!h_wait(k + 2 * j)) break;
-                            tc_fence_after();
-                            qk(j, k + 2 * j);
-                            tc_commit(h_empty + 8 * ((k + 2 * j) % HS));
-                        }
-                        for (int j = 0; j < n && alive; ++j) {
-                            const int x = j & 1;
-                            const uint32_t kt = k + 2 * j;
-                            if (!wait(p_ready + 8 * x, steps[x]++ & 1) || !h_wait(kt + 1)) break;
-                            tc_fence_after();
-                            pv(x, kt + 1, j >= 2);
-                            if (j + 2 < n) {
-                                tc_commit(h_empty + 8 * ((kt + 1) % HS));
-                                if (!h_wait(kt + 4)) break;
-                                tc_fence_after();
-                                qk(x, kt + 4);
-                                tc_commit(h_empty + 8 * ((kt + 4) % HS));
+                    const int n = w.until - w.from, mine = steps_of(w.it, n, x);
+                    if (mine == 0) {
+                        if (TILES == 2)                           // not this tile's: the operands go back from here at once
+                            for (int j = 0; j < 2 * n && h_wait(k0 + j); ++j) mbar_arrive(h_empty + 8 * ((k0 + j) % HS));
+                    } else {
+                        uint32_t kt = k0 + (TILES == 1 ? 2 * x : 0);      // the step's keys; its values are kt + 1
+                        if (!wait(q_ready + 8 * x, parts++ & 1) || !h_wait(kt)) break;
+                        qk(kt);
+                        tc_commit(h_empty + 8 * (kt % HS));
+                        for (int j = 0; j < mine; ++j, kt += 2 * EACH) {
+                            if (!wait(p_ready + 8 * x, steps++ & 1) || !h_wait(kt + 1)) break;
+                            pv(kt + 1, j > 0);
+                            if (j + 1 < mine) {
+                                const uint32_t next = kt + 2 * EACH;
+                                // TILES 1: the next keys may need the slot of these values' successor, so they go first
+                                if (TILES == 1) tc_commit(h_empty + 8 * ((kt + 1) % HS));
+                                if (!h_wait(next)) break;
+                                qk(next);
+                                if (TILES == 2) tc_commit(h_empty + 8 * ((kt + 1) % HS));
+                                tc_commit(h_empty + 8 * (next % HS));
                             } else {
                                 tc_commit(o_full + 8 * x);
                                 tc_commit(h_empty + 8 * ((kt + 1) % HS));
                             }
                         }
-                        k += 2 * n;
-                    } else {
-                        const int nx = steps_of(w.it, n, 1) ? 2 : 1;
-                        if (!h_wait(k)) break;
-                        for (int x = 0; x < nx; ++x) {
-                            if (!wait(q_ready + 8 * x, parts[x]++ & 1)) break;
-                            tc_fence_after();
-                            qk(x, k);
-                        }
-                        if (!alive) break;
-                        tc_commit(h_empty + 8 * (k % HS));
-                        for (int j = 0; j < n && alive; ++j, k += 2) {
-                            if (!h_wait(k + 1)) break;
-                            const bool more = j + 1 < n;
-                            for (int x = 0; x < nx; ++x) {
-                                if (!wait(p_ready + 8 * x, steps[x]++ & 1)) break;
-                                tc_fence_after();
-                                pv(x, k + 1, j > 0);
-                                if (more) {
-                                    if (x == 0 && !h_wait(k + 2)) break;
-                                    tc_fence_after();
-                                    qk(x, k + 2);
-                                } else {
-                                    tc_commit(o_full + 8 * x);
-                                }
-                            }
-                            if (!alive) break;
-                            tc_commit(h_empty + 8 * ((k + 1) % HS));
-                            if (more) tc_commit(h_empty + 8 * ((k + 2) % HS));
-                        }
                     }
+                    k0 += 2 * n;
                 }
                 if (!alive) {  // let the products in flight end before the tensor memory goes: nothing else waits for this
-                    tc_commit(q_ready);
-                    mbar_wait(q_ready, parts[0] & 1, 10000000, never);
+                    tc_commit(q_ready + 8 * x);
+                    mbar_wait(q_ready + 8 * x, parts & 1, 10000000, never);
                 }
             }
             __syncwarp();
@@ -771,7 +777,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                             set_err(a.b.err, DEV_INDEX);
                             pid = 0;
                         }
-                        row1 = (pid * a.c.Hkv + w.h) * a.c.page + tok % a.c.page;
+                        row1 = (pid * a.c.Hkv + w.at.h) * a.c.page + tok % a.c.page;
                         s1 = make_float2(__ldg(a.c.s[0] + row1 / BLK), __ldg(a.c.s[1] + row1 / BLK));
                     }
                 };
