@@ -1,5 +1,5 @@
 // Attention over the 8-bit cache for few query rows per sequence (single tokens,
-// short guesses): at most 16 rows of one KV head, a row being a (token, head of the
+// short guesses): at most 32 rows of one KV head, a row being a (token, head of the
 // group) pair.
 //
 // Bound by HBM: the cache is read once.  The work is the list of all visible blocks
@@ -33,7 +33,7 @@ namespace cq {
 namespace kv8 {
 namespace {
 
-constexpr int ROWS = 16;
+constexpr int ROWS = 32;
 constexpr int MAX_CTAS = 256;         // workspace bound
 constexpr int MAX_NW = 12;
 constexpr int P_EXP = 15;             // weights carry 2^15
@@ -52,14 +52,18 @@ struct Space {
     int seg[MAX_CTAS][2];             // segment of cta[i][0] (began earlier) and cta[i][1] (began here, goes on), or -1
 };
 
-// NT: n8 tiles of rows.  One tile fits 12 warps with two blocks each (registers), two tiles 8 warps with three.
+// NT: n8 tiles of rows.  One tile fits 12 warps with two blocks each (registers), more tiles 8 warps with three, or
+// two beside the queries, which three tiles and more keep in shared memory.
 template <int D, int NT>
 struct Ring {
     static constexpr int NW = NT == 1 ? 12 : 8;
-    static constexpr int ST = (NT == 1 ? 2 : 3) * (128 / D);   // blocks in the ring of a warp: 192 KB a CTA
+    static constexpr bool QS = NT > 2;
+    static constexpr int ST = (NT == 2 ? 3 : 2) * (128 / D);   // blocks in the ring of a warp: 192 KB a CTA
     static constexpr int TILE = BLK * D;                       // bytes of a block's keys or values
-    static constexpr int BYTES = NW * ST * 2 * TILE;
-    static_assert(ST * 2 * TILE >= (int)sizeof(Part<D>) && NW <= MAX_NW, "a partial fits the ring of its warp");
+    static constexpr int QB = QS ? NT * D * 16 : 0;            // a warp's queries, in its lanes' order
+    static constexpr int Q = NW * ST * 2 * TILE;
+    static constexpr int BYTES = Q + NW * QB;
+    static_assert(ST * 2 * TILE + QB >= NT * 8 * D * 4 + 2 * ROWS * 4 && NW <= MAX_NW, "a partial fits a warp's memory");
 };
 
 struct Seq {

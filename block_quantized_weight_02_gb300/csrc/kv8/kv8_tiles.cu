@@ -8,7 +8,8 @@
 // two row tiles (TILES 2, items of 256 rows), or, where no sequence has more than 128 rows,
 // the even and the odd steps of one row tile (TILES 1), whose two results are joined at the end.
 //   warps 0, 2      issue the products of the two tiles (one thread each: a wait or a commit costs a
-//                   thread about 100 cycles, which the other's products cover)
+//                   thread about 100 cycles, which the other's products cover), in turns: left to
+//                   themselves the tiles fall into step, and both softmaxes run while no products do
 //   warp 1          TMA loads of the codes by page, 32 tokens a box, and their scales
 //   warps 4-7, 8-11 softmax of the two tiles, one row a thread; queries in, outputs out
 //   warps 12-15     codes -> fp16 (exactly), into the 128-byte-swizzled operand tiles
@@ -30,8 +31,8 @@ constexpr int TM = 128;                // rows of a tensor-core tile
 constexpr int TN = 128;                // tokens of a step
 constexpr int NB = TN / BLK;           // blocks of a step
 constexpr int MAX_CTAS = 256;          // workspace bound
-constexpr int THREADS = 512;           // four warpgroups of 128 registers a thread at launch
 constexpr int MMA_WARP = 0, LOAD_WARP = 1, MMA_WARP2 = 2, SOFT_WARP = 4, CONV_WARP = 12;
+constexpr int THREADS = 512;           // four warpgroups of 128 registers a thread at launch
 constexpr int REGS_SOFTMAX = 184, REGS_CONV = 72, REGS_ISSUE = 72;
 static_assert(2 * REGS_SOFTMAX + REGS_CONV + REGS_ISSUE <= 4 * 128, "what the launch has");
 constexpr int PLAN_THREADS = 1024;
@@ -161,7 +162,7 @@ struct Smem {
     static constexpr int HT = TN * D * 2;         // an fp16 operand tile, the same
     static constexpr int RT = TN * D;             // codes
     static constexpr int Q = 0, H = TILES * QT, R = H + HS * HT, MISC = R + RS * RT;
-    static constexpr int NBAR = 2 * RS + 2 * HS + SS + 9;
+    static constexpr int NBAR = 2 * RS + 2 * HS + SS + 11;
     static constexpr int SC = MISC + NBAR * 8;    // float2 [SS][NB]
     static constexpr int END = SC + SS * NB * 8 + 16;
 };
@@ -213,6 +214,11 @@ __device__ __forceinline__ Scale scale_of(float2 s, float qf) {
     const bool nan = s.y != s.y;
     return {qf * (nan ? s.y : s.x), nan ? -64 : exp_of(s.y)};
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 // Two floats in one register pair: one instruction for both.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
     uint64_t r;
@@ -258,7 +264,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
     const uint32_t sb = smem_u32(smem), raw_full = sb + M::MISC, raw_empty = raw_full + 8 * M::RS,
                    h_full = raw_empty + 8 * M::RS, h_empty = h_full + 8 * HS, sc_full = h_empty + 8 * HS,
                    q_ready = sc_full + 8 * SS, s_full = q_ready + 16, p_ready = s_full + 16, o_full = p_ready + 16,
-                   odd_full = o_full + 16;
+                   odd_full = o_full + 16, turn = odd_full + 8;
     float2* scales = reinterpret_cast<float2*>(smem + M::SC);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + M::SC + SS * NB * 8);
     volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -271,6 +277,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
             mbar_init(s_full + 8 * i, 1);
             mbar_init(p_ready + 8 * i, 4);
             mbar_init(o_full + 8 * i, 1);
+            mbar_init(turn + 8 * i, 1);
         }
         mbar_init(odd_full, 4);
         for (int i = 0; i < M::RS; ++i) {
@@ -336,7 +343,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
     if (warp >= CONV_WARP) {
         regs_down<REGS_CONV>();
         // ---- codes -> fp16: thread = token; keys and values of a step alternate
-        const int tok = threadIdx.x - CONV_WARP * 32;
+        const int tok = threadIdx.x & 127;
         uint32_t k = 0;                          // operand tiles so far
         for (bool first = true; alive && w.next(a, sp, first); first = false) {
             for (int j = 0; j < 2 * (w.until - w.from) && alive; ++j, ++k) {
@@ -464,12 +471,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
             int ref = -64;
             for (int j = 0; j < mine; ++j, ++steps) {
                 const uint32_t tile = tile0 + j * EACH + (TILES == 1 ? x : 0);
-                if (!wait_warp(s_full + 8 * x, steps & 1) || !wait_warp(sc_full + 8 * (tile % SS), tile / SS & 1)) break;
-                if (u0.wl < u0.wf) {         // no rows: whatever lies there as weights only meets its own rows
-                    if (lane == 0) mbar_arrive(p_ready + 8 * x);
-                    continue;
-                }
-                tc_fence_after();
+                if (!wait_warp(sc_full + 8 * (tile % SS), tile / SS & 1)) break;
                 const int t0 = w.it.tok0 + (w.from + (int)(tile - tile0)) * TN;
                 const float2* sc = scales + tile % SS * NB;
                 int nref = ref;
@@ -480,6 +482,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                     nref = max(nref, k.lv);
                     if (!(k.k > 0.f && k.k < INFINITY)) odd_k |= 1u << c;
                 }
+                const bool prep = __any_sync(0xffffffffu, t0 < free_lo || t0 + TN > free_hi || odd_k != 0);
+                bool again = PT == 2 || nref != ref || __any_sync(0xffffffffu, !(fabsf(m) <= 1048576.f));
+                if (!wait_warp(s_full + 8 * x, steps & 1)) break;
+                if (u0.wl < u0.wf) {         // no rows: whatever lies there as weights only meets its own rows
+                    if (lane == 0) mbar_arrive(p_ready + 8 * x);
+                    continue;
+                }
+                tc_fence_after();
                 // Scores that a row does not see become -inf.  Blocks with an odd factor are multiplied here.
                 auto prepare = [&](uint32_t full) {
 #pragma unroll 1
@@ -497,7 +507,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                     tmem_st_wait();
                 };
                 uint32_t full = 0;
-                if (__any_sync(0xffffffffu, t0 < free_lo || t0 + TN > free_hi || odd_k != 0)) {
+                if (prep) {
                     // one choice of blocks for the warp: a factor that is odd in one row is taken in full in all
                     full = __reduce_or_sync(0xffffffffu, odd_k);
                     prepare(full);
@@ -505,7 +515,6 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                 // One pass: weights against the m so far, kept in registers until the step's maximum is known.  Where
                 // that has grown by more than GROW (and at first) the maximum comes before them.  f32 outputs
                 // (whose weights take twice the registers) always take the maximum first.
-                bool again = PT == 2 || nref != ref || __any_sync(0xffffffffu, !(fabsf(m) <= 1048576.f));
                 while (true) {
                     if (again) {
                         float top = -INFINITY;
@@ -516,7 +525,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                             tmem_ld_wait();
                             float mx = -INFINITY;
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) mx = fmaxf(mx, __uint_as_float(y[e]));
+                            for (int e = 0; e < 32; e += 2) mx = max3(mx, __uint_as_float(y[e]), __uint_as_float(y[e + 1]));
                             top = fmaxf(top, full >> c & 1 ? mx : mx * scale_of(sc[c], qf).k);
                         }
                         const bool grow = top > m + GROW;
@@ -565,7 +574,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
                             const float a0 = __uint_as_float(y[2 * e]), a1 = __uint_as_float(y[2 * e + 1]);
-                            if (PT == 1) mx = fmaxf(mx, fmaxf(a0, a1));
+                            if (PT == 1) mx = max3(mx, a0, a1);
                             const float2 z = unpair(fma2(pair(a0, a1), k2, sub2));
                             weights<PT>(ex2(z.x), ex2(z.y), sum, pc[e], p2[e]);
                         }
@@ -702,9 +711,15 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
             if (lane == 0) {
                 constexpr uint32_t id_qk = idesc_f16(TM, TN, 0), id_pv = idesc_f16(TM, D, 0) | (1u << 16);
                 const int x = warp == MMA_WARP2;
-                uint32_t k0 = 0, parts = 0, steps = 0;            // k0: operand tiles before the part
+                uint32_t k0 = 0, parts = 0, steps = 0, turns = 0; // k0: operand tiles before the part
+                // The first turn is tile 0's; the last of a part hands it back to tile 0.  (TILES 1 measured 5 % slower
+                // with turns: its loads set the pace.)
+                auto take = [&](bool both) { return !both || wait(turn + 8 * x, (turns++ + (x == 0)) & 1); };
+                auto pass = [&](bool both, bool last) {
+                    if (both) mbar_arrive(turn + 8 * (last ? 0 : 1 - x));
+                };
                 auto h_wait = [&](uint32_t kt) { return wait(h_full + 8 * (kt % HS), kt / HS & 1); };
-                auto qk = [&](uint32_t kt) {
+                auto qk = [&](uint32_t kt, bool both) {
                     const uint64_t qa = smem_desc_sw128(sb + M::Q + (TILES == 1 ? 0 : x) * M::QT);
                     const uint64_t ka = smem_desc_sw128(sb + M::H + (kt % HS) * M::HT);
                     tc_fence_after();
@@ -712,6 +727,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                     for (int s = 0; s < D / 16; ++s) {
                         const uint32_t off = ((s >> 2) * (TM * 128) + (s & 3) * 32) >> 4;
                         tc_mma_f16(tm_s(x), qa + off, ka + off, id_qk, s > 0);
+                        if (s == D / 32 - 1) pass(both, false);   // the turn takes 300 cycles to reach the other thread
                     }
                     tc_commit(s_full + 8 * x);
                 };
@@ -731,23 +747,25 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                         if (TILES == 2)                           // not this tile's: the operands go back from here at once
                             for (int j = 0; j < 2 * n && h_wait(k0 + j); ++j) mbar_arrive(h_empty + 8 * ((k0 + j) % HS));
                     } else {
+                        const bool both = TILES == 2 && steps_of(w.it, n, 1) > 0;
                         uint32_t kt = k0 + (TILES == 1 ? 2 * x : 0);      // the step's keys; its values are kt + 1
-                        if (!wait(q_ready + 8 * x, parts++ & 1) || !h_wait(kt)) break;
-                        qk(kt);
+                        if (!wait(q_ready + 8 * x, parts++ & 1) || !h_wait(kt) || !take(both)) break;
+                        qk(kt, both);
                         tc_commit(h_empty + 8 * (kt % HS));
                         for (int j = 0; j < mine; ++j, kt += 2 * EACH) {
-                            if (!wait(p_ready + 8 * x, steps++ & 1) || !h_wait(kt + 1)) break;
+                            // what is mostly there already is waited for first: each such wait takes 100 cycles, which
+                            // would come between the weights and their product
+                            const uint32_t next = kt + 2 * EACH;
+                            if (!h_wait(kt + 1) || (j + 1 < mine && !h_wait(next)) || !take(both)) break;
+                            if (!wait(p_ready + 8 * x, steps++ & 1)) break;
                             pv(kt + 1, j > 0);
                             if (j + 1 < mine) {
-                                const uint32_t next = kt + 2 * EACH;
-                                // TILES 1: the next keys may need the slot of these values' successor, so they go first
-                                if (TILES == 1) tc_commit(h_empty + 8 * ((kt + 1) % HS));
-                                if (!h_wait(next)) break;
-                                qk(next);
-                                if (TILES == 2) tc_commit(h_empty + 8 * ((kt + 1) % HS));
+                                qk(next, both);
+                                tc_commit(h_empty + 8 * ((kt + 1) % HS));
                                 tc_commit(h_empty + 8 * (next % HS));
                             } else {
                                 tc_commit(o_full + 8 * x);
+                                pass(both, x == 1);
                                 tc_commit(h_empty + 8 * ((kt + 1) % HS));
                             }
                         }
