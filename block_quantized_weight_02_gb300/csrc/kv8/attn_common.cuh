@@ -60,8 +60,8 @@ __device__ __forceinline__ int row_lo(int i, int n, int L, int64_t window) {
 // An unfinished result: O before the division, the maximum (log2 units) and the sum of each row.
 template <int D, int R>
 struct PartOf {
-    float o[R][D];
     float m[R], l[R];
+    float o[R][D];
     __device__ __forceinline__ const float4* quad(int r, int d) const { return reinterpret_cast<const float4*>(&o[r][d]); }
 };
 constexpr int JOIN = 8;   // partials in flight while joining

@@ -61,9 +61,10 @@ struct Ring {
     static constexpr int ST = (NT == 2 ? 3 : 2) * (128 / D);   // blocks in the ring of a warp: 192 KB a CTA
     static constexpr int TILE = BLK * D;                       // bytes of a block's keys or values
     static constexpr int QB = QS ? NT * D * 16 : 0;            // a warp's queries, in its lanes' order
-    static constexpr int Q = NW * ST * 2 * TILE;
-    static constexpr int BYTES = Q + NW * QB;
-    static_assert(ST * 2 * TILE + QB >= NT * 8 * D * 4 + 2 * ROWS * 4 && NW <= MAX_NW, "a partial fits a warp's memory");
+    static constexpr int WARP = ST * 2 * TILE + QB;
+    static constexpr int BYTES = NW * WARP;
+    static_assert(WARP >= NT * 8 * D * 4 + 2 * ROWS * 4 && NW <= MAX_NW, "a partial fits a warp's memory");
+    static_assert(WARP % 1024 == 0, "alignment of swizzled copies");
 };
 
 struct Seq {
@@ -105,6 +106,9 @@ __device__ __forceinline__ uint2 lds64(uint32_t p) {
     return v;
 }
 
+__device__ __forceinline__ void sts128(uint32_t p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -185,9 +189,9 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     uint8_t* ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    const uint32_t ring0 = smem_u32(ring) + warp * (R::ST * 2 * R::TILE);
+    const uint32_t ring0 = smem_u32(ring) + warp * R::WARP, qs0 = ring0 + R::ST * 2 * R::TILE + lane * 16;
     // a warp's partial of the segment that its share ends in goes to its ring, which is done by then
-    auto last_part = [&](int w) { return reinterpret_cast<Part<D>*>(ring + w * (R::ST * 2 * R::TILE)); };
+    auto last_part = [&](int w) { return reinterpret_cast<Part<D>*>(ring + w * R::WARP); };
     Space<D>* sp = static_cast<Space<D>*>(a.ws);
     if (lane == 0)
         for (int i = 0; i < R::ST; ++i) mbar_init(smem_u32(&bars[warp][i]), 3);   // the copies' bytes, two scales
@@ -308,9 +312,8 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
             const Seq s = cons.s;
             const int h = cons.h, from = cons.i;
             const int until = (int)min((int64_t)s.units, from + (u1 - u));
-            uint32_t q[NT][KS][2];
+            uint32_t q[R::QS ? 1 : NT][KS][2];
             float qf[NT][2];                      // score to log2 units, without the block's scale
-            int rlo[NT][2], rhi[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const int r = 8 * n + g;          // this lane holds row r of Q
@@ -344,16 +347,16 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
                 }
 #pragma unroll
                 for (int j = 0; j < KS; ++j) {
-                    q[n][j][0] = v[2 * j];
-                    q[n][j][1] = v[2 * j + 1];
+                    if (!R::QS) {
+                        q[R::QS ? 0 : n][j][0] = v[2 * j];
+                        q[R::QS ? 0 : n][j][1] = v[2 * j + 1];
+                    } else if (j % 2 == 0) {
+                        sts128(qs0 + (n * (KS / 2) + j / 2) * 512, v[2 * j], v[2 * j + 1], v[2 * j + 2], v[2 * j + 3]);
+                    }
                 }
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {     // and its scores and outputs are of rows 2 t, 2 t + 1
+                for (int k = 0; k < 2; ++k)       // and its scores and outputs are of rows 2 t, 2 t + 1
                     qf[n][k] = __shfl_sync(0xffffffffu, f, (2 * t + k) * 4);
-                    const int rr = 8 * n + 2 * t + k, i = rr / G;
-                    rhi[n][k] = rr < s.n * G ? row_hi(i, s.n, s.L, a.causal) : 0;
-                    rlo[n][k] = rr < s.n * G ? row_lo(i, s.n, s.L, a.window) : 0;
-                }
             }
             // blocks in [free_lo, free_hi) tokens need no mask
             const int free_hi = row_hi(0, s.n, s.L, a.causal), free_lo = row_lo(s.n - 1, s.n, s.L, a.window);
@@ -381,32 +384,41 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
 #pragma unroll
                     for (int mt = 0; mt < 2; ++mt) x[n][mt][0] = x[n][mt][1] = x[n][mt][2] = x[n][mt][3] = 0.f;
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt) {
-                    uint32_t w[2][KS];            // tokens 16 mt + g, + 8
+                for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int r = 16 * mt + 8 * e + g;
+                    for (int c = 0; c < D / 64; ++c) {
+                        uint4 w[2];               // tokens 16 mt + g, + 8: four k16 steps
 #pragma unroll
-                        for (int c = 0; c < D / 64; ++c) {
-                            const uint32_t at = D == 128 ? kt + r * 128 + (((2 * t + c) ^ (r & 7)) << 4)
-                                                         : kt + r * 64 + ((t ^ ((r >> 1) & 3)) << 4);
-                            const uint4 y = lds128(at);
-                            w[e][4 * c] = y.x ^ 0x80808080u;
-                            w[e][4 * c + 1] = y.y ^ 0x80808080u;
-                            w[e][4 * c + 2] = y.z ^ 0x80808080u;
-                            w[e][4 * c + 3] = y.w ^ 0x80808080u;
+                        for (int e = 0; e < 2; ++e) {
+                            const int r = 16 * mt + 8 * e + g;
+                            w[e] = lds128(D == 128 ? kt + r * 128 + (((2 * t + c) ^ (r & 7)) << 4) : kt + r * 64 + ((t ^ ((r >> 1) & 3)) << 4));
+                        }
+#pragma unroll
+                        for (int jj = 0; jj < 2; ++jj) {
+                            uint32_t ka[2][4];
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const uint32_t y0 = (jj ? (j ? w[0].w : w[0].z) : (j ? w[0].y : w[0].x)) ^ 0x80808080u;
+                                const uint32_t y1 = (jj ? (j ? w[1].w : w[1].z) : (j ? w[1].y : w[1].x)) ^ 0x80808080u;
+                                ka[j][0] = codes_f16(y0, 0x4140u);
+                                ka[j][1] = codes_f16(y1, 0x4140u);
+                                ka[j][2] = codes_f16(y0, 0x4342u);
+                                ka[j][3] = codes_f16(y1, 0x4342u);
+                            }
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                const int j0 = 4 * c + 2 * jj;
+                                uint4 y;
+                                if (R::QS) y = lds128(qs0 + (n * (KS / 2) + j0 / 2) * 512);
+                                else y = make_uint4(q[R::QS ? 0 : n][j0][0], q[R::QS ? 0 : n][j0][1], q[R::QS ? 0 : n][j0 + 1][0], q[R::QS ? 0 : n][j0 + 1][1]);
+                                mma_16816_f16(x[n][mt], ka[0], y.x, y.y);
+                                mma_16816_f16(x[n][mt], ka[1], y.z, y.w);
+                            }
                         }
                     }
-#pragma unroll
-                    for (int j = 0; j < KS; ++j) {
-                        const uint32_t ka[4] = {codes_f16(w[0][j], 0x4140u), codes_f16(w[1][j], 0x4140u),
-                                                codes_f16(w[0][j], 0x4342u), codes_f16(w[1][j], 0x4342u)};
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) mma_16816_f16(x[n][mt], ka, q[n][j][0], q[n][j][1]);
-                    }
-                }
                 // scores in log2 units; a value scale of NaN spoils them like a key scale of NaN
                 const float ks = bs.y == bs.y ? bs.x : bs.y;
+                const bool masked = tok0 < free_lo || tok0 + BLK > free_hi;
                 float mx[NT][2];
                 bool grows = false;
 #pragma unroll
@@ -415,13 +427,19 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
                     for (int k = 0; k < 2; ++k) {
                         const float f = qf[n][k] * ks;
                         float m = acc.m[n][k];
+                        int lo = 0, hi = 0;
+                        if (masked) {
+                            const int rr = 8 * n + 2 * t + k, row = rr / G;
+                            hi = rr < s.n * G ? row_hi(row, s.n, s.L, a.causal) : 0;
+                            lo = row_lo(row, s.n, s.L, a.window);
+                        }
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             float& y = x[n][e >> 1][2 * (e & 1) + k];
                             y *= f;
-                            if (tok0 < free_lo || tok0 + BLK > free_hi) {
+                            if (masked) {
                                 const int tok = tok0 + 8 * e + g;
-                                if (tok < rlo[n][k] || tok >= rhi[n][k]) y = -INFINITY;
+                                if (tok < lo || tok >= hi) y = -INFINITY;
                             }
                             m = fmaxf(m, y);
                         }
@@ -646,7 +664,8 @@ cudaError_t run_as(const AttnArgs& a, cudaStream_t s) {
 }
 template <int D>
 cudaError_t run_d(const AttnArgs& a, cudaStream_t s) {
-    return a.max_q * (a.Hq / a.c.Hkv) <= 8 ? run_as<D, 1>(a, s) : run_as<D, 2>(a, s);
+    const int tiles = (a.max_q * (a.Hq / a.c.Hkv) + 7) / 8;
+    return tiles == 1 ? run_as<D, 1>(a, s) : tiles == 2 ? run_as<D, 2>(a, s) : tiles == 3 ? run_as<D, 3>(a, s) : run_as<D, 4>(a, s);
 }
 
 }  // namespace
