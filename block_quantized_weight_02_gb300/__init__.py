@@ -284,6 +284,10 @@ class cq_kv8_cache:
         ldt = table.stride(0) if table.shape[0] > 1 else table.shape[1]
         self.desc = _kv8_desc(Kq.data_ptr(), Ks.data_ptr(), Vq.data_ptr(), Vs.data_ptr(), pages, Hkv, page, D,
                               table.data_ptr(), ldt, table.shape[0])
+        # read on every call: plain attributes cost less than the descriptor's fields
+        self.Hkv, self.D, self.B, self._ref = Hkv, D, table.shape[0], ctypes.byref(self.desc)
+        self._types = {torch.float16: CQ_F16, torch.bfloat16: CQ_BF16, torch.float32: CQ_F32}
+        self._int32, self._float32, self._cuda = torch.int32, torch.float32, torch._C
 
     @staticmethod
     def empty(pages, Hkv, page, D, table, device="cuda"):
@@ -293,31 +297,37 @@ class cq_kv8_cache:
         s = lambda: torch.zeros(pages, Hkv, page // 32, dtype=torch.float32, device=device)
         return cq_kv8_cache(q(), s(), q(), s(), table)
 
+    def _rows(self, t, what, heads):
+        """(T, row pitch) of a [T][heads][D] tensor whose rows are dense."""
+        sh, st = t.shape, t.stride()
+        if len(sh) != 3 or sh[1] != heads or sh[2] != self.D or st[2] != 1 or (heads > 1 and st[1] != self.D):
+            raise ValueError(f"{what} must be [T][{heads}][{self.D}] with dense rows, got shape {tuple(sh)}, strides {st}")
+        return sh[0], (st[0] if sh[0] > 1 else heads * self.D)
 
-def _kv8_rows(t, what, heads, D):
-    """Row pitch of a [T][heads][D] tensor whose rows are dense."""
-    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, D) or t.stride(2) != 1 or (heads > 1 and t.stride(1) != D):
-        raise ValueError(f"{what} must be [T][{heads}][{D}] with dense rows, got shape {tuple(t.shape)}, strides {t.stride()}")
-    return t.stride(0) if t.shape[0] > 1 else heads * D
+    def _index(self, t, what, n):
+        if t.dtype is not self._int32 or t.shape != (n,) or not t.is_contiguous():
+            raise ValueError(f"{what} must be a dense int32 tensor of {n} entries, got {t.dtype} {tuple(t.shape)}")
+        return t.data_ptr()
 
+    def _kv(self, K, V):
+        T, ldk = self._rows(K, "K", self.Hkv)
+        T2, ldv = self._rows(V, "V", self.Hkv)
+        if T != T2 or V.dtype != K.dtype:
+            raise ValueError("K and V must have one type and shape")
+        return K.data_ptr(), V.data_ptr(), self._types.get(K.dtype, -1), T, ldk, ldv
 
-def _kv8_index(t, what, n):
-    import torch
-    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{what} must be a dense int32 tensor of {n} entries, got {t.dtype} {tuple(t.shape)}")
-    return _ptr(t)
+    def _stream(self, stream):
+        """The given stream, else the current one of the current device (as a handle: a tenth of the time of a stream object)."""
+        return self._cuda._cuda_getCurrentRawStream(self._cuda._cuda_getDevice()) if stream is None else _stream(stream)
 
 
 def cq_kv8_write(cache, K, V, q_start, lens, stream=None, raise_on_error=True):
     """The rows of K, V ([T][Hkv][D], fp16/bf16/f32; rows q_start[b] .. q_start[b+1]
     - 1 of sequence b) become the last tokens of their sequences, which hold
     lens[b] tokens afterwards."""
-    c = cache.desc
-    ldk, ldv = _kv8_rows(K, "K", c.Hkv, c.D), _kv8_rows(V, "V", c.Hkv, c.D)
-    if V.dtype != K.dtype or V.shape != K.shape:
-        raise ValueError("K and V must have one type and shape")
-    st = lib().cq_kv8_write(ctypes.byref(c), _ptr(K), _ptr(V), _xt(K), K.shape[0], ldk, ldv,
-                            _kv8_index(q_start, "q_start", c.B + 1), _kv8_index(lens, "lens", c.B), _stream(stream))
+    k, v, xt, T, ldk, ldv = cache._kv(K, V)
+    st = lib().cq_kv8_write(cache._ref, k, v, xt, T, ldk, ldv, cache._index(q_start, "q_start", cache.B + 1),
+                            cache._index(lens, "lens", cache.B), cache._stream(stream))
     if raise_on_error:
         _check(st)
     return st
@@ -326,13 +336,9 @@ def cq_kv8_write(cache, K, V, q_start, lens, stream=None, raise_on_error=True):
 def cq_kv8_read(cache, first, out_start, K, V, stream=None, raise_on_error=True):
     """Rows out_start[b] .. out_start[b+1] - 1 of K, V ([T][Hkv][D], fp16/bf16/f32)
     become the values of tokens first[b] .. of sequence b (first None: from 0)."""
-    c = cache.desc
-    ldk, ldv = _kv8_rows(K, "K", c.Hkv, c.D), _kv8_rows(V, "V", c.Hkv, c.D)
-    if V.dtype != K.dtype or V.shape != K.shape:
-        raise ValueError("K and V must have one type and shape")
-    st = lib().cq_kv8_read(ctypes.byref(c), None if first is None else _kv8_index(first, "first", c.B),
-                           _kv8_index(out_start, "out_start", c.B + 1), _ptr(K), _ptr(V), _xt(K), K.shape[0], ldk, ldv,
-                           _stream(stream))
+    k, v, yt, T, ldk, ldv = cache._kv(K, V)
+    st = lib().cq_kv8_read(cache._ref, None if first is None else cache._index(first, "first", cache.B),
+                           cache._index(out_start, "out_start", cache.B + 1), k, v, yt, T, ldk, ldv, cache._stream(stream))
     if raise_on_error:
         _check(st)
     return st
@@ -347,18 +353,21 @@ def cq_attn_kv8(Q, cache, q_start, lens, max_q, O, ws, scale=None, causal=True, 
     """O[T][Hq][D] = softmax attention of Q [T][Hq][D] (fp16/bf16) over the cache;
     the rows of sequence b are the last of its lens[b] tokens.  scale None:
     1 / sqrt(D).  lse (f32 [T][Hq]) takes each row's log of the sum of exponentials."""
-    import torch
-    c = cache.desc
+    if Q.dim() != 3:
+        raise ValueError(f"Q must be [T][Hq][{cache.D}], got shape {tuple(Q.shape)}")
     Hq = Q.shape[1]
-    ldq, ldo = _kv8_rows(Q, "Q", Hq, c.D), _kv8_rows(O, "O", Hq, c.D)
-    if O.shape != Q.shape:
+    T, ldq = cache._rows(Q, "Q", Hq)
+    T2, ldo = cache._rows(O, "O", Hq)
+    if T != T2:
         raise ValueError("O must have the shape of Q")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != tuple(Q.shape[:2]) or not lse.is_contiguous()):
+    if lse is not None and (lse.dtype is not cache._float32 or lse.shape != (T, Hq) or not lse.is_contiguous()):
         raise ValueError("lse must be a dense f32 tensor [T][Hq]")
-    st = lib().cq_attn_kv8(_ptr(Q), _xt(Q), Q.shape[0], Hq, ldq, ctypes.byref(c), _kv8_index(q_start, "q_start", c.B + 1),
-                           _kv8_index(lens, "lens", c.B), max_q, c.D ** -0.5 if scale is None else scale,
-                           1 if causal else 0, window, _ptr(O), _xt(O), ldo, _ptr(lse), _ptr(ws),
-                           0 if ws is None else ws.numel() * ws.element_size(), _stream(stream))
+    st = lib().cq_attn_kv8(Q.data_ptr(), cache._types.get(Q.dtype, -1), T, Hq, ldq, cache._ref,
+                           cache._index(q_start, "q_start", cache.B + 1), cache._index(lens, "lens", cache.B), max_q,
+                           cache.D ** -0.5 if scale is None else scale, 1 if causal else 0, window, O.data_ptr(),
+                           cache._types.get(O.dtype, -1), ldo, None if lse is None else lse.data_ptr(),
+                           None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(),
+                           cache._stream(stream))
     if raise_on_error:
         _check(st)
     return st
