@@ -12,8 +12,9 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libcq.so")
 SOURCES = ["cq_api.cu", "k_aux.cu", "k_skinny.cu", "k_tc.cu", "k_tc_ffn.cu", "k_tc_q4a.cu", "k_tc_q8b.cu", "k_rows.cu", "cq_noalloc.cu",
-           "kv8/kv8_api.cu", "kv8/kv8_store.cu", "kv8/kv8_attn.cu", "kv8/kv8_decode.cu", "kv8/kv8_tiles.cu"]
-HEADERS = ["cq_internal.h", "cq_ptx.cuh", "k_tc.cuh", "kv8/kv8.cuh", "kv8/attn_common.cuh"]
+           "kv8/kv8_api.cu", "kv8/kv8_store.cu", "kv8/kv8_attn.cu", "kv8/kv8_decode.cu", "kv8/kv8_tiles.cu", "kv8/kv8_narrow.cu"]
+HEADERS = ["cq_internal.h", "cq_ptx.cuh", "k_tc.cuh", "kv8/kv8.cuh", "kv8/attn_common.cuh",
+           "kv8/tiles_common.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(HERE, "..", "include")]

@@ -40,6 +40,11 @@ __device__ __forceinline__ int guard_of(float amax) {
     return amax == 0.f || e == 128 ? 0 : min(max(13 - e, -114), 126);
 }
 
+__device__ __forceinline__ void store_out(void* p, int64_t i, int t, float v) {
+    if (t == CQ_F32) static_cast<float*>(p)[i] = v;
+    else if (t == CQ_F16) static_cast<__half*>(p)[i] = __float2half_rn(v);
+    else static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+}
 // Four neighbouring outputs (i a multiple of four).
 __device__ __forceinline__ void store_out4(void* p, int64_t i, int t, float a, float b, float c, float d) {
     if (t == CQ_F32) {

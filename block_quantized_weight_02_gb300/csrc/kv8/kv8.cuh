@@ -54,6 +54,9 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s);
 bool decode_serves(int64_t rows);                     // rows: query rows of a sequence that share a KV head
 size_t decode_workspace(int64_t D);
 cudaError_t launch_decode(const AttnArgs& a, cudaStream_t s);
+bool narrow_serves(int64_t rows);
+size_t narrow_workspace(int64_t T, int64_t G, int64_t D, int64_t B);
+cudaError_t launch_narrow(const AttnArgs& a, cudaStream_t s);
 size_t tiles_workspace(int64_t T, int64_t G, int64_t D, int64_t B, int64_t max_q);
 cudaError_t launch_tiles(const AttnArgs& a, cudaStream_t s);
 size_t attn_workspace(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q);

@@ -670,7 +670,7 @@ cudaError_t run_d(const AttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-bool decode_serves(int64_t rows) { return rows <= ROWS; }
+bool decode_serves(int64_t rows) { return rows <= 8; }
 size_t decode_workspace(int64_t D) { return D == 128 ? sizeof(Space<128>) : sizeof(Space<64>); }
 
 cudaError_t launch_decode(const AttnArgs& a, cudaStream_t s) { return a.D == 128 ? run_d<128>(a, s) : run_d<64>(a, s); }

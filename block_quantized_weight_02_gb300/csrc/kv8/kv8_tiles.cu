@@ -21,30 +21,16 @@
 // The work is the list of all (row tile, KV head, step), cut into one equal share per SM.  A
 // first small kernel lays the list out (only the device knows the lengths), a third joins the
 // row tiles that lie across shares, in share order.
-#include "attn_common.cuh"
+#include "tiles_common.cuh"
 
 namespace cq {
 namespace kv8 {
 namespace {
 
-constexpr int TM = 128;                // rows of a tensor-core tile
-constexpr int TN = 128;                // tokens of a step
-constexpr int NB = TN / BLK;           // blocks of a step
-constexpr int MAX_CTAS = 256;          // workspace bound
 constexpr int MMA_WARP = 0, LOAD_WARP = 1, MMA_WARP2 = 2, SOFT_WARP = 4, CONV_WARP = 12;
 constexpr int THREADS = 512;           // four warpgroups of 128 registers a thread at launch
 constexpr int REGS_SOFTMAX = 184, REGS_CONV = 72, REGS_ISSUE = 72;
 static_assert(2 * REGS_SOFTMAX + REGS_CONV + REGS_ISSUE <= 4 * 128, "what the launch has");
-constexpr int PLAN_THREADS = 1024;
-constexpr int ITEM_COST = 3;           // of beginning and ending an item, in steps
-constexpr float W_EXP = 10.f, GROW = 5.f;
-constexpr int HS = 4;                  // fp16 operand tiles in the ring (keys and values alternate)
-constexpr int SS = 8;                  // steps whose scales are kept
-constexpr int LB = 32 / NB;            // steps that the loading warp looks up at a time
-
-struct Maps {
-    CUtensorMap t[2];
-};
 
 // An unfinished result, channels in fours with the rows side by side, as the threads hold them.
 template <int D, int TILES>
@@ -53,106 +39,13 @@ struct Part {
     float m[TILES * TM], l[TILES * TM];
     __device__ __forceinline__ const float4* quad(int r, int d) const { return &o[d / 4][r]; }
 };
-struct alignas(16) Item {
-    int b, f0, tok0, steps;            // sequence, first row, first token, steps (none visible: 1)
-};
-struct Start {
-    int slot, h, step;                 // where a CTA's share begins
-};
-// Workspace: partials, the CTAs' segments and starts, the list.
+// Workspace: partials, then the list.
 template <int D, int TILES>
 struct Space {
     Part<D, TILES> cta[MAX_CTAS][2];
     Part<D, TILES> odd[TILES == 1 ? MAX_CTAS : 1];   // TILES 1: the odd steps' result
-    int seg[MAX_CTAS][2];              // (slot * Hkv + h) of cta[i][0] (began earlier) and cta[i][1] (began here, goes on)
-    Start start[MAX_CTAS + 1];
-    int ok, pad[3];                    // the list stands
-    Item item[1];                      // [slots]
+    List list;
 };
-
-int64_t slots_of(int64_t T, int64_t G, int64_t B, int rows) { return T * G / rows + B; }
-
-// ---- the list ------------------------------------------------------------------------------------------------------
-// Sequence b owns the slots floor(q_start[b] G / ROWS) + b .., since n tokens make at most floor(n G / ROWS) + 1 items.
-template <int D, int TILES>
-__global__ void __launch_bounds__(PLAN_THREADS) k_tiles_plan(const AttnArgs a, int slots, int ctas) {
-    pdl_launch_dependents();
-    pdl_wait();
-    constexpr int ROWS = TILES * TM;
-    __shared__ int64_t wsum[PLAN_THREADS / 32];
-    Space<D, TILES>* sp = static_cast<Space<D, TILES>*>(a.ws);
-    const int G = a.Hq / a.c.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    bool bad = false;
-    for (int b = threadIdx.x; b < a.c.B; b += PLAN_THREADS) {
-        const int L = __ldg(a.b.lens + b);
-        if (!rows_ok(__ldg(a.b.q_start + b), __ldg(a.b.q_start + b + 1), a.b.T, a.max_q) || L < 0 || L > a.c.ldt * a.c.page) bad = true;
-    }
-    for (int i = threadIdx.x; i < MAX_CTAS; i += PLAN_THREADS) sp->seg[i][0] = sp->seg[i][1] = -1;
-    if (__syncthreads_or(bad)) {
-        if (threadIdx.x == 0) {
-            set_err(a.b.err, DEV_INDEX);
-            sp->ok = 0;
-        }
-        return;
-    }
-    const int per = (slots + PLAN_THREADS - 1) / PLAN_THREADS;      // neighbouring slots of a thread
-    const int s0 = min(threadIdx.x * per, slots), s1 = min(s0 + per, slots);
-    auto key = [&](int b) { return (int64_t)__ldg(a.b.q_start + b) * G / ROWS + b; };
-    int64_t mine = 0;
-    int b = 0, n = a.c.B;
-    if (s0 < s1)
-        while (n > 1) {                                            // the largest b whose slots start at or before s0
-            const int half = n / 2;
-            if (key(b + half) <= s0) b += half, n -= half; else n = half;
-        }
-    for (int s = s0; s < s1; ++s) {
-        while (b + 1 < a.c.B && key(b + 1) <= s) ++b;
-        Item it = {b, 0, 0, 0};
-        const int q0 = __ldg(a.b.q_start + b), nq = __ldg(a.b.q_start + b + 1) - q0, L = __ldg(a.b.lens + b);
-        const int64_t f0 = (s - key(b)) * ROWS, rows = (int64_t)nq * G;
-        if (f0 >= 0 && f0 < rows) {
-            const int first = (int)(f0 / G), last = (int)((min(f0 + ROWS, rows) - 1) / G);
-            const int lo = row_lo(first, nq, L, a.window) / BLK * BLK, hi = row_hi(last, nq, L, a.causal);
-            it.f0 = (int)f0;
-            it.tok0 = lo;
-            it.steps = hi > lo ? (hi - lo + TN - 1) / TN : 1;
-        }
-        sp->item[s] = it;
-        if (it.steps) mine += (int64_t)(it.steps + ITEM_COST) * a.c.Hkv;
-    }
-    int64_t inc = mine;
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-    }
-    if (lane == 31) wsum[warp] = inc;
-    __syncthreads();
-    int64_t at = inc - mine, total = 0;
-    for (int i = 0; i < PLAN_THREADS / 32; ++i) {
-        if (i < warp) at += wsum[i];
-        total += wsum[i];
-    }
-    if (threadIdx.x == 0) {
-        sp->ok = 1;
-        sp->start[ctas] = {slots, 0, 0};
-    }
-    // the shares that begin in this thread's slots: share i at cost i q + min(i, rem)
-    const int64_t q = total / ctas, rem = total % ctas;
-    for (int s = s0; s < s1; ++s) {
-        const int cost = sp->item[s].steps + ITEM_COST;
-        if (cost == ITEM_COST) continue;
-        const int64_t end = at + (int64_t)cost * a.c.Hkv;
-        for (int64_t i = at / (q + 1); i < ctas; ++i) {
-            const int64_t u = i * q + min(i, rem);
-            if (u >= end) break;
-            if (u >= at) sp->start[i] = {s, (int)((u - at) / cost), max((int)((u - at) % cost) - ITEM_COST, 0)};
-        }
-        at = end;
-    }
-    // shares past the list (there are more CTAs than cost)
-    for (int64_t i = threadIdx.x; i < ctas; i += PLAN_THREADS)
-        if (i * q + min(i, rem) >= total) sp->start[i] = {slots, 0, 0};
-}
 
 // ---- shared memory -------------------------------------------------------------------------------------------------
 template <int D, int TILES>
@@ -167,44 +60,6 @@ struct Smem {
     static constexpr int END = SC + SS * NB * 8 + 16;
 };
 
-// MN-major operand (rows of 64 16-bit elements along N, one row per k; 128-byte swizzle): 8-row
-// groups 1024 bytes apart, the next 64 elements of N `lbo` bytes on.
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t lbo) {
-    return (smem_desc_sw128(saddr) & ~(0x3FFFull << 16)) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16);
-}
-
-// The parts of items that a CTA's share is made of, in order; every role walks the same list.
-struct Walk {
-    Start at, end;
-    Item it;
-    int from, until;      // steps of the current part
-    template <class S>
-    __device__ __forceinline__ bool next(const AttnArgs& a, const S* sp, bool first) {
-        if (!first) {
-            at.step = until;
-            if (until == it.steps) {
-                at.step = 0;
-                if (++at.h == a.c.Hkv) {
-                    at.h = 0;
-                    ++at.slot;
-                }
-            }
-        }
-        while (true) {
-            const bool last = at.slot == end.slot && at.h == end.h;
-            if (at.slot > end.slot || (at.slot == end.slot && at.h > end.h) || (last && at.step >= end.step)) return false;
-            const int4 v = __ldcg(reinterpret_cast<const int4*>(&sp->item[at.slot]));
-            if (v.w != 0) {
-                it = {v.x, v.y, v.z, v.w};
-                from = at.step;
-                until = last ? end.step : v.w;
-                return true;
-            }
-            ++at.slot;
-        }
-    }
-};
-
 // A block's factor from products to scores in log2 units (NaN if either scale is) and its value exponent.
 struct Scale {
     float k;
@@ -213,11 +68,6 @@ struct Scale {
 __device__ __forceinline__ Scale scale_of(float2 s, float qf) {
     const bool nan = s.y != s.y;
     return {qf * (nan ? s.y : s.x), nan ? -64 : exp_of(s.y)};
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
 }
 // Two floats in one register pair: one instruction for both.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
@@ -250,12 +100,6 @@ __device__ __forceinline__ void weights(float y0, float y1, uint64_t& sum, uint3
         p2 = pack_f16(y0 - h.x, y1 - h.y);
     }
 }
-// Registers of a warpgroup from here on (a multiple of 8; the groups' shares add up to the launch's).
-template <int N>
-__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
 template <int D, int PT, int TILES>
 __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Maps maps, const AttnArgs a, uint64_t wait_ns) {
     using M = Smem<D, TILES>;
@@ -308,16 +152,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
 
     Space<D, TILES>* sp = static_cast<Space<D, TILES>*>(a.ws);
     const int G = a.Hq / a.c.Hkv;
+    List* list = &sp->list;
     Walk w;
-    w.at = w.end = {0, 0, 0};
-    if (__ldcg(&sp->ok)) {
-        auto get = [&](int i) {
-            const Start* p = &sp->start[i];
-            return Start{__ldcg(&p->slot), __ldcg(&p->h), __ldcg(&p->step)};
-        };
-        w.at = get(blockIdx.x);
-        w.end = get(blockIdx.x + 1);
-    }
+    w.begin(list);
     // Every wait is bounded; the first to give up stops the CTA.
     bool alive = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
@@ -345,25 +182,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
         // ---- codes -> fp16: thread = token; keys and values of a step alternate
         const int tok = threadIdx.x & 127;
         uint32_t k = 0;                          // operand tiles so far
-        for (bool first = true; alive && w.next(a, sp, first); first = false) {
+        for (bool first = true; alive && w.next(a, list, first); first = false) {
             for (int j = 0; j < 2 * (w.until - w.from) && alive; ++j, ++k) {
                 const uint32_t rs = k % M::RS, hs = k % HS;
                 if (!wait_warp(raw_full + 8 * rs, k / M::RS & 1) || !wait_warp(h_empty + 8 * hs, (k / HS & 1) ^ 1)) break;
-                const uint8_t* src = smem + M::R + rs * M::RT + tok * D;
-                uint8_t* dst = smem + M::H + hs * M::HT + tok * 128;
-#pragma unroll
-                for (int c = 0; c < D / 16; ++c) {
-                    const int at = D == 128 ? (c ^ (tok & 7)) : (c ^ ((tok >> 1) & 3));
-                    const uint4 v = *reinterpret_cast<const uint4*>(src + at * 16);
-                    const uint32_t u[4] = {v.x ^ 0x80808080u, v.y ^ 0x80808080u, v.z ^ 0x80808080u, v.w ^ 0x80808080u};
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int ch = (2 * c + e) & 7;       // 16-byte chunk of the 64-channel row
-                        *reinterpret_cast<uint4*>(dst + (c >> 2) * (TN * 128) + ((ch ^ (tok & 7)) << 4)) =
-                            make_uint4(codes_f16(u[2 * e], 0x4140u), codes_f16(u[2 * e], 0x4342u),
-                                       codes_f16(u[2 * e + 1], 0x4140u), codes_f16(u[2 * e + 1], 0x4342u));
-                    }
-                }
+                convert_tile<D>(smem + M::R + rs * M::RT, smem + M::H + hs * M::HT, tok);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
@@ -416,7 +239,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
         };
         // The next part that this tile has steps of.
         auto advance = [&](bool first) {
-            while (w.next(a, sp, first)) {
+            while (w.next(a, list, first)) {
                 if (steps_of(w.it, w.until - w.from, x)) return true;
                 tile0 += w.until - w.from;
                 first = false;
@@ -702,7 +525,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                 __syncwarp();
                 if (lane == 0) mbar_arrive(odd_full);
             }
-            if (!whole && x == 0 && row == 0) sp->seg[blockIdx.x][begins ? 1 : 0] = cur.at.slot * a.c.Hkv + cur.at.h;
+            if (!whole && x == 0 && row == 0) list->seg[blockIdx.x][begins ? 1 : 0] = cur.at.slot * a.c.Hkv + cur.at.h;
         }
     } else {
         regs_down<REGS_ISSUE>();
@@ -741,7 +564,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                             tc_mma_f16_ts(tm_o(x), tm_s(x) + (s >> 1) * 32 + (s & 1) * 8 + z * 16, va + s * (2048 >> 4), id_pv,
                                           acc || s > 0 || z > 0);
                 };
-                for (bool first = true; alive && w.next(a, sp, first); first = false) {
+                for (bool first = true; alive && w.next(a, list, first); first = false) {
                     const int n = w.until - w.from, mine = steps_of(w.it, n, x);
                     if (mine == 0) {
                         if (TILES == 2)                           // not this tile's: the operands go back from here at once
@@ -779,48 +602,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
             }
             __syncwarp();
         } else if (warp == LOAD_WARP) {
-            // ---- loads: lane NB i + c has block c of step i of a batch of LB steps
-            uint32_t k = 0, tile = 0;
-            for (bool first = true; alive && w.next(a, sp, first); first = false) {
-                const int L = __ldg(a.b.lens + w.it.b);
-                int row1 = 0;
-                float2 s1;
-                auto look_up = [&](int j) {       // of the batch that begins at step j
-                    const int tok = w.it.tok0 + j * TN + lane * BLK;
-                    row1 = -1;
-                    s1 = make_float2(1.f, pow2i(-64));
-                    if (j + lane / NB < w.until && tok < L) {
-                        int pid = __ldg(a.c.table + w.it.b * a.c.ldt + tok / a.c.page);
-                        if (pid < 0 || pid >= a.c.pages) {       // read some page instead: the result is void
-                            set_err(a.b.err, DEV_INDEX);
-                            pid = 0;
-                        }
-                        row1 = (pid * a.c.Hkv + w.at.h) * a.c.page + tok % a.c.page;
-                        s1 = make_float2(__ldg(a.c.s[0] + row1 / BLK), __ldg(a.c.s[1] + row1 / BLK));
-                    }
-                };
-                look_up(w.from);
-                for (int j0 = w.from; j0 < w.until && alive; j0 += LB) {
-                    const int row = row1;
-                    const float2 s = s1;
-                    if (j0 + LB < w.until) look_up(j0 + LB);
-                    for (int i = 0; i < min(LB, w.until - j0) && alive; ++i, ++tile) {
-                        const bool me = lane / NB == i, have = me && row >= 0;
-                        const uint32_t blocks = __popc(__ballot_sync(0xffffffffu, have));
-                        for (int z = 0; z < 2 && alive; ++z, ++k) {
-                            const uint32_t rs = k % M::RS, bar = raw_full + 8 * rs;
-                            if (!wait_warp(raw_empty + 8 * rs, (k / M::RS & 1) ^ 1)) break;
-                            if (lane == 0) mbar_arrive_expect_tx(bar, blocks * BLK * D);
-                            __syncwarp();
-                            if (have) tma_load_2d(sb + M::R + rs * M::RT + lane % NB * BLK * D, &maps.t[z], bar, 0, row);
-                        }
-                        if (!alive) break;
-                        if (me) scales[tile % SS * NB + lane % NB] = s;
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(sc_full + 8 * (tile % SS));
-                    }
-                }
-            }
+            load_codes<D, M::RS>(a, list, w, maps, sb + M::R, raw_full, raw_empty, scales, sc_full, wait_warp, alive);
             if (!alive) {      // copies in flight land in memory that must still be this CTA's
                 for (int i = 0; i < M::RS; ++i)
                     for (uint32_t par = 0; par < 2; ++par) mbar_wait(raw_full + 8 * i, par, 10000000, never);
@@ -838,17 +620,10 @@ __global__ void __launch_bounds__(256) k_tiles_join(const AttnArgs a, int ctas) 
     pdl_launch_dependents();
     pdl_wait();
     const Space<D, TILES>* sp = static_cast<const Space<D, TILES>*>(a.ws);
-    const int i = blockIdx.x, lane = threadIdx.x & 31, seg = __ldcg(&sp->seg[i][1]);
-    int cnt = 1;
-    while (true) {
-        const int j = i + cnt + lane;
-        const bool more = j < ctas && __ldcg(&sp->seg[j][0]) == seg;
-        const int k = __ffs(~__ballot_sync(0xffffffffu, more));
-        cnt += k ? k - 1 : 32;
-        if (k) break;
-    }
+    const List* list = &sp->list;
+    const int i = blockIdx.x, seg = __ldcg(&list->seg[i][1]), cnt = shares_of(list, i, ctas, seg);
     if (seg < 0) return;
-    const int4 it = __ldcg(reinterpret_cast<const int4*>(&sp->item[seg / a.c.Hkv]));
+    const int4 it = __ldcg(reinterpret_cast<const int4*>(&list->item[seg / a.c.Hkv]));
     const int q0 = __ldg(a.b.q_start + it.x), n = __ldg(a.b.q_start + it.x + 1) - q0;
     const int rows = (int)min((int64_t)TILES * TM, (int64_t)n * (a.Hq / a.c.Hkv) - it.y);
     for (int k = threadIdx.x; k < 32 * (D / 4); k += 256) {
@@ -862,18 +637,13 @@ __global__ void __launch_bounds__(256) k_tiles_join(const AttnArgs a, int ctas) 
 template <int D, int PT, int TILES>
 cudaError_t run(const AttnArgs& a, cudaStream_t s) {
     Maps maps;
-    const uint64_t dims[2] = {(uint64_t)D, (uint64_t)a.c.pages * a.c.Hkv * a.c.page}, strides[1] = {(uint64_t)D};
-    const uint32_t box[2] = {(uint32_t)D, (uint32_t)BLK};
-    for (int i = 0; i < 2; ++i)
-        if (!encode_tiled(&maps.t[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, a.c.q[i], dims, strides, box,
-                          D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
-            return cudaErrorInvalidValue;
+    if (!make_maps(a, maps)) return cudaErrorInvalidValue;
     constexpr size_t smem = Smem<D, TILES>::END + 1024;
     static_assert(smem <= 232448, "shared memory");
     cudaError_t e = cudaFuncSetAttribute(k_tiles<D, PT, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int ctas = std::min(num_sms(), MAX_CTAS), G = a.Hq / a.c.Hkv, rows = TILES * TM;
-    e = launch_pdl(k_tiles_plan<D, TILES>, dim3(1), dim3(PLAN_THREADS), 0, s, a, (int)slots_of(a.b.T, G, a.c.B, rows), ctas);
+    e = launch_pdl(k_tiles_plan<TILES * TM>, dim3(1), dim3(PLAN_THREADS), 0, s, a, &static_cast<Space<D, TILES>*>(a.ws)->list, (int)slots_of(a.b.T, G, a.c.B, rows), ctas);
     if (e != cudaSuccess) return e;
     e = launch_pdl(k_tiles<D, PT, TILES>, dim3(ctas), dim3(THREADS), smem, s, maps, a, (uint64_t)options().wait_ns.load());
     if (e != cudaSuccess) return e;
