@@ -7,6 +7,19 @@ namespace kv8 {
 
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 
+// A wait for an mbarrier's phase that ends after limit_ns or once *stop is set (false then).  Short code: the kernels
+// have many waits, and their loops have to stay in the instruction cache.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, uint64_t limit_ns, const volatile int* stop) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 0; !mbar_try_wait(bar, parity); ++i) {
+        if (i & 63u) continue;
+        const uint64_t t = global_timer_ns();
+        if (i == 0) t0 = t;
+        if (*stop || t - t0 > limit_ns) return false;
+    }
+    return true;
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
             int ref = -64;                        // largest value-scale exponent so far
 
             for (int i = from; i < until && s.L > 0; ++i) {
-                if (!mbar_wait_spin(smem_u32(&bars[warp][stage]), parity, wait_ns, &stop)) {
+                if (!wait_bar(smem_u32(&bars[warp][stage]), parity, wait_ns, &stop)) {
                     alive = false;
                     break;
                 }
@@ -576,7 +576,7 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
             }
             const volatile int never = 0;
             for (int i = 0; i < R::ST; ++i) {
-                mbar_wait(smem_u32(&bars[warp][stage]), parity, wait_ns, &never);
+                wait_bar(smem_u32(&bars[warp][stage]), parity, wait_ns, &never);
                 stage = stage + 1 == R::ST ? 0 : stage + 1;
                 parity ^= stage == 0;
             }

@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
     // Every wait is bounded; the first to give up stops the CTA.
     bool alive = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (alive && !mbar_wait_spin(bar, parity, wait_ns, stop)) {
+        if (alive && !wait_bar(bar, parity, wait_ns, stop)) {
             alive = false;
             *stop = 1;
             set_err(a.b.err, DEV_TIMEOUT);
@@ -376,17 +376,17 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
             const bool whole = w.from == 0 && w.until == w.it.steps;
             const float un = pow2i(rows->ref - (int)W_EXP);
             Part<D>* part = &sp->cta[blockIdx.x][w.from == 0 ? 1 : 0];
-            uint32_t y[16];
-            tmem_ld_32x32b_x16(to + 16 * x, y);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int r = 16 * x + e, f = w.it.f0 + r;
-                if (r >= nrows) continue;
+            // (a loop: what runs once a part should not push the loops of every step out of the instruction cache)
+#pragma unroll 1
+            for (int r = 16 * x; r < min(16 * x + 16, nrows); ++r) {
+                const int f = w.it.f0 + r;
+                uint32_t y;
+                asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(y) : "r"(to + r));
+                tmem_ld_wait();
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) sum += rows->sum[i][r];
-                const float m = -rows->rc[r].y, o = __uint_as_float(y[e]) * un;
+                const float m = -rows->rc[r].y, o = __uint_as_float(y) * un;
                 if (whole) {
                     const int64_t row = q0 + f / G, head = w.at.h * G + f % G;
                     if (tid < D) store_out(a.O, row * a.ldo + head * D + tid, a.yt, o * inv_sum(sum));
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                 }
                 if (!alive) {  // let the products in flight end before the tensor memory goes: nothing else waits for this
                     tc_commit(q_ready);
-                    mbar_wait(q_ready, parts & 1, 10000000, never);
+                    wait_bar(q_ready, parts & 1, 10000000, never);
                 }
             }
             __syncwarp();
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
             load_codes<D, M::RS>(a, list, w, maps, sb + M::R, raw_full, raw_empty, scales, sc_full, wait_warp, alive);
             if (!alive) {      // copies in flight land in memory that must still be this CTA's
                 for (int i = 0; i < M::RS; ++i)
-                    for (uint32_t par = 0; par < 2; ++par) mbar_wait(raw_full + 8 * i, par, 10000000, never);
+                    for (uint32_t par = 0; par < 2; ++par) wait_bar(raw_full + 8 * i, par, 10000000, never);
             }
         }
     }

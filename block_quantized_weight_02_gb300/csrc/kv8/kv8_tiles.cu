@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
     // Every wait is bounded; the first to give up stops the CTA.
     bool alive = true;
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (alive && !mbar_wait_spin(bar, parity, wait_ns, stop)) {
+        if (alive && !wait_bar(bar, parity, wait_ns, stop)) {
             alive = false;
             *stop = 1;
             set_err(a.b.err, DEV_TIMEOUT);
@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                 }
                 if (!alive) {  // let the products in flight end before the tensor memory goes: nothing else waits for this
                     tc_commit(q_ready + 8 * x);
-                    mbar_wait(q_ready + 8 * x, parts & 1, 10000000, never);
+                    wait_bar(q_ready + 8 * x, parts & 1, 10000000, never);
                 }
             }
             __syncwarp();
@@ -605,7 +605,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
             load_codes<D, M::RS>(a, list, w, maps, sb + M::R, raw_full, raw_empty, scales, sc_full, wait_warp, alive);
             if (!alive) {      // copies in flight land in memory that must still be this CTA's
                 for (int i = 0; i < M::RS; ++i)
-                    for (uint32_t par = 0; par < 2; ++par) mbar_wait(raw_full + 8 * i, par, 10000000, never);
+                    for (uint32_t par = 0; par < 2; ++par) wait_bar(raw_full + 8 * i, par, 10000000, never);
             }
         }
     }
