@@ -57,9 +57,7 @@ struct Smem {
 };
 
 // Second operand with N = 32 contiguous (64-byte rows, one per k; 64-byte swizzle): 8-row groups 512 bytes apart.
-__device__ __forceinline__ uint64_t smem_desc_mn_sw64(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFF) >> 4) | (uint64_t)(512 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)4 << 61;
-}
+constexpr uint32_t DESC_SW64 = (512u >> 4) | (1u << 14) | (4u << 29);
 
 // Lane r gets the maximum (or sum) over the warp of v[r].
 template <bool MAX>
@@ -406,56 +404,63 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
     } else {
         regs_down<REGS_ISSUE>();
         if (warp == MMA_WARP) {
-            // ---- products, from one thread
-            if (lane == 0) {
-                // S^T: 128 tokens x 32 rows, both along the channels; O^T: 128 channels x 32 rows, both across the tokens
-                constexpr uint32_t id_qk = idesc_f16(TN, NR, 0), id_pv = idesc_f16(TM, NR, 0) | (1u << 15) | (1u << 16);
-                uint32_t k0 = 0, parts = 0, steps[2] = {0, 0};
-                auto h_wait = [&](uint32_t kt) { return wait(h_full + 8 * (kt % HS), kt / HS & 1); };
-                auto qk = [&](int x, uint32_t kt) {
-                    const uint64_t ka = smem_desc_sw128(sb + M::H + (kt % HS) * M::HT), qa = smem_desc_sw128(sb + M::Q);
-                    tc_fence_after();
+            // ---- products
+            // S^T: 128 tokens x 32 rows, both along the channels; O^T: 128 channels x 32 rows, both across the tokens
+            constexpr uint32_t id_qk = idesc_f16(TN, NR, 0), id_pv = idesc_f16(TM, NR, 0) | (1u << 15) | (1u << 16);
+            const uint32_t qa = uniform(desc_inner(sb + M::Q)), d_s = uniform(tmem), d_o = uniform(tm_o);
+            uint32_t k0 = 0, parts = 0, steps[2] = {0, 0};
+            auto h_wait = [&](uint32_t kt) { return wait_warp(h_full + 8 * (kt % HS), kt / HS & 1); };
+            auto qk = [&](int x, uint32_t kt) {
+                const uint32_t ka = uniform(desc_inner(sb + M::H + (kt % HS) * M::HT)), d = uniform(d_s + x * NR);
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
                     for (int s = 0; s < D / 16; ++s)
-                        tc_mma_f16(tmem + x * NR, ka + (((s >> 2) * (TN * 128) + (s & 3) * 32) >> 4),
-                                   qa + (((s >> 2) * (NR * 128) + (s & 3) * 32) >> 4), id_qk, s > 0);
+                        tc_mma_f16(d, desc_of(ka + (((s >> 2) * (TN * 128) + (s & 3) * 32) >> 4), DESC_SW128),
+                                   desc_of(qa + (((s >> 2) * (NR * 128) + (s & 3) * 32) >> 4), DESC_SW128), id_qk, s > 0);
                     tc_commit(s_full + 8 * x);
                     tc_commit(h_empty + 8 * (kt % HS));
-                };
-                for (bool first = true; alive && w.next(a, list, first); first = false) {
-                    const int n = w.until - w.from;
-                    if (!wait(q_ready, parts++ & 1)) break;
-                    for (int j = 0; j < min(n, 2); ++j) {
-                        if (!h_wait(k0 + 2 * j)) break;
-                        qk(j, k0 + 2 * j);
-                    }
-                    for (int j = 0; j < n && alive; ++j) {
-                        const int x = j & 1;
-                        const uint32_t vt = k0 + 2 * j + 1;
-                        if (!h_wait(vt) || !wait(p_ready + 8 * x, steps[x]++ & 1)) break;
-                        tc_fence_after();
-                        // (D 64: the tile's upper 64 channels are the lower ones again, and unused)
-                        const uint64_t va = smem_desc_mn_sw128(sb + M::H + (vt % HS) * M::HT, D == 128 ? TN * 128 : 0);
-                        const uint64_t pb = smem_desc_mn_sw64(sb + M::P + (M::PBUF == 1 ? 0 : x) * PT * M::PT_BYTES);
+                }
+                __syncwarp();
+            };
+            for (bool first = true; alive && w.next(a, list, first); first = false) {
+                const int n = w.until - w.from;
+                if (!wait_warp(q_ready, parts++ & 1)) break;
+                for (int j = 0; j < min(n, 2); ++j) {
+                    if (!h_wait(k0 + 2 * j)) break;
+                    qk(j, k0 + 2 * j);
+                }
+                for (int j = 0; j < n && alive; ++j) {
+                    const int x = j & 1;
+                    const uint32_t vt = k0 + 2 * j + 1;
+                    if (!h_wait(vt) || !wait_warp(p_ready + 8 * x, steps[x]++ & 1)) break;
+                    tc_fence_after();
+                    // (D 64: the tile's upper 64 channels are the lower ones again, and unused)
+                    const uint32_t va = uniform(desc_outer(sb + M::H + (vt % HS) * M::HT, D == 128 ? TN * 128 : 0));
+                    const uint32_t pb = uniform(desc_outer(sb + M::P + (M::PBUF == 1 ? 0 : x) * PT * M::PT_BYTES, 0));
+                    const uint32_t acc = j > 0;
+                    if (elect_one()) {
 #pragma unroll
                         for (int z = 0; z < PT; ++z)
 #pragma unroll
                             for (int s = 0; s < TN / 16; ++s)
-                                tc_mma_f16(tm_o, va + s * (2048 >> 4), pb + ((z * M::PT_BYTES + s * 1024) >> 4), id_pv, j > 0 || s > 0 || z > 0);
+                                tc_mma_f16(d_o, desc_of(va + s * (2048 >> 4), DESC_SW128),
+                                           desc_of(pb + ((z * M::PT_BYTES + s * 1024) >> 4), DESC_SW64), id_pv, s > 0 || z > 0 ? 1u : acc);
                         tc_commit(pv_done);
                         if (j + 1 == n) tc_commit(o_full);
                         tc_commit(h_empty + 8 * (vt % HS));
-                        if (j + 2 < n) {
-                            if (!h_wait(vt + 3)) break;
-                            qk(x, vt + 3);
-                        }
                     }
-                    k0 += 2 * n;
+                    __syncwarp();
+                    if (j + 2 < n) {
+                        if (!h_wait(vt + 3)) break;
+                        qk(x, vt + 3);
+                    }
                 }
-                if (!alive) {  // let the products in flight end before the tensor memory goes: nothing else waits for this
-                    tc_commit(q_ready);
-                    wait_bar(q_ready, parts & 1, 10000000, never);
-                }
+                k0 += 2 * n;
+            }
+            if (!alive) {      // let the products in flight end before the tensor memory goes: nothing else waits for this
+                if (elect_one()) tc_commit(q_ready);
+                wait_bar(q_ready, parts & 1, 10000000, never);
             }
             __syncwarp();
         } else if (warp == LOAD_WARP) {

@@ -530,75 +530,85 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
     } else {
         regs_down<REGS_ISSUE>();
         if (warp == MMA_WARP || warp == MMA_WARP2) {
-            // ---- products of tile x, from one thread
-            if (lane == 0) {
-                constexpr uint32_t id_qk = idesc_f16(TM, TN, 0), id_pv = idesc_f16(TM, D, 0) | (1u << 16);
-                const int x = warp == MMA_WARP2;
-                uint32_t k0 = 0, parts = 0, steps = 0, turns = 0; // k0: operand tiles before the part
-                // The first turn is tile 0's; the last of a part hands it back to tile 0.  (TILES 1 measured 5 % slower
-                // with turns: its loads set the pace.)
-                auto take = [&](bool both) { return !both || wait(turn + 8 * x, (turns++ + (x == 0)) & 1); };
-                auto pass = [&](bool both, bool last) {
-                    if (both) mbar_arrive(turn + 8 * (last ? 0 : 1 - x));
-                };
-                auto h_wait = [&](uint32_t kt) { return wait(h_full + 8 * (kt % HS), kt / HS & 1); };
-                auto qk = [&](uint32_t kt, bool both) {
-                    const uint64_t qa = smem_desc_sw128(sb + M::Q + (TILES == 1 ? 0 : x) * M::QT);
-                    const uint64_t ka = smem_desc_sw128(sb + M::H + (kt % HS) * M::HT);
-                    tc_fence_after();
+            // ---- products of tile x
+            constexpr uint32_t id_qk = idesc_f16(TM, TN, 0), id_pv = idesc_f16(TM, D, 0) | (1u << 16);
+            const int x = warp == MMA_WARP2;
+            const uint32_t d_s = uniform(tm_s(x)), d_o = uniform(tm_o(x));
+            const uint32_t qa = uniform(desc_inner(sb + M::Q + (TILES == 1 ? 0 : x) * M::QT));
+            uint32_t k0 = 0, parts = 0, steps = 0, turns = 0;     // k0: operand tiles before the part
+            // The first turn is tile 0's; the last of a part hands it back to tile 0.  (TILES 1 measured 5 % slower
+            // with turns: its loads set the pace.)
+            auto take = [&](bool both) { return !both || wait_warp(turn + 8 * x, (turns++ + (x == 0)) & 1); };
+            auto pass = [&](bool both, bool last) {
+                if (both) mbar_arrive(turn + 8 * (last ? 0 : 1 - x));
+            };
+            auto h_wait = [&](uint32_t kt) { return wait_warp(h_full + 8 * (kt % HS), kt / HS & 1); };
+            auto release = [&](uint32_t kt) { tc_commit(h_empty + 8 * (kt % HS)); };
+            auto qk = [&](uint32_t kt, bool both) {
+                const uint32_t ka = uniform(desc_inner(sb + M::H + (kt % HS) * M::HT));
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
                     for (int s = 0; s < D / 16; ++s) {
                         const uint32_t off = ((s >> 2) * (TM * 128) + (s & 3) * 32) >> 4;
-                        tc_mma_f16(tm_s(x), qa + off, ka + off, id_qk, s > 0);
+                        tc_mma_f16(d_s, desc_of(qa + off, DESC_SW128), desc_of(ka + off, DESC_SW128), id_qk, s > 0);
                         if (s == D / 32 - 1) pass(both, false);   // the turn takes 300 cycles to reach the other thread
                     }
                     tc_commit(s_full + 8 * x);
-                };
-                auto pv = [&](uint32_t vt, bool acc) {
-                    const uint64_t va = smem_desc_mn_sw128(sb + M::H + (vt % HS) * M::HT, TN * 128);
-                    tc_fence_after();
+                }
+                __syncwarp();
+            };
+            auto pv = [&](uint32_t vt, uint32_t acc) {
+                const uint32_t va = uniform(desc_outer(sb + M::H + (vt % HS) * M::HT, TN * 128));
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
                     for (int z = 0; z < PT; ++z)
 #pragma unroll
                         for (int s = 0; s < TN / 16; ++s)
-                            tc_mma_f16_ts(tm_o(x), tm_s(x) + (s >> 1) * 32 + (s & 1) * 8 + z * 16, va + s * (2048 >> 4), id_pv,
-                                          acc || s > 0 || z > 0);
-                };
-                for (bool first = true; alive && w.next(a, list, first); first = false) {
-                    const int n = w.until - w.from, mine = steps_of(w.it, n, x);
-                    if (mine == 0) {
-                        if (TILES == 2)                           // not this tile's: the operands go back from here at once
-                            for (int j = 0; j < 2 * n && h_wait(k0 + j); ++j) mbar_arrive(h_empty + 8 * ((k0 + j) % HS));
-                    } else {
-                        const bool both = TILES == 2 && steps_of(w.it, n, 1) > 0;
-                        uint32_t kt = k0 + (TILES == 1 ? 2 * x : 0);      // the step's keys; its values are kt + 1
-                        if (!wait(q_ready + 8 * x, parts++ & 1) || !h_wait(kt) || !take(both)) break;
-                        qk(kt, both);
-                        tc_commit(h_empty + 8 * (kt % HS));
-                        for (int j = 0; j < mine; ++j, kt += 2 * EACH) {
-                            // what is mostly there already is waited for first: each such wait takes 100 cycles, which
-                            // would come between the weights and their product
-                            const uint32_t next = kt + 2 * EACH;
-                            if (!h_wait(kt + 1) || (j + 1 < mine && !h_wait(next)) || !take(both)) break;
-                            if (!wait(p_ready + 8 * x, steps++ & 1)) break;
-                            pv(kt + 1, j > 0);
-                            if (j + 1 < mine) {
-                                qk(next, both);
-                                tc_commit(h_empty + 8 * ((kt + 1) % HS));
-                                tc_commit(h_empty + 8 * (next % HS));
-                            } else {
-                                tc_commit(o_full + 8 * x);
-                                pass(both, x == 1);
-                                tc_commit(h_empty + 8 * ((kt + 1) % HS));
+                            tc_mma_f16_ts(d_o, d_s + (s >> 1) * 32 + (s & 1) * 8 + z * 16, desc_of(va + s * (2048 >> 4), DESC_SW128),
+                                          id_pv, s > 0 || z > 0 ? 1u : acc);
+                }
+                __syncwarp();
+            };
+            for (bool first = true; alive && w.next(a, list, first); first = false) {
+                const int n = w.until - w.from, mine = steps_of(w.it, n, x);
+                if (mine == 0) {
+                    if (TILES == 2)                               // not this tile's: the operands go back from here at once
+                        for (int j = 0; j < 2 * n && h_wait(k0 + j); ++j)
+                            if (lane == 0) mbar_arrive(h_empty + 8 * ((k0 + j) % HS));
+                } else {
+                    const bool both = TILES == 2 && steps_of(w.it, n, 1) > 0;
+                    uint32_t kt = k0 + (TILES == 1 ? 2 * x : 0);  // the step's keys; its values are kt + 1
+                    if (!wait_warp(q_ready + 8 * x, parts++ & 1) || !h_wait(kt) || !take(both)) break;
+                    qk(kt, both);
+                    if (elect_one()) release(kt);
+                    for (int j = 0; j < mine; ++j, kt += 2 * EACH) {
+                        // what is mostly there already is waited for first: each such wait takes 100 cycles, which
+                        // would come between the weights and their product
+                        const uint32_t next = kt + 2 * EACH;
+                        if (!h_wait(kt + 1) || (j + 1 < mine && !h_wait(next)) || !take(both)) break;
+                        if (!wait_warp(p_ready + 8 * x, steps++ & 1)) break;
+                        pv(kt + 1, j > 0);
+                        if (j + 1 < mine) {
+                            qk(next, both);
+                            if (elect_one()) {
+                                release(kt + 1);
+                                release(next);
                             }
+                        } else if (elect_one()) {
+                            tc_commit(o_full + 8 * x);
+                            pass(both, x == 1);
+                            release(kt + 1);
                         }
+                        __syncwarp();
                     }
-                    k0 += 2 * n;
                 }
-                if (!alive) {  // let the products in flight end before the tensor memory goes: nothing else waits for this
-                    tc_commit(q_ready + 8 * x);
-                    wait_bar(q_ready + 8 * x, parts & 1, 10000000, never);
-                }
+                k0 += 2 * n;
+            }
+            if (!alive) {      // let the products in flight end before the tensor memory goes: nothing else waits for this
+                if (elect_one()) tc_commit(q_ready + 8 * x);
+                wait_bar(q_ready + 8 * x, parts & 1, 10000000, never);
             }
             __syncwarp();
         } else if (warp == LOAD_WARP) {

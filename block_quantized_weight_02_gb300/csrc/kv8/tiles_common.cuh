@@ -128,11 +128,23 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tiles_plan(const AttnArgs a, L
         if (i * q + min(i, rem) >= total) sp->start[i] = {slots, 0, 0};
 }
 
-// MN-major operand (rows of 64 16-bit elements along N, one row per k; 128-byte swizzle): 8-row
-// groups 1024 bytes apart, the next 64 elements of N `lbo` bytes on.
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t lbo) {
-    return (smem_desc_sw128(saddr) & ~(0x3FFFull << 16)) | ((uint64_t)((lbo >> 4) & 0x3FFF) << 16);
+// ---- issuing products.  A whole warp runs the issuing loops and one elected lane the instructions, on values the
+// compiler can keep in uniform registers: with one lane in a branch of its own each product took 44 instructions and
+// about 100 cycles.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
 }
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// Operand descriptors as (low, high) words; the low word moves by (bytes >> 4).
+// Rows of 128 bytes, 128-byte swizzle, 8-row groups 1024 bytes apart.  Inner operands (rows = M or N) lie along k; outer
+// ones (rows = k) have the next 64 elements of M or N `next` bytes on.
+constexpr uint32_t DESC_SW128 = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_inner(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_outer(uint32_t saddr, uint32_t next) { return ((saddr & 0x3FFFFu) >> 4) | ((next >> 4) << 16); }
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo, uint32_t hi) { return (uint64_t)hi << 32 | lo; }
 
 // The parts of items that a CTA's share is made of, in order; every role walks the same list.
 struct Walk {
