@@ -294,6 +294,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
             int ref = -64;
             for (int j = 0; j < mine; ++j, ++steps) {
                 const uint32_t tile = tile0 + j * EACH + (TILES == 1 ? x : 0);
+                // A part's first scores are waited for before its first scales: a tile that takes no part in some items
+                // does not see every phase of the scales' barriers, and these scores come after all phases but the last.
+                if (j == 0 && !wait_warp(s_full + 8 * x, steps & 1)) break;
                 if (!wait_warp(sc_full + 8 * (tile % SS), tile / SS & 1)) break;
                 const int t0 = w.it.tok0 + (w.from + (int)(tile - tile0)) * TN;
                 const float2* sc = scales + tile % SS * NB;
@@ -307,7 +310,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                 }
                 const bool prep = __any_sync(0xffffffffu, t0 < free_lo || t0 + TN > free_hi || odd_k != 0);
                 bool again = PT == 2 || nref != ref || __any_sync(0xffffffffu, !(fabsf(m) <= 1048576.f));
-                if (!wait_warp(s_full + 8 * x, steps & 1)) break;
+                if (j > 0 && !wait_warp(s_full + 8 * x, steps & 1)) break;
                 if (u0.wl < u0.wf) {         // no rows: whatever lies there as weights only meets its own rows
                     if (lane == 0) mbar_arrive(p_ready + 8 * x);
                     continue;
@@ -457,10 +460,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                 w1 *= inv;
             }
             // Outputs go through the query tile (its products are done), so that neighbouring lanes store
-            // neighbouring chunks of a row: 16-bit rows whole, f32 rows half at a time.
+            // neighbouring chunks of a row: 16-bit rows whole, f32 rows half at a time.  They lie as the queries do, so
+            // that a warp stays inside its own rows: another may have its next queries there already.
             constexpr int RB = 2 * D, LPR = RB / 16, RPI = 32 / LPR;  // staged bytes and chunks of a row, rows a store
             uint8_t* stage = smem + M::Q + (TILES == 1 ? 0 : x) * M::QT;
-            auto chunk = [&](int rr, int c) { return reinterpret_cast<uint4*>(stage + rr * RB + ((c ^ (rr & 7)) << 4)); };
+            auto chunk = [&](int rr, int c) { return reinterpret_cast<uint4*>(stage + (c >> 3) * (TM * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)); };
             const int es = a.yt == CQ_F32 ? 4 : 2;
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {

@@ -390,6 +390,66 @@ def test_many_sequences():
     s.check_attend([1] * 300, 2)
 
 
+def exact(s, q, counts, causal, window):
+    """kv8ref.attend for a batch, in 64 bits on the device, from the cache as cq_kv8_read gives it (exact in f32)."""
+    kc, vc = (x.double() for x in s.read("f32"))
+    cols = [[], [], [], [], []]
+    at = tok = 0
+    for n, L in zip(counts, s.len):
+        k, v = kc[tok:tok + L].transpose(0, 1), vc[tok:tok + L].transpose(0, 1)            # [Hkv][L][D]
+        x = q[at:at + n].double().view(n, s.Hkv, -1, s.D).permute(1, 2, 0, 3).flatten(1, 2)  # [Hkv][group n][D]
+        p = torch.arange(L - n, L, device=DEV).repeat(x.shape[1] // max(n, 1))[:, None]
+        j = torch.arange(L, device=DEV)[None]
+        see = (j <= p) & (j > p - (window or L + 1)) if causal else torch.ones_like(j <= p)
+        z = (x @ k.transpose(1, 2) * s.D ** -0.5).masked_fill(~see, float("-inf"))
+        lse = torch.logsumexp(z, 2)
+        w = torch.exp(z - lse[..., None])
+        reach = ((x.abs() @ k.abs().transpose(1, 2)) * s.D ** -0.5).masked_fill(~see, 0).amax(2)
+        top = torch.where(see, v.abs().amax(2)[:, None], 0.0).amax(2)
+        for c, t in zip(cols, (w @ v, lse[..., None], w @ v.abs(), top[..., None], reach[..., None])):
+            c.append(t.view(s.Hkv, -1, n, t.shape[2]).permute(2, 0, 1, 3).flatten(1, 2).cpu().numpy())
+        at, tok = at + n, tok + L
+    o, lse, mass, top, reach = (np.concatenate(c) for c in cols)
+    return o, lse[..., 0], mass, top[..., 0], reach[..., 0]
+
+
+@pytest.mark.parametrize("Hkv,group,B,rows,held", [
+    (16, 1, 1, [1], [3, 200, 40, 900]),               # single tokens
+    (16, 4, 48, [1, 2, 4], [1, 300, 70, 900]),        # up to 16 rows of a head
+    (16, 5, 48, [5, 1, 4, 5], [1, 300, 70, 900]),     # up to 25
+    (16, 8, 48, [4, 3], [1, 300, 70, 900]),           # 32
+    (16, 11, 32, [3, 1], [5, 700, 100]),              # 33
+    (16, 2, 48, [64, 1, 33], [0, 300, 70, 900]),      # 128
+    (16, 1, 32, [256, 100, 30, 600], [1500, 2000, 1100]),   # items whose second half has rows and ones where it has none
+    (8, 3, 24, [43, 200, 86, 1], [1300, 10, 700]),
+])
+@pytest.mark.parametrize("D,out", [(128, "bf16"), (128, "f32"), (64, "f32")])
+def test_several_items_a_block(Hkv, group, B, rows, held, D, out):
+    """More items than the GPU has room for at once, each unlike the one before it: rows, lengths, and values whose size
+    differs by 2^16 from sequence to sequence."""
+    counts = [rows[b % len(rows)] for b in range(B)]
+    lens = [held[b % len(held)] + counts[b] for b in range(B)]
+    s = Setup(38, lens, Hkv, D, 64)
+    v = s.rows(sum(lens), Hkv, "f32", 0.5)
+    at = 0
+    for b, n in enumerate(lens):
+        v[at:at + n] *= 2.0 ** (16 * (b % 2))
+        at += n
+    s.len = lens
+    cq.cq_kv8_write(s.cache, s.rows(sum(lens), Hkv, "f32", 0.5), v, starts(lens), i32(lens))
+    q = s.rows(sum(counts), Hkv * group, "bf16", 0.3)
+    for causal, window in ((True, 0), (True, 150), (False, 0)):
+        ro, rz, mass, top, reach = exact(s, q, counts, causal, window)
+        lim = kv8ref.bound(ro, mass, top, reach, out)
+        first = None
+        for _ in range(3):
+            _, o, z = s.attend(counts, group, "bf16", out, causal, window, q=q)
+            assert first is None or torch.equal(o, first)
+            first = o
+        assert np.all(np.abs(f64(o) - ro) <= lim)
+        assert np.all(np.abs(f64(z) - rz) <= kv8ref.lse_bound(rz, reach))
+
+
 def test_max_q_larger_than_the_batch():
     """max_q only has to bound the rows: the result stays within the same bounds."""
     s = Setup(35, [100, 50], 2, 64, 32)
