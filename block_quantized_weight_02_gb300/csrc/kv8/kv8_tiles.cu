@@ -29,7 +29,7 @@ namespace {
 
 constexpr int MMA_WARP = 0, LOAD_WARP = 1, MMA_WARP2 = 2, SOFT_WARP = 4, CONV_WARP = 12;
 constexpr int THREADS = 512;           // four warpgroups of 128 registers a thread at launch
-constexpr int REGS_SOFTMAX = 184, REGS_CONV = 72, REGS_ISSUE = 72;
+constexpr int REGS_SOFTMAX = 200, REGS_CONV = 56, REGS_ISSUE = 56;
 static_assert(2 * REGS_SOFTMAX + REGS_CONV + REGS_ISSUE <= 4 * 128, "what the launch has");
 
 // An unfinished result, channels in fours with the rows side by side, as the threads hold them.

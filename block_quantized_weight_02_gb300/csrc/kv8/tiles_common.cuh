@@ -12,7 +12,7 @@ constexpr int TN = 128;                // tokens of a step
 constexpr int NB = TN / BLK;           // blocks of a step
 constexpr int MAX_CTAS = 256;          // workspace bound
 constexpr int PLAN_THREADS = 1024;
-constexpr int ITEM_COST = 3;           // of beginning and ending an item, in steps
+constexpr int ITEM_COST = 7;           // of beginning and ending an item, in steps
 constexpr int SS = 8;                  // steps whose scales are kept
 constexpr int LB = 32 / NB;            // steps that the loading warp looks up at a time
 constexpr int HS = 4;                  // fp16 operand tiles in the ring (keys and values alternate)
