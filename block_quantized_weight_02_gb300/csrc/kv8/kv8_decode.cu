@@ -1,5 +1,5 @@
 // Attention over the 8-bit cache for few query rows per sequence (single tokens,
-// short guesses): at most 32 rows of one KV head, a row being a (token, head of the
+// short guesses): at most 16 rows of one KV head, a row being a (token, head of the
 // group) pair.
 //
 // Bound by HBM: the cache is read once.  The work is the list of all visible blocks
@@ -33,7 +33,7 @@ namespace cq {
 namespace kv8 {
 namespace {
 
-constexpr int ROWS = 32;
+constexpr int ROWS = 16;
 constexpr int MAX_CTAS = 256;         // workspace bound
 constexpr int MAX_NW = 12;
 constexpr int P_EXP = 15;             // weights carry 2^15
@@ -52,16 +52,13 @@ struct Space {
     int seg[MAX_CTAS][2];             // segment of cta[i][0] (began earlier) and cta[i][1] (began here, goes on), or -1
 };
 
-// NT: n8 tiles of rows.  One tile fits 12 warps with two blocks each (registers), more tiles 8 warps with three, or
-// two beside the queries, which three tiles and more keep in shared memory.
+// NT: n8 tiles of rows.  One tile's registers allow 12 warps, with two blocks each; two allow 8, with three.
 template <int D, int NT>
 struct Ring {
     static constexpr int NW = NT == 1 ? 12 : 8;
-    static constexpr bool QS = NT > 2;
     static constexpr int ST = (NT == 2 ? 3 : 2) * (128 / D);   // blocks in the ring of a warp: 192 KB a CTA
     static constexpr int TILE = BLK * D;                       // bytes of a block's keys or values
-    static constexpr int QB = QS ? NT * D * 16 : 0;            // a warp's queries, in its lanes' order
-    static constexpr int WARP = ST * 2 * TILE + QB;
+    static constexpr int WARP = ST * 2 * TILE;
     static constexpr int BYTES = NW * WARP;
     static_assert(WARP >= NT * 8 * D * 4 + 2 * ROWS * 4 && NW <= MAX_NW, "a partial fits a warp's memory");
     static_assert(WARP % 1024 == 0, "alignment of swizzled copies");
@@ -106,9 +103,6 @@ __device__ __forceinline__ uint2 lds64(uint32_t p) {
     return v;
 }
 
-__device__ __forceinline__ void sts128(uint32_t p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
-}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t y;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -189,7 +183,7 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     uint8_t* ring = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    const uint32_t ring0 = smem_u32(ring) + warp * R::WARP, qs0 = ring0 + R::ST * 2 * R::TILE + lane * 16;
+    const uint32_t ring0 = smem_u32(ring) + warp * R::WARP;
     // a warp's partial of the segment that its share ends in goes to its ring, which is done by then
     auto last_part = [&](int w) { return reinterpret_cast<Part<D>*>(ring + w * R::WARP); };
     Space<D>* sp = static_cast<Space<D>*>(a.ws);
@@ -312,7 +306,7 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
             const Seq s = cons.s;
             const int h = cons.h, from = cons.i;
             const int until = (int)min((int64_t)s.units, from + (u1 - u));
-            uint32_t q[R::QS ? 1 : NT][KS][2];
+            uint32_t q[NT][KS][2];
             float qf[NT][2];                      // score to log2 units, without the block's scale
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -347,12 +341,8 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
                 }
 #pragma unroll
                 for (int j = 0; j < KS; ++j) {
-                    if (!R::QS) {
-                        q[R::QS ? 0 : n][j][0] = v[2 * j];
-                        q[R::QS ? 0 : n][j][1] = v[2 * j + 1];
-                    } else if (j % 2 == 0) {
-                        sts128(qs0 + (n * (KS / 2) + j / 2) * 512, v[2 * j], v[2 * j + 1], v[2 * j + 2], v[2 * j + 3]);
-                    }
+                    q[n][j][0] = v[2 * j];
+                    q[n][j][1] = v[2 * j + 1];
                 }
 #pragma unroll
                 for (int k = 0; k < 2; ++k)       // and its scores and outputs are of rows 2 t, 2 t + 1
@@ -408,11 +398,8 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
                                 const int j0 = 4 * c + 2 * jj;
-                                uint4 y;
-                                if (R::QS) y = lds128(qs0 + (n * (KS / 2) + j0 / 2) * 512);
-                                else y = make_uint4(q[R::QS ? 0 : n][j0][0], q[R::QS ? 0 : n][j0][1], q[R::QS ? 0 : n][j0 + 1][0], q[R::QS ? 0 : n][j0 + 1][1]);
-                                mma_16816_f16(x[n][mt], ka[0], y.x, y.y);
-                                mma_16816_f16(x[n][mt], ka[1], y.z, y.w);
+                                mma_16816_f16(x[n][mt], ka[0], q[n][j0][0], q[n][j0][1]);
+                                mma_16816_f16(x[n][mt], ka[1], q[n][j0 + 1][0], q[n][j0 + 1][1]);
                             }
                         }
                     }
@@ -664,13 +651,12 @@ cudaError_t run_as(const AttnArgs& a, cudaStream_t s) {
 }
 template <int D>
 cudaError_t run_d(const AttnArgs& a, cudaStream_t s) {
-    const int tiles = (a.max_q * (a.Hq / a.c.Hkv) + 7) / 8;
-    return tiles == 1 ? run_as<D, 1>(a, s) : tiles == 2 ? run_as<D, 2>(a, s) : tiles == 3 ? run_as<D, 3>(a, s) : run_as<D, 4>(a, s);
+    return a.max_q * (a.Hq / a.c.Hkv) <= 8 ? run_as<D, 1>(a, s) : run_as<D, 2>(a, s);
 }
 
 }  // namespace
 
-bool decode_serves(int64_t rows) { return rows <= 8; }
+bool decode_serves(int64_t rows) { return rows <= ROWS; }
 size_t decode_workspace(int64_t D) { return D == 128 ? sizeof(Space<128>) : sizeof(Space<64>); }
 
 cudaError_t launch_decode(const AttnArgs& a, cudaStream_t s) { return a.D == 128 ? run_d<128>(a, s) : run_d<64>(a, s); }

@@ -1,4 +1,4 @@
-// Attention over the 8-bit cache for 9 to 32 query rows of a KV head (wide groups, short
+// Attention over the 8-bit cache for 17 to 32 query rows of a KV head (wide groups, short
 // guesses), on the 5th-generation tensor cores with the rows as the narrow side.
 //
 // Bound by HBM.  Per 128 tokens (a step) S^T = K Q^T (128 tokens x 32 rows) and O^T += V^T P^T
