@@ -82,67 +82,79 @@ struct PartOf {
     float o[R][D];
     __device__ __forceinline__ const float4* quad(int r, int d) const { return reinterpret_cast<const float4*>(&o[r][d]); }
 };
-constexpr int JOIN = 8;   // partials in flight while joining
-
 __device__ __forceinline__ float inv_sum(float l) { return l == 0.f ? 0.f : 1.0f / l; }
 __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
 }
 
-// Joins the partials part(0) .. part(cnt - 1) of KV head h's row f (a (token, head) pair of the sequence whose
-// first tensor row is q0), row r of the partials, channels d .. d + 3: into `out` (nullable), else the output.  JOIN partials are read at a time; FAR ones come from other CTAs.
+// Joins the partials part(0) .. part(cnt - 1) of KV head h's row f (a (token, head) pair of the sequence whose first
+// tensor row is q0), row r of the partials, NQ x 4 channels from d on: into `out` (nullable), else the output.  AT
+// partials are read at a time; FAR ones come from other CTAs.
 template <bool FAR, class T>
 __device__ __forceinline__ T part_ld(const T* p) { return FAR ? __ldcg(p) : *p; }
-template <bool FAR, int D, class P, class F>
+template <bool FAR, int D, int NQ, int AT, class P, class F>
 __device__ __forceinline__ void join(const AttnArgs& a, int q0, int h, int f, int r, int d, int cnt, F part, P* out) {
     float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int j0 = 0; j0 < cnt; j0 += JOIN) {
-        float pm[JOIN], pl[JOIN];
-        float4 v[JOIN];
+    float4 o[NQ];
 #pragma unroll
-        for (int j = 0; j < JOIN; ++j) {
+    for (int q = 0; q < NQ; ++q) o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = 0; j0 < cnt; j0 += AT) {
+        float pm[AT], pl[AT];
+        float4 v[AT][NQ];
+#pragma unroll
+        for (int j = 0; j < AT; ++j) {
             pm[j] = -INFINITY;
             pl[j] = 0.f;
-            v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) v[j][q] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (j0 + j < cnt) {
                 const P* p = part(j0 + j);
                 pm[j] = part_ld<FAR>(&p->m[r]);
                 pl[j] = part_ld<FAR>(&p->l[r]);
-                v[j] = part_ld<FAR>(p->quad(r, d));
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) v[j][q] = part_ld<FAR>(p->quad(r, d + 4 * q));
             }
         }
         float top = m;
 #pragma unroll
-        for (int j = 0; j < JOIN; ++j) top = fmaxf(top, pm[j]);
+        for (int j = 0; j < AT; ++j) top = fmaxf(top, pm[j]);
         const float keep = m == -INFINITY ? 0.f : ex2(m - top);
         l *= keep;
-        o.x *= keep;
-        o.y *= keep;
-        o.z *= keep;
-        o.w *= keep;
 #pragma unroll
-        for (int j = 0; j < JOIN; ++j) {
+        for (int q = 0; q < NQ; ++q) {
+            o[q].x *= keep;
+            o[q].y *= keep;
+            o[q].z *= keep;
+            o[q].w *= keep;
+        }
+#pragma unroll
+        for (int j = 0; j < AT; ++j) {
             if (pm[j] == -INFINITY && pl[j] == 0.f) continue;    // saw nothing
             const float w = pm[j] == -INFINITY ? 1.f : ex2(pm[j] - top);   // -inf with a sum: NaN scores
             l = fmaf(pl[j], w, l);
-            o.x = fmaf(v[j].x, w, o.x);
-            o.y = fmaf(v[j].y, w, o.y);
-            o.z = fmaf(v[j].z, w, o.z);
-            o.w = fmaf(v[j].w, w, o.w);
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) {
+                o[q].x = fmaf(v[j][q].x, w, o[q].x);
+                o[q].y = fmaf(v[j][q].y, w, o[q].y);
+                o[q].z = fmaf(v[j][q].z, w, o[q].z);
+                o[q].w = fmaf(v[j][q].w, w, o[q].w);
+            }
         }
         m = top;
     }
     if (out) {
-        *const_cast<float4*>(out->quad(r, d)) = o;
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) *const_cast<float4*>(out->quad(r, d + 4 * q)) = o[q];
         if (d == 0) {
             out->m[r] = m;
             out->l[r] = l;
         }
     } else {
         const int G = a.Hq / a.c.Hkv, row = q0 + f / G, head = h * G + f % G;
+        const int64_t at = row * a.ldo + (int64_t)head * D + d;
         const float n = inv_sum(l);
-        store_out4(a.O, row * a.ldo + (int64_t)head * D + d, a.yt, o.x * n, o.y * n, o.z * n, o.w * n);
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) store_out4(a.O, at + 4 * q, a.yt, o[q].x * n, o[q].y * n, o[q].z * n, o[q].w * n);
         if (a.lse && d == 0) a.lse[(int64_t)row * a.Hq + head] = lse_of(m, l);
     }
 }

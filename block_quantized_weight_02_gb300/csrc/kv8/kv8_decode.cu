@@ -598,13 +598,13 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
             left &= left - 1;
             return (const Part<D>*)(w & 1 ? last_part(w >> 1) : &sp->warp[blockIdx.x * NW + (w >> 1)]);
         };
-        join<false, D>(a, s.q0, h, r, r, d, __popc(run), part, begins && ends ? nullptr : &sp->cta[blockIdx.x][begins ? 1 : 0]);
+        join<false, D, 1, 8>(a, s.q0, h, r, r, d, __popc(run), part, begins && ends ? nullptr : &sp->cta[blockIdx.x][begins ? 1 : 0]);
         if (!(begins && ends) && r == 0 && d == 0) sp->seg[blockIdx.x][begins ? 1 : 0] = seg;
     }
 }
 
-// Joins the segments that lie across CTAs: CTA i takes the one that began in share i.
-constexpr int JOIN_THREADS = 256;
+// Joins the segments that lie across CTAs: the CTAs (i, .) take the one that began in share i, four channels a thread.
+constexpr int JOIN_THREADS = 128;
 template <int D>
 __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(const AttnArgs a) {
     pdl_launch_dependents();
@@ -621,9 +621,10 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(const AttnArgs a) {
     }
     if (seg < 0) return;
     const Seq s = seq_of(a, seg / a.c.Hkv);
-    for (int k = threadIdx.x; k < s.n * (a.Hq / a.c.Hkv) * (D / 4); k += JOIN_THREADS)
-        join<true, D>(a, s.q0, seg % a.c.Hkv, k / (D / 4), k / (D / 4), k % (D / 4) * 4, cnt,
-                [&](int j) { return j == 0 ? &sp->cta[i][1] : &sp->cta[i + j][0]; }, (Part<D>*)nullptr);
+    const int k = blockIdx.y * JOIN_THREADS + threadIdx.x;
+    if (k < s.n * (a.Hq / a.c.Hkv) * (D / 4))
+        join<true, D, 1, 8>(a, s.q0, seg % a.c.Hkv, k / (D / 4), k / (D / 4), k % (D / 4) * 4, cnt,
+                            [&](int j) { return j == 0 ? &sp->cta[i][1] : &sp->cta[i + j][0]; }, (Part<D>*)nullptr);
 }
 
 template <int D, int NT, int PT>
@@ -642,7 +643,7 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
     const unsigned ctas = (unsigned)std::min(num_sms(), MAX_CTAS);
     e = launch_pdl(k_attn_decode<D, NT, PT>, dim3(ctas), dim3(R::NW * 32), smem, s, maps, a, (uint64_t)options().wait_ns.load());
     if (e != cudaSuccess) return e;
-    return launch_pdl(k_attn_join<D>, dim3(ctas), dim3(JOIN_THREADS), 0, s, a);
+    return launch_pdl(k_attn_join<D>, dim3(ctas, NT * 8 * (D / 4) / JOIN_THREADS), dim3(JOIN_THREADS), 0, s, a);
 }
 
 template <int D, int NT>

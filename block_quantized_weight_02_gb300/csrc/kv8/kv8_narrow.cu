@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
     if (warp == MMA_WARP) tmem_dealloc(tmem, 128);
 }
 
-// Joins the items that lie across shares: CTA i takes the one that began in share i.
+// Joins the items that lie across shares: the CTAs (i, .) take the one that began in share i, four channels a thread.
 template <int D>
 __global__ void __launch_bounds__(256) k_narrow_join(const AttnArgs a, int ctas) {
     pdl_launch_dependents();
@@ -488,9 +488,10 @@ __global__ void __launch_bounds__(256) k_narrow_join(const AttnArgs a, int ctas)
     const int4 it = __ldcg(reinterpret_cast<const int4*>(&list->item[seg / a.c.Hkv]));
     const int q0 = __ldg(a.b.q_start + it.x), n = __ldg(a.b.q_start + it.x + 1) - q0;
     const int rows = (int)min((int64_t)NR, (int64_t)n * (a.Hq / a.c.Hkv) - it.y);
-    for (int k = threadIdx.x; k < rows * (D / 4); k += 256)
-        join<true, D>(a, q0, seg % a.c.Hkv, it.y + k / (D / 4), k / (D / 4), k % (D / 4) * 4, cnt,
-                      [&](int j) { return j == 0 ? &sp->cta[i][1] : &sp->cta[i + j][0]; }, (Part<D>*)nullptr);
+    const int k = blockIdx.y * 256 + threadIdx.x;
+    if (k < rows * (D / 4))
+        join<true, D, 1, 8>(a, q0, seg % a.c.Hkv, it.y + k / (D / 4), k / (D / 4), k % (D / 4) * 4, cnt,
+                            [&](int j) { return j == 0 ? &sp->cta[i][1] : &sp->cta[i + j][0]; }, (Part<D>*)nullptr);
 }
 
 template <int D, int PT>
@@ -507,7 +508,7 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     e = launch_pdl(k_narrow<D, PT>, dim3(ctas), dim3(THREADS), smem, s, maps, a, (uint64_t)options().wait_ns.load());
     if (e != cudaSuccess) return e;
-    return launch_pdl(k_narrow_join<D>, dim3(ctas), dim3(256), 0, s, a, ctas);
+    return launch_pdl(k_narrow_join<D>, dim3(ctas, NR * (D / 4) / 256), dim3(256), 0, s, a, ctas);
 }
 
 }  // namespace

@@ -628,7 +628,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
     if (warp == MMA_WARP) tmem_dealloc(tmem, 512);
 }
 
-// Joins the items that lie across shares: CTA (i, y) takes rows 32 y .. of the one that began in share i.
+// Joins the items that lie across shares: CTA (i, y) takes rows 32 y .. of the one that began in share i, a warp an
+// eighth of the channels.
 template <int D, int TILES>
 __global__ void __launch_bounds__(256) k_tiles_join(const AttnArgs a, int ctas) {
     pdl_launch_dependents();
@@ -640,12 +641,10 @@ __global__ void __launch_bounds__(256) k_tiles_join(const AttnArgs a, int ctas) 
     const int4 it = __ldcg(reinterpret_cast<const int4*>(&list->item[seg / a.c.Hkv]));
     const int q0 = __ldg(a.b.q_start + it.x), n = __ldg(a.b.q_start + it.x + 1) - q0;
     const int rows = (int)min((int64_t)TILES * TM, (int64_t)n * (a.Hq / a.c.Hkv) - it.y);
-    for (int k = threadIdx.x; k < 32 * (D / 4); k += 256) {
-        const int r = blockIdx.y * 32 + k % 32;
-        if (r < rows)
-            join<true, D>(a, q0, seg % a.c.Hkv, it.y + r, r, k / 32 * 4, cnt,
-                          [&](int j) { return j == 0 ? &sp->cta[i][1] : &sp->cta[i + j][0]; }, (Part<D, TILES>*)nullptr);
-    }
+    const int r = blockIdx.y * 32 + threadIdx.x % 32;
+    if (r < rows)
+        join<true, D, D / 32, 4>(a, q0, seg % a.c.Hkv, it.y + r, r, threadIdx.x / 32 * (D / 8), cnt,
+                                 [&](int j) { return j == 0 ? &sp->cta[i][1] : &sp->cta[i + j][0]; }, (Part<D, TILES>*)nullptr);
 }
 
 template <int D, int PT, int TILES>
