@@ -10,7 +10,7 @@ namespace {
 constexpr int TM = 128;                // rows or channels of a tensor-core tile
 constexpr int TN = 128;                // tokens of a step
 constexpr int NB = TN / BLK;           // blocks of a step
-constexpr int MAX_CTAS = 256;          // workspace bound
+constexpr int MAX_CTAS = 256;          // workspace bound, and no more than a plan's threads
 constexpr int PLAN_THREADS = 1024;
 constexpr int ITEM_COST = 7;           // of beginning and ending an item, in steps
 constexpr int SS = 8;                  // steps whose scales are kept
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tiles_plan(const AttnArgs a, L
         const int q0 = __ldg(a.b.q_start + b), nq = __ldg(a.b.q_start + b + 1) - q0, L = __ldg(a.b.lens + b);
         const int64_t f0 = (s - key(b)) * ROWS, rows = (int64_t)nq * G;
         if (f0 >= 0 && f0 < rows) {
-            const int first = (int)(f0 / G), last = (int)((min(f0 + ROWS, rows) - 1) / G);
+            const int first = (int)f0 / G, last = (int)(min(f0 + ROWS, rows) - 1) / G;
             const int lo = row_lo(first, nq, L, a.window) / BLK * BLK, hi = row_hi(last, nq, L, a.causal);
             it.f0 = (int)f0;
             it.tok0 = lo;
@@ -94,38 +94,49 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tiles_plan(const AttnArgs a, L
         sp->item[s] = it;
         if (it.steps) mine += (int64_t)(it.steps + ITEM_COST) * a.c.Hkv;
     }
-    int64_t inc = mine;
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
-    }
+    __shared__ int64_t before[PLAN_THREADS + 1];                   // cost of the slots ahead of each thread's
+    auto scan = [&](int64_t v) {
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
+        }
+        return v;
+    };
+    const int64_t inc = scan(mine);
     if (lane == 31) wsum[warp] = inc;
     __syncthreads();
-    int64_t at = inc - mine, total = 0;
-    for (int i = 0; i < PLAN_THREADS / 32; ++i) {
-        if (i < warp) at += wsum[i];
-        total += wsum[i];
-    }
+    const int64_t sums = scan(wsum[lane]);
+    const int64_t ahead = __shfl_sync(0xffffffffu, sums, warp) - wsum[warp], total = __shfl_sync(0xffffffffu, sums, 31);
+    before[threadIdx.x] = ahead + inc - mine;
     if (threadIdx.x == 0) {
+        before[PLAN_THREADS] = total;
         sp->ok = 1;
         sp->start[ctas] = {slots, 0, 0};
     }
-    // the shares that begin in this thread's slots: share i at cost i q + min(i, rem)
-    const int64_t q = total / ctas, rem = total % ctas;
-    for (int s = s0; s < s1; ++s) {
-        const int cost = sp->item[s].steps + ITEM_COST;
-        if (cost == ITEM_COST) continue;
-        const int64_t end = at + (int64_t)cost * a.c.Hkv;
-        for (int64_t i = at / (q + 1); i < ctas; ++i) {
-            const int64_t u = i * q + min(i, rem);
-            if (u >= end) break;
-            if (u >= at) sp->start[i] = {s, (int)((u - at) / cost), max((int)((u - at) % cost) - ITEM_COST, 0)};
+    __syncthreads();
+    // a thread finds where share i begins: at cost i q + min(i, rem)
+    const int i = threadIdx.x;
+    if (i >= ctas) return;
+    const int64_t u = i * (total / ctas) + min((int64_t)i, total % ctas);
+    Start at = {slots, 0, 0};                                      // (past the list: there are more CTAs than cost)
+    if (u < total) {
+        int t = 0;                                                 // the last thread with before[t] <= u: it has slots
+        for (int o = PLAN_THREADS / 2; o; o >>= 1)
+            if (before[t + o] <= u) t += o;
+        int64_t rest = u - before[t];
+        for (int s = min(t * per, slots);; ++s) {
+            const int cost = sp->item[s].steps + ITEM_COST;
+            if (cost == ITEM_COST) continue;
+            const int64_t all = (int64_t)cost * a.c.Hkv;
+            if (rest < all) {
+                const int h = (int)(rest / cost);
+                at = {s, h, max((int)(rest - (int64_t)h * cost) - ITEM_COST, 0)};
+                break;
+            }
+            rest -= all;
         }
-        at = end;
     }
-    // shares past the list (there are more CTAs than cost)
-    for (int64_t i = threadIdx.x; i < ctas; i += PLAN_THREADS)
-        if (i * q + min(i, rem) >= total) sp->start[i] = {slots, 0, 0};
+    sp->start[i] = at;
 }
 
 // ---- issuing products.  A whole warp runs the issuing loops and one elected lane the instructions, on values the
@@ -152,14 +163,13 @@ struct Walk {
     Item it;
     int from, until;      // steps of the current part
     __device__ __forceinline__ void begin(const List* sp) {
-        at = end = {0, 0, 0};
-        if (!__ldcg(&sp->ok)) return;
         auto get = [&](int i) {
             const Start* p = &sp->start[i];
             return Start{__ldcg(&p->slot), __ldcg(&p->h), __ldcg(&p->step)};
         };
         at = get(blockIdx.x);
         end = get(blockIdx.x + 1);
+        if (!__ldcg(&sp->ok)) at = end = {0, 0, 0};
     }
     __device__ __forceinline__ bool next(const AttnArgs& a, const List* sp, bool first) {
         if (!first) {
