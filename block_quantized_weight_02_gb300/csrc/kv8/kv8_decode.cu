@@ -503,19 +503,25 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
                     for (int j = 0; j < W; ++j) {
 #pragma unroll
                         for (int e = 0; e < 4; ++e) v[e][j] ^= 0x80808080u;
-                        const uint32_t a01 = prmt(v[0][j], v[1][j], 0x5140u), a23 = prmt(v[0][j], v[1][j], 0x7362u);
-                        const uint32_t b01 = prmt(v[2][j], v[3][j], 0x5140u), b23 = prmt(v[2][j], v[3][j], 0x7362u);
-                        const uint32_t va[2][4] = {{codes_f16(a01, 0x4140u), codes_f16(a01, 0x4342u), codes_f16(b01, 0x4140u),
-                                                    codes_f16(b01, 0x4342u)},
-                                                   {codes_f16(a23, 0x4140u), codes_f16(a23, 0x4342u), codes_f16(b23, 0x4140u),
-                                                    codes_f16(b23, 0x4342u)}};
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
+                        for (int e = 0; e < 2; ++e) {
+                            const uint32_t sel = e ? 0x7362u : 0x5140u;
+                            const uint32_t ya = prmt(v[0][j], v[1][j], sel), yb = prmt(v[2][j], v[3][j], sel);
+                            const uint32_t va[4] = {codes_f16(ya, 0x4140u), codes_f16(ya, 0x4342u), codes_f16(yb, 0x4140u), codes_f16(yb, 0x4342u)};
 #pragma unroll
-                            for (int n = 0; n < NT; ++n)
+                            for (int n = 0; n < NT; ++n) {
+                                float(&o)[4] = acc.o[n][2 * j + e];
+                                if (PT == 1) {
+                                    mma_16816_f16(o, va, p[n][0][2 * kk], p[n][0][2 * kk + 1]);
+                                } else {          // the products truncate what they add up: long sums are added here
+                                    float y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                                for (int z = 0; z < PT; ++z)
-                                    mma_16816_f16(acc.o[n][2 * j + e], va[e], p[n][z][2 * kk], p[n][z][2 * kk + 1]);
+                                    for (int z = 0; z < PT; ++z) mma_16816_f16(y, va, p[n][z][2 * kk], p[n][z][2 * kk + 1]);
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) o[i] += y[i];
+                                }
+                            }
+                        }
                     }
                 }
                 __syncwarp();                     // the stage is free

@@ -41,6 +41,7 @@ struct Rows {
     float fac[NR];                     // what the last move of the maxima scaled sums by
     float wmax[2][4][NR];              // maxima of the warps' tokens
     float sum[8][NR];                  // row sums of the warps
+    float m_sum[NR];                   // maxima of the sum in the workspace
     int ref, moves;                    // largest value exponent so far; moves of (maxima, ref) so far
 };
 
@@ -238,6 +239,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
 #pragma unroll
             for (int r = 0; r < NR; ++r) l[r] = 0.f;
             int moves = 0;
+            Part<D>* part = &sp->cta[blockIdx.x][w.from == 0 ? 1 : 0];
             for (int j = x; j < n; j += 2, ++steps) {
                 const uint32_t tile = tile0 + j;
                 wait_warp(sc_full + 8 * (tile % SS), tile / SS & 1);
@@ -266,6 +268,28 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                     for (int r = 0; r < NR; ++r) l[r] *= rows->fac[r];
                 }
                 int ref = rows->ref;
+                const bool fresh = starts_fresh<PT>(j);      // (the even steps' group only)
+                if (PT == 2 && fresh && j > 0) {
+                    wait_warp(pv_done, (done0 + j - 1) & 1);
+                    tc_fence_after();
+                    const float un = pow2i(ref - (int)W_EXP);
+#pragma unroll 1
+                    for (int c = 0; c < NR / 16; ++c) {
+                        uint32_t y[16];
+                        tmem_ld_32x32b_x16(to + 16 * c, y);
+                        tmem_ld_wait();
+                        if (tid < D)
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const int r = 16 * c + e;
+                                float* o = &part->o[r][tid];
+                                const float z = j > FRESH ? *o * since(rows->m_sum[r], -rows->rc[r].y) : 0.f;
+                                *o = fmaf(__uint_as_float(y[e]), un, z);
+                            }
+                    }
+                    any_of(false, 1 + x, 128);               // all have read the old maxima
+                    if (quarter == 0) rows->m_sum[lane] = -rows->rc[lane].y;
+                }
                 const bool masked = __any_sync(0xffffffffu, tok < free_lo || tok >= free_hi);
                 float over = -INFINITY;
 #pragma unroll
@@ -294,7 +318,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                     const float nm = grow ? top : m, fac = grow ? ex2(m - nm) : 1.f;
                     nref = max(nref, ref);
                     const float fo = fac * pow2i(max(ref - nref, -126));
-                    if (j > 0) {                 // all products so far are in O^T
+                    if (!fresh) {                // all products so far are in O^T
                         wait_warp(pv_done, (done0 + j - 1) & 1);
                         tc_fence_after();
                         uint32_t y[32];
@@ -373,7 +397,6 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
             // O^T: thread = channel; this group's half of the rows
             const bool whole = w.from == 0 && w.until == w.it.steps;
             const float un = pow2i(rows->ref - (int)W_EXP);
-            Part<D>* part = &sp->cta[blockIdx.x][w.from == 0 ? 1 : 0];
             // (a loop: what runs once a part should not push the loops of every step out of the instruction cache)
 #pragma unroll 1
             for (int r = 16 * x; r < min(16 * x + 16, nrows); ++r) {
@@ -384,7 +407,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) sum += rows->sum[i][r];
-                const float m = -rows->rc[r].y, o = __uint_as_float(y) * un;
+                const float m = -rows->rc[r].y;
+                float o = __uint_as_float(y) * un;
+                if (PT == 2 && n > FRESH && tid < D) o = fmaf(part->o[r][tid], since(rows->m_sum[r], m), o);
                 if (whole) {
                     const int64_t row = q0 + f / G, head = w.at.h * G + f % G;
                     if (tid < D) store_out(a.O, row * a.ldo + head * D + tid, a.yt, o * inv_sum(sum));
@@ -438,7 +463,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                     // (D 64: the tile's upper 64 channels are the lower ones again, and unused)
                     const uint32_t va = uniform(desc_outer(sb + M::H + (vt % HS) * M::HT, D == 128 ? TN * 128 : 0));
                     const uint32_t pb = uniform(desc_outer(sb + M::P + (M::PBUF == 1 ? 0 : x) * PT * M::PT_BYTES, 0));
-                    const uint32_t acc = j > 0;
+                    const uint32_t acc = !starts_fresh<PT>(j);
                     if (elect_one()) {
 #pragma unroll
                         for (int z = 0; z < PT; ++z)

@@ -292,6 +292,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
             const int free_lo = u0.wf <= u0.wl ? row_lo(u0.wl / G, u0.nq, u0.L, a.window) : 0;
             float m = -INFINITY, l = 0.f;
             int ref = -64;
+            // this tile's partial, and its sum in the meantime: against the maximum m_sum
+            Part<D, TILES>* part = TILES == 1 && x == 1 ? &sp->odd[blockIdx.x] : &sp->cta[blockIdx.x][w.from == 0 ? 1 : 0];
+            float m_sum = -INFINITY;
+            bool summed = false;
             for (int j = 0; j < mine; ++j, ++steps) {
                 const uint32_t tile = tile0 + j * EACH + (TILES == 1 ? x : 0);
                 // A part's first scores are waited for before its first scales: a tile that takes no part in some items
@@ -316,6 +320,28 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                     continue;
                 }
                 tc_fence_after();
+                const bool fresh = starts_fresh<PT>(j);
+                if (PT == 2 && fresh && j > 0) {        // the scores came after all products so far
+                    const float un = pow2i(ref - (int)W_EXP), keep = since(m_sum, m);
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t y[32];
+                        tmem_ld_32x32b_x32(tm_o(x) + lanes + 32 * c, y);
+                        tmem_ld_wait();
+                        if (u0.in)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                float4* o = &part->o[8 * c + e][u0.r];
+                                const float4 z = summed ? *o : make_float4(0.f, 0.f, 0.f, 0.f);
+                                *o = make_float4(fmaf(z.x, keep, __uint_as_float(y[4 * e]) * un),
+                                                 fmaf(z.y, keep, __uint_as_float(y[4 * e + 1]) * un),
+                                                 fmaf(z.z, keep, __uint_as_float(y[4 * e + 2]) * un),
+                                                 fmaf(z.w, keep, __uint_as_float(y[4 * e + 3]) * un));
+                            }
+                    }
+                    m_sum = m;
+                    summed = true;
+                }
                 // Scores that a row does not see become -inf.  Blocks with an odd factor are multiplied here.
                 auto prepare = [&](uint32_t full) {
 #pragma unroll 1
@@ -361,7 +387,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                             m = nm;
                             l *= fm;
                             ref = nref;
-                            if (j > 0) {
+                            if (!fresh) {
 #pragma unroll 1
                                 for (int c = 0; c < D / 32; ++c) {
                                     uint32_t y[32];
@@ -440,23 +466,24 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
             // TILES 1: the odd steps' result goes to the even steps' threads
             Part<D, TILES>* odd = &sp->odd[TILES == 1 ? blockIdx.x : 0];
             const bool both = TILES == 1 && n > 1;
-            float w0 = un, w1 = 0.f;
+            float w0 = un, w1 = 0.f, ws = since(m_sum, m);
             if (both && x == 0) {
                 if (!wait_warp(odd_full, odds++ & 1)) break;
                 if (u0.in) {
                     const float m1 = odd->m[u0.r], l1 = odd->l[u0.r], top = fmaxf(m, m1);
                     const float e0 = m == -INFINITY ? 1.f : ex2(m - top), e1 = m1 == -INFINITY ? 1.f : ex2(m1 - top);
                     w0 = un * e0;
+                    ws *= e0;
                     w1 = e1;
                     l = l * e0 + l1 * e1;
                     m = top;
                 }
             }
-            Part<D, TILES>* part = both && x == 1 ? odd : &sp->cta[blockIdx.x][begins ? 1 : 0];
             const bool direct = whole && !(both && x == 1);
             if (direct) {
                 const float inv = inv_sum(l);
                 w0 *= inv;
+                ws *= inv;
                 w1 *= inv;
             }
             // Outputs go through the query tile (its products are done), so that neighbouring lanes store
@@ -474,6 +501,16 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                 float y[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(v[e]) * w0;
+                if (PT == 2 && summed && u0.in) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float4 z = part->o[8 * c + e][u0.r];
+                        y[4 * e] = fmaf(z.x, ws, y[4 * e]);
+                        y[4 * e + 1] = fmaf(z.y, ws, y[4 * e + 1]);
+                        y[4 * e + 2] = fmaf(z.z, ws, y[4 * e + 2]);
+                        y[4 * e + 3] = fmaf(z.w, ws, y[4 * e + 3]);
+                    }
+                }
                 if (both && x == 0 && u0.in) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -593,7 +630,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                         const uint32_t next = kt + 2 * EACH;
                         if (!h_wait(kt + 1) || (j + 1 < mine && !h_wait(next)) || !take(both)) break;
                         if (!wait_warp(p_ready + 8 * x, steps++ & 1)) break;
-                        pv(kt + 1, j > 0);
+                        pv(kt + 1, !starts_fresh<PT>(j));
                         if (j + 1 < mine) {
                             qk(next, both);
                             if (elect_one()) {
