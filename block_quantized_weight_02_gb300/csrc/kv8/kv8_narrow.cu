@@ -14,6 +14,10 @@
 // decision to move it follows the decision of the step before (a barrier hands it on; the
 // exponentials of neighbouring steps overlap), and whoever moves it rescales O^T in tensor memory.
 // Scales, weights and the list of work as in the kernel for many rows.
+//
+// Measured: 25 rows of 8 heads of 128 channels, 24 sequences of 300 to 9000 tokens: 80 us, 2.8 TB/s; f32 outputs 108 us.
+// Bound by a step's chain (scores, vote, weights to shared memory, product), two of which are under way at a time, and by
+// 10 us for the list and the joins.
 #include "tiles_common.cuh"
 
 namespace cq {
@@ -295,8 +299,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
 #pragma unroll
                 for (int r = 0; r < NR; r += 2) {
                     const float4 c = *reinterpret_cast<const float4*>(&rows->rc[r]);
-                    s[r] *= ks * c.x;
-                    s[r + 1] *= ks * c.z;
+                    s[r] = __fmul_rn(s[r], ks * c.x);            // rounded as for the maximum: a fused step would leave
+                    s[r + 1] = __fmul_rn(s[r + 1], ks * c.z);    // a huge score's rounding
                     if (masked) {
                         const int4 lim = *reinterpret_cast<const int4*>(&rows->lim[r]);
                         if (tok < lim.x || tok >= lim.y) s[r] = -INFINITY;

@@ -7,8 +7,8 @@
 // keeps two tiles going, so that the tensor cores have one while the other's softmax runs:
 // two row tiles (TILES 2, items of 256 rows), or, where no sequence has more than 128 rows,
 // the even and the odd steps of one row tile (TILES 1), whose two results are joined at the end.
-//   warps 0, 2      issue the products of the two tiles (one thread each: a wait or a commit costs a
-//                   thread about 100 cycles, which the other's products cover), in turns: left to
+//   warps 0, 2      issue the products of the two tiles (an elected lane each: a wait or a commit costs
+//                   about 100 cycles, which the other's products cover), in turns: left to
 //                   themselves the tiles fall into step, and both softmaxes run while no products do
 //   warp 1          TMA loads of the codes by page, 32 tokens a box, and their scales
 //   warps 4-7, 8-11 softmax of the two tiles, one row a thread; queries in, outputs out
@@ -21,6 +21,12 @@
 // The work is the list of all (row tile, KV head, step), cut into one equal share per SM.  A
 // first small kernel lays the list out (only the device knows the lengths), a third joins the
 // row tiles that lie across shares, in share order.
+//
+// Measured, 128 channels, bf16 outputs: a 16384-token prompt of 32 heads over 8 KV heads 1800 us, 1220 TFLOP/s; prompts
+// of up to 2000 tokens behind up to 3000 266 us, 850; 2 x 1024 rows against 4500 to 5100 tokens, 24 heads, 135 us, 896.  f32
+// outputs: the ragged prompts 435 us.  A step of two tiles takes 1.85 us where its products alone would take 1.1: a tile's
+// products wait for its exponentials (four cycles a warp and scheduler each) and each hand-over between the two costs a few
+// hundred cycles, which the other tile covers only in part.
 #include "tiles_common.cuh"
 
 namespace cq {
@@ -342,8 +348,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                     m_sum = m;
                     summed = true;
                 }
-                // Scores that a row does not see become -inf.  Blocks with an odd factor are multiplied here.
-                auto prepare = [&](uint32_t full) {
+                // Scores that a row does not see become -inf.  Blocks with an odd factor are multiplied here; `off` is taken off.
+                auto prepare = [&](uint32_t full, float off) {
 #pragma unroll 1
                     for (int c = 0; c < TN / 16; ++c) {
                         uint32_t y[16];
@@ -353,7 +359,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                         const int lo = rlo - t0 - 16 * c, hi = rhi - t0 - 16 * c;
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            y[e] = e >= lo && e < hi ? __float_as_uint(__uint_as_float(y[e]) * k) : 0xFF800000u;
+                            y[e] = e >= lo && e < hi ? __float_as_uint(__fmul_rn(__uint_as_float(y[e]), k) - off) : 0xFF800000u;
                         tmem_st_32x32b_x16(tm_s(x) + lanes + 16 * c, y);
                     }
                     tmem_st_wait();
@@ -362,8 +368,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                 if (prep) {
                     // one choice of blocks for the warp: a factor that is odd in one row is taken in full in all
                     full = __reduce_or_sync(0xffffffffu, odd_k);
-                    prepare(full);
+                    prepare(full, 0.f);
                 }
+                bool less = false;           // m has been taken off
                 // One pass: weights against the m so far, kept in registers until the step's maximum is known.  Where
                 // that has grown by more than GROW (and at first) the maximum comes before them.  f32 outputs
                 // (whose weights take twice the registers) always take the maximum first.
@@ -399,14 +406,15 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                                 }
                             }
                         }
-                        // Scores of 2^20 and more are rounded before m is taken off, as they were for m: a fused step
-                        // would leave their own rounding, which is then no longer small.
-                        if (full != (1u << NB) - 1 && __any_sync(0xffffffffu, fabsf(m) > 1048576.f && m != -INFINITY)) {
-                            prepare(~full & ((1u << NB) - 1));
+                        // From 2^20 on scores are rounded before m is taken off, as they were for m, and the exponent is
+                        // added after that: a fused step would leave their own rounding, which is then no longer small.
+                        if (__any_sync(0xffffffffu, fabsf(m) > 1048576.f && m != -INFINITY)) {
+                            prepare(~full & ((1u << NB) - 1), m == -INFINITY ? 0.f : m);
                             full = (1u << NB) - 1;
+                            less = true;
                         }
                     }
-                    const float m0 = m == -INFINITY ? 0.f : m;
+                    const float m0 = less || m == -INFINITY ? 0.f : m;
                     float top = -INFINITY, add = 0.f;
                     uint32_t s[2][32], p[PT == 1 ? NB : 1][16], p2[16];
                     tmem_ld_32x32b_x32(tm_s(x) + lanes, s[0]);

@@ -304,6 +304,35 @@ def test_large_and_growing_scores(n):
         s.check_attend([n], 4, q=q)
 
 
+@pytest.mark.parametrize("n,group", [(1, 4), (3, 5), (5, 5), (8, 4), (25, 4), (100, 4)])
+@pytest.mark.parametrize("size", [1e2, 1e4, 1e6, 1e9])
+def test_huge_scores(n, group, size):
+    """Scores whose own rounding is far above 1: the largest one's value is the result, to the last weight."""
+    s = Setup(39, [300], 2, 128, 64)
+    k = s.rows(300, 2, "f32", 0.1) * size
+    s.write([300], "f32", k=k)
+    q = (s.rows(n, 2 * group, "f32", 0.1) * size).bfloat16()
+    for out in ("f32", "bf16"):
+        _, o, z = s.attend([n], group, out=out, q=q)
+        assert torch.isfinite(o).all() and torch.isfinite(z).all()
+        kc, vc, go = s.ref.values(0, 0), s.ref.values(1, 0), f64(o)
+        near = 0
+        for i in range(n):
+            L = 300 - n + i + 1
+            for h in range(2 * group):
+                x = f64(q[i, h]) * 128 ** -0.5
+                sc = kc[:L, h // group] @ x
+                reach = (np.abs(kc[:L, h // group]) @ np.abs(x)).max()
+                a, b = np.argsort(sc)[::-1][:2]
+                if sc[a] - sc[b] < 100 + 2.0 ** -14 * reach:      # apart by more than the scores' error, e^-100 of the rest
+                    near += 1
+                    continue
+                v = vc[a, h // group]
+                u = 2.0 ** -20 if out == "f32" else 2.0 ** -8
+                assert np.all(np.abs(go[i, h] - v) <= u * np.abs(v) + 1e-30), (i, h)
+        assert near < n * 2 * group / 2
+
+
 @pytest.mark.parametrize("n", [1, 60])
 def test_query_range(n):
     """bf16 queries beyond fp16's range, tiny ones, and a row of zeros."""
