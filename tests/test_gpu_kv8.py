@@ -479,6 +479,23 @@ def test_several_items_a_block(Hkv, group, B, rows, held, D, out):
         assert np.all(np.abs(f64(z) - rz) <= kv8ref.lse_bound(rz, reach))
 
 
+@pytest.mark.parametrize("n,group", [(1, 2), (3, 4), (5, 5), (60, 1), (200, 1), (1000, 1)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_shares(n, group, D):
+    """f32 outputs where one SM adds up thousands of tokens.  An accumulator takes at most 256 truncated sums (16 steps of
+    16 products), on average a quarter of 2^-24 of it each: 4e-6; scores and weights add 2e-6 and less."""
+    B, Hkv = 20, 16
+    lens = [6000 - 31 * b for b in range(B)]
+    s = Setup(40, lens, Hkv, D, 128)
+    s.len = lens
+    cq.cq_kv8_write(s.cache, s.rows(sum(lens), Hkv, "f32", 0.3), s.rows(sum(lens), Hkv, "f32", 0.3), starts(lens), i32(lens))
+    counts = [n if b < 3 or n < 100 else 1 for b in range(B)]
+    q, o, z = s.attend(counts, group, "f16", "f32")
+    ro, rz, _, _, reach = exact(s, q, counts, True, 0)
+    assert np.linalg.norm(f64(o) - ro) <= 1e-5 * np.linalg.norm(ro)
+    assert np.all(np.abs(f64(z) - rz) <= kv8ref.lse_bound(rz, reach))
+
+
 def test_max_q_larger_than_the_batch():
     """max_q only has to bound the rows: the result stays within the same bounds."""
     s = Setup(35, [100, 50], 2, 64, 32)
