@@ -136,6 +136,7 @@ cq_status cq_attn_kv8(const void* Q, int xt, int64_t T, int64_t Hq, int64_t ldq,
         return fail(CQ_ERR_ARG, "%s: causal must be 0 or 1, window >= 0 and only with causal", who);
     if (!aligned(q_start, 4) || !aligned(lens, 4) || !aligned(lse, 4)) return fail(CQ_ERR_ALIGN, "%s: index arrays and lse must be 4-byte aligned", who);
     max_q = std::min(max_q, T);
+    window = std::min<int64_t>(window, INT32_MAX);   // the same tokens (positions are 31-bit), and no overflow of p - window
     const size_t need = attn_workspace(T, Hq, cache->Hkv, cache->D, cache->B, max_q);
     if (!aligned(ws, 256) || ws_bytes < need) return fail(CQ_ERR_WORKSPACE, "%s: workspace needs %zu bytes, 256-aligned", who, need);
     if ((st = check_device())) return st;

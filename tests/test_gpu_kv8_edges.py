@@ -1,0 +1,37 @@
+"""The 8-bit cache and its attention at the edges of what their header allows,
+against the plain 64-bit reference of kv8ref."""
+import numpy as np
+import pytest
+import torch
+
+import block_quantized_weight_02_gb300 as cq
+import kv8ref
+from cqtest import DEV
+from test_gpu_kv8 import Setup, f64, i32, starts
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built(cuda_dev):
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+# one size for each attention kernel, by the query rows of a KV head: few, narrow, one row tile, two row tiles
+FORMS = [(1, 4), (5, 4), (20, 4), (70, 4)]
+
+
+# ---- windows and lengths -----------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("window", [2 ** 63 - 1, 2 ** 62, 2 ** 31, 2 ** 31 - 1])
+@pytest.mark.parametrize("n,group", FORMS + [(16, 1)])
+def test_windows_without_end(n, group, window):
+    """A window past every length is no window, in sequences with more rows than tokens too."""
+    held = [2, 0, 40]
+    s = Setup(51, [100] * 3, 1, 64, 32)
+    s.write(held)
+    counts = [n, 1, n]
+    q, o, z = s.check_attend(counts, group, window=window)
+    _, o0, z0 = s.attend(counts, group, q=q)
+    assert torch.equal(o, o0) and torch.equal(z, z0)
