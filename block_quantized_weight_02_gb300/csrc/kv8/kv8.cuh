@@ -98,6 +98,11 @@ __device__ __forceinline__ int warp_find(int B, int64_t x, Key key) {
     return lo;
 }
 
+// A length that attention takes: its pages are in the table, and the tokens that a kernel looks up ahead of it (up to 1024
+// past the last) have 31-bit numbers.
+constexpr int MAX_LEN = INT32_MAX - 2047;
+__device__ __forceinline__ bool length_ok(const Cache& c, int L) { return L >= 0 && L <= MAX_LEN && L <= c.ldt * c.page; }
+
 // A ragged batch's entry b: rows [qs, qe) in [0, T], at most max_rows of them.
 __device__ __forceinline__ bool rows_ok(int qs, int qe, int T, int max_rows) {
     return qs >= 0 && qe >= qs && qe <= T && qe - qs <= max_rows;

@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
     bool bad = false;
     for (int b = threadIdx.x * per; b < min((int)(threadIdx.x + 1) * per, a.c.B); ++b) {
         const int qs = __ldg(a.b.q_start + b), qe = __ldg(a.b.q_start + b + 1), L = __ldg(a.b.lens + b);
-        if (!rows_ok(qs, qe, a.b.T, a.max_q) || L < 0 || L > a.c.ldt * a.c.page) bad = true;
+        if (!rows_ok(qs, qe, a.b.T, a.max_q) || !length_ok(a.c, L)) bad = true;
         else mine += (int64_t)seq_of(a, b).units * a.c.Hkv;
     }
     if (__syncthreads_or(bad)) {

@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) k_tiles_plan(const AttnArgs a, L
     bool bad = false;
     for (int b = threadIdx.x; b < a.c.B; b += PLAN_THREADS) {
         const int L = __ldg(a.b.lens + b);
-        if (!rows_ok(__ldg(a.b.q_start + b), __ldg(a.b.q_start + b + 1), a.b.T, a.max_q) || L < 0 || L > a.c.ldt * a.c.page) bad = true;
+        if (!rows_ok(__ldg(a.b.q_start + b), __ldg(a.b.q_start + b + 1), a.b.T, a.max_q) || !length_ok(a.c, L)) bad = true;
     }
     for (int i = threadIdx.x; i < MAX_CTAS; i += PLAN_THREADS) sp->seg[i][0] = sp->seg[i][1] = -1;
     if (__syncthreads_or(bad)) {

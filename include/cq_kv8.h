@@ -46,8 +46,9 @@ typedef struct {
 /* Shape rules of the descriptor: pages >= 1, 1 <= Hkv <= 1024, page >= 32 and
  * page % 32 == 0, D 64 or 128, pages * Hkv * page < 2^31, ldt >= 1,
  * 1 <= B <= 65536.  Kq, Vq, Ks, Vs 16-byte aligned, table 4-byte aligned.
- * Device-detected (CQ_ERR_INDEX): a length outside [0, ldt * page], a q_start that
- * descends or leaves [0, T], a page number outside [0, pages).  The rows of a
+ * Device-detected (CQ_ERR_INDEX): a length outside [0, ldt * page] (attention: or
+ * above 2^31 - 2048), a q_start that descends or leaves [0, T], a page number outside
+ * [0, pages).  The rows of a
  * sequence with such an entry are unspecified, nothing outside the tensors is
  * touched. */
 

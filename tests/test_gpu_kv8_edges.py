@@ -35,3 +35,21 @@ def test_windows_without_end(n, group, window):
     q, o, z = s.check_attend(counts, group, window=window)
     _, o0, z0 = s.attend(counts, group, q=q)
     assert torch.equal(o, o0) and torch.equal(z, z0)
+
+
+@pytest.mark.parametrize("n,group", FORMS)
+def test_lengths_up_to_31_bits(n, group):
+    """A table of one page over and over holds 2^31 tokens; attention declines lengths whose tokens' numbers would overflow."""
+    s = Setup(52, [1024], 1, 64, 1024)
+    table = torch.full((1, 2 ** 21 + 1), int(s.table[0, 0]), dtype=torch.int32, device=DEV)
+    s.cache = cq.cq_kv8_cache(s.cache.Kq, s.cache.Ks, s.cache.Vq, s.cache.Vs, table)
+    s.write([1024])
+    q, o = s.rows(n, group, "bf16"), torch.zeros(n, group, 64, device=DEV)
+    ws = torch.empty(cq.cq_attn_kv8_workspace_bytes(n, group, 1, 64, 1, n), dtype=torch.uint8, device=DEV)
+    for L, status in ((2 ** 31 - 1, 5), (2 ** 31 - 2047, 5), (2 ** 31 - 2048, 0), (1024, 0)):
+        cq.cq_attn_kv8(q, s.cache, starts([n]), i32([L]), n, o, ws, window=900)
+        assert cq.cq_get_device_error() == status, L
+    # the last window of the longest length is the page's: rows end at token 1023 of it
+    cq.cq_attn_kv8(q, s.cache, starts([n]), i32([2 ** 31 - 2048]), n, o, ws, window=900)
+    _, want, _ = s.attend([n], group, q=q, window=900)
+    assert torch.equal(o, want)
