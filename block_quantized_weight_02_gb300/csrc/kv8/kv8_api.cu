@@ -144,7 +144,8 @@ cq_status cq_attn_kv8(const void* Q, int xt, int64_t T, int64_t Hq, int64_t ldq,
     int* err = stream_error_word(s);
     if (!err) return CQ_ERR_CUDA;
     const Batch b = {q_start, lens, nullptr, (int)T, err};
-    const AttnArgs a = {c, b, Q, O, lse, ldq, ldo, xt, yt, (int)Hq, (int)cache->D, (int)max_q, causal, window, scale, ws};
+    const AttnArgs a = {c, b, Q, O, lse, ldq, ldo, xt, yt, (int)Hq, (int)cache->D, (int)max_q, causal, window, scale, ws,
+                        (int)options().test_stall.exchange(0)};
     return launched(launch_attn(a, s), "attention");
 }
 

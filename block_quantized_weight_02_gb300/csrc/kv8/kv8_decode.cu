@@ -285,8 +285,8 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
                 }
                 const int r = __shfl_sync(0xffffffffu, row, used);
                 const uint32_t bar = smem_u32(&bars[warp][pstage]);
-                if (lane < 2) copy4_async(smem_u32(&scales[warp][pstage]) + 4 * lane, a.c.s[lane] + r / BLK, bar);
-                if (lane == 0) {
+                if (lane < 2 && !a.stall) copy4_async(smem_u32(&scales[warp][pstage]) + 4 * lane, a.c.s[lane] + r / BLK, bar);
+                if (lane == 0 && !a.stall) {
                     const uint32_t dst = ring0 + pstage * 2 * R::TILE;
                     mbar_arrive_expect_tx(bar, 2 * R::TILE);
                     tma_load_2d(dst, &maps.t[0], bar, 0, r);
@@ -368,7 +368,9 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
             int ref = -64;                        // largest value-scale exponent so far
 
             for (int i = from; i < until && s.L > 0; ++i) {
-                if (!wait_bar(smem_u32(&bars[warp][stage]), parity, wait_ns, &stop)) {
+                // one answer for the warp: what follows takes all its lanes
+                const bool here = wait_bar(smem_u32(&bars[warp][stage]), parity, wait_ns, &stop);
+                if (!__all_sync(0xffffffffu, here)) {
                     alive = false;
                     break;
                 }

@@ -53,3 +53,29 @@ def test_lengths_up_to_31_bits(n, group):
     cq.cq_attn_kv8(q, s.cache, starts([n]), i32([2 ** 31 - 2048]), n, o, ws, window=900)
     _, want, _ = s.attend([n], group, q=q, window=900)
     assert torch.equal(o, want)
+
+
+# ---- waits that run out ------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("n,group", FORMS[:1])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_wait_timeout_reports_status_and_the_next_call_is_right(n, group, out):
+    """Copies that never come: the kernel ends by its limit and reports it, and what follows is as if it had not been."""
+    s = Setup(53, [3000, 500], 2, 128, 64)
+    s.write([3000, 500])
+    q, want, z = s.attend([n, n], group, out=out)
+    o = torch.empty_like(want)
+    ws = torch.empty(cq.cq_attn_kv8_workspace_bytes(2 * n, 2 * group, 2, 128, 2, n), dtype=torch.uint8, device=DEV)
+    old = cq.cq_get_option(cq.CQ_OPT_WAIT_NS)
+    try:
+        cq.cq_set_option(cq.CQ_OPT_WAIT_NS, 20_000_000)       # 20 ms
+        cq.cq_set_option(cq.CQ_OPT_TEST_STALL, 1)
+        cq.cq_attn_kv8(q, s.cache, starts([n, n]), i32(s.len), n, o, ws)
+        assert cq.cq_get_option(cq.CQ_OPT_TEST_STALL) == 0     # of one call only
+        assert cq.cq_get_device_error() == 8                   # CQ_ERR_TIMEOUT
+        assert cq.cq_get_device_error() == 0
+    finally:
+        cq.cq_set_option(cq.CQ_OPT_WAIT_NS, old)
+        cq.cq_set_option(cq.CQ_OPT_TEST_STALL, 0)
+    _, o, z2 = s.attend([n, n], group, out=out, q=q)
+    assert torch.equal(o, want) and torch.equal(z, z2)
