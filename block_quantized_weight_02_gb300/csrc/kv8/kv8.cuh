@@ -44,7 +44,7 @@ struct AttnArgs {
     int64_t window;
     float scale;
     void* ws;
-    int stall;             // test only: copies are left out, so that a wait runs out
+    int stall;             // test only: copies are left out (few rows: all; else all but a CTA's first tile), so that a wait runs out
 };
 
 cudaError_t launch_write(const Cache& c, const Batch& b, int D, const void* K, const void* V, int xt, int64_t ldk,

@@ -56,8 +56,8 @@ struct Smem {
     static constexpr int QT = NR * D * 2;         // queries: D/64 chunks of [32 rows][128 B], swizzled
     static constexpr int HT = TN * D * 2, RT = TN * D, PT_BYTES = TN * NR * 2;
     static constexpr int H = 0, R = H + HS * HT, P = R + RS * RT, Q = P + PBUF * PT * PT_BYTES, BARS = Q + QT;
-    static constexpr int NBAR = 2 * RS + 2 * HS + SS + 9;
-    static constexpr int SC = BARS + NBAR * 8 + 8, ROWS = SC + SS * NB * 8, END = ROWS + (int)sizeof(Rows) + 16;
+    static constexpr int NBAR = 2 * RS + 2 * HS + SS + 10;
+    static constexpr int SC = BARS + NBAR * 8, ROWS = SC + SS * NB * 8, END = ROWS + (int)sizeof(Rows) + 16;
     static_assert(Q % 1024 == 0 && SC % 16 == 0 && ROWS % 16 == 0, "alignment");
 };
 
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
     const uint32_t sb = smem_u32(smem), raw_full = sb + M::BARS, raw_empty = raw_full + 8 * M::RS,
                    h_full = raw_empty + 8 * M::RS, h_empty = h_full + 8 * HS, sc_full = h_empty + 8 * HS,
                    q_ready = sc_full + 8 * SS, s_full = q_ready + 8, p_ready = s_full + 16, decided = p_ready + 16,
-                   pv_done = decided + 16, o_full = pv_done + 8;
+                   pv_done = decided + 16, o_full = pv_done + 8, drain = o_full + 8;
     float2* scales = reinterpret_cast<float2*>(smem + M::SC);
     Rows* rows = reinterpret_cast<Rows*>(smem + M::ROWS);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + M::END - 16);
@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
         mbar_init(q_ready, 4);
         mbar_init(pv_done, 1);
         mbar_init(o_full, 1);
+        mbar_init(drain, 1);
         tmem_slot[1] = tmem_slot[2] = 0;
         fence_mbar_init();
     }
@@ -488,8 +489,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                 k0 += 2 * n;
             }
             if (!alive) {      // let the products in flight end before the tensor memory goes: nothing else waits for this
-                if (elect_one()) tc_commit(q_ready);
-                wait_bar(q_ready, parts & 1, 10000000, never);
+                if (elect_one()) tc_commit(drain);
+                wait_bar(drain, 0, 10000000, never);
             }
             __syncwarp();
         } else if (warp == LOAD_WARP) {

@@ -61,7 +61,7 @@ struct Smem {
     static constexpr int HT = TN * D * 2;         // an fp16 operand tile, the same
     static constexpr int RT = TN * D;             // codes
     static constexpr int Q = 0, H = TILES * QT, R = H + HS * HT, MISC = R + RS * RT;
-    static constexpr int NBAR = 2 * RS + 2 * HS + SS + 11;
+    static constexpr int NBAR = 2 * RS + 2 * HS + SS + 13;
     static constexpr int SC = MISC + NBAR * 8;    // float2 [SS][NB]
     static constexpr int END = SC + SS * NB * 8 + 16;
 };
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
     const uint32_t sb = smem_u32(smem), raw_full = sb + M::MISC, raw_empty = raw_full + 8 * M::RS,
                    h_full = raw_empty + 8 * M::RS, h_empty = h_full + 8 * HS, sc_full = h_empty + 8 * HS,
                    q_ready = sc_full + 8 * SS, s_full = q_ready + 16, p_ready = s_full + 16, o_full = p_ready + 16,
-                   odd_full = o_full + 16, turn = odd_full + 8;
+                   odd_full = o_full + 16, turn = odd_full + 8, drain = turn + 16;
     float2* scales = reinterpret_cast<float2*>(smem + M::SC);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + M::SC + SS * NB * 8);
     volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -128,6 +128,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
             mbar_init(p_ready + 8 * i, 4);
             mbar_init(o_full + 8 * i, 1);
             mbar_init(turn + 8 * i, 1);
+            mbar_init(drain + 8 * i, 1);
         }
         mbar_init(odd_full, 4);
         for (int i = 0; i < M::RS; ++i) {
@@ -656,8 +657,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                 k0 += 2 * n;
             }
             if (!alive) {      // let the products in flight end before the tensor memory goes: nothing else waits for this
-                if (elect_one()) tc_commit(q_ready + 8 * x);
-                wait_bar(q_ready + 8 * x, parts & 1, 10000000, never);
+                if (elect_one()) tc_commit(drain + 8 * x);
+                wait_bar(drain + 8 * x, 0, 10000000, never);
             }
             __syncwarp();
         } else if (warp == LOAD_WARP) {

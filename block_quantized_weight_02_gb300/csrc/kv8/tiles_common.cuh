@@ -247,9 +247,10 @@ __device__ __forceinline__ void load_codes(const AttnArgs& a, const List* list, 
                 for (int z = 0; z < 2 && alive; ++z, ++k) {
                     const uint32_t rs = k % RS, bar = raw_full + 8 * rs;
                     if (!wait(raw_empty + 8 * rs, (k / RS & 1) ^ 1)) break;
-                    if (lane == 0) mbar_arrive_expect_tx(bar, blocks * BLK * D);
+                    const bool issue = !a.stall || k == 0;
+                    if (lane == 0 && issue) mbar_arrive_expect_tx(bar, blocks * BLK * D);
                     __syncwarp();
-                    if (have) tma_load_2d(ring + rs * (TN * D) + lane % NB * BLK * D, &maps.t[z], bar, 0, row);
+                    if (have && issue) tma_load_2d(ring + rs * (TN * D) + lane % NB * BLK * D, &maps.t[z], bar, 0, row);
                 }
                 if (!alive) break;
                 if (me) scales[tile % SS * NB + lane % NB] = s;

@@ -325,7 +325,7 @@ typedef enum {
     CQ_OPT_SMALL_T_MAX = 0,  /* largest T served by the weight-streaming path (default 32, max 32) */
     CQ_OPT_FORCE_PATH = 1,   /* 0 auto, 1 weight-streaming, 2 tensor-memory (tcgen05) path */
     CQ_OPT_WAIT_NS = 2,      /* time limit of every device pipeline wait, ns (default 1e9) */
-    CQ_OPT_TEST_STALL = 3,   /* test only: 1 makes the next tcgen05 GEMM's or attention call's loader issue nothing */
+    CQ_OPT_TEST_STALL = 3,   /* test only: 1 makes the next tcgen05 GEMM's or attention call's loaders stop short */
     CQ_OPT_TRACE = 4,        /* 1 prints the chosen path and grid of each call to stderr */
     CQ_OPT_TC_BN = 5,        /* tcgen05 token tile: 0 auto (default), or 32, 64, 128, 192 (CTA pairs only, no K split), 256 */
     CQ_OPT_TC_KSPLIT = 6,    /* tcgen05 K split over a 2-CTA cluster (partials exchanged in shared memory): 0 auto, 1, 2 */

@@ -57,7 +57,7 @@ def test_lengths_up_to_31_bits(n, group):
 
 # ---- waits that run out ------------------------------------------------------------------------------------------
 
-@pytest.mark.parametrize("n,group", FORMS[:1])
+@pytest.mark.parametrize("n,group", FORMS)
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 def test_wait_timeout_reports_status_and_the_next_call_is_right(n, group, out):
     """Copies that never come: the kernel ends by its limit and reports it, and what follows is as if it had not been."""
