@@ -26,8 +26,9 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-// Exponent of a scale (a power of two of at least 2^-64, or NaN).
-__device__ __forceinline__ int exp_of(float s) { return (int)(__float_as_uint(s) >> 23) - 127; }
+// Exponent lv of a value block's scale: a power of two of at least 2^-64 (less, if no token was ever written: codes are 0
+// then), or NaN (whose scores are NaN).
+__device__ __forceinline__ int value_exp(float s) { return s == s ? max((int)(__float_as_uint(s) >> 23) - 127, -64) : -64; }
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
@@ -75,7 +76,20 @@ __device__ __forceinline__ int row_lo(int i, int n, int L, int64_t window) {
     return window ? (int)max((int64_t)0, (int64_t)(L - n + i) - window + 1) : 0;
 }
 
-// An unfinished result: O before the division, the maximum (log2 units) and the sum of each row.
+// The softmax's maximum is not taken over the scores s (log2 units) but over z = s + lv, the log2 of what a token's weight
+// times its value block's scale comes to: m = max z, p = 2^(z - m) multiplies the codes, and the normaliser takes
+// 2^(s - m) = p 2^-lv.  So the fp16 weights are fine where the result is large, whatever the scales of the blocks are, and a
+// block that a row does not see, or sees under scores that leave it no weight, does not enter.  It costs nothing: lv is the
+// addend of the multiplication that makes s.
+//
+// In f32 p is 0 below 2^-126, where p 2^-lv may still count if lv is far below that of the maximum (zeros beside values of
+// 2^30 and more).  A block whose exponent is more than FAR below the largest so far, which is always more than the weights
+// need, gets its part of the normaliser from exponentials of its own.
+constexpr int FAR = 80;
+// A normaliser may be large where the factor 2^d that lowers it is too small for f32: it is lowered by the root, twice.
+__device__ __forceinline__ float root_of(float d) { return ex2(0.5f * d); }
+
+// An unfinished result: O before the division, the maximum (of z) and the normaliser of each row.
 template <int D, int R>
 struct PartOf {
     float m[R], l[R];
@@ -118,8 +132,8 @@ __device__ __forceinline__ void join(const AttnArgs& a, int q0, int h, int f, in
         float top = m;
 #pragma unroll
         for (int j = 0; j < AT; ++j) top = fmaxf(top, pm[j]);
-        const float keep = m == -INFINITY ? 0.f : ex2(m - top);
-        l *= keep;
+        const float kr = m == -INFINITY ? 0.f : root_of(m - top), keep = kr * kr;
+        l = l * kr * kr;
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
             o[q].x *= keep;
@@ -130,8 +144,8 @@ __device__ __forceinline__ void join(const AttnArgs& a, int q0, int h, int f, in
 #pragma unroll
         for (int j = 0; j < AT; ++j) {
             if (pm[j] == -INFINITY && pl[j] == 0.f) continue;    // saw nothing
-            const float w = pm[j] == -INFINITY ? 1.f : ex2(pm[j] - top);   // -inf with a sum: NaN scores
-            l = fmaf(pl[j], w, l);
+            const float wr = pm[j] == -INFINITY ? 1.f : root_of(pm[j] - top), w = wr * wr;   // -inf with a sum: NaN scores
+            l = fmaf(pl[j] * wr, wr, l);
 #pragma unroll
             for (int q = 0; q < NQ; ++q) {
                 o[q].x = fmaf(v[j][q].x, w, o[q].x);

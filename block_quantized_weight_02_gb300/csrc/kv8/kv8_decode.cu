@@ -27,9 +27,9 @@
 // under the copies' swizzle.
 //
 // A key block's scale multiplies the scores in f32.  A value block's scale 2^lv joins the
-// exponent, w = 2^(s - m + 15 + lv - ref) with ref the largest lv so far, so the weights
-// fill fp16's range (11 bits down to 2^-29 of the largest weight) whatever the scales are;
-// the normaliser takes w 2^(ref - lv).
+// exponent, w = 2^(s + lv - m + 15) with m the row's largest s + lv, so the weights fill
+// fp16's range (11 bits down to 2^-29 of the largest) whatever the scales are; the
+// normaliser takes w 2^-lv.
 //
 // Shares that do not hold a whole (sequence, head) leave (O, m, l) partials; the CTA's own
 // are joined after a barrier, those across CTAs by a second small kernel, always in share
@@ -365,15 +365,12 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
                 acc.m[n][0] = acc.m[n][1] = -INFINITY;
                 acc.l[n][0] = acc.l[n][1] = 0.f;
             }
-            int ref = -64;                        // largest value-scale exponent so far
+            int hi = -64;                         // largest value exponent so far, seen or not
 
             for (int i = from; i < until && s.L > 0; ++i) {
-                // one answer for the warp: what follows takes all its lanes
+                // one answer for the warp, as what follows takes all its lanes: it joins the vote on the maxima, and
+                // what is computed until then from a block that did not come is dropped
                 const bool here = wait_bar(smem_u32(&bars[warp][stage]), parity, wait_ns, &stop);
-                if (!__all_sync(0xffffffffu, here)) {
-                    alive = false;
-                    break;
-                }
                 const uint32_t kt = ring0 + stage * 2 * R::TILE, vt = kt + R::TILE;
                 const float2 bs = scales[warp][stage];
                 const int tok0 = (s.first + i) * BLK;
@@ -412,11 +409,13 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
                             }
                         }
                     }
-                // scores in log2 units; a value scale of NaN spoils them like a key scale of NaN
+                // z = score in log2 units + value exponent; a value scale of NaN spoils it like a key scale of NaN
                 const float ks = bs.y == bs.y ? bs.x : bs.y;
+                const int lv = value_exp(bs.y);
+                hi = max(hi, lv);
                 const bool masked = tok0 < free_lo || tok0 + BLK > free_hi;
                 float mx[NT][2];
-                bool grows = false;
+                bool grows = !here;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -432,7 +431,7 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             float& y = x[n][e >> 1][2 * (e & 1) + k];
-                            y = __fmul_rn(y, f);      // rounded as for the maximum: a fused step would leave a huge score's rounding
+                            y = fmaf(y, f, (float)lv);
                             if (masked) {
                                 const int tok = tok0 + 8 * e + g;
                                 if (tok < lo || tok >= hi) y = -INFINITY;
@@ -445,38 +444,46 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
                         mx[n][k] = m;
                         grows |= m > acc.m[n][k];
                     }
-                const int lv0 = bs.y == bs.y ? exp_of(bs.y) : ref;
-                if (__any_sync(0xffffffffu, grows) || lv0 > ref) {
-                    const int nref = max(ref, lv0);
-                    const float rf = pow2i(max(ref - nref, -126));
-                    ref = nref;
+                if (__any_sync(0xffffffffu, grows)) {
+                    if (!__all_sync(0xffffffffu, here)) {
+                        alive = false;
+                        break;
+                    }
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const float f = mx[n][k] > acc.m[n][k] ? ex2(acc.m[n][k] - mx[n][k]) : 1.f;
+                            const float root = mx[n][k] > acc.m[n][k] ? root_of(acc.m[n][k] - mx[n][k]) : 1.f, f = root * root;
                             acc.m[n][k] = mx[n][k];
-                            acc.l[n][k] *= f;
+                            acc.l[n][k] = acc.l[n][k] * root * root;
 #pragma unroll
                             for (int i2 = 0; i2 < D / 16; ++i2) {
-                                acc.o[n][i2][k] *= f * rf;
-                                acc.o[n][i2][2 + k] *= f * rf;
+                                acc.o[n][i2][k] *= f;
+                                acc.o[n][i2][2 + k] *= f;
                             }
                         }
                 }
-                const int lv = max(lv0, ref - 64);
-                const float back = pow2i(ref - lv - P_EXP);
+                const bool far = lv < hi - FAR;
+                const float back = far ? 0.f : pow2i(-lv);
+                if (far)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                acc.l[n][k] += ex2((x[n][e >> 1][2 * (e & 1) + k] - (acc.m[n][k] == -INFINITY ? 0.f : acc.m[n][k])) + (float)(P_EXP - lv));
                 uint32_t p[NT][PT][4];            // weights of tokens 8 e + 2 t, + 1, row g
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        const float m0 = acc.m[n][k] == -INFINITY ? 0.f : acc.m[n][k], add = (float)(P_EXP + lv - ref);
+                        const float m0 = acc.m[n][k] == -INFINITY ? 0.f : acc.m[n][k];
                         float sum = 0.f;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             float& y = x[n][e >> 1][2 * (e & 1) + k];
-                            y = ex2((y - m0) + add);      // (beside a huge m0 the exponent would be rounded away)
+                            y = ex2((y - m0) + (float)P_EXP);      // (beside a huge m0 the exponent would be rounded away)
                             sum += y;
                         }
                         acc.l[n][k] = fmaf(sum, back, acc.l[n][k]);
@@ -542,7 +549,7 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
             if (!alive) break;
             // ---- the segment's end, or the share's
             u += until - from;
-            const float un = pow2i(ref - P_EXP);
+            const float un = pow2i(-P_EXP);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -554,6 +561,7 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
                     acc.l[n][k] += __shfl_xor_sync(0xffffffffu, acc.l[n][k], 4);
                     acc.l[n][k] += __shfl_xor_sync(0xffffffffu, acc.l[n][k], 8);
                     acc.l[n][k] += __shfl_xor_sync(0xffffffffu, acc.l[n][k], 16);
+                    acc.l[n][k] *= un;
                 }
             }
             if (from == 0 && until == s.units) {

@@ -40,13 +40,13 @@ struct Space {
 
 // What the softmax groups share of a part.
 struct Rows {
-    float2 rc[NR];                     // score factor; minus the maximum (+inf: nothing seen yet)
+    float2 rc[NR];                     // score factor; minus the maximum of z (+inf: nothing seen yet)
     int2 lim[NR];                      // visible tokens
-    float fac[NR];                     // what the last move of the maxima scaled sums by
+    float fac[NR];                     // the root of what the last move of the maxima scaled sums by
     float wmax[2][4][NR];              // maxima of the warps' tokens
     float sum[8][NR];                  // row sums of the warps
     float m_sum[NR];                   // maxima of the sum in the workspace
-    int ref, moves;                    // largest value exponent so far; moves of (maxima, ref) so far
+    int moves;                         // moves of the maxima so far
 };
 
 template <int D, int PT>
@@ -57,7 +57,7 @@ struct Smem {
     static constexpr int HT = TN * D * 2, RT = TN * D, PT_BYTES = TN * NR * 2;
     static constexpr int H = 0, R = H + HS * HT, P = R + RS * RT, Q = P + PBUF * PT * PT_BYTES, BARS = Q + QT;
     static constexpr int NBAR = 2 * RS + 2 * HS + SS + 10;
-    static constexpr int SC = BARS + NBAR * 8, ROWS = SC + SS * NB * 8, END = ROWS + (int)sizeof(Rows) + 16;
+    static constexpr int SC = BARS + NBAR * 8, ROWS = SC + SS * NB * (int)sizeof(Block), END = ROWS + (int)sizeof(Rows) + 16;
     static_assert(Q % 1024 == 0 && SC % 16 == 0 && ROWS % 16 == 0, "alignment");
 };
 
@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                    h_full = raw_empty + 8 * M::RS, h_empty = h_full + 8 * HS, sc_full = h_empty + 8 * HS,
                    q_ready = sc_full + 8 * SS, s_full = q_ready + 8, p_ready = s_full + 16, decided = p_ready + 16,
                    pv_done = decided + 16, o_full = pv_done + 8, drain = o_full + 8;
-    float2* scales = reinterpret_cast<float2*>(smem + M::SC);
+    Block* scales = reinterpret_cast<Block*>(smem + M::SC);
     Rows* rows = reinterpret_cast<Rows*>(smem + M::ROWS);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + M::END - 16);
     volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -225,13 +225,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                     *reinterpret_cast<uint4*>(smem + M::Q + (ch >> 3) * (NR * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v[c];
                 }
                 if (qd == 0) {
-                    rows->rc[r] = make_float2(qf, in ? INFINITY : 0.f);
+                    rows->rc[r] = make_float2(qf, in ? INFINITY : -INFINITY);     // (no row: no weights)
                     rows->lim[r] = in ? make_int2(row_lo(f / G, nq, L, a.window), row_hi(f / G, nq, L, a.causal)) : make_int2(0, 0);
                 }
-                if (tid == 0) {
-                    rows->ref = -64;
-                    rows->moves = 0;
-                }
+                if (tid == 0) rows->moves = 0;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(q_ready);
@@ -248,13 +245,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
             for (int j = x; j < n; j += 2, ++steps) {
                 const uint32_t tile = tile0 + j;
                 wait_warp(sc_full + 8 * (tile % SS), tile / SS & 1);
-                const float2* sc = scales + tile % SS * NB;
-                int nref = -64;                  // of the step's blocks
-#pragma unroll
-                for (int c = 0; c < NB; ++c) nref = max(nref, sc[c].y == sc[c].y ? exp_of(sc[c].y) : -64);
-                const float2 mine = sc[quarter];     // this warp's 32 tokens are one block
-                const float ks = mine.y == mine.y ? mine.x : mine.y;
-                const int lv = mine.y == mine.y ? exp_of(mine.y) : -64;
+                const Block blk = scales[tile % SS * NB + quarter];   // this warp's 32 tokens are one block
                 const int tok = w.it.tok0 + (w.from + j) * TN + tid;
                 wait_warp(s_full + 8 * x, steps & 1);
                 tc_fence_after();
@@ -269,15 +260,16 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                 if (j > 0) wait_warp(decided + 8 * x, took++ & 1);    // the step before has decided
                 if (moves != rows->moves) {      // and moved the maxima
                     moves = rows->moves;
+#pragma unroll 1
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) l[r] *= rows->fac[r];
+                        for (int r = 0; r < NR; ++r) l[r] *= rows->fac[r];
                 }
-                int ref = rows->ref;
                 const bool fresh = starts_fresh<PT>(j);      // (the even steps' group only)
                 if (PT == 2 && fresh && j > 0) {
                     wait_warp(pv_done, (done0 + j - 1) & 1);
                     tc_fence_after();
-                    const float un = pow2i(ref - (int)W_EXP);
+                    const float un = pow2i(-(int)W_EXP);
 #pragma unroll 1
                     for (int c = 0; c < NR / 16; ++c) {
                         uint32_t y[16];
@@ -300,8 +292,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
 #pragma unroll
                 for (int r = 0; r < NR; r += 2) {
                     const float4 c = *reinterpret_cast<const float4*>(&rows->rc[r]);
-                    s[r] = __fmul_rn(s[r], ks * c.x);            // rounded as for the maximum: a fused step would leave
-                    s[r + 1] = __fmul_rn(s[r + 1], ks * c.z);    // a huge score's rounding
+                    s[r] = fmaf(s[r], blk.k * c.x, blk.lv);            // z, rounded as for the maximum: a fused step on to z - m
+                    s[r + 1] = fmaf(s[r + 1], blk.k * c.z, blk.lv);    // would leave a huge score's rounding
                     if (masked) {
                         const int4 lim = *reinterpret_cast<const int4*>(&rows->lim[r]);
                         if (tok < lim.x || tok >= lim.y) s[r] = -INFINITY;
@@ -309,7 +301,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                     }
                     over = max3(over, s[r] + c.y, s[r + 1] + c.w);
                 }
-                if (any_of(over > GROW || nref > ref || !alive, 1 + x, 128)) {
+                if (any_of(over > GROW || !alive, 1 + x, 128)) {
                     alive = !any_of(!alive, 1 + x, 128);
                     if (!alive) break;
                     // Move the maxima: lane r has row r.
@@ -320,9 +312,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
 #pragma unroll
                     for (int i = 0; i < 4; ++i) top = fmaxf(top, rows->wmax[x][i][lane]);
                     const bool grow = top > m + GROW;
-                    const float nm = grow ? top : m, fac = grow ? ex2(m - nm) : 1.f;
-                    nref = max(nref, ref);
-                    const float fo = fac * pow2i(max(ref - nref, -126));
+                    const float nm = grow ? top : m, fac = grow ? root_of(m - nm) : 1.f, fo = fac * fac;
                     if (!fresh) {                // all products so far are in O^T
                         wait_warp(pv_done, (done0 + j - 1) & 1);
                         tc_fence_after();
@@ -334,21 +324,19 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                         tmem_st_32x32b_x32(to, y);
                         tmem_st_wait();
                     }
+#pragma unroll 1
+                    for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int r = 0; r < NR; ++r) l[r] *= __shfl_sync(0xffffffffu, fac, r);
+                        for (int r = 0; r < NR; ++r) l[r] *= __shfl_sync(0xffffffffu, fac, r);
                     alive = !any_of(!alive, 1 + x, 128);     // all have read the old maxima
                     if (!alive) break;
                     if (quarter == 0) {
                         rows->rc[lane].y = -nm;
                         rows->fac[lane] = fac;
-                        if (lane == 0) {
-                            rows->ref = nref;
-                            rows->moves = moves + 1;
-                        }
+                        if (lane == 0) rows->moves = moves + 1;
                     }
                     any_of(false, 1 + x, 128);
                     ++moves;
-                    ref = nref;
                 }
                 // the maxima come off before the next step may move them
 #pragma unroll
@@ -359,19 +347,25 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                 }
                 __syncwarp();
                 if (j + 1 < n && lane == 0) mbar_arrive(decided + 8 * (1 - x));
-                const int lc = max(lv, ref - 64);
-                const float base = W_EXP + (float)(lc - ref), back = pow2i(ref - lc - (int)W_EXP);
                 uint32_t p[NR / 2], p2[NR / 2];
+                // (a far block's part of the normaliser comes in a round before the weights: a loop, as more code would
+                // push this one out of the instruction cache)
+                float base = blk.far ? W_EXP - blk.lv : W_EXP, back = blk.far ? 1.f : blk.back;
+#pragma unroll 1
+                for (int i = blk.far ? 2 : 1; i > 0; --i) {
 #pragma unroll
-                for (int r = 0; r < NR; r += 2) {
-                    const float y0 = ex2(s[r] + base), y1 = ex2(s[r + 1] + base);
-                    l[r] = fmaf(y0, back, l[r]);
-                    l[r + 1] = fmaf(y1, back, l[r + 1]);
-                    p[r / 2] = pack_f16(y0, y1);
-                    if (PT == 2) {
-                        const float2 h = unpack_f16(p[r / 2]);
-                        p2[r / 2] = pack_f16(y0 - h.x, y1 - h.y);
+                    for (int r = 0; r < NR; r += 2) {
+                        const float y0 = ex2(s[r] + base), y1 = ex2(s[r + 1] + base);
+                        l[r] = fmaf(y0, back, l[r]);
+                        l[r + 1] = fmaf(y1, back, l[r + 1]);
+                        p[r / 2] = pack_f16(y0, y1);
+                        if (PT == 2) {
+                            const float2 h = unpack_f16(p[r / 2]);
+                            p2[r / 2] = pack_f16(y0 - h.x, y1 - h.y);
+                        }
                     }
+                    base = W_EXP;
+                    back = 0.f;
                 }
                 if (M::PBUF == 1 && j > 0) wait_warp(pv_done, (done0 + j - 1) & 1);   // (a failure shows at the next meeting)
                 uint8_t* buf = smem + M::P + (M::PBUF == 1 ? 0 : x) * PT * M::PT_BYTES + tid * 64;
@@ -393,15 +387,17 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
             // (a group whose last step came before the other's last move)
             if (any_of(!alive, 3, 256)) break;
             if (moves != rows->moves) {
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int r = 0; r < NR; ++r) l[r] *= rows->fac[r];
+                    for (int r = 0; r < NR; ++r) l[r] *= rows->fac[r];
             }
             rows->sum[x * 4 + quarter][lane] = across<false>(l);
             any_of(false, 3, 256);
             tc_fence_after();
             // O^T: thread = channel; this group's half of the rows
             const bool whole = w.from == 0 && w.until == w.it.steps;
-            const float un = pow2i(rows->ref - (int)W_EXP);
+            const float un = pow2i(-(int)W_EXP);
             // (a loop: what runs once a part should not push the loops of every step out of the instruction cache)
 #pragma unroll 1
             for (int r = 16 * x; r < min(16 * x + 16, nrows); ++r) {
@@ -412,6 +408,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) sum += rows->sum[i][r];
+                sum *= un;
                 const float m = -rows->rc[r].y;
                 float o = __uint_as_float(y) * un;
                 if (PT == 2 && n > FRESH && tid < D) o = fmaf(part->o[r][tid], since(rows->m_sum[r], m), o);

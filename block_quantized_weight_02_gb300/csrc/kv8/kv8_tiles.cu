@@ -14,9 +14,9 @@
 //   warps 4-7, 8-11 softmax of the two tiles, one row a thread; queries in, outputs out
 //   warps 12-15     codes -> fp16 (exactly), into the 128-byte-swizzled operand tiles
 // A key block's scale joins the scores in f32, a value block's scale 2^lv the exponent:
-// w = 2^(s - m + 10 + lv - ref), with m at most 5 below the row's maximum (O is only rescaled
-// when the maximum has grown by more) and ref the largest lv so far; the normaliser takes
-// w 2^(ref - lv).  For f32 outputs P goes in two fp16 terms, two products each.
+// w = 2^(s + lv - m + 10), with m at most 5 below the row's largest s + lv (O is only rescaled
+// when that has grown by more); the normaliser takes w 2^-lv.  For f32 outputs P goes in two
+// fp16 terms, two products each.
 //
 // The work is the list of all (row tile, KV head, step), cut into one equal share per SM.  A
 // first small kernel lays the list out (only the device knows the lengths), a third joins the
@@ -62,19 +62,10 @@ struct Smem {
     static constexpr int RT = TN * D;             // codes
     static constexpr int Q = 0, H = TILES * QT, R = H + HS * HT, MISC = R + RS * RT;
     static constexpr int NBAR = 2 * RS + 2 * HS + SS + 13;
-    static constexpr int SC = MISC + NBAR * 8;    // float2 [SS][NB]
-    static constexpr int END = SC + SS * NB * 8 + 16;
+    static constexpr int SC = (MISC + NBAR * 8 + 15) / 16 * 16;   // Block [SS][NB]
+    static constexpr int END = SC + SS * NB * (int)sizeof(Block) + 16;
 };
 
-// A block's factor from products to scores in log2 units (NaN if either scale is) and its value exponent.
-struct Scale {
-    float k;
-    int lv;
-};
-__device__ __forceinline__ Scale scale_of(float2 s, float qf) {
-    const bool nan = s.y != s.y;
-    return {qf * (nan ? s.y : s.x), nan ? -64 : exp_of(s.y)};
-}
 // Two floats in one register pair: one instruction for both.
 __device__ __forceinline__ uint64_t pair(float a, float b) {
     uint64_t r;
@@ -115,8 +106,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                    h_full = raw_empty + 8 * M::RS, h_empty = h_full + 8 * HS, sc_full = h_empty + 8 * HS,
                    q_ready = sc_full + 8 * SS, s_full = q_ready + 16, p_ready = s_full + 16, o_full = p_ready + 16,
                    odd_full = o_full + 16, turn = odd_full + 8, drain = turn + 16;
-    float2* scales = reinterpret_cast<float2*>(smem + M::SC);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + M::SC + SS * NB * 8);
+    Block* scales = reinterpret_cast<Block*>(smem + M::SC);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + M::END - 16);
     volatile int* stop = reinterpret_cast<volatile int*>(tmem_slot + 1);
     const volatile int* never = reinterpret_cast<const volatile int*>(tmem_slot + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -297,8 +288,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
             // steps inside [free_lo, free_hi) need no mask in this warp (rows past the item's take no part)
             const int free_hi = u0.wf <= u0.wl ? row_hi(u0.wf / G, u0.nq, u0.L, a.causal) : INT32_MAX;
             const int free_lo = u0.wf <= u0.wl ? row_lo(u0.wl / G, u0.nq, u0.L, a.window) : 0;
-            float m = -INFINITY, l = 0.f;
-            int ref = -64;
+            float m = -INFINITY, l = 0.f;    // of z; the normaliser (with the weights' 2^10)
             // this tile's partial, and its sum in the meantime: against the maximum m_sum
             Part<D, TILES>* part = TILES == 1 && x == 1 ? &sp->odd[blockIdx.x] : &sp->cta[blockIdx.x][w.from == 0 ? 1 : 0];
             float m_sum = -INFINITY;
@@ -310,17 +300,17 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                 if (j == 0 && !wait_warp(s_full + 8 * x, steps & 1)) break;
                 if (!wait_warp(sc_full + 8 * (tile % SS), tile / SS & 1)) break;
                 const int t0 = w.it.tok0 + (w.from + (int)(tile - tile0)) * TN;
-                const float2* sc = scales + tile % SS * NB;
-                int nref = ref;
+                const Block* sc = scales + tile % SS * NB;
                 uint32_t odd_k = 0;          // blocks whose factor is no positive number: their scores are taken in full below
+                bool far = false;
 #pragma unroll
                 for (int c = 0; c < NB; ++c) {
-                    const Scale k = scale_of(sc[c], qf);
-                    nref = max(nref, k.lv);
-                    if (!(k.k > 0.f && k.k < INFINITY)) odd_k |= 1u << c;
+                    const float k = qf * sc[c].k;
+                    if (!(k > 0.f && k < INFINITY)) odd_k |= 1u << c;
+                    far |= sc[c].far;
                 }
                 const bool prep = __any_sync(0xffffffffu, t0 < free_lo || t0 + TN > free_hi || odd_k != 0);
-                bool again = PT == 2 || nref != ref || __any_sync(0xffffffffu, !(fabsf(m) <= 1048576.f));
+                bool again = PT == 2 || far || __any_sync(0xffffffffu, !(fabsf(m) <= 1048576.f));
                 if (j > 0 && !wait_warp(s_full + 8 * x, steps & 1)) break;
                 if (u0.wl < u0.wf) {         // no rows: whatever lies there as weights only meets its own rows
                     if (lane == 0) mbar_arrive(p_ready + 8 * x);
@@ -329,7 +319,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                 tc_fence_after();
                 const bool fresh = starts_fresh<PT>(j);
                 if (PT == 2 && fresh && j > 0) {        // the scores came after all products so far
-                    const float un = pow2i(ref - (int)W_EXP), keep = since(m_sum, m);
+                    const float un = pow2i(-(int)W_EXP), keep = since(m_sum, m);
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t y[32];
@@ -349,18 +339,19 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                     m_sum = m;
                     summed = true;
                 }
-                // Scores that a row does not see become -inf.  Blocks with an odd factor are multiplied here; `off` is taken off.
-                auto prepare = [&](uint32_t full, float off) {
+                // Scores that a row does not see become -inf.  Blocks with an odd factor are multiplied here; or all become z - m.
+                auto prepare = [&](uint32_t full, bool less, float off) {
 #pragma unroll 1
                     for (int c = 0; c < TN / 16; ++c) {
                         uint32_t y[16];
                         tmem_ld_32x32b_x16(tm_s(x) + lanes + 16 * c, y);
                         tmem_ld_wait();
-                        const float k = full >> (c >> 1) & 1 ? scale_of(sc[c >> 1], qf).k : 1.f;
+                        const float k = full >> (c >> 1) & 1 ? qf * sc[c >> 1].k : 1.f;
+                        const float lv = less ? sc[c >> 1].lv : 0.f;
                         const int lo = rlo - t0 - 16 * c, hi = rhi - t0 - 16 * c;
 #pragma unroll
                         for (int e = 0; e < 16; ++e)
-                            y[e] = e >= lo && e < hi ? __float_as_uint(__fmul_rn(__uint_as_float(y[e]), k) - off) : 0xFF800000u;
+                            y[e] = e >= lo && e < hi ? __float_as_uint(fmaf(__uint_as_float(y[e]), k, lv) - off) : 0xFF800000u;
                         tmem_st_32x32b_x16(tm_s(x) + lanes + 16 * c, y);
                     }
                     tmem_st_wait();
@@ -369,7 +360,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                 if (prep) {
                     // one choice of blocks for the warp: a factor that is odd in one row is taken in full in all
                     full = __reduce_or_sync(0xffffffffu, odd_k);
-                    prepare(full, 0.f);
+                    prepare(full, false, 0.f);
                 }
                 bool less = false;           // m has been taken off
                 // One pass: weights against the m so far, kept in registers until the step's maximum is known.  Where
@@ -386,15 +377,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                             float mx = -INFINITY;
 #pragma unroll
                             for (int e = 0; e < 32; e += 2) mx = max3(mx, __uint_as_float(y[e]), __uint_as_float(y[e + 1]));
-                            top = fmaxf(top, full >> c & 1 ? mx : mx * scale_of(sc[c], qf).k);
+                            top = fmaxf(top, fmaf(mx, full >> c & 1 ? 1.f : qf * sc[c].k, sc[c].lv));
                         }
                         const bool grow = top > m + GROW;
-                        if (__any_sync(0xffffffffu, grow) || nref > ref) {
-                            const float nm = grow ? top : m;
-                            const float fm = grow ? ex2(m - nm) : 1.f, fo = fm * pow2i(max(ref - nref, -126));
-                            m = nm;
-                            l *= fm;
-                            ref = nref;
+                        if (__any_sync(0xffffffffu, grow)) {
+                            const float root = grow ? root_of(m - top) : 1.f, fo = root * root;
+                            m = grow ? top : m;
+                            l = l * root * root;
                             if (!fresh) {
 #pragma unroll 1
                                 for (int c = 0; c < D / 32; ++c) {
@@ -407,12 +396,26 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                                 }
                             }
                         }
-                        // From 2^20 on scores are rounded before m is taken off, as they were for m, and the exponent is
-                        // added after that: a fused step would leave their own rounding, which is then no longer small.
+                        // From 2^20 on z is rounded before m is taken off, as it was for m, and the exponent is
+                        // added after that: a fused step would leave its own rounding, which is then no longer small.
                         if (__any_sync(0xffffffffu, fabsf(m) > 1048576.f && m != -INFINITY)) {
-                            prepare(~full & ((1u << NB) - 1), m == -INFINITY ? 0.f : m);
+                            prepare(~full & ((1u << NB) - 1), true, m == -INFINITY ? 0.f : m);
                             full = (1u << NB) - 1;
                             less = true;
+                        }
+                        if (far) {           // m is settled: their part of the normaliser
+#pragma unroll 1
+                            for (int c = 0; c < TN / 16; ++c) {
+                                const Block b = sc[c >> 1];
+                                if (!b.far) continue;
+                                uint32_t y[16];
+                                tmem_ld_32x32b_x16(tm_s(x) + lanes + 16 * c, y);
+                                tmem_ld_wait();
+                                const float kc = full >> (c >> 1) & 1 ? 1.f : qf * b.k;
+                                const float sub = W_EXP - (less ? b.lv : m == -INFINITY ? 0.f : m);
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) l += ex2(fmaf(__uint_as_float(y[e]), kc, sub));
+                            }
                         }
                     }
                     const float m0 = less || m == -INFINITY ? 0.f : m;
@@ -423,10 +426,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                     for (int c = 0; c < NB; ++c) {
                         tmem_ld_wait();
                         if (c + 1 < NB) tmem_ld_32x32b_x32(tm_s(x) + lanes + 32 * (c + 1), s[(c + 1) & 1]);
-                        const Scale k = scale_of(sc[c], qf);
-                        const float kc = full >> c & 1 ? 1.f : k.k;
-                        const int lc = max(k.lv, ref - 64);
-                        const float sub = W_EXP + (float)(lc - ref) - m0;
+                        const Block b = sc[c];
+                        const float kc = full >> c & 1 ? 1.f : qf * b.k;
+                        const float sub = W_EXP + (less ? 0.f : b.lv - m0);
                         const uint64_t k2 = pair(kc, kc), sub2 = pair(sub, sub);
                         const uint32_t(&y)[32] = s[c & 1];
                         uint32_t(&pc)[16] = p[PT == 1 ? c : 0];
@@ -439,9 +441,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                             const float2 z = unpair(fma2(pair(a0, a1), k2, sub2));
                             weights<PT>(ex2(z.x), ex2(z.y), sum, pc[e], p2[e]);
                         }
-                        top = fmaxf(top, mx * kc);
+                        top = fmaxf(top, fmaf(mx, kc, b.lv));
                         const float2 z = unpair(sum);
-                        add = fmaf(z.x + z.y, pow2i(ref - lc - (int)W_EXP), add);
+                        add = fmaf(z.x + z.y, b.back, add);
                         if (PT == 2) {
                             tmem_st_32x32b_x16(tm_s(x) + lanes + 32 * c, pc);
                             tmem_st_32x32b_x16(tm_s(x) + lanes + 32 * c + 16, p2);
@@ -471,7 +473,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
             ++parts;
             tc_fence_after();
             const bool begins = cur.from == 0, ends = cur.until == cur.it.steps, whole = begins && ends;
-            const float un = pow2i(ref - (int)W_EXP);
+            const float un = pow2i(-(int)W_EXP);
+            l *= un;
             // TILES 1: the odd steps' result goes to the even steps' threads
             Part<D, TILES>* odd = &sp->odd[TILES == 1 ? blockIdx.x : 0];
             const bool both = TILES == 1 && n > 1;
@@ -480,11 +483,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                 if (!wait_warp(odd_full, odds++ & 1)) break;
                 if (u0.in) {
                     const float m1 = odd->m[u0.r], l1 = odd->l[u0.r], top = fmaxf(m, m1);
-                    const float e0 = m == -INFINITY ? 1.f : ex2(m - top), e1 = m1 == -INFINITY ? 1.f : ex2(m1 - top);
-                    w0 = un * e0;
-                    ws *= e0;
-                    w1 = e1;
-                    l = l * e0 + l1 * e1;
+                    const float r0 = m == -INFINITY ? 1.f : root_of(m - top), r1 = m1 == -INFINITY ? 1.f : root_of(m1 - top);
+                    w0 = un * r0 * r0;
+                    ws = ws * r0 * r0;
+                    w1 = r1 * r1;
+                    l = l * r0 * r0 + l1 * r1 * r1;
                     m = top;
                 }
             }

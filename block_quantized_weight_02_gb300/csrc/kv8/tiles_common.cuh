@@ -29,6 +29,14 @@ template <int PT>
 __device__ __forceinline__ bool starts_fresh(int j) { return PT == 2 ? j % FRESH == 0 : j == 0; }
 constexpr float W_EXP = 10.f, GROW = 5.f;   // weights carry 2^10 and grow by 2^5 before the maximum moves
 
+// What the softmax needs of a block (written by the loading warp, which has the time).
+struct alignas(16) Block {
+    float k;               // the keys' scale (NaN if either scale is)
+    float lv;              // the values' exponent
+    float back;            // 2^-lv, or 0 if far
+    int far;               // lv is more than FAR below the part's largest so far
+};
+
 struct Maps {
     CUtensorMap t[2];                  // keys, values: {D, pages * Hkv * page}, box {D, 32}
 };
@@ -214,7 +222,7 @@ struct Walk {
 // and values in turn; `wait` is a bounded wait with one answer for the warp.
 template <int D, int RS, class W>
 __device__ __forceinline__ void load_codes(const AttnArgs& a, const List* list, Walk w, const Maps& maps, uint32_t ring,
-                                           uint32_t raw_full, uint32_t raw_empty, float2* scales, uint32_t sc_full, W wait,
+                                           uint32_t raw_full, uint32_t raw_empty, Block* scales, uint32_t sc_full, W wait,
                                            const bool& alive) {
     const int lane = threadIdx.x & 31;
     uint32_t k = 0, tile = 0;
@@ -237,9 +245,11 @@ __device__ __forceinline__ void load_codes(const AttnArgs& a, const List* list, 
             }
         };
         look_up(w.from);
+        int hi = -64;                     // largest value exponent of the part up to this batch
         for (int j0 = w.from; j0 < w.until && alive; j0 += LB) {
             const int row = row1;
             const float2 s = s1;
+            Block blk;
             if (j0 + LB < w.until) look_up(j0 + LB);
             for (int i = 0; i < min(LB, w.until - j0) && alive; ++i, ++tile) {
                 const bool me = lane / NB == i, have = me && row >= 0;
@@ -253,7 +263,13 @@ __device__ __forceinline__ void load_codes(const AttnArgs& a, const List* list, 
                     if (have && issue) tma_load_2d(ring + rs * (TN * D) + lane % NB * BLK * D, &maps.t[z], bar, 0, row);
                 }
                 if (!alive) break;
-                if (me) scales[tile % SS * NB + lane % NB] = s;
+                if (i == 0) {                       // of the whole batch (now that the first copies are on their way)
+                    const int lv = value_exp(s.y);
+                    hi = max(hi, __reduce_max_sync(0xffffffffu, lv));
+                    const bool far = row >= 0 && lv < hi - FAR;
+                    blk = {s.y == s.y ? s.x : s.y, (float)lv, far ? 0.f : pow2i(-lv), far};
+                }
+                if (me) scales[tile % SS * NB + lane % NB] = blk;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(sc_full + 8 * (tile % SS));
             }

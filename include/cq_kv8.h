@@ -92,9 +92,10 @@ cq_status cq_kv8_read(const cq_kv8_cache* cache, const int32_t* first, const int
  * T * Hq < 2^31, scale finite and > 0, window >= 0.
  * Arithmetic: products of fp16 operands in f32: queries as given (bf16 queries to
  * fp16 behind a per-row power of two, exact for every value within 2^27 of the
- * row's largest), codes exactly, softmax weights as one fp16 term for 16-bit outputs
- * (11 bits over a range of at least 2^24) and as two for f32 outputs (22 bits);
- * maxima, sums, scores and accumulators in f32; one rounding to yt.  The tensor
+ * row's largest), codes exactly, softmax weights times their value block's scale as
+ * one fp16 term for 16-bit outputs (11 bits) and as two for f32 outputs (22 bits), in
+ * both cases to 2^-35 of the row's largest such product; tokens that a row does not
+ * see, or that have no weight, do not enter, whatever their scale; maxima, sums, scores and accumulators in f32; one rounding to yt.  The tensor
  * cores truncate as they accumulate: f32 outputs lose at most 5e-6 to that, 16-bit
  * ones about 1e-9 a token that one SM takes in turn (6e-5 for 60000).  Results do
  * not depend on timing: the same call gives the same bits.

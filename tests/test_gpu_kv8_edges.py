@@ -79,3 +79,115 @@ def test_wait_timeout_reports_status_and_the_next_call_is_right(n, group, out):
         cq.cq_set_option(cq.CQ_OPT_TEST_STALL, 0)
     _, o, z2 = s.attend([n, n], group, out=out, q=q)
     assert torch.equal(o, want) and torch.equal(z, z2)
+
+
+# ---- values far apart --------------------------------------------------------------------------------------------
+
+def attend(cache, b, q, scale, causal, window, out):
+    """(o, lse, bound of o, bound of lse) of rows q [n][Hq][D], the last of sequence b, in 64 bits.
+
+    The bound, relative to the sum of the weighted values' magnitudes unless said otherwise.  A score: exact products,
+    eight truncated sums and two roundings of at most 2^-23 of the products' magnitudes (`reach`), less than 2^-19 of it,
+    once in the weight and once in the normaliser: 2^-18 reach.  The block's exponent, up to 128 in size, joins it and
+    the maximum comes off: two roundings of at most 2^-18 each, as often: 2^-16.  f32 outputs: weights in two terms
+    2^-22, exponential 2^-21, truncated sums 5e-6: with the exponent's less than 2^-15.  16-bit outputs: weights in one
+    term 2^-11, all else 2^-14.
+    Weights are fp16 numbers against a largest (weight times block scale) of at least 2^10: each is off by up to 2^-25,
+    and meets codes up to 127: tokens * 2^-28 of that largest.  The output rounds once."""
+    n, Hq, D = q.shape
+    k, v, L = cache.values(0, b), cache.values(1, b), len(cache.q[0][b])
+    vs = cache.s[1][b][np.arange(L) // kv8ref.BLOCK]
+    g, o, lse, e = Hq // cache.Hkv, np.zeros((n, Hq, D)), np.full((n, Hq), -np.inf), np.zeros((n, Hq, D))
+    reach = np.zeros((n, Hq))
+    for i in range(n):
+        p = L - n + i
+        lo, hi = (max(0, p - window + 1) if window else 0, p + 1) if causal else (0, L)
+        if hi <= lo:
+            continue
+        for h in range(Hq):
+            kk, vv = k[lo:hi, h // g], v[lo:hi, h // g]
+            s = scale * (kk @ q[i, h])
+            w = np.exp(s - s.max())
+            z = w.sum()
+            w /= z
+            o[i, h], lse[i, h] = w @ vv, s.max() + np.log(z)
+            reach[i, h] = scale * (np.abs(kk) @ np.abs(q[i, h])).max()
+            rel = (2.0 ** -15 if out == "f32" else 2.0 ** -11 + 2.0 ** -14) + 2.0 ** -18 * reach[i, h]
+            e[i, h] = rel * (w @ np.abs(vv)) + (hi - lo) * 2.0 ** -28 * (w * vs[lo:hi, h // g]).max()
+    u = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11, "f32": 2.0 ** -24}[out]
+    e = e + u * np.exp2(np.floor(np.log2(np.abs(o) + e + 1e-300))) + (2.0 ** -25 if out == "f16" else 0.0)
+    return o, lse, e, kv8ref.lse_bound(lse, reach)
+
+
+def check(s, counts, group, out, causal=True, window=0, **kw):
+    q, o, z = s.attend(counts, group, out=out, causal=causal, window=window, **kw)
+    at = 0
+    for b, n in enumerate(counts):
+        if n:
+            ro, rz, eo, ez = attend(s.ref, b, f64(q[at:at + n]), s.D ** -0.5, causal, window, out)
+            err = np.abs(f64(o[at:at + n]) - ro)
+            assert np.all(err <= eo), (b, float(np.nanmax(err / np.maximum(eo, 1e-300))), int((~(err <= eo)).sum()), err.size)
+            gz = f64(z[at:at + n])
+            seen = np.isfinite(rz)
+            assert np.array_equal(np.isneginf(gz), ~seen) and np.all(np.abs(gz[seen] - rz[seen]) <= ez[seen])
+        at += n
+
+
+FAR = [(2, 4), (5, 4), (2, 16), (20, 4), (12, 2), (70, 4), (64, 1), (200, 1)]
+
+
+@pytest.mark.parametrize("n,group", FAR)
+@pytest.mark.parametrize("bits", [20, 40, 70, 110])
+@pytest.mark.parametrize("D,out", [(64, "bf16"), (128, "f32")])
+def test_values_that_a_row_does_not_see(n, group, bits, D, out):
+    """Large values in a block behind a row's position, or ahead of its window, are nothing to it."""
+    s = Setup(54, [400], 1, D, 32)
+    edge = 96
+    v = s.rows(edge + n // 2, 1, "f32", 0.3)
+    v[edge:] *= 2.0 ** bits                         # rows from n / 2 on see this block, those before it do not
+    s.write([len(v)], "f32", k=s.rows(len(v), 1, "f32", 0.3), v=v)
+    check(s, [n], group, out)
+    s = Setup(55, [400], 1, D, 32)
+    v = s.rows(edge + n, 1, "f32", 0.3)
+    v[:32] *= 2.0 ** bits                           # rows before n / 2 see this block, later ones' windows begin behind it
+    s.write([len(v)], "f32", k=s.rows(len(v), 1, "f32", 0.3), v=v)
+    check(s, [n], group, out, window=65 + n // 2)
+
+
+@pytest.mark.parametrize("n,group", [(1, 4)] + FAR)
+@pytest.mark.parametrize("bits", [20, 40, 60])
+@pytest.mark.parametrize("D,out", [(64, "bf16"), (128, "f32")])
+def test_values_without_weight(n, group, bits, D, out):
+    """Large values under scores far below the row's largest count as their weights do: here not at all."""
+    for block in (0, 3, 7):
+        s = Setup(56, [300], 1, D, 64)
+        k, v = s.rows(300, 1, "f32", 0.3), s.rows(300, 1, "f32", 0.3)
+        v[32 * block:32 * block + 32] *= 2.0 ** bits
+        k[:, 0, 7] = 0
+        k[32 * block:32 * block + 32, 0, 7] = -30
+        s.write([300], "f32", k=k, v=v)
+        q = s.rows(n, group, "bf16", 0.3)
+        q[:, :, 7] = 100
+        check(s, [n], group, out, q=q)
+
+
+@pytest.mark.parametrize("n,group", [(1, 1)] + FAR)
+@pytest.mark.parametrize("seed", range(4))
+@pytest.mark.parametrize("D,out", [(64, "f32"), (128, "bf16")])
+def test_values_and_scores_far_apart(n, group, seed, D, out):
+    """Every block of a size of its own, from 2^-60 to 2^60, some zero, and scores of a level of its own."""
+    s = Setup(100 + seed, [700], 1, D, 64)
+    L = 330 + n + 50 * seed
+    k, v = s.rows(L, 1, "f32", 0.3), s.rows(L, 1, "f32", 0.3)
+    blocks = -(-L // 32)
+    size = s.rng.uniform(-60, 60, blocks)
+    level = -s.rng.uniform(0, 90, blocks)           # in units of 2: up to 2^90
+    f = np.where(s.rng.random(blocks) < 0.2, 0.0, 2.0 ** size)
+    at = np.arange(L) // 32
+    v *= torch.from_numpy(f[at]).to(DEV).float()[:, None, None]
+    k[:, 0, 7] = torch.from_numpy(level[at] * np.log(2) * D ** 0.5 / 100).to(DEV).float()
+    s.write([L], "f32", k=k, v=v)
+    q = s.rows(n, group, "bf16", 0.3)
+    q[:, :, 7] = 100
+    for causal, window in ((True, 0), (False, 0), (True, 100)):
+        check(s, [n], group, out, causal, window, q=q)
