@@ -83,9 +83,9 @@ __device__ __forceinline__ int row_lo(int i, int n, int L, int64_t window) {
 // addend of the multiplication that makes s.
 //
 // In f32 p is 0 below 2^-126, where p 2^-lv may still count if lv is far below that of the maximum (zeros beside values of
-// 2^30 and more).  A block whose exponent is more than FAR below the largest so far, which is always more than the weights
+// 2^30 and more).  A block whose exponent is more than APART below the largest so far, which is always more than the weights
 // need, gets its part of the normaliser from exponentials of its own.
-constexpr int FAR = 80;
+constexpr int APART = 80;
 // A normaliser may be large where the factor 2^d that lowers it is too small for f32: it is lowered by the root, twice.
 __device__ __forceinline__ float root_of(float d) { return ex2(0.5f * d); }
 
@@ -96,18 +96,27 @@ struct PartOf {
     float o[R][D];
     __device__ __forceinline__ const float4* quad(int r, int d) const { return reinterpret_cast<const float4*>(&o[r][d]); }
 };
+// What ends a row.  Its normaliser is 0 if it sees no token (O = 0, lse = -inf), and if it sees only scores of -inf, whose
+// softmax is 0 / 0: that one's normaliser becomes NaN.  Rows see a token from `first_seeing` on: of n rows behind fewer
+// tokens the first stand before token 0.
+__device__ __forceinline__ int first_seeing(const AttnArgs& a, int n, int L) {
+    return a.causal ? max(n - L, 0) * (a.Hq / a.c.Hkv) : L > 0 ? 0 : INT32_MAX;
+}
+__device__ __forceinline__ float row_sum(float l, int f, int first) {
+    return l == 0.f && f >= first ? __uint_as_float(0x7FC00000u) : l;
+}
 __device__ __forceinline__ float inv_sum(float l) { return l == 0.f ? 0.f : 1.0f / l; }
 __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
 }
 
 // Joins the partials part(0) .. part(cnt - 1) of KV head h's row f (a (token, head) pair of the sequence whose first
-// tensor row is q0), row r of the partials, NQ x 4 channels from d on: into `out` (nullable), else the output.  AT
-// partials are read at a time; FAR ones come from other CTAs.
+// tensor row is q0; rows from `first` on see a token), row r of the partials, NQ x 4 channels from d on: into `out`
+// (nullable), else the output.  AT partials are read at a time; FAR ones come from other CTAs.
 template <bool FAR, class T>
 __device__ __forceinline__ T part_ld(const T* p) { return FAR ? __ldcg(p) : *p; }
 template <bool FAR, int D, int NQ, int AT, class P, class F>
-__device__ __forceinline__ void join(const AttnArgs& a, int q0, int h, int f, int r, int d, int cnt, F part, P* out) {
+__device__ __forceinline__ void join(const AttnArgs& a, int q0, int first, int h, int f, int r, int d, int cnt, F part, P* out) {
     float m = -INFINITY, l = 0.f;
     float4 o[NQ];
 #pragma unroll
@@ -166,9 +175,10 @@ __device__ __forceinline__ void join(const AttnArgs& a, int q0, int h, int f, in
     } else {
         const int G = a.Hq / a.c.Hkv, row = q0 + f / G, head = h * G + f % G;
         const int64_t at = row * a.ldo + (int64_t)head * D + d;
-        const float n = inv_sum(l);
+        l = row_sum(l, f, first);
+        const float inv = inv_sum(l);
 #pragma unroll
-        for (int q = 0; q < NQ; ++q) store_out4(a.O, at + 4 * q, a.yt, o[q].x * n, o[q].y * n, o[q].z * n, o[q].w * n);
+        for (int q = 0; q < NQ; ++q) store_out4(a.O, at + 4 * q, a.yt, o[q].x * inv, o[q].y * inv, o[q].z * inv, o[q].w * inv);
         if (a.lse && d == 0) a.lse[(int64_t)row * a.Hq + head] = lse_of(m, l);
     }
 }

@@ -152,7 +152,7 @@ __device__ __forceinline__ void write_part(Part<D>* p, const Acc<D, NT>& c, int 
 
 template <int D, int NT>
 __device__ __forceinline__ void write_out(const AttnArgs& a, const Acc<D, NT>& c, const Seq& s, int h) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, G = a.Hq / a.c.Hkv;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, G = a.Hq / a.c.Hkv, first = first_seeing(a, s.n, s.L);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -160,13 +160,13 @@ __device__ __forceinline__ void write_out(const AttnArgs& a, const Acc<D, NT>& c
             const int r = 8 * n + 2 * t + k;
             if (r >= s.n * G) continue;
             const int row = s.q0 + r / G, head = h * G + r % G;
-            const float f = inv_sum(c.l[n][k]);
+            const float l = row_sum(c.l[n][k], r, first), f = inv_sum(l);
             const int64_t at = row * a.ldo + (int64_t)head * D + g * Acc<D, NT>::DL;
 #pragma unroll
             for (int i = 0; i < Acc<D, NT>::DL / 4; ++i)
                 store_out4(a.O, at + 4 * i, a.yt, c.ch(n, k, 4 * i) * f, c.ch(n, k, 4 * i + 1) * f,
                            c.ch(n, k, 4 * i + 2) * f, c.ch(n, k, 4 * i + 3) * f);
-            if (a.lse && g == 0) a.lse[(int64_t)row * a.Hq + head] = lse_of(c.m[n][k], c.l[n][k]);
+            if (a.lse && g == 0) a.lse[(int64_t)row * a.Hq + head] = lse_of(c.m[n][k], l);
         }
 }
 
@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
                             }
                         }
                 }
-                const bool far = lv < hi - FAR;
+                const bool far = lv < hi - APART;
                 const float back = far ? 0.f : pow2i(-lv);
                 if (far)
 #pragma unroll
@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
             left &= left - 1;
             return (const Part<D>*)(w & 1 ? last_part(w >> 1) : &sp->warp[blockIdx.x * NW + (w >> 1)]);
         };
-        join<false, D, 1, 8>(a, s.q0, h, r, r, d, __popc(run), part, begins && ends ? nullptr : &sp->cta[blockIdx.x][begins ? 1 : 0]);
+        join<false, D, 1, 8>(a, s.q0, first_seeing(a, s.n, s.L), h, r, r, d, __popc(run), part, begins && ends ? nullptr : &sp->cta[blockIdx.x][begins ? 1 : 0]);
         if (!(begins && ends) && r == 0 && d == 0) sp->seg[blockIdx.x][begins ? 1 : 0] = seg;
     }
 }
@@ -644,9 +644,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_attn_join(const AttnArgs a) {
     }
     if (seg < 0) return;
     const Seq s = seq_of(a, seg / a.c.Hkv);
-    const int k = blockIdx.y * JOIN_THREADS + threadIdx.x;
-    if (k < s.n * (a.Hq / a.c.Hkv) * (D / 4))
-        join<true, D, 1, 8>(a, s.q0, seg % a.c.Hkv, k / (D / 4), k / (D / 4), k % (D / 4) * 4, cnt,
+    const int k = blockIdx.y * JOIN_THREADS + threadIdx.x, r = k / (D / 4);
+    if (r < s.n * (a.Hq / a.c.Hkv))
+        join<true, D, 1, 8>(a, s.q0, first_seeing(a, s.n, s.L), seg % a.c.Hkv, r, r, k % (D / 4) * 4, cnt,
                             [&](int j) { return j == 0 ? &sp->cta[i][1] : &sp->cta[i + j][0]; }, (Part<D>*)nullptr);
 }
 

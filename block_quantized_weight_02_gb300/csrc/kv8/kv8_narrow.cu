@@ -18,6 +18,8 @@
 // Measured: 25 rows of 8 heads of 128 channels, 24 sequences of 300 to 9000 tokens: 80 us, 2.8 TB/s; f32 outputs 108 us.
 // Bound by a step's chain (scores, vote, weights to shared memory, product), two of which are under way at a time, and by
 // 10 us for the list and the joins.
+#include <cfloat>
+
 #include "tiles_common.cuh"
 
 namespace cq {
@@ -40,7 +42,7 @@ struct Space {
 
 // What the softmax groups share of a part.
 struct Rows {
-    float2 rc[NR];                     // score factor; minus the maximum of z (+inf: nothing seen yet)
+    float2 rc[NR];                     // score factor; minus the maximum of z (FLT_MAX: nothing seen yet, which keeps -inf apart)
     int2 lim[NR];                      // visible tokens
     float fac[NR];                     // the root of what the last move of the maxima scaled sums by
     float wmax[2][4][NR];              // maxima of the warps' tokens
@@ -225,7 +227,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                     *reinterpret_cast<uint4*>(smem + M::Q + (ch >> 3) * (NR * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v[c];
                 }
                 if (qd == 0) {
-                    rows->rc[r] = make_float2(qf, in ? INFINITY : -INFINITY);     // (no row: no weights)
+                    rows->rc[r] = make_float2(qf, in ? FLT_MAX : -INFINITY);     // (no row: no weights)
                     rows->lim[r] = in ? make_int2(row_lo(f / G, nq, L, a.window), row_hi(f / G, nq, L, a.causal)) : make_int2(0, 0);
                 }
                 if (tid == 0) rows->moves = 0;
@@ -342,8 +344,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
 #pragma unroll
                 for (int r = 0; r < NR; r += 2) {
                     const float4 c = *reinterpret_cast<const float4*>(&rows->rc[r]);
-                    s[r] = masked && s[r] == -INFINITY ? s[r] : s[r] + c.y;      // (nothing seen yet: -inf + inf)
-                    s[r + 1] = masked && s[r + 1] == -INFINITY ? s[r + 1] : s[r + 1] + c.w;
+                    s[r] += c.y;
+                    s[r + 1] += c.w;
                 }
                 __syncwarp();
                 if (j + 1 < n && lane == 0) mbar_arrive(decided + 8 * (1 - x));
@@ -413,13 +415,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                 float o = __uint_as_float(y) * un;
                 if (PT == 2 && n > FRESH && tid < D) o = fmaf(part->o[r][tid], since(rows->m_sum[r], m), o);
                 if (whole) {
+                    sum = row_sum(sum, f, first_seeing(a, nq, L));
                     const int64_t row = q0 + f / G, head = w.at.h * G + f % G;
                     if (tid < D) store_out(a.O, row * a.ldo + head * D + tid, a.yt, o * inv_sum(sum));
                     if (tid == 0 && a.lse) a.lse[row * a.Hq + head] = lse_of(m, sum);
                 } else {
                     if (tid < D) part->o[r][tid] = o;
                     if (tid == 0) {
-                        part->m[r] = m;
+                        part->m[r] = sum == 0.f ? -INFINITY : m;
                         part->l[r] = sum;
                     }
                 }
@@ -515,9 +518,9 @@ __global__ void __launch_bounds__(256) k_narrow_join(const AttnArgs a, int ctas)
     const int4 it = __ldcg(reinterpret_cast<const int4*>(&list->item[seg / a.c.Hkv]));
     const int q0 = __ldg(a.b.q_start + it.x), n = __ldg(a.b.q_start + it.x + 1) - q0;
     const int rows = (int)min((int64_t)NR, (int64_t)n * (a.Hq / a.c.Hkv) - it.y);
-    const int k = blockIdx.y * 256 + threadIdx.x;
-    if (k < rows * (D / 4))
-        join<true, D, 1, 8>(a, q0, seg % a.c.Hkv, it.y + k / (D / 4), k / (D / 4), k % (D / 4) * 4, cnt,
+    const int k = blockIdx.y * 256 + threadIdx.x, r = k / (D / 4);
+    if (r < rows)
+        join<true, D, 1, 8>(a, q0, first_seeing(a, n, __ldg(a.b.lens + it.x)), seg % a.c.Hkv, it.y + r, r, k % (D / 4) * 4, cnt,
                             [&](int j) { return j == 0 ? &sp->cta[i][1] : &sp->cta[i + j][0]; }, (Part<D>*)nullptr);
 }
 

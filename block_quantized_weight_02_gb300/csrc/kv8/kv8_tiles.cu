@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                         }
                         // From 2^20 on z is rounded before m is taken off, as it was for m, and the exponent is
                         // added after that: a fused step would leave its own rounding, which is then no longer small.
-                        if (__any_sync(0xffffffffu, fabsf(m) > 1048576.f && m != -INFINITY)) {
+                        if (__any_sync(0xffffffffu, fabsf(m) > 1048576.f && fabsf(m) < INFINITY)) {
                             prepare(~full & ((1u << NB) - 1), true, m == -INFINITY ? 0.f : m);
                             full = (1u << NB) - 1;
                             less = true;
@@ -493,6 +493,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
             }
             const bool direct = whole && !(both && x == 1);
             if (direct) {
+                if (u0.in) l = row_sum(l, u0.f, first_seeing(a, u0.nq, u0.L));
                 const float inv = inv_sum(l);
                 w0 *= inv;
                 ws *= inv;
@@ -692,7 +693,7 @@ __global__ void __launch_bounds__(256) k_tiles_join(const AttnArgs a, int ctas) 
     const int rows = (int)min((int64_t)TILES * TM, (int64_t)n * (a.Hq / a.c.Hkv) - it.y);
     const int r = blockIdx.y * 32 + threadIdx.x % 32;
     if (r < rows)
-        join<true, D, D / 32, 4>(a, q0, seg % a.c.Hkv, it.y + r, r, threadIdx.x / 32 * (D / 8), cnt,
+        join<true, D, D / 32, 4>(a, q0, first_seeing(a, n, __ldg(a.b.lens + it.x)), seg % a.c.Hkv, it.y + r, r, threadIdx.x / 32 * (D / 8), cnt,
                                  [&](int j) { return j == 0 ? &sp->cta[i][1] : &sp->cta[i + j][0]; }, (Part<D, TILES>*)nullptr);
 }
 

@@ -34,7 +34,7 @@ struct alignas(16) Block {
     float k;               // the keys' scale (NaN if either scale is)
     float lv;              // the values' exponent
     float back;            // 2^-lv, or 0 if far
-    int far;               // lv is more than FAR below the part's largest so far
+    int far;               // lv is more than APART below the part's largest so far
 };
 
 struct Maps {
@@ -266,7 +266,7 @@ __device__ __forceinline__ void load_codes(const AttnArgs& a, const List* list, 
                 if (i == 0) {                       // of the whole batch (now that the first copies are on their way)
                     const int lv = value_exp(s.y);
                     hi = max(hi, __reduce_max_sync(0xffffffffu, lv));
-                    const bool far = row >= 0 && lv < hi - FAR;
+                    const bool far = row >= 0 && lv < hi - APART;
                     blk = {s.y == s.y ? s.x : s.y, (float)lv, far ? 0.f : pow2i(-lv), far};
                 }
                 if (me) scales[tile % SS * NB + lane % NB] = blk;

@@ -82,7 +82,8 @@ cq_status cq_kv8_read(const cq_kv8_cache* cache, const int32_t* first, const int
  * stands at position p = lens[b] - n_b + i.  causal = 1: it sees
  * max(0, p - window + 1) .. p (window = 0: from token 0); causal = 0: it sees all
  * lens[b] tokens (window must be 0).  A row that sees nothing gets O = 0 and
- * lse = -inf.  Head h of Q reads head h / (Hq / Hkv) of the cache.
+ * lse = -inf; one whose scores are all -inf, or one of them +inf or NaN, gets NaN.
+ * Head h of Q reads head h / (Hq / Hkv) of the cache.
  * Q: xt fp16 or bf16 [T][Hq][D], row pitch ldq (a multiple of 8, >= Hq * D),
  * 16-byte aligned.  O: yt fp16, bf16 or f32 [T][Hq][D], row pitch ldo (a multiple
  * of 16 bytes), 16-byte aligned.  lse: f32 [T][Hq].

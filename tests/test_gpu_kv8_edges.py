@@ -191,3 +191,49 @@ def test_values_and_scores_far_apart(n, group, seed, D, out):
     q[:, :, 7] = 100
     for causal, window in ((True, 0), (False, 0), (True, 100)):
         check(s, [n], group, out, causal, window, q=q)
+
+
+# ---- scores that are not finite ----------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("n,group", [(1, 1)] + FAR)
+@pytest.mark.parametrize("dtype,out", [("f16", "f16"), ("bf16", "bf16"), ("bf16", "f32")])
+def test_infinite_queries(n, group, dtype, out):
+    """An infinity in a query makes every score of its row -inf, or +inf: NaN either way, not a row that sees nothing, in
+    its own row only.  Short and long contexts, whole and in shares."""
+    for L in (n, 150 + n, 3000 + n):
+        s = Setup(57, [L], 1, 64, 64)
+        k = s.rows(L, 1, "f32", 0.1)
+        k[:, 0, 5] = 3.0
+        s.write([L], "f32", k=k)
+        for causal, window in ((True, 0), (False, 0), (True, 60)):
+            q, o, z = s.attend([n], group, dtype, out, causal, window)
+            assert torch.isfinite(o).all() and torch.isfinite(z).all()
+            for inf in (float("-inf"), float("inf")):
+                bad = q.clone()
+                bad[n // 2, group - 1, 5] = inf
+                _, o2, z2 = s.attend([n], group, dtype, out, causal, window, q=bad)
+                assert torch.isnan(o2[n // 2, group - 1]).all() and torch.isnan(z2[n // 2, group - 1])
+                keep = torch.ones(n, group, dtype=torch.bool, device=DEV)
+                keep[n // 2, group - 1] = False
+                assert torch.equal(o2[keep], o[keep]) and torch.equal(z2[keep], z[keep])
+
+
+@pytest.mark.parametrize("n,group", [(1, 1)] + FAR)
+@pytest.mark.parametrize("block", [0, 2, 40])
+def test_some_scores_overflow(n, group, block):
+    """Scores below f32's range in one block weigh nothing; the row is the mean of what it sees besides."""
+    L = 1400
+    s = Setup(58, [L + n], 1, 64, 64)
+    k, v = torch.zeros(L + n, 1, 64, device=DEV), s.rows(L + n, 1, "f32", 0.3)
+    k[32 * block:32 * block + 32, 0, 5] = 1e30
+    s.write([L + n], "f32", k=k, v=v)
+    q = torch.zeros(n, group, 64, device=DEV, dtype=torch.bfloat16)
+    q[:, :, 5] = -1e38
+    _, o, z = s.attend([n], group, q=q)
+    values = s.ref.values(1, 0)[:, 0]
+    for i in range(n):
+        seen = np.arange(L + i + 1)
+        seen = seen[seen // 32 != block]
+        want, mass = values[seen].mean(0), np.abs(values[seen]).mean(0)
+        assert np.all(np.abs(f64(o[i]) - want) <= 2.0 ** -15 * mass)
+        assert np.all(np.abs(f64(z[i]) - np.log(len(seen))) <= 2.0 ** -14)
