@@ -60,7 +60,8 @@ size_t narrow_workspace(int64_t T, int64_t G, int64_t D, int64_t B);
 cudaError_t launch_narrow(const AttnArgs& a, cudaStream_t s);
 size_t tiles_workspace(int64_t T, int64_t G, int64_t D, int64_t B, int64_t max_q);
 cudaError_t launch_tiles(const AttnArgs& a, cudaStream_t s);
-size_t attn_workspace(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q);
+size_t attn_workspace(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q);        // of a call
+size_t attn_workspace_upto(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q);   // and of any smaller one
 
 template <class... KArgs, class... Args>
 cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args... args) {

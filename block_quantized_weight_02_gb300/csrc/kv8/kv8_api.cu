@@ -111,7 +111,7 @@ cq_status cq_kv8_read(const cq_kv8_cache* cache, const int32_t* first, const int
 
 size_t cq_attn_kv8_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q) {
     if (T < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv || D < 1 || B < 1 || max_q < 1) return 0;
-    return attn_workspace(T, Hq, Hkv, D, B, max_q);
+    return attn_workspace_upto(T, Hq, Hkv, D, B, max_q);
 }
 
 cq_status cq_attn_kv8(const void* Q, int xt, int64_t T, int64_t Hq, int64_t ldq, const cq_kv8_cache* cache,

@@ -16,6 +16,15 @@ size_t attn_workspace(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, 
     return narrow_serves(rows) ? narrow_workspace(T, G, D, B) : tiles_workspace(T, G, D, B, std::min(max_q, T));
 }
 
+// A batch with fewer rows a sequence may go to another kernel, whose partials are larger: what serves max_q is what any
+// smaller one takes too (each kernel's own need grows with T, B and max_q).
+size_t attn_workspace_upto(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q) {
+    const int64_t G = Hq / Hkv, rows = std::min(max_q, T) * G;
+    size_t n = attn_workspace(T, Hq, Hkv, D, B, max_q);
+    for (int64_t q = 1; q * G <= 128 && q * G <= rows; ++q) n = std::max(n, attn_workspace(T, Hq, Hkv, D, B, q));
+    return n;
+}
+
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s) {
     const int64_t rows = (int64_t)a.max_q * (a.Hq / a.c.Hkv);
     return decode_serves(rows) ? launch_decode(a, s) : narrow_serves(rows) ? launch_narrow(a, s) : launch_tiles(a, s);

@@ -100,7 +100,8 @@ cq_status cq_kv8_read(const cq_kv8_cache* cache, const int32_t* first, const int
  * cores truncate as they accumulate: f32 outputs lose at most 5e-6 to that, 16-bit
  * ones about 1e-9 a token that one SM takes in turn (6e-5 for 60000).  Results do
  * not depend on timing: the same call gives the same bits.
- * Workspace: cq_attn_kv8_workspace_bytes(...) bytes, 256-byte aligned.
+ * Workspace: cq_attn_kv8_workspace_bytes(...) bytes, 256-byte aligned; a buffer for
+ * the largest T, B and max_q serves every call with smaller ones.
  * ------------------------------------------------------------------------- */
 size_t cq_attn_kv8_workspace_bytes(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q);
 cq_status cq_attn_kv8(const void* Q, int xt, int64_t T, int64_t Hq, int64_t ldq, const cq_kv8_cache* cache,

@@ -237,3 +237,19 @@ def test_some_scores_overflow(n, group, block):
         want, mass = values[seen].mean(0), np.abs(values[seen]).mean(0)
         assert np.all(np.abs(f64(o[i]) - want) <= 2.0 ** -15 * mass)
         assert np.all(np.abs(f64(z[i]) - np.log(len(seen))) <= 2.0 ** -14)
+
+
+# ---- buffers and descriptors -------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("most", [5, 20, 200])
+def test_one_workspace_for_every_step(most):
+    """A buffer for the longest guesses or prompts serves single tokens as well."""
+    s = Setup(59, [700] * 3, 2, 128, 64)
+    s.write([500, 300, 700])
+    ws = torch.empty(cq.cq_attn_kv8_workspace_bytes(3 * most, 10, 2, 128, 3, most), dtype=torch.uint8, device=DEV)
+    for n in (1, 3, 5, 7, 20, 25, 200):
+        if n <= most:
+            q, want, _ = s.attend([n] * 3, 5)
+            o = torch.empty_like(want)
+            cq.cq_attn_kv8(q, s.cache, starts([n] * 3), i32(s.len), n, o, ws)
+            assert torch.equal(o, want)
