@@ -265,13 +265,21 @@ class _kv8_desc(ctypes.Structure):
                 ("page", _c_i64), ("D", _c_i64), ("table", _c_p), ("ldt", _c_i64), ("B", _c_i64)]
 
 
+def _described(name):
+    return property(lambda self: self._held[name], lambda self, t: self._describe(**{**self._held, name: t}))
+
+
 class cq_kv8_cache:
     """One layer's 8-bit cache: Kq, Vq int8 [pages][Hkv][page][D], Ks, Vs f32
     [pages][Hkv][page / 32], table int32 [B][ldt].  Holds the tensors (which
     must be dense; a table's rows may be a slice of a wider one) and the C
-    descriptor of the same name."""
+    descriptor of the same name.  A tensor that is assigned to one of these
+    names is checked like the first ones and takes its place in the descriptor."""
 
     def __init__(self, Kq, Ks, Vq, Vs, table):
+        self._describe(Kq, Ks, Vq, Vs, table)
+
+    def _describe(self, Kq, Ks, Vq, Vs, table):
         import torch
         pages, Hkv, page, D = Kq.shape
         for t, dt, shape in ((Kq, torch.int8, (pages, Hkv, page, D)), (Vq, torch.int8, (pages, Hkv, page, D)),
@@ -280,14 +288,16 @@ class cq_kv8_cache:
                 raise ValueError(f"a dense {dt} tensor of shape {shape} is needed, got {t.dtype} {tuple(t.shape)}")
         if table.dtype != torch.int32 or table.dim() != 2 or table.stride(1) != 1:
             raise ValueError("the table must be int32 [B][ldt]")
-        self.Kq, self.Ks, self.Vq, self.Vs, self.table = Kq, Ks, Vq, Vs, table
         ldt = table.stride(0) if table.shape[0] > 1 else table.shape[1]
+        self._held = {"Kq": Kq, "Ks": Ks, "Vq": Vq, "Vs": Vs, "table": table}
         self.desc = _kv8_desc(Kq.data_ptr(), Ks.data_ptr(), Vq.data_ptr(), Vs.data_ptr(), pages, Hkv, page, D,
                               table.data_ptr(), ldt, table.shape[0])
         # read on every call: plain attributes cost less than the descriptor's fields
         self.Hkv, self.D, self.B, self._ref = Hkv, D, table.shape[0], ctypes.byref(self.desc)
         self._types = {torch.float16: CQ_F16, torch.bfloat16: CQ_BF16, torch.float32: CQ_F32}
         self._int32, self._float32, self._cuda = torch.int32, torch.float32, torch._C
+
+    Kq, Ks, Vq, Vs, table = map(_described, ("Kq", "Ks", "Vq", "Vs", "table"))
 
     @staticmethod
     def empty(pages, Hkv, page, D, table, device="cuda"):
