@@ -272,7 +272,8 @@ def _described(name):
 class cq_kv8_cache:
     """One layer's 8-bit cache: Kq, Vq int8 [pages][Hkv][page][D], Ks, Vs f32
     [pages][Hkv][page / 32], table int32 [B][ldt].  Holds the tensors (which
-    must be dense; a table's rows may be a slice of a wider one) and the C
+    must be dense; a table's rows may be a slice of a wider one
+    that holds the last row's pitch too) and the C
     descriptor of the same name.  A tensor that is assigned to one of these
     names is checked like the first ones and takes its place in the descriptor."""
 
@@ -289,6 +290,9 @@ class cq_kv8_cache:
         if table.dtype != torch.int32 or table.dim() != 2 or table.stride(1) != 1:
             raise ValueError("the table must be int32 [B][ldt]")
         ldt = table.stride(0) if table.shape[0] > 1 else table.shape[1]
+        if table.storage_offset() + table.shape[0] * ldt > table.untyped_storage().nbytes() // 4:
+            raise ValueError(f"a table's rows must be readable up to their pitch, also the last one: {table.shape[0]} rows of {ldt}"
+                             f" from entry {table.storage_offset()} on leave their memory")
         self._held = {"Kq": Kq, "Ks": Ks, "Vq": Vq, "Vs": Vs, "table": table}
         self.desc = _kv8_desc(Kq.data_ptr(), Ks.data_ptr(), Vq.data_ptr(), Vs.data_ptr(), pages, Hkv, page, D,
                               table.data_ptr(), ldt, table.shape[0])

@@ -40,7 +40,8 @@ typedef struct {
     int8_t* Vq;
     float* Vs;
     int64_t pages, Hkv, page, D;
-    const int32_t* table;  /* [B][ldt] page numbers; entries past a sequence's pages are not read */
+    const int32_t* table;  /* [B][ldt] page numbers; entries past a sequence's pages may hold anything and are read only
+                              where a length is wrong: all B * ldt must be readable */
     int64_t ldt, B;
 } cq_kv8_cache;
 /* Shape rules of the descriptor: pages >= 1, 1 <= Hkv <= 1024, page >= 32 and

@@ -48,3 +48,14 @@ def test_descriptor_follows_the_tensors():
             setattr(c, name, t)
         for n, x in before.items():
             assert getattr(c, n) is x and getattr(c.desc, n) == x.data_ptr()
+
+
+def test_table_rows_are_readable_to_their_pitch():
+    """A length is checked against the pitch, so a wrong one may read up to it: not past the table's memory."""
+    wide = torch.zeros(4, 8, dtype=torch.int32)
+    for ok in (wide, wide[:, :3], wide[:3, 5:], wide[3:, 5:], wide[1:2, 2:4]):
+        c = cache(table=ok)
+        assert c.desc.table == ok.data_ptr()
+    for bad in (wide[:, 5:], wide[2:, 1:4]):
+        with pytest.raises(ValueError, match="pitch"):
+            cache(table=bad)
