@@ -7,6 +7,7 @@ import torch
 import block_quantized_weight_02_gb300 as cq
 import kv8ref
 from cqtest import DEV
+from kv8tight import attend
 from test_gpu_kv8 import Setup, f64, i32, starts
 
 pytestmark = pytest.mark.gpu
@@ -82,42 +83,6 @@ def test_wait_timeout_reports_status_and_the_next_call_is_right(n, group, out):
 
 
 # ---- values far apart --------------------------------------------------------------------------------------------
-
-def attend(cache, b, q, scale, causal, window, out):
-    """(o, lse, bound of o, bound of lse) of rows q [n][Hq][D], the last of sequence b, in 64 bits.
-
-    The bound, relative to the sum of the weighted values' magnitudes unless said otherwise.  A score: exact products,
-    eight truncated sums and two roundings of at most 2^-23 of the products' magnitudes (`reach`), less than 2^-19 of it,
-    once in the weight and once in the normaliser: 2^-18 reach.  The block's exponent, up to 128 in size, joins it and
-    the maximum comes off: two roundings of at most 2^-18 each, as often: 2^-16.  f32 outputs: weights in two terms
-    2^-22, exponential 2^-21, truncated sums 5e-6: with the exponent's less than 2^-15.  16-bit outputs: weights in one
-    term 2^-11, all else 2^-14.
-    Weights are fp16 numbers against a largest (weight times block scale) of at least 2^10: each is off by up to 2^-25,
-    and meets codes up to 127: tokens * 2^-28 of that largest.  The output rounds once."""
-    n, Hq, D = q.shape
-    k, v, L = cache.values(0, b), cache.values(1, b), len(cache.q[0][b])
-    vs = cache.s[1][b][np.arange(L) // kv8ref.BLOCK]
-    g, o, lse, e = Hq // cache.Hkv, np.zeros((n, Hq, D)), np.full((n, Hq), -np.inf), np.zeros((n, Hq, D))
-    reach = np.zeros((n, Hq))
-    for i in range(n):
-        p = L - n + i
-        lo, hi = (max(0, p - window + 1) if window else 0, p + 1) if causal else (0, L)
-        if hi <= lo:
-            continue
-        for h in range(Hq):
-            kk, vv = k[lo:hi, h // g], v[lo:hi, h // g]
-            s = scale * (kk @ q[i, h])
-            w = np.exp(s - s.max())
-            z = w.sum()
-            w /= z
-            o[i, h], lse[i, h] = w @ vv, s.max() + np.log(z)
-            reach[i, h] = scale * (np.abs(kk) @ np.abs(q[i, h])).max()
-            rel = (2.0 ** -15 if out == "f32" else 2.0 ** -11 + 2.0 ** -14) + 2.0 ** -18 * reach[i, h]
-            e[i, h] = rel * (w @ np.abs(vv)) + (hi - lo) * 2.0 ** -28 * (w * vs[lo:hi, h // g]).max()
-    u = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11, "f32": 2.0 ** -24}[out]
-    e = e + u * np.exp2(np.floor(np.log2(np.abs(o) + e + 1e-300))) + (2.0 ** -25 if out == "f16" else 0.0)
-    return o, lse, e, kv8ref.lse_bound(lse, reach)
-
 
 def check(s, counts, group, out, causal=True, window=0, **kw):
     q, o, z = s.attend(counts, group, out=out, causal=causal, window=window, **kw)
@@ -253,3 +218,55 @@ def test_one_workspace_for_every_step(most):
             o = torch.empty_like(want)
             cq.cq_attn_kv8(q, s.cache, starts([n] * 3), i32(s.len), n, o, ws)
             assert torch.equal(o, want)
+
+
+# ---- f32 outputs, element by element -----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("Hkv,group,counts,held", [
+    (2, 4, [1, 1, 1, 1], [0, 40, 700, 1990]),             # single tokens
+    (1, 3, [4, 1, 0, 5], [3, 300, 9, 1500]),              # up to 16 rows of a head
+    (2, 5, [5, 1, 6, 3], [0, 64, 900, 1500]),             # up to 32
+    (1, 8, [16, 7, 1, 12], [40, 0, 2000, 333]),           # up to 128
+    (2, 2, [130, 1, 200, 40], [0, 700, 500, 1200]),       # more
+])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 77), (False, 0)])
+def test_f32_outputs(Hkv, group, counts, held, D, causal, window):
+    s = Setup(60, [a + b for a, b in zip(held, counts)], Hkv, D, 64)
+    s.write(held, spread=0.4)
+    s.write(counts, spread=0.4)
+    check(s, counts, group, "f32", causal, window)
+
+
+@pytest.mark.parametrize("n,group", [(1, 4), (5, 5), (20, 4), (60, 4)])
+def test_f32_outputs_joined(n, group):
+    """One long sequence: its work is cut into a share for every SM, and partials are joined."""
+    s = Setup(61, [12000], 1, 64, 128)
+    s.write([12000 - n], spread=0.4)
+    s.write([n], spread=0.4)
+    check(s, [n], group, "f32")
+    check(s, [n], group, "f32", window=5000)
+
+
+# ---- rejected tokens ---------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+def test_rejected_tokens(dtype):
+    """Lengths that go back and are written over: a block that keeps tokens keeps its scale (and its NaN) too, one that
+    is begun again does not."""
+    s = Setup(62, [200, 200, 200], 2, 64, 32)
+    s.write([70, 33, 64], dtype)
+    for keep, new, big in (([66, 31, 64], [5, 5, 1], 8.0), ([64, 33, 40], [7, 1, 30], 1.0), ([65, 32, 0], [1, 40, 3], 0.01),
+                           ([60, 70, 2], [100, 1, 31], 1.0)):
+        k, v = s.rows(sum(new), 2, "f32", 0.5) * big, s.rows(sum(new), 2, "f32", 0.5) * big
+        k, v = k.to(kv8ref.TORCH[dtype]), v.to(kv8ref.TORCH[dtype])
+        if big == 1.0:
+            v[3, 1, 9] = float("inf")
+        s.len = [a + b for a, b in zip(keep, new)]
+        cq.cq_kv8_write(s.cache, k, v, starts(new), i32(s.len))
+        assert cq.cq_get_device_error() == 0
+        at = 0
+        for b, n in enumerate(new):
+            s.ref.write(b, f64(k[at:at + n]), f64(v[at:at + n]), at=keep[b])
+            at += n
+        s.check_values()

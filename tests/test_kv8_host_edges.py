@@ -1,9 +1,12 @@
 """Host-side properties of the 8-bit cache's entry points that a program relies
 on between calls."""
+import numpy as np
 import pytest
 import torch
 
 import block_quantized_weight_02_gb300 as cq
+import kv8ref
+import kv8tight
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -59,3 +62,30 @@ def test_table_rows_are_readable_to_their_pitch():
     for bad in (wide[:, 5:], wide[2:, 1:4]):
         with pytest.raises(ValueError, match="pitch"):
             cache(table=bad)
+
+
+# ---- the bounds of the GPU tests are themselves checked ----------------------------------------------------------
+
+def one_term(cache, q, scale):
+    """kv8tight.attend's causal output with every weight rounded to one fp16 term."""
+    k, v = cache.values(0, 0)[:, 0], cache.values(1, 0)[:, 0]
+    n, Hq, _ = q.shape
+    o = np.zeros_like(q)
+    for i in range(n):
+        hi = len(k) - n + i + 1
+        for h in range(Hq):
+            s = scale * (k[:hi] @ q[i, h])
+            w = np.exp(s - s.max())
+            o[i, h] = (w * 2.0 ** 12).astype(np.float16).astype(float) / 2.0 ** 12 @ v[:hi] / w.sum()
+    return o
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_f32_bound_notices_a_missing_term(D):
+    rng = np.random.default_rng(3)
+    c = kv8ref.Cache(1, 1, D)
+    c.write(0, rng.standard_normal((300, 1, D)), rng.standard_normal((300, 1, D)))
+    q = rng.standard_normal((4, 4, D))
+    for out, ok in (("bf16", True), ("f16", True), ("f32", False)):
+        o, _, lim, _ = kv8tight.attend(c, 0, q, D ** -0.5, True, 0, out)
+        assert np.all(np.abs(one_term(c, q, D ** -0.5) - o) <= lim) == ok
