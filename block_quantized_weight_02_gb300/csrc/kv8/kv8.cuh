@@ -63,6 +63,9 @@ cudaError_t launch_tiles(const AttnArgs& a, cudaStream_t s);
 size_t attn_workspace(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q);        // of a call
 size_t attn_workspace_upto(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q);   // and of any smaller one
 
+// A kernel that starts under the ones before it.  What those may have written (queries, codes, scales, the workspace) is read
+// after pdl_wait() and not through the read-only path (__ldg), which is for data that no kernel writes while this one runs;
+// q_start, lens and the table come from the caller.
 template <class... KArgs, class... Args>
 cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args... args) {
     cudaLaunchConfig_t cfg = {};

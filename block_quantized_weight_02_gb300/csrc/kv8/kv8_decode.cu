@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
                                   2 * ((s.q0 + r / G) * a.ldq + (int64_t)(h * G + r % G) * D + t * (D / 4));
                 uint4 w[KS / 2];
 #pragma unroll
-                for (int j = 0; j < KS / 2; ++j) w[j] = in ? __ldg(reinterpret_cast<const uint4*>(src) + j) : make_uint4(0, 0, 0, 0);
+                for (int j = 0; j < KS / 2; ++j) w[j] = in ? __ldcg(reinterpret_cast<const uint4*>(src) + j) : make_uint4(0, 0, 0, 0);
                 float f = a.scale * LOG2E;
                 uint32_t v[KS * 2];
 #pragma unroll

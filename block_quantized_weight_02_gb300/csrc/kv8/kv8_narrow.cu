@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                 for (int c = 0; c < D / 32; ++c) {
                     v[c] = make_uint4(0, 0, 0, 0);
                     if (in)
-                        v[c] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.Q) + (q0 + f / G) * a.ldq +
+                        v[c] = __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.Q) + (q0 + f / G) * a.ldq +
                                                                     (int64_t)(w.at.h * G + f % G) * D + qd * (D / 4)) + c);
                 }
                 float qf = in ? a.scale * LOG2E : 0.f;

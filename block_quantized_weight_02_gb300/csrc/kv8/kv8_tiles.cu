@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
 #pragma unroll
                 for (int k = 0; k < 32 / QRPI; ++k) {
                     v[k] = make_uint4(0, 0, 0, 0);
-                    if (ff <= t.wl) v[k] = __ldg(reinterpret_cast<const uint4*>(Q + (t.q0 + tok) * a.ldq + g * D) + lane % QLPR);
+                    if (ff <= t.wl) v[k] = __ldcg(reinterpret_cast<const uint4*>(Q + (t.q0 + tok) * a.ldq + g * D) + lane % QLPR);
                     ff += QRPI;
                     for (g += QRPI; g >= G; g -= G) ++tok;
                 }
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c) {
                     v[c] = make_uint4(0, 0, 0, 0);
-                    if (t.in) v[c] = __ldg(reinterpret_cast<const uint4*>(Q + (t.q0 + t.f / G) * a.ldq + t.f % G * D) + c);
+                    if (t.in) v[c] = __ldcg(reinterpret_cast<const uint4*>(Q + (t.q0 + t.f / G) * a.ldq + t.f % G * D) + c);
                 }
             }
         };

@@ -241,7 +241,7 @@ __device__ __forceinline__ void load_codes(const AttnArgs& a, const List* list, 
                     pid = 0;
                 }
                 row1 = (pid * a.c.Hkv + w.at.h) * a.c.page + tok % a.c.page;
-                s1 = make_float2(__ldg(a.c.s[0] + row1 / BLK), __ldg(a.c.s[1] + row1 / BLK));
+                s1 = make_float2(__ldcg(a.c.s[0] + row1 / BLK), __ldcg(a.c.s[1] + row1 / BLK));
             }
         };
         look_up(w.from);

@@ -270,3 +270,43 @@ def test_rejected_tokens(dtype):
             s.ref.write(b, f64(k[at:at + n]), f64(v[at:at + n]), at=keep[b])
             at += n
         s.check_values()
+
+
+# ---- calls in a chain --------------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("n,group", FORMS)
+def test_calls_in_a_chain(n, group):
+    """Writes and attention that follow each other without a pause see each other's results: queries and tokens from the
+    kernel before, blocks whose scale grows from step to step, one workspace."""
+    s = Setup(63, [400, 400], 2, 64, 32)
+    s.write([50, 200])
+    steps = [(s.rows(2 * n, 2, "bf16", 0.5) * 1.3 ** i, s.rows(2 * n, 2, "bf16", 0.5) * 1.3 ** i, s.rows(2 * n, 2 * group, "bf16", 0.3))
+             for i in range(30)]
+    counts, first = [n, n], [50, 200]
+    last = [[min(400, a + n * (i % 3 + 1)) for a in first] for i in range(30)]
+    lens = [i32(x) for x in last]
+    ws = torch.empty(cq.cq_attn_kv8_workspace_bytes(2 * n, 2 * group, 2, 64, 2, n), dtype=torch.uint8, device=DEV)
+    before = [t.clone() for t in (s.cache.Kq, s.cache.Ks, s.cache.Vq, s.cache.Vs)]
+    k, v, q = (torch.empty_like(t) for t in steps[0])
+    qs = starts(counts)
+
+    def run(pause):
+        for t, b in zip((s.cache.Kq, s.cache.Ks, s.cache.Vq, s.cache.Vs), before):
+            t.copy_(b)
+        out = []
+        for i, x in enumerate(steps):
+            for t, y in zip((k, v, q), x):
+                t.copy_(y)
+                pause()
+            o, z = torch.empty(2 * n, 2 * group, 64, device=DEV), torch.empty(2 * n, 2 * group, device=DEV)
+            for f in (lambda: cq.cq_kv8_write(s.cache, k.bfloat16(), v.bfloat16(), qs, lens[i]),
+                      lambda: cq.cq_attn_kv8(q.bfloat16(), s.cache, qs, lens[i], n, o, ws, lse=z)):
+                f()
+                pause()
+            out += [o, z]
+        torch.cuda.synchronize()
+        return out
+
+    want, got = run(torch.cuda.synchronize), run(lambda: None)
+    assert cq.cq_get_device_error() == 0
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
