@@ -2,9 +2,10 @@
 // sequence has for one KV head.
 // Up to 16 rows each warp makes its own products out of registers; the legacy tensor path's work grows
 // with the rows.  24 sequences of 300 to 9000 tokens, 8 KV heads of 128 channels, bf16 out: 10 rows take
-// 74 us there against 79 us in the narrow kernel, 15 rows 81 against 79, 20 rows 108 against 81; 16 rows
-// of 3 x 110000 tokens 87 against 108.  From 17 rows on the products are tcgen05's.  33 rows and more no
-// longer fit the narrow kernel's 32 columns.
+// 74 us there against 77 us in the narrow kernel, 15 rows 80 against 79; f32 out 89 against 98 and 97
+// against 99; 16 rows of 3 x 110000 tokens 86 against 97 with f16 out, 105 against 122 with f32.  From 17
+// rows on the products are tcgen05's: 20 rows took 108 us of the first kind against 81.  33 rows and more
+// no longer fit the narrow kernel's 32 columns.
 #include "kv8.cuh"
 
 namespace cq {

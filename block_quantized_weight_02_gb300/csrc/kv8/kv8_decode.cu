@@ -15,11 +15,12 @@
 // up to 8 rows takes half the products that rows x tokens would (they pad rows to 16).
 // For f32 outputs a weight goes in two fp16 terms.
 //
-// Measured: 4 rows of 8 heads of 128 channels, 32 sequences of 1000 to 32767 tokens, 177 us, 6.1 TB/s (the shares are
-// equal, but a third of the SMs draw 10 % less from memory and end last).  16 rows over 3 x 110000 tokens, 4 heads, f32
-// outputs: 107 us, 3.1 TB/s, bound by instructions (conversions, products, exponentials).  One row of 16 heads of 64
-// channels behind a window of 1024 tokens, 48 sequences: 34 us, 2.7 TB/s, of which the list and the first load take 6
-// and the joins 8.  8 rows of 4 heads of one sequence of 777 tokens: 13 us of latency.
+// Measured, calls in a chain: 4 rows of 8 heads of 128 channels, 32 sequences of 1000 to 32767 tokens, 178 us, 6.1 TB/s
+// (the shares are equal, but a third of the SMs draw 10 % less from memory and end last).  16 rows over 3 x 110000 tokens,
+// 4 heads: 86 us with f16 outputs, 3.9 TB/s, 105 with f32, bound by instructions (conversions, products, exponentials).
+// One row of 16 heads of 64 channels behind a window of 1024 tokens, 48 sequences: 38 us, 2.4 TB/s (35 out of a graph), of
+// which the list and the first load take 6 and the joins 8.  8 rows of 4 heads of one sequence of 777 tokens: 14 us of
+// latency.
 // The codes become fp16 in registers, exactly.  The operands' inner order is free as long
 // as both sides agree: a lane takes 4 neighbouring codes of its token as one k16 step's
 // part (keys), and D/8 neighbouring channels of its tokens as the output tiles (values),
