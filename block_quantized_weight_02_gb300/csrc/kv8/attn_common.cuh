@@ -89,6 +89,9 @@ constexpr int APART = 80;
 // A normaliser may be large where the factor 2^d that lowers it is too small for f32: it is lowered by the root, twice.
 __device__ __forceinline__ float root_of(float d) { return ex2(0.5f * d); }
 
+// What a sum against the maximum m0 counts against m.
+__device__ __forceinline__ float since(float m0, float m) { return m0 == -INFINITY ? 1.f : ex2(m0 - m); }
+
 // An unfinished result: O before the division, the maximum (of z) and the normaliser of each row.
 template <int D, int R>
 struct PartOf {

@@ -42,9 +42,12 @@ namespace kv8 {
 namespace {
 
 constexpr int ROWS = 16;
-constexpr int MAX_CTAS = 256;         // workspace bound
+constexpr int MAX_CTAS = 160;         // workspace bound: a full GB300 has no more SMs
 constexpr int MAX_NW = 12;
 constexpr int P_EXP = 15;             // weights carry 2^15
+// One-term weights' products add up in the tensor cores, which truncate (up to 3e-9 of the sum a token): after so many blocks
+// of a segment the accumulators go to a sum in the workspace, 5e-5 at most.
+constexpr int WINDOW = 512;
 
 struct Maps {
     CUtensorMap t[2];                 // keys, values: {D, pages * Hkv * page}, box {D, 32}
@@ -52,10 +55,11 @@ struct Maps {
 
 template <int D>
 using Part = PartOf<D, ROWS>;
-// Workspace: partials of segments that end inside a warp's share, partials of the CTAs, the CTAs' two segments.
+// Workspace: partials of segments that end inside a warp's share, sums, partials of the CTAs, the CTAs' two segments.
 template <int D>
 struct Space {
     Part<D> warp[MAX_CTAS * MAX_NW];
+    Part<D> sum[MAX_CTAS * MAX_NW];   // of a warp's earlier windows
     Part<D> cta[MAX_CTAS][2];
     int seg[MAX_CTAS][2];             // segment of cta[i][0] (began earlier) and cta[i][1] (began here, goes on), or -1
 };
@@ -148,6 +152,53 @@ __device__ __forceinline__ void write_part(Part<D>* p, const Acc<D, NT>& c, int 
                 p->m[r] = c.m[n][k];
                 p->l[r] = c.l[n][k];
             }
+        }
+}
+
+// The accumulators join the sum of the segment's windows so far (none: first), and start afresh.
+template <int D, int NT>
+__device__ __forceinline__ void write_sum(Part<D>* p, Acc<D, NT>& c, int rows, bool first) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int r = 8 * n + 2 * t + k;
+            const float keep = first || r >= rows ? 0.f : since(p->m[r], c.m[n][k]);
+            float4* o = reinterpret_cast<float4*>(&p->o[r][g * Acc<D, NT>::DL]);
+#pragma unroll
+            for (int i = 0; i < Acc<D, NT>::DL / 4; ++i) {
+                const float4 z = first || r >= rows ? make_float4(0.f, 0.f, 0.f, 0.f) : o[i];
+                if (r < rows)
+                    o[i] = make_float4(fmaf(z.x, keep, c.ch(n, k, 4 * i)), fmaf(z.y, keep, c.ch(n, k, 4 * i + 1)),
+                                       fmaf(z.z, keep, c.ch(n, k, 4 * i + 2)), fmaf(z.w, keep, c.ch(n, k, 4 * i + 3)));
+            }
+        }
+    __syncwarp();                      // all have read the old maxima
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (g == 0 && 8 * n + 2 * t + k < rows) p->m[8 * n + 2 * t + k] = c.m[n][k];
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) c.o[n][i][k] = c.o[n][i][2 + k] = 0.f;
+        }
+    __syncwarp();
+}
+// The sum comes back to the accumulators.
+template <int D, int NT>
+__device__ __forceinline__ void read_sum(const Part<D>* p, Acc<D, NT>& c, int rows) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int r = 8 * n + 2 * t + k;
+            if (r >= rows) continue;
+            const float keep = since(p->m[r], c.m[n][k]);
+#pragma unroll
+            for (int ch = 0; ch < Acc<D, NT>::DL; ++ch)
+                c.o[n][ch / 2][2 * (ch & 1) + k] = fmaf(p->o[r][g * Acc<D, NT>::DL + ch], keep, c.o[n][ch / 2][2 * (ch & 1) + k]);
         }
 }
 
@@ -368,186 +419,193 @@ __global__ void __launch_bounds__(Ring<D, NT>::NW * 32, 1) k_attn_decode(const _
             }
             int hi = -64;                         // largest value exponent so far, seen or not
 
-            for (int i = from; i < until && s.L > 0; ++i) {
-                // one answer for the warp, as what follows takes all its lanes: it joins the vote on the maxima, and
-                // what is computed until then from a block that did not come is dropped
-                const bool here = wait_bar(smem_u32(&bars[warp][stage]), parity, wait_ns, &stop);
-                const uint32_t kt = ring0 + stage * 2 * R::TILE, vt = kt + R::TILE;
-                const float2 bs = scales[warp][stage];
-                const int tok0 = (s.first + i) * BLK;
-                float x[NT][2][4];                // tokens 16 mt + g (rows 2 t, 2 t + 1), + 8 (the same)
+            // in windows (two-term weights' products are added outside the tensor cores: in one)
+            Part<D>* sum = &sp->sum[blockIdx.x * NW + warp];
+            for (int i0 = from, end; i0 < until && s.L > 0 && alive; i0 = end) {
+                end = PT == 1 ? min(until, i0 + WINDOW) : until;
+                if (PT == 1 && i0 > from) write_sum<D, NT>(sum, acc, s.n * G, i0 == from + WINDOW);
+                for (int i = i0; i < end; ++i) {
+                    // one answer for the warp, as what follows takes all its lanes: it joins the vote on the maxima, and
+                    // what is computed until then from a block that did not come is dropped
+                    const bool here = wait_bar(smem_u32(&bars[warp][stage]), parity, wait_ns, &stop);
+                    const uint32_t kt = ring0 + stage * 2 * R::TILE, vt = kt + R::TILE;
+                    const float2 bs = scales[warp][stage];
+                    const int tok0 = (s.first + i) * BLK;
+                    float x[NT][2][4];                // tokens 16 mt + g (rows 2 t, 2 t + 1), + 8 (the same)
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int mt = 0; mt < 2; ++mt) x[n][mt][0] = x[n][mt][1] = x[n][mt][2] = x[n][mt][3] = 0.f;
+                        for (int mt = 0; mt < 2; ++mt) x[n][mt][0] = x[n][mt][1] = x[n][mt][2] = x[n][mt][3] = 0.f;
 #pragma unroll
-                for (int mt = 0; mt < 2; ++mt)
+                    for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-                    for (int c = 0; c < D / 64; ++c) {
-                        uint4 w[2];               // tokens 16 mt + g, + 8: four k16 steps
+                        for (int c = 0; c < D / 64; ++c) {
+                            uint4 w[2];               // tokens 16 mt + g, + 8: four k16 steps
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int r = 16 * mt + 8 * e + g;
-                            w[e] = lds128(D == 128 ? kt + r * 128 + (((2 * t + c) ^ (r & 7)) << 4) : kt + r * 64 + ((t ^ ((r >> 1) & 3)) << 4));
-                        }
-#pragma unroll
-                        for (int jj = 0; jj < 2; ++jj) {
-                            uint32_t ka[2][4];
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const uint32_t y0 = (jj ? (j ? w[0].w : w[0].z) : (j ? w[0].y : w[0].x)) ^ 0x80808080u;
-                                const uint32_t y1 = (jj ? (j ? w[1].w : w[1].z) : (j ? w[1].y : w[1].x)) ^ 0x80808080u;
-                                ka[j][0] = codes_f16(y0, 0x4140u);
-                                ka[j][1] = codes_f16(y1, 0x4140u);
-                                ka[j][2] = codes_f16(y0, 0x4342u);
-                                ka[j][3] = codes_f16(y1, 0x4342u);
+                            for (int e = 0; e < 2; ++e) {
+                                const int r = 16 * mt + 8 * e + g;
+                                w[e] = lds128(D == 128 ? kt + r * 128 + (((2 * t + c) ^ (r & 7)) << 4) : kt + r * 64 + ((t ^ ((r >> 1) & 3)) << 4));
                             }
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                const int j0 = 4 * c + 2 * jj;
-                                mma_16816_f16(x[n][mt], ka[0], q[n][j0][0], q[n][j0][1]);
-                                mma_16816_f16(x[n][mt], ka[1], q[n][j0 + 1][0], q[n][j0 + 1][1]);
+                            for (int jj = 0; jj < 2; ++jj) {
+                                uint32_t ka[2][4];
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    const uint32_t y0 = (jj ? (j ? w[0].w : w[0].z) : (j ? w[0].y : w[0].x)) ^ 0x80808080u;
+                                    const uint32_t y1 = (jj ? (j ? w[1].w : w[1].z) : (j ? w[1].y : w[1].x)) ^ 0x80808080u;
+                                    ka[j][0] = codes_f16(y0, 0x4140u);
+                                    ka[j][1] = codes_f16(y1, 0x4140u);
+                                    ka[j][2] = codes_f16(y0, 0x4342u);
+                                    ka[j][3] = codes_f16(y1, 0x4342u);
+                                }
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) {
+                                    const int j0 = 4 * c + 2 * jj;
+                                    mma_16816_f16(x[n][mt], ka[0], q[n][j0][0], q[n][j0][1]);
+                                    mma_16816_f16(x[n][mt], ka[1], q[n][j0 + 1][0], q[n][j0 + 1][1]);
+                                }
                             }
                         }
-                    }
-                // z = score in log2 units + value exponent; a value scale of NaN spoils it like a key scale of NaN
-                const float ks = bs.y == bs.y ? bs.x : bs.y;
-                const int lv = value_exp(bs.y);
-                hi = max(hi, lv);
-                const bool masked = tok0 < free_lo || tok0 + BLK > free_hi;
-                float mx[NT][2];
-                bool grows = !here;
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float f = qf[n][k] * ks;
-                        float m = acc.m[n][k];
-                        int lo = 0, hi = 0;
-                        if (masked) {
-                            const int rr = 8 * n + 2 * t + k, row = rr / G;
-                            hi = rr < s.n * G ? row_hi(row, s.n, s.L, a.causal) : 0;
-                            lo = row_lo(row, s.n, s.L, a.window);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float& y = x[n][e >> 1][2 * (e & 1) + k];
-                            y = fmaf(y, f, (float)lv);
-                            if (masked) {
-                                const int tok = tok0 + 8 * e + g;
-                                if (tok < lo || tok >= hi) y = -INFINITY;
-                            }
-                            m = fmaxf(m, y);
-                        }
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-                        mx[n][k] = m;
-                        grows |= m > acc.m[n][k];
-                    }
-                if (__any_sync(0xffffffffu, grows)) {
-                    if (!__all_sync(0xffffffffu, here)) {
-                        alive = false;
-                        break;
-                    }
+                    // z = score in log2 units + value exponent; a value scale of NaN spoils it like a key scale of NaN
+                    const float ks = bs.y == bs.y ? bs.x : bs.y;
+                    const int lv = value_exp(bs.y);
+                    hi = max(hi, lv);
+                    const bool masked = tok0 < free_lo || tok0 + BLK > free_hi;
+                    float mx[NT][2];
+                    bool grows = !here;
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const float root = mx[n][k] > acc.m[n][k] ? root_of(acc.m[n][k] - mx[n][k]) : 1.f, f = root * root;
-                            acc.m[n][k] = mx[n][k];
-                            acc.l[n][k] = acc.l[n][k] * root * root;
-#pragma unroll
-                            for (int i2 = 0; i2 < D / 16; ++i2) {
-                                acc.o[n][i2][k] *= f;
-                                acc.o[n][i2][2 + k] *= f;
+                            const float f = qf[n][k] * ks;
+                            float m = acc.m[n][k];
+                            int lo = 0, hi = 0;
+                            if (masked) {
+                                const int rr = 8 * n + 2 * t + k, row = rr / G;
+                                hi = rr < s.n * G ? row_hi(row, s.n, s.L, a.causal) : 0;
+                                lo = row_lo(row, s.n, s.L, a.window);
                             }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                float& y = x[n][e >> 1][2 * (e & 1) + k];
+                                y = fmaf(y, f, (float)lv);
+                                if (masked) {
+                                    const int tok = tok0 + 8 * e + g;
+                                    if (tok < lo || tok >= hi) y = -INFINITY;
+                                }
+                                m = fmaxf(m, y);
+                            }
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                            mx[n][k] = m;
+                            grows |= m > acc.m[n][k];
                         }
-                }
-                const bool far = lv < hi - APART;
-                const float back = far ? 0.f : pow2i(-lv);
-                if (far)
+                    if (__any_sync(0xffffffffu, grows)) {
+                        if (!__all_sync(0xffffffffu, here)) {
+                            alive = false;
+                            break;
+                        }
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
+                            for (int k = 0; k < 2; ++k) {
+                                const float root = mx[n][k] > acc.m[n][k] ? root_of(acc.m[n][k] - mx[n][k]) : 1.f, f = root * root;
+                                acc.m[n][k] = mx[n][k];
+                                acc.l[n][k] = acc.l[n][k] * root * root;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                acc.l[n][k] += ex2((x[n][e >> 1][2 * (e & 1) + k] - (acc.m[n][k] == -INFINITY ? 0.f : acc.m[n][k])) + (float)(P_EXP - lv));
-                uint32_t p[NT][PT][4];            // weights of tokens 8 e + 2 t, + 1, row g
+                                for (int i2 = 0; i2 < D / 16; ++i2) {
+                                    acc.o[n][i2][k] *= f;
+                                    acc.o[n][i2][2 + k] *= f;
+                                }
+                            }
+                    }
+                    const bool far = lv < hi - APART;
+                    const float back = far ? 0.f : pow2i(-lv);
+                    if (far)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
+                        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float m0 = acc.m[n][k] == -INFINITY ? 0.f : acc.m[n][k];
-                        float sum = 0.f;
+                            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    acc.l[n][k] += ex2((x[n][e >> 1][2 * (e & 1) + k] - (acc.m[n][k] == -INFINITY ? 0.f : acc.m[n][k])) + (float)(P_EXP - lv));
+                    uint32_t p[NT][PT][4];            // weights of tokens 8 e + 2 t, + 1, row g
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float m0 = acc.m[n][k] == -INFINITY ? 0.f : acc.m[n][k];
+                            float sum = 0.f;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                float& y = x[n][e >> 1][2 * (e & 1) + k];
+                                y = ex2((y - m0) + (float)P_EXP);      // (beside a huge m0 the exponent would be rounded away)
+                                sum += y;
+                            }
+                            acc.l[n][k] = fmaf(sum, back, acc.l[n][k]);
+                        }
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            float& y = x[n][e >> 1][2 * (e & 1) + k];
-                            y = ex2((y - m0) + (float)P_EXP);      // (beside a huge m0 the exponent would be rounded away)
-                            sum += y;
-                        }
-                        acc.l[n][k] = fmaf(sum, back, acc.l[n][k]);
-                    }
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float y0 = x[n][e >> 1][2 * (e & 1)], y1 = x[n][e >> 1][2 * (e & 1) + 1];
-                        const uint32_t hi = pack_f16(y0, y1);
-                        p[n][0][e] = transpose8(hi);
-                        if (PT == 2) {
-                            const float2 r = unpack_f16(hi);
-                            p[n][PT - 1][e] = transpose8(pack_f16(y0 - r.x, y1 - r.y));
-                        }
-                    }
-                }
-#pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
-                    // tokens 16 kk + 2 t, + 1, + 8, + 9: D/8 neighbouring channels each
-                    constexpr int W = D / 32;
-                    uint32_t v[4][W];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int r = 16 * kk + 2 * t + (e & 1) + 8 * (e >> 1);
-                        if constexpr (D == 128) {
-                            const uint4 y = lds128(vt + r * 128 + ((g ^ (r & 7)) << 4));
-                            v[e][0] = y.x, v[e][1] = y.y, v[e][2] = y.z, v[e][3] = y.w;
-                        } else {
-                            const uint2 y = lds64(vt + r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8);
-                            v[e][0] = y.x, v[e][1] = y.y;
+                            const float y0 = x[n][e >> 1][2 * (e & 1)], y1 = x[n][e >> 1][2 * (e & 1) + 1];
+                            const uint32_t hi = pack_f16(y0, y1);
+                            p[n][0][e] = transpose8(hi);
+                            if (PT == 2) {
+                                const float2 r = unpack_f16(hi);
+                                p[n][PT - 1][e] = transpose8(pack_f16(y0 - r.x, y1 - r.y));
+                            }
                         }
                     }
 #pragma unroll
-                    for (int j = 0; j < W; ++j) {
+                    for (int kk = 0; kk < 2; ++kk) {
+                        // tokens 16 kk + 2 t, + 1, + 8, + 9: D/8 neighbouring channels each
+                        constexpr int W = D / 32;
+                        uint32_t v[4][W];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) v[e][j] ^= 0x80808080u;
+                        for (int e = 0; e < 4; ++e) {
+                            const int r = 16 * kk + 2 * t + (e & 1) + 8 * (e >> 1);
+                            if constexpr (D == 128) {
+                                const uint4 y = lds128(vt + r * 128 + ((g ^ (r & 7)) << 4));
+                                v[e][0] = y.x, v[e][1] = y.y, v[e][2] = y.z, v[e][3] = y.w;
+                            } else {
+                                const uint2 y = lds64(vt + r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8);
+                                v[e][0] = y.x, v[e][1] = y.y;
+                            }
+                        }
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const uint32_t sel = e ? 0x7362u : 0x5140u;
-                            const uint32_t ya = prmt(v[0][j], v[1][j], sel), yb = prmt(v[2][j], v[3][j], sel);
-                            const uint32_t va[4] = {codes_f16(ya, 0x4140u), codes_f16(ya, 0x4342u), codes_f16(yb, 0x4140u), codes_f16(yb, 0x4342u)};
+                        for (int j = 0; j < W; ++j) {
 #pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                float(&o)[4] = acc.o[n][2 * j + e];
-                                if (PT == 1) {
-                                    mma_16816_f16(o, va, p[n][0][2 * kk], p[n][0][2 * kk + 1]);
-                                } else {          // the products truncate what they add up: long sums are added here
-                                    float y[4] = {0.f, 0.f, 0.f, 0.f};
+                            for (int e = 0; e < 4; ++e) v[e][j] ^= 0x80808080u;
 #pragma unroll
-                                    for (int z = 0; z < PT; ++z) mma_16816_f16(y, va, p[n][z][2 * kk], p[n][z][2 * kk + 1]);
+                            for (int e = 0; e < 2; ++e) {
+                                const uint32_t sel = e ? 0x7362u : 0x5140u;
+                                const uint32_t ya = prmt(v[0][j], v[1][j], sel), yb = prmt(v[2][j], v[3][j], sel);
+                                const uint32_t va[4] = {codes_f16(ya, 0x4140u), codes_f16(ya, 0x4342u), codes_f16(yb, 0x4140u), codes_f16(yb, 0x4342u)};
 #pragma unroll
-                                    for (int i = 0; i < 4; ++i) o[i] += y[i];
+                                for (int n = 0; n < NT; ++n) {
+                                    float(&o)[4] = acc.o[n][2 * j + e];
+                                    if (PT == 1) {
+                                        mma_16816_f16(o, va, p[n][0][2 * kk], p[n][0][2 * kk + 1]);
+                                    } else {          // the products truncate what they add up: long sums are added here
+                                        float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                                        for (int z = 0; z < PT; ++z) mma_16816_f16(y, va, p[n][z][2 * kk], p[n][z][2 * kk + 1]);
+#pragma unroll
+                                        for (int i = 0; i < 4; ++i) o[i] += y[i];
+                                    }
                                 }
                             }
                         }
                     }
+                    __syncwarp();                     // the stage is free
+                    stage = stage + 1 == R::ST ? 0 : stage + 1;
+                    parity ^= stage == 0;
+                    produce();
                 }
-                __syncwarp();                     // the stage is free
-                stage = stage + 1 == R::ST ? 0 : stage + 1;
-                parity ^= stage == 0;
-                produce();
             }
             if (s.L == 0) produce();
             if (!alive) break;
+            if (PT == 1 && until - from > WINDOW && s.L > 0) read_sum<D, NT>(sum, acc, s.n * G);
             // ---- the segment's end, or the share's
             u += until - from;
             const float un = pow2i(-P_EXP);

@@ -245,34 +245,26 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
             for (int r = 0; r < NR; ++r) l[r] = 0.f;
             int moves = 0;
             Part<D>* part = &sp->cta[blockIdx.x][w.from == 0 ? 1 : 0];
-            for (int j = x; j < n; j += 2, ++steps) {
-                const uint32_t tile = tile0 + j;
-                wait_warp(sc_full + 8 * (tile % SS), tile / SS & 1);
-                const Block blk = scales[tile % SS * NB + quarter];   // this warp's 32 tokens are one block
-                const int tok = w.it.tok0 + (w.from + j) * TN + tid;
-                wait_warp(s_full + 8 * x, steps & 1);
-                tc_fence_after();
-                float s[NR];
-                {
-                    uint32_t y[32];
-                    tmem_ld_32x32b_x32(ts, y);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int r = 0; r < NR; ++r) s[r] = __uint_as_float(y[r]);
-                }
-                if (j > 0) wait_warp(decided + 8 * x, took++ & 1);    // the step before has decided
-                if (moves != rows->moves) {      // and moved the maxima
+            // the step before has decided, and perhaps moved the maxima
+            auto follow = [&]() {
+                wait_warp(decided + 8 * x, took++ & 1);
+                if (moves != rows->moves) {
                     moves = rows->moves;
 #pragma unroll 1
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
                         for (int r = 0; r < NR; ++r) l[r] *= rows->fac[r];
                 }
-                const bool fresh = starts_fresh<PT>(j);      // (the even steps' group only)
-                if (PT == 2 && fresh && j > 0) {
-                    wait_warp(pv_done, (done0 + j - 1) & 1);
+            };
+            bool gone = false;
+            for (int j0 = 0; j0 < n && !gone; j0 += window<PT>()) {
+                if (__builtin_expect(j0 > 0 && x == 0, PT == 2)) {    // the next window: what the last one holds goes to the sum
+                    // (the window's first scores come after all products but the last, whose phase follows on theirs)
+                    wait_warp(s_full, steps & 1);
+                    follow();
+                    wait_warp(pv_done, (done0 + j0 - 1) & 1);
                     tc_fence_after();
-                    const float un = pow2i(-(int)W_EXP);
+                    const float un = acc_unit<PT>(window<PT>());
 #pragma unroll 1
                     for (int c = 0; c < NR / 16; ++c) {
                         uint32_t y[16];
@@ -283,105 +275,123 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                             for (int e = 0; e < 16; ++e) {
                                 const int r = 16 * c + e;
                                 float* o = &part->o[r][tid];
-                                const float z = j > FRESH ? *o * since(rows->m_sum[r], -rows->rc[r].y) : 0.f;
+                                const float z = j0 > window<PT>() ? *o * since(rows->m_sum[r], -rows->rc[r].y) : 0.f;
                                 *o = fmaf(__uint_as_float(y[e]), un, z);
                             }
                     }
                     any_of(false, 1 + x, 128);               // all have read the old maxima
                     if (quarter == 0) rows->m_sum[lane] = -rows->rc[lane].y;
                 }
-                const bool masked = __any_sync(0xffffffffu, tok < free_lo || tok >= free_hi);
-                float over = -INFINITY;
-#pragma unroll
-                for (int r = 0; r < NR; r += 2) {
-                    const float4 c = *reinterpret_cast<const float4*>(&rows->rc[r]);
-                    s[r] = fmaf(s[r], blk.k * c.x, blk.lv);            // z, rounded as for the maximum: a fused step on to z - m
-                    s[r + 1] = fmaf(s[r + 1], blk.k * c.z, blk.lv);    // would leave a huge score's rounding
-                    if (masked) {
-                        const int4 lim = *reinterpret_cast<const int4*>(&rows->lim[r]);
-                        if (tok < lim.x || tok >= lim.y) s[r] = -INFINITY;
-                        if (tok < lim.z || tok >= lim.w) s[r + 1] = -INFINITY;
-                    }
-                    over = max3(over, s[r] + c.y, s[r + 1] + c.w);
-                }
-                if (any_of(over > GROW || !alive, 1 + x, 128)) {
-                    alive = !any_of(!alive, 1 + x, 128);
-                    if (!alive) break;
-                    // Move the maxima: lane r has row r.
-                    rows->wmax[x][quarter][lane] = across<true>(s);
-                    any_of(false, 1 + x, 128);
-                    const float m = -rows->rc[lane].y;
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) top = fmaxf(top, rows->wmax[x][i][lane]);
-                    const bool grow = top > m + GROW;
-                    const float nm = grow ? top : m, fac = grow ? root_of(m - nm) : 1.f, fo = fac * fac;
-                    if (!fresh) {                // all products so far are in O^T
-                        wait_warp(pv_done, (done0 + j - 1) & 1);
-                        tc_fence_after();
+                for (int j = j0 + x; j < min(j0 + window<PT>(), n); j += 2, ++steps) {
+                    const uint32_t tile = tile0 + j;
+                    wait_warp(sc_full + 8 * (tile % SS), tile / SS & 1);
+                    const Block blk = scales[tile % SS * NB + quarter];   // this warp's 32 tokens are one block
+                    const int tok = w.it.tok0 + (w.from + j) * TN + tid;
+                    wait_warp(s_full + 8 * x, steps & 1);
+                    tc_fence_after();
+                    float s[NR];
+                    {
                         uint32_t y[32];
-                        tmem_ld_32x32b_x32(to, y);
+                        tmem_ld_32x32b_x32(ts, y);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int r = 0; r < NR; ++r) y[r] = __float_as_uint(__uint_as_float(y[r]) * __shfl_sync(0xffffffffu, fo, r));
-                        tmem_st_32x32b_x32(to, y);
-                        tmem_st_wait();
+                        for (int r = 0; r < NR; ++r) s[r] = __uint_as_float(y[r]);
                     }
-#pragma unroll 1
-                    for (int i = 0; i < 2; ++i)
-#pragma unroll
-                        for (int r = 0; r < NR; ++r) l[r] *= __shfl_sync(0xffffffffu, fac, r);
-                    alive = !any_of(!alive, 1 + x, 128);     // all have read the old maxima
-                    if (!alive) break;
-                    if (quarter == 0) {
-                        rows->rc[lane].y = -nm;
-                        rows->fac[lane] = fac;
-                        if (lane == 0) rows->moves = moves + 1;
-                    }
-                    any_of(false, 1 + x, 128);
-                    ++moves;
-                }
-                // the maxima come off before the next step may move them
-#pragma unroll
-                for (int r = 0; r < NR; r += 2) {
-                    const float4 c = *reinterpret_cast<const float4*>(&rows->rc[r]);
-                    s[r] += c.y;
-                    s[r + 1] += c.w;
-                }
-                __syncwarp();
-                if (j + 1 < n && lane == 0) mbar_arrive(decided + 8 * (1 - x));
-                uint32_t p[NR / 2], p2[NR / 2];
-                // (a far block's part of the normaliser comes in a round before the weights: a loop, as more code would
-                // push this one out of the instruction cache)
-                float base = blk.far ? W_EXP - blk.lv : W_EXP, back = blk.far ? 1.f : blk.back;
-#pragma unroll 1
-                for (int i = blk.far ? 2 : 1; i > 0; --i) {
+                    if (j > j0) follow();
+                    const bool fresh = j == j0;      // (the even steps' group only)
+                    const bool masked = __any_sync(0xffffffffu, tok < free_lo || tok >= free_hi);
+                    float over = -INFINITY;
 #pragma unroll
                     for (int r = 0; r < NR; r += 2) {
-                        const float y0 = ex2(s[r] + base), y1 = ex2(s[r + 1] + base);
-                        l[r] = fmaf(y0, back, l[r]);
-                        l[r + 1] = fmaf(y1, back, l[r + 1]);
-                        p[r / 2] = pack_f16(y0, y1);
-                        if (PT == 2) {
-                            const float2 h = unpack_f16(p[r / 2]);
-                            p2[r / 2] = pack_f16(y0 - h.x, y1 - h.y);
+                        const float4 c = *reinterpret_cast<const float4*>(&rows->rc[r]);
+                        s[r] = fmaf(s[r], blk.k * c.x, blk.lv);            // z, rounded as for the maximum: a fused step on to z - m
+                        s[r + 1] = fmaf(s[r + 1], blk.k * c.z, blk.lv);    // would leave a huge score's rounding
+                        if (masked) {
+                            const int4 lim = *reinterpret_cast<const int4*>(&rows->lim[r]);
+                            if (tok < lim.x || tok >= lim.y) s[r] = -INFINITY;
+                            if (tok < lim.z || tok >= lim.w) s[r + 1] = -INFINITY;
                         }
+                        over = max3(over, s[r] + c.y, s[r + 1] + c.w);
                     }
-                    base = W_EXP;
-                    back = 0.f;
-                }
-                if (M::PBUF == 1 && j > 0) wait_warp(pv_done, (done0 + j - 1) & 1);   // (a failure shows at the next meeting)
-                uint8_t* buf = smem + M::P + (M::PBUF == 1 ? 0 : x) * PT * M::PT_BYTES + tid * 64;
+                    if (any_of(over > GROW || !alive, 1 + x, 128)) {
+                        alive = !any_of(!alive, 1 + x, 128);
+                        if ((gone = !alive)) break;
+                        // Move the maxima: lane r has row r.
+                        rows->wmax[x][quarter][lane] = across<true>(s);
+                        any_of(false, 1 + x, 128);
+                        const float m = -rows->rc[lane].y;
+                        float top = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint4* at = reinterpret_cast<uint4*>(buf + ((c ^ ((tid >> 1) & 3)) << 4));
-                    *at = make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
-                    if (PT == 2) *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(at) + M::PT_BYTES) = make_uint4(p2[4 * c], p2[4 * c + 1], p2[4 * c + 2], p2[4 * c + 3]);
+                        for (int i = 0; i < 4; ++i) top = fmaxf(top, rows->wmax[x][i][lane]);
+                        const bool grow = top > m + GROW;
+                        const float nm = grow ? top : m, fac = grow ? root_of(m - nm) : 1.f, fo = fac * fac;
+                        if (!fresh) {                // all products so far are in O^T
+                            wait_warp(pv_done, (done0 + j - 1) & 1);
+                            tc_fence_after();
+                            uint32_t y[32];
+                            tmem_ld_32x32b_x32(to, y);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int r = 0; r < NR; ++r) y[r] = __float_as_uint(__uint_as_float(y[r]) * __shfl_sync(0xffffffffu, fo, r));
+                            tmem_st_32x32b_x32(to, y);
+                            tmem_st_wait();
+                        }
+#pragma unroll 1
+                        for (int i = 0; i < 2; ++i)
+#pragma unroll
+                            for (int r = 0; r < NR; ++r) l[r] *= __shfl_sync(0xffffffffu, fac, r);
+                        alive = !any_of(!alive, 1 + x, 128);     // all have read the old maxima
+                        if ((gone = !alive)) break;
+                        if (quarter == 0) {
+                            rows->rc[lane].y = -nm;
+                            rows->fac[lane] = fac;
+                            if (lane == 0) rows->moves = moves + 1;
+                        }
+                        any_of(false, 1 + x, 128);
+                        ++moves;
+                    }
+                    // the maxima come off before the next step may move them
+#pragma unroll
+                    for (int r = 0; r < NR; r += 2) {
+                        const float4 c = *reinterpret_cast<const float4*>(&rows->rc[r]);
+                        s[r] += c.y;
+                        s[r + 1] += c.w;
+                    }
+                    __syncwarp();
+                    if (j + 1 < n && lane == 0) mbar_arrive(decided + 8 * (1 - x));
+                    uint32_t p[NR / 2], p2[NR / 2];
+                    // (a far block's part of the normaliser comes in a round before the weights: a loop, as more code would
+                    // push this one out of the instruction cache)
+                    float base = blk.far ? W_EXP - blk.lv : W_EXP, back = blk.far ? 1.f : blk.back;
+#pragma unroll 1
+                    for (int i = blk.far ? 2 : 1; i > 0; --i) {
+#pragma unroll
+                        for (int r = 0; r < NR; r += 2) {
+                            const float y0 = ex2(s[r] + base), y1 = ex2(s[r + 1] + base);
+                            l[r] = fmaf(y0, back, l[r]);
+                            l[r + 1] = fmaf(y1, back, l[r + 1]);
+                            p[r / 2] = pack_f16(y0, y1);
+                            if (PT == 2) {
+                                const float2 h = unpack_f16(p[r / 2]);
+                                p2[r / 2] = pack_f16(y0 - h.x, y1 - h.y);
+                            }
+                        }
+                        base = W_EXP;
+                        back = 0.f;
+                    }
+                    if (M::PBUF == 1 && j > 0) wait_warp(pv_done, (done0 + j - 1) & 1);   // (a failure shows at the next meeting)
+                    uint8_t* buf = smem + M::P + (M::PBUF == 1 ? 0 : x) * PT * M::PT_BYTES + tid * 64;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint4* at = reinterpret_cast<uint4*>(buf + ((c ^ ((tid >> 1) & 3)) << 4));
+                        *at = make_uint4(p[4 * c], p[4 * c + 1], p[4 * c + 2], p[4 * c + 3]);
+                        if (PT == 2) *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(at) + M::PT_BYTES) = make_uint4(p2[4 * c], p2[4 * c + 1], p2[4 * c + 2], p2[4 * c + 3]);
+                    }
+                    tc_fence_before();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_ready + 8 * x);
                 }
-                tc_fence_before();
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_ready + 8 * x);
             }
             done0 += n;
             tile0 += n;
@@ -400,7 +410,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
             tc_fence_after();
             // O^T: thread = channel; this group's half of the rows
             const bool whole = w.from == 0 && w.until == w.it.steps;
-            const float un = pow2i(-(int)W_EXP);
+            const float un = acc_unit<PT>((n - 1) % window<PT>() + 1);
             // (a loop: what runs once a part should not push the loops of every step out of the instruction cache)
 #pragma unroll 1
             for (int r = 16 * x; r < min(16 * x + 16, nrows); ++r) {
@@ -411,10 +421,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) sum += rows->sum[i][r];
-                sum *= un;
+                sum *= pow2i(-(int)W_EXP);
                 const float m = -rows->rc[r].y;
                 float o = __uint_as_float(y) * un;
-                if (PT == 2 && n > FRESH && tid < D) o = fmaf(part->o[r][tid], since(rows->m_sum[r], m), o);
+                if (n > window<PT>() && tid < D) o = fmaf(part->o[r][tid], since(rows->m_sum[r], m), o);
                 if (whole) {
                     sum = row_sum(sum, f, first_seeing(a, nq, L));
                     const int64_t row = q0 + f / G, head = w.at.h * G + f % G;
@@ -469,7 +479,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                     // (D 64: the tile's upper 64 channels are the lower ones again, and unused)
                     const uint32_t va = uniform(desc_outer(sb + M::H + (vt % HS) * M::HT, D == 128 ? TN * 128 : 0));
                     const uint32_t pb = uniform(desc_outer(sb + M::P + (M::PBUF == 1 ? 0 : x) * PT * M::PT_BYTES, 0));
-                    const uint32_t acc = !starts_fresh<PT>(j);
+                    const uint32_t acc = j % window<PT>() != 0;
                     if (elect_one()) {
 #pragma unroll
                         for (int z = 0; z < PT; ++z)

@@ -293,33 +293,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
             Part<D, TILES>* part = TILES == 1 && x == 1 ? &sp->odd[blockIdx.x] : &sp->cta[blockIdx.x][w.from == 0 ? 1 : 0];
             float m_sum = -INFINITY;
             bool summed = false;
-            for (int j = 0; j < mine; ++j, ++steps) {
-                const uint32_t tile = tile0 + j * EACH + (TILES == 1 ? x : 0);
+            for (int j0 = 0; j0 < mine; j0 += window<PT>()) {
                 // A part's first scores are waited for before its first scales: a tile that takes no part in some items
                 // does not see every phase of the scales' barriers, and these scores come after all phases but the last.
-                if (j == 0 && !wait_warp(s_full + 8 * x, steps & 1)) break;
-                if (!wait_warp(sc_full + 8 * (tile % SS), tile / SS & 1)) break;
-                const int t0 = w.it.tok0 + (w.from + (int)(tile - tile0)) * TN;
-                const Block* sc = scales + tile % SS * NB;
-                uint32_t odd_k = 0;          // blocks whose factor is no positive number: their scores are taken in full below
-                bool far = false;
-#pragma unroll
-                for (int c = 0; c < NB; ++c) {
-                    const float k = qf * sc[c].k;
-                    if (!(k > 0.f && k < INFINITY)) odd_k |= 1u << c;
-                    far |= sc[c].far;
-                }
-                const bool prep = __any_sync(0xffffffffu, t0 < free_lo || t0 + TN > free_hi || odd_k != 0);
-                bool again = PT == 2 || far || __any_sync(0xffffffffu, !(fabsf(m) <= 1048576.f));
-                if (j > 0 && !wait_warp(s_full + 8 * x, steps & 1)) break;
-                if (u0.wl < u0.wf) {         // no rows: whatever lies there as weights only meets its own rows
-                    if (lane == 0) mbar_arrive(p_ready + 8 * x);
-                    continue;
-                }
-                tc_fence_after();
-                const bool fresh = starts_fresh<PT>(j);
-                if (PT == 2 && fresh && j > 0) {        // the scores came after all products so far
-                    const float un = pow2i(-(int)W_EXP), keep = since(m_sum, m);
+                if (!wait_warp(s_full + 8 * x, steps & 1)) break;
+                if (j0 > 0 && u0.wf <= u0.wl) {         // the next window: its scores came after all products so far
+                    tc_fence_after();
+                    const float un = acc_unit<PT>(window<PT>()), keep = since(m_sum, m);
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t y[32];
@@ -339,131 +319,155 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                     m_sum = m;
                     summed = true;
                 }
-                // Scores that a row does not see become -inf.  Blocks with an odd factor are multiplied here; or all become z - m.
-                auto prepare = [&](uint32_t full, bool less, float off) {
-#pragma unroll 1
-                    for (int c = 0; c < TN / 16; ++c) {
-                        uint32_t y[16];
-                        tmem_ld_32x32b_x16(tm_s(x) + lanes + 16 * c, y);
-                        tmem_ld_wait();
-                        const float k = full >> (c >> 1) & 1 ? qf * sc[c >> 1].k : 1.f;
-                        const float lv = less ? sc[c >> 1].lv : 0.f;
-                        const int lo = rlo - t0 - 16 * c, hi = rhi - t0 - 16 * c;
+                for (int j = j0; j < min(j0 + window<PT>(), mine); ++j, ++steps) {
+                    const uint32_t tile = tile0 + j * EACH + (TILES == 1 ? x : 0);
+                    if (!wait_warp(sc_full + 8 * (tile % SS), tile / SS & 1)) break;
+                    const int t0 = w.it.tok0 + (w.from + (int)(tile - tile0)) * TN;
+                    const Block* sc = scales + tile % SS * NB;
+                    uint32_t odd_k = 0;          // blocks whose factor is no positive number: their scores are taken in full below
+                    bool far = false;
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            y[e] = e >= lo && e < hi ? __float_as_uint(fmaf(__uint_as_float(y[e]), k, lv) - off) : 0xFF800000u;
-                        tmem_st_32x32b_x16(tm_s(x) + lanes + 16 * c, y);
+                    for (int c = 0; c < NB; ++c) {
+                        const float k = qf * sc[c].k;
+                        if (!(k > 0.f && k < INFINITY)) odd_k |= 1u << c;
+                        far |= sc[c].far;
                     }
-                    tmem_st_wait();
-                };
-                uint32_t full = 0;
-                if (prep) {
-                    // one choice of blocks for the warp: a factor that is odd in one row is taken in full in all
-                    full = __reduce_or_sync(0xffffffffu, odd_k);
-                    prepare(full, false, 0.f);
-                }
-                bool less = false;           // m has been taken off
-                // One pass: weights against the m so far, kept in registers until the step's maximum is known.  Where
-                // that has grown by more than GROW (and at first) the maximum comes before them.  f32 outputs
-                // (whose weights take twice the registers) always take the maximum first.
-                while (true) {
-                    if (again) {
-                        float top = -INFINITY;
+                    const bool prep = __any_sync(0xffffffffu, t0 < free_lo || t0 + TN > free_hi || odd_k != 0);
+                    bool again = PT == 2 || far || __any_sync(0xffffffffu, !(fabsf(m) <= 1048576.f));
+                    if (j > j0 && !wait_warp(s_full + 8 * x, steps & 1)) break;
+                    if (u0.wl < u0.wf) {         // no rows: whatever lies there as weights only meets its own rows
+                        if (lane == 0) mbar_arrive(p_ready + 8 * x);
+                        continue;
+                    }
+                    tc_fence_after();
+                    const bool fresh = j == j0;
+                    // Scores that a row does not see become -inf.  Blocks with an odd factor are multiplied here; or all become z - m.
+                    auto prepare = [&](uint32_t full, bool less, float off) {
 #pragma unroll 1
-                        for (int c = 0; c < NB; ++c) {
-                            uint32_t y[32];
-                            tmem_ld_32x32b_x32(tm_s(x) + lanes + 32 * c, y);
+                        for (int c = 0; c < TN / 16; ++c) {
+                            uint32_t y[16];
+                            tmem_ld_32x32b_x16(tm_s(x) + lanes + 16 * c, y);
                             tmem_ld_wait();
-                            float mx = -INFINITY;
+                            const float k = full >> (c >> 1) & 1 ? qf * sc[c >> 1].k : 1.f;
+                            const float lv = less ? sc[c >> 1].lv : 0.f;
+                            const int lo = rlo - t0 - 16 * c, hi = rhi - t0 - 16 * c;
 #pragma unroll
-                            for (int e = 0; e < 32; e += 2) mx = max3(mx, __uint_as_float(y[e]), __uint_as_float(y[e + 1]));
-                            top = fmaxf(top, fmaf(mx, full >> c & 1 ? 1.f : qf * sc[c].k, sc[c].lv));
+                            for (int e = 0; e < 16; ++e)
+                                y[e] = e >= lo && e < hi ? __float_as_uint(fmaf(__uint_as_float(y[e]), k, lv) - off) : 0xFF800000u;
+                            tmem_st_32x32b_x16(tm_s(x) + lanes + 16 * c, y);
                         }
-                        const bool grow = top > m + GROW;
-                        if (__any_sync(0xffffffffu, grow)) {
-                            const float root = grow ? root_of(m - top) : 1.f, fo = root * root;
-                            m = grow ? top : m;
-                            l = l * root * root;
-                            if (!fresh) {
+                        tmem_st_wait();
+                    };
+                    uint32_t full = 0;
+                    if (prep) {
+                        // one choice of blocks for the warp: a factor that is odd in one row is taken in full in all
+                        full = __reduce_or_sync(0xffffffffu, odd_k);
+                        prepare(full, false, 0.f);
+                    }
+                    bool less = false;           // m has been taken off
+                    // One pass: weights against the m so far, kept in registers until the step's maximum is known.  Where
+                    // that has grown by more than GROW (and at first) the maximum comes before them.  f32 outputs
+                    // (whose weights take twice the registers) always take the maximum first.
+                    while (true) {
+                        if (again) {
+                            float top = -INFINITY;
 #pragma unroll 1
-                                for (int c = 0; c < D / 32; ++c) {
-                                    uint32_t y[32];
-                                    tmem_ld_32x32b_x32(tm_o(x) + lanes + 32 * c, y);
-                                    tmem_ld_wait();
+                            for (int c = 0; c < NB; ++c) {
+                                uint32_t y[32];
+                                tmem_ld_32x32b_x32(tm_s(x) + lanes + 32 * c, y);
+                                tmem_ld_wait();
+                                float mx = -INFINITY;
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * fo);
-                                    tmem_st_32x32b_x32(tm_o(x) + lanes + 32 * c, y);
+                                for (int e = 0; e < 32; e += 2) mx = max3(mx, __uint_as_float(y[e]), __uint_as_float(y[e + 1]));
+                                top = fmaxf(top, fmaf(mx, full >> c & 1 ? 1.f : qf * sc[c].k, sc[c].lv));
+                            }
+                            const bool grow = top > m + GROW;
+                            if (__any_sync(0xffffffffu, grow)) {
+                                const float root = grow ? root_of(m - top) : 1.f, fo = root * root;
+                                m = grow ? top : m;
+                                l = l * root * root;
+                                if (!fresh) {
+#pragma unroll 1
+                                    for (int c = 0; c < D / 32; ++c) {
+                                        uint32_t y[32];
+                                        tmem_ld_32x32b_x32(tm_o(x) + lanes + 32 * c, y);
+                                        tmem_ld_wait();
+#pragma unroll
+                                        for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * fo);
+                                        tmem_st_32x32b_x32(tm_o(x) + lanes + 32 * c, y);
+                                    }
+                                }
+                            }
+                            // From 2^20 on z is rounded before m is taken off, as it was for m, and the exponent is
+                            // added after that: a fused step would leave its own rounding, which is then no longer small.
+                            if (__any_sync(0xffffffffu, fabsf(m) > 1048576.f && fabsf(m) < INFINITY)) {
+                                prepare(~full & ((1u << NB) - 1), true, m == -INFINITY ? 0.f : m);
+                                full = (1u << NB) - 1;
+                                less = true;
+                            }
+                            if (far) {           // m is settled: their part of the normaliser
+#pragma unroll 1
+                                for (int c = 0; c < TN / 16; ++c) {
+                                    const Block b = sc[c >> 1];
+                                    if (!b.far) continue;
+                                    uint32_t y[16];
+                                    tmem_ld_32x32b_x16(tm_s(x) + lanes + 16 * c, y);
+                                    tmem_ld_wait();
+                                    const float kc = full >> (c >> 1) & 1 ? 1.f : qf * b.k;
+                                    const float sub = W_EXP - (less ? b.lv : m == -INFINITY ? 0.f : m);
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) l += ex2(fmaf(__uint_as_float(y[e]), kc, sub));
                                 }
                             }
                         }
-                        // From 2^20 on z is rounded before m is taken off, as it was for m, and the exponent is
-                        // added after that: a fused step would leave its own rounding, which is then no longer small.
-                        if (__any_sync(0xffffffffu, fabsf(m) > 1048576.f && fabsf(m) < INFINITY)) {
-                            prepare(~full & ((1u << NB) - 1), true, m == -INFINITY ? 0.f : m);
-                            full = (1u << NB) - 1;
-                            less = true;
-                        }
-                        if (far) {           // m is settled: their part of the normaliser
-#pragma unroll 1
-                            for (int c = 0; c < TN / 16; ++c) {
-                                const Block b = sc[c >> 1];
-                                if (!b.far) continue;
-                                uint32_t y[16];
-                                tmem_ld_32x32b_x16(tm_s(x) + lanes + 16 * c, y);
-                                tmem_ld_wait();
-                                const float kc = full >> (c >> 1) & 1 ? 1.f : qf * b.k;
-                                const float sub = W_EXP - (less ? b.lv : m == -INFINITY ? 0.f : m);
+                        const float m0 = less || m == -INFINITY ? 0.f : m;
+                        float top = -INFINITY, add = 0.f;
+                        uint32_t s[2][32], p[PT == 1 ? NB : 1][16], p2[16];
+                        tmem_ld_32x32b_x32(tm_s(x) + lanes, s[0]);
 #pragma unroll
-                                for (int e = 0; e < 16; ++e) l += ex2(fmaf(__uint_as_float(y[e]), kc, sub));
+                        for (int c = 0; c < NB; ++c) {
+                            tmem_ld_wait();
+                            if (c + 1 < NB) tmem_ld_32x32b_x32(tm_s(x) + lanes + 32 * (c + 1), s[(c + 1) & 1]);
+                            const Block b = sc[c];
+                            const float kc = full >> c & 1 ? 1.f : qf * b.k;
+                            const float sub = W_EXP + (less ? 0.f : b.lv - m0);
+                            const uint64_t k2 = pair(kc, kc), sub2 = pair(sub, sub);
+                            const uint32_t(&y)[32] = s[c & 1];
+                            uint32_t(&pc)[16] = p[PT == 1 ? c : 0];
+                            uint64_t sum = 0;
+                            float mx = -INFINITY;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const float a0 = __uint_as_float(y[2 * e]), a1 = __uint_as_float(y[2 * e + 1]);
+                                if (PT == 1) mx = max3(mx, a0, a1);
+                                const float2 z = unpair(fma2(pair(a0, a1), k2, sub2));
+                                weights<PT>(ex2(z.x), ex2(z.y), sum, pc[e], p2[e]);
+                            }
+                            top = fmaxf(top, fmaf(mx, kc, b.lv));
+                            const float2 z = unpair(sum);
+                            add = fmaf(z.x + z.y, b.back, add);
+                            if (PT == 2) {
+                                tmem_st_32x32b_x16(tm_s(x) + lanes + 32 * c, pc);
+                                tmem_st_32x32b_x16(tm_s(x) + lanes + 32 * c + 16, p2);
                             }
                         }
-                    }
-                    const float m0 = less || m == -INFINITY ? 0.f : m;
-                    float top = -INFINITY, add = 0.f;
-                    uint32_t s[2][32], p[PT == 1 ? NB : 1][16], p2[16];
-                    tmem_ld_32x32b_x32(tm_s(x) + lanes, s[0]);
-#pragma unroll
-                    for (int c = 0; c < NB; ++c) {
-                        tmem_ld_wait();
-                        if (c + 1 < NB) tmem_ld_32x32b_x32(tm_s(x) + lanes + 32 * (c + 1), s[(c + 1) & 1]);
-                        const Block b = sc[c];
-                        const float kc = full >> c & 1 ? 1.f : qf * b.k;
-                        const float sub = W_EXP + (less ? 0.f : b.lv - m0);
-                        const uint64_t k2 = pair(kc, kc), sub2 = pair(sub, sub);
-                        const uint32_t(&y)[32] = s[c & 1];
-                        uint32_t(&pc)[16] = p[PT == 1 ? c : 0];
-                        uint64_t sum = 0;
-                        float mx = -INFINITY;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const float a0 = __uint_as_float(y[2 * e]), a1 = __uint_as_float(y[2 * e + 1]);
-                            if (PT == 1) mx = max3(mx, a0, a1);
-                            const float2 z = unpair(fma2(pair(a0, a1), k2, sub2));
-                            weights<PT>(ex2(z.x), ex2(z.y), sum, pc[e], p2[e]);
+                        if (PT == 1 && !again && __any_sync(0xffffffffu, top > m + GROW)) {
+                            again = true;
+                            continue;
                         }
-                        top = fmaxf(top, fmaf(mx, kc, b.lv));
-                        const float2 z = unpair(sum);
-                        add = fmaf(z.x + z.y, b.back, add);
-                        if (PT == 2) {
-                            tmem_st_32x32b_x16(tm_s(x) + lanes + 32 * c, pc);
-                            tmem_st_32x32b_x16(tm_s(x) + lanes + 32 * c + 16, p2);
-                        }
-                    }
-                    if (PT == 1 && !again && __any_sync(0xffffffffu, top > m + GROW)) {
-                        again = true;
-                        continue;
-                    }
-                    l += add;
-                    if (PT == 1) {
+                        l += add;
+                        if (PT == 1) {
 #pragma unroll
-                        for (int c = 0; c < NB; ++c) tmem_st_32x32b_x16(tm_s(x) + lanes + 32 * c, p[PT == 1 ? c : 0]);
+                            for (int c = 0; c < NB; ++c) tmem_st_32x32b_x16(tm_s(x) + lanes + 32 * c, p[PT == 1 ? c : 0]);
+                        }
+                        break;
                     }
-                    break;
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_ready + 8 * x);
                 }
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_ready + 8 * x);
+                if (!alive) break;
             }
             const Walk cur = w;              // this part; w goes on to the next
             tile0 += n;
@@ -473,8 +477,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
             ++parts;
             tc_fence_after();
             const bool begins = cur.from == 0, ends = cur.until == cur.it.steps, whole = begins && ends;
-            const float un = pow2i(-(int)W_EXP);
-            l *= un;
+            const float un = acc_unit<PT>((mine - 1) % window<PT>() + 1);
+            l *= pow2i(-(int)W_EXP);
             // TILES 1: the odd steps' result goes to the even steps' threads
             Part<D, TILES>* odd = &sp->odd[TILES == 1 ? blockIdx.x : 0];
             const bool both = TILES == 1 && n > 1;
@@ -514,7 +518,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                 float y[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(v[e]) * w0;
-                if (PT == 2 && summed && u0.in) {
+                if (summed && u0.in) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float4 z = part->o[8 * c + e][u0.r];
@@ -643,7 +647,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                         const uint32_t next = kt + 2 * EACH;
                         if (!h_wait(kt + 1) || (j + 1 < mine && !h_wait(next)) || !take(both)) break;
                         if (!wait_warp(p_ready + 8 * x, steps++ & 1)) break;
-                        pv(kt + 1, !starts_fresh<PT>(j));
+                        pv(kt + 1, j % window<PT>() != 0);
                         if (j + 1 < mine) {
                             qk(next, both);
                             if (elect_one()) {

@@ -10,7 +10,7 @@ namespace {
 constexpr int TM = 128;                // rows or channels of a tensor-core tile
 constexpr int TN = 128;                // tokens of a step
 constexpr int NB = TN / BLK;           // blocks of a step
-constexpr int MAX_CTAS = 256;          // workspace bound, and no more than a plan's threads
+constexpr int MAX_CTAS = 160;          // workspace bound: a full GB300 has no more SMs (and no more than a plan's threads)
 constexpr int PLAN_THREADS = 1024;
 // Beginning and ending an item counts as so many steps in the shares.  Counted too low, the shares of many short items end
 // last: a 16384-token prompt took 2234 us with 3, 1811 with 5, 1824 with 7, 1867 with 12; 25 rows of 24 sequences 106, 92, 82
@@ -19,15 +19,19 @@ constexpr int ITEM_COST = 7;
 constexpr int SS = 8;                  // steps whose scales are kept
 constexpr int LB = 32 / NB;            // steps that the loading warp looks up at a time
 constexpr int HS = 4;                  // fp16 operand tiles in the ring (keys and values alternate)
-// The tensor cores truncate as they add to an accumulator: about a quarter of 2^-24 of it per product of 16 tokens, always
-// towards zero (measured: 3.3e-6 after 12.5 steps of two terms).  For f32 outputs a part's accumulator starts afresh every
-// FRESH of a tile's steps, and what it held is added, rounded to nearest, to a sum in the workspace: 4e-6 at most (and 5 % of
-// the time).  For 16-bit outputs (eight products a step, one term) the loss stays below 6e-5 up to 60000 tokens in one share,
-// under their own rounding, and is left: the test alone cost 6 %.
-constexpr int FRESH = 16;
+// The tensor cores truncate what they add to an accumulator, a product of 16 tokens at a time: 0.4e-8 to 3.3e-8 of it each, the
+// most where the values have one sign, always towards zero (measured: 16 steps of two terms lost 8.8e-6).  So an accumulator
+// starts afresh every window<PT>() of a tile's steps, and what it held is added, rounded to nearest, to a sum in the workspace.
+// f32 outputs: 8 steps (16: 4 % faster, 4: 8 % slower for ragged prompts), and LOST a product is put back, the middle of what
+// short windows lose: what is left is 2e-6 at most and a few 1e-7 mostly.  16-bit outputs (half the products): 128 steps, 7e-5
+// at most, under their own rounding.
 template <int PT>
-__device__ __forceinline__ bool starts_fresh(int j) { return PT == 2 ? j % FRESH == 0 : j == 0; }
-constexpr float W_EXP = 10.f, GROW = 5.f;   // weights carry 2^10 and grow by 2^5 before the maximum moves
+constexpr int window() { return PT == 2 ? 8 : 128; }
+constexpr float LOST = 1.1e-8f;
+// From an accumulator that holds `steps` steps to O.
+template <int PT>
+__device__ __forceinline__ float acc_unit(int steps) { return PT == 2 ? fmaf((float)steps, LOST * (PT * TN / 16), 1.f) * 0x1p-10f : 0x1p-10f; }
+constexpr float W_EXP = 10.f, GROW = 5.f;   // weights carry 2^10 (acc_unit takes it off) and grow by 2^5 before the maximum moves
 
 // What the softmax needs of a block (written by the loading warp, which has the time).
 struct alignas(16) Block {
@@ -297,8 +301,6 @@ __device__ __forceinline__ void convert_tile(const uint8_t* raw, uint8_t* out, i
     }
 }
 
-// What a sum against the maximum m0 counts against m.
-__device__ __forceinline__ float since(float m0, float m) { return m0 == -INFINITY ? 1.f : ex2(m0 - m); }
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));

@@ -101,10 +101,11 @@ cq_status cq_kv8_read(const cq_kv8_cache* cache, const int32_t* first, const int
  * row's largest), codes exactly, softmax weights times their value block's scale as
  * one fp16 term for 16-bit outputs (11 bits) and as two for f32 outputs (22 bits), in
  * both cases to 2^-35 of the row's largest such product; tokens that a row does not
- * see, or that have no weight, do not enter, whatever their scale; maxima, sums, scores and accumulators in f32; one rounding to yt.  The tensor
- * cores truncate as they accumulate: f32 outputs lose at most 5e-6 to that, 16-bit
- * ones about 1e-9 a token that one SM takes in turn (6e-5 for 60000).  Results do
- * not depend on timing: the same call gives the same bits.
+ * see, or that have no weight, do not enter, whatever their scale; maxima, sums,
+ * scores and accumulators in f32; one rounding to yt.  The tensor cores truncate as
+ * they accumulate, so accumulators are added up in windows: f32 outputs lose at most
+ * 5e-6 of sums of one sign to that (a few 1e-7 mostly), 16-bit ones 7e-5, whatever
+ * the length.  Results do not depend on timing: the same call gives the same bits.
  * Workspace: cq_attn_kv8_workspace_bytes(...) bytes, 256-byte aligned; a buffer for
  * the largest T, B and max_q serves every call with smaller ones.
  * ------------------------------------------------------------------------- */

@@ -310,3 +310,30 @@ def test_calls_in_a_chain(n, group):
     want, got = run(torch.cuda.synchronize), run(lambda: None)
     assert cq.cq_get_device_error() == 0
     assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+# ---- sums that the tensor cores truncate -------------------------------------------------------------------------
+
+@pytest.mark.parametrize("n,group", [(1, 4), (1, 16), (5, 5), (16, 4), (150, 1)])
+@pytest.mark.parametrize("out", ["f32", "f16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_sums_of_one_sign(n, group, out, D):
+    """Values of one sign over 40960 tokens that one SM (few rows: one warp) takes in turn.  Truncation shrinks such sums
+    the most, all alike: the results' projection on the exact ones may be off by 5e-6 for f32 outputs (a window of 128
+    products, at most 4.3e-8 each) and 7e-5 for 16-bit ones (1024 products, measured at most 6.6e-8 each)."""
+    B, Hkv, L, page = 64, 16, 40960, 1024
+    s = Setup(64, [L], Hkv, D, page, spare=0)
+    s.len = [L]
+    k, v = s.rows(L, Hkv, "bf16", 0.3), s.rows(L, Hkv, "bf16", 0.3).abs()
+    cq.cq_kv8_write(s.cache, k, v, starts([L]), i32([L]))
+    k, v = (x.double().transpose(0, 1) for x in s.read("f32"))
+    s.cache = cq.cq_kv8_cache(s.cache.Kq, s.cache.Ks, s.cache.Vq, s.cache.Vs, s.table.repeat(B, 1))   # all over the same pages
+    s.B, s.len = B, [L] * B
+    q, o, _ = s.attend([n] * B, group, "f16", out, causal=False, lse=False)
+    for b in (0, 30, 63):
+        x = q[b * n:b * n + n].double().view(n, Hkv, group, D).permute(1, 0, 2, 3).reshape(Hkv, n * group, D)
+        w = torch.softmax(x @ k.transpose(1, 2) * D ** -0.5, 2)
+        ref = (w @ v).view(Hkv, n, group, D).transpose(0, 1).reshape(n, Hkv * group, D)
+        err = o[b * n:b * n + n].double() - ref
+        along = float((err * ref).sum() / (ref * ref).sum())
+        assert abs(along) <= (5e-6 if out == "f32" else 7e-5), along
