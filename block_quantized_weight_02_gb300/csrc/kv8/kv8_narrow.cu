@@ -90,7 +90,7 @@ __device__ __forceinline__ float across(const float (&v)[NR]) {
     return t[0];
 }
 
-template <int D, int PT>
+template <int D, int PT, bool WIN>
 __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ Maps maps, const AttnArgs a, uint64_t wait_ns) {
     using M = Smem<D, PT>;
     extern __shared__ __align__(1024) uint8_t raw[];
@@ -257,8 +257,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                 }
             };
             bool gone = false;
-            for (int j0 = 0; j0 < n && !gone; j0 += window<PT>()) {
-                if (__builtin_expect(j0 > 0 && x == 0, PT == 2)) {    // the next window: what the last one holds goes to the sum
+            for (int j0 = 0; j0 < n && !gone; j0 += WIN ? window<PT>() : n) {
+                if (WIN && __builtin_expect(j0 > 0 && x == 0, PT == 2)) {    // the next window: what the last one holds goes to the sum
                     // (the window's first scores come after all products but the last, whose phase follows on theirs)
                     wait_warp(s_full, steps & 1);
                     follow();
@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                     any_of(false, 1 + x, 128);               // all have read the old maxima
                     if (quarter == 0) rows->m_sum[lane] = -rows->rc[lane].y;
                 }
-                for (int j = j0 + x; j < min(j0 + window<PT>(), n); j += 2, ++steps) {
+                for (int j = j0 + x; j < (WIN ? min(j0 + window<PT>(), n) : n); j += 2, ++steps) {
                     const uint32_t tile = tile0 + j;
                     wait_warp(sc_full + 8 * (tile % SS), tile / SS & 1);
                     const Block blk = scales[tile % SS * NB + quarter];   // this warp's 32 tokens are one block
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                 sum *= pow2i(-(int)W_EXP);
                 const float m = -rows->rc[r].y;
                 float o = __uint_as_float(y) * un;
-                if (n > window<PT>() && tid < D) o = fmaf(part->o[r][tid], since(rows->m_sum[r], m), o);
+                if (WIN && n > window<PT>() && tid < D) o = fmaf(part->o[r][tid], since(rows->m_sum[r], m), o);
                 if (whole) {
                     sum = row_sum(sum, f, first_seeing(a, nq, L));
                     const int64_t row = q0 + f / G, head = w.at.h * G + f % G;
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                     // (D 64: the tile's upper 64 channels are the lower ones again, and unused)
                     const uint32_t va = uniform(desc_outer(sb + M::H + (vt % HS) * M::HT, D == 128 ? TN * 128 : 0));
                     const uint32_t pb = uniform(desc_outer(sb + M::P + (M::PBUF == 1 ? 0 : x) * PT * M::PT_BYTES, 0));
-                    const uint32_t acc = j % window<PT>() != 0;
+                    const uint32_t acc = WIN ? j % window<PT>() != 0 : j > 0;
                     if (elect_one()) {
 #pragma unroll
                         for (int z = 0; z < PT; ++z)
@@ -535,21 +535,27 @@ __global__ void __launch_bounds__(256) k_narrow_join(const AttnArgs a, int ctas)
                             [&](int j) { return j == 0 ? &sp->cta[i][1] : &sp->cta[i + j][0]; }, (Part<D>*)nullptr);
 }
 
-template <int D, int PT>
+template <int D, int PT, bool WIN>
 cudaError_t run(const AttnArgs& a, cudaStream_t s) {
     Maps maps;
     if (!make_maps(a, maps)) return cudaErrorInvalidValue;
     constexpr size_t smem = Smem<D, PT>::END + 1024;
     static_assert(smem <= 232448, "shared memory");
-    cudaError_t e = cudaFuncSetAttribute(k_narrow<D, PT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(k_narrow<D, PT, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int ctas = std::min(num_sms(), MAX_CTAS), G = a.Hq / a.c.Hkv;
     e = launch_pdl(k_tiles_plan<NR>, dim3(1), dim3(PLAN_THREADS), 0, s, a, &static_cast<Space<D>*>(a.ws)->list,
                    (int)slots_of(a.b.T, G, a.c.B, NR), ctas);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(k_narrow<D, PT>, dim3(ctas), dim3(THREADS), smem, s, maps, a, (uint64_t)options().wait_ns.load());
+    e = launch_pdl(k_narrow<D, PT, WIN>, dim3(ctas), dim3(THREADS), smem, s, maps, a, (uint64_t)options().wait_ns.load());
     if (e != cudaSuccess) return e;
     return launch_pdl(k_narrow_join<D>, dim3(ctas, NR * (D / 4) / 256), dim3(256), 0, s, a, ctas);
+}
+
+template <int D>
+cudaError_t run_d(const AttnArgs& a, cudaStream_t s) {
+    if (a.yt == CQ_F32) return run<D, 2, true>(a, s);
+    return needs_windows(a) ? run<D, 1, true>(a, s) : run<D, 1, false>(a, s);
 }
 
 }  // namespace
@@ -558,10 +564,7 @@ bool narrow_serves(int64_t rows) { return rows <= NR; }
 size_t narrow_workspace(int64_t T, int64_t G, int64_t D, int64_t B) {
     return (D == 128 ? sizeof(Space<128>) : sizeof(Space<64>)) + slots_of(T, G, B, NR) * sizeof(Item);
 }
-cudaError_t launch_narrow(const AttnArgs& a, cudaStream_t s) {
-    if (a.D == 128) return a.yt == CQ_F32 ? run<128, 2>(a, s) : run<128, 1>(a, s);
-    return a.yt == CQ_F32 ? run<64, 2>(a, s) : run<64, 1>(a, s);
-}
+cudaError_t launch_narrow(const AttnArgs& a, cudaStream_t s) { return a.D == 128 ? run_d<128>(a, s) : run_d<64>(a, s); }
 
 }  // namespace kv8
 }  // namespace cq

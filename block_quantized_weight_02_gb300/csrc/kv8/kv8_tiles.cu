@@ -97,7 +97,7 @@ __device__ __forceinline__ void weights(float y0, float y1, uint64_t& sum, uint3
         p2 = pack_f16(y0 - h.x, y1 - h.y);
     }
 }
-template <int D, int PT, int TILES>
+template <int D, int PT, int TILES, bool WIN>
 __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Maps maps, const AttnArgs a, uint64_t wait_ns) {
     using M = Smem<D, TILES>;
     extern __shared__ __align__(1024) uint8_t raw[];
@@ -293,11 +293,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
             Part<D, TILES>* part = TILES == 1 && x == 1 ? &sp->odd[blockIdx.x] : &sp->cta[blockIdx.x][w.from == 0 ? 1 : 0];
             float m_sum = -INFINITY;
             bool summed = false;
-            for (int j0 = 0; j0 < mine; j0 += window<PT>()) {
+            for (int j0 = 0; j0 < mine; j0 += WIN ? window<PT>() : mine) {
                 // A part's first scores are waited for before its first scales: a tile that takes no part in some items
                 // does not see every phase of the scales' barriers, and these scores come after all phases but the last.
                 if (!wait_warp(s_full + 8 * x, steps & 1)) break;
-                if (j0 > 0 && u0.wf <= u0.wl) {         // the next window: its scores came after all products so far
+                if (WIN && j0 > 0 && u0.wf <= u0.wl) {  // the next window: its scores came after all products so far
                     tc_fence_after();
                     const float un = acc_unit<PT>(window<PT>()), keep = since(m_sum, m);
 #pragma unroll 1
@@ -319,7 +319,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                     m_sum = m;
                     summed = true;
                 }
-                for (int j = j0; j < min(j0 + window<PT>(), mine); ++j, ++steps) {
+                for (int j = j0; j < (WIN ? min(j0 + window<PT>(), mine) : mine); ++j, ++steps) {
                     const uint32_t tile = tile0 + j * EACH + (TILES == 1 ? x : 0);
                     if (!wait_warp(sc_full + 8 * (tile % SS), tile / SS & 1)) break;
                     const int t0 = w.it.tok0 + (w.from + (int)(tile - tile0)) * TN;
@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                 float y[32];
 #pragma unroll
                 for (int e = 0; e < 32; ++e) y[e] = __uint_as_float(v[e]) * w0;
-                if (summed && u0.in) {
+                if (WIN && summed && u0.in) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float4 z = part->o[8 * c + e][u0.r];
@@ -647,7 +647,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                         const uint32_t next = kt + 2 * EACH;
                         if (!h_wait(kt + 1) || (j + 1 < mine && !h_wait(next)) || !take(both)) break;
                         if (!wait_warp(p_ready + 8 * x, steps++ & 1)) break;
-                        pv(kt + 1, j % window<PT>() != 0);
+                        pv(kt + 1, WIN ? j % window<PT>() != 0 : j > 0);
                         if (j + 1 < mine) {
                             qk(next, both);
                             if (elect_one()) {
@@ -701,18 +701,18 @@ __global__ void __launch_bounds__(256) k_tiles_join(const AttnArgs a, int ctas) 
                                  [&](int j) { return j == 0 ? &sp->cta[i][1] : &sp->cta[i + j][0]; }, (Part<D, TILES>*)nullptr);
 }
 
-template <int D, int PT, int TILES>
+template <int D, int PT, int TILES, bool WIN>
 cudaError_t run(const AttnArgs& a, cudaStream_t s) {
     Maps maps;
     if (!make_maps(a, maps)) return cudaErrorInvalidValue;
     constexpr size_t smem = Smem<D, TILES>::END + 1024;
     static_assert(smem <= 232448, "shared memory");
-    cudaError_t e = cudaFuncSetAttribute(k_tiles<D, PT, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(k_tiles<D, PT, TILES, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int ctas = std::min(num_sms(), MAX_CTAS), G = a.Hq / a.c.Hkv, rows = TILES * TM;
     e = launch_pdl(k_tiles_plan<TILES * TM>, dim3(1), dim3(PLAN_THREADS), 0, s, a, &static_cast<Space<D, TILES>*>(a.ws)->list, (int)slots_of(a.b.T, G, a.c.B, rows), ctas);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(k_tiles<D, PT, TILES>, dim3(ctas), dim3(THREADS), smem, s, maps, a, (uint64_t)options().wait_ns.load());
+    e = launch_pdl(k_tiles<D, PT, TILES, WIN>, dim3(ctas), dim3(THREADS), smem, s, maps, a, (uint64_t)options().wait_ns.load());
     if (e != cudaSuccess) return e;
     const unsigned y = (unsigned)((std::min<int64_t>(rows, (int64_t)a.max_q * G) + 31) / 32);
     return launch_pdl(k_tiles_join<D, TILES>, dim3(ctas, y), dim3(256), 0, s, a, ctas);
@@ -720,7 +720,8 @@ cudaError_t run(const AttnArgs& a, cudaStream_t s) {
 
 template <int D, int TILES>
 cudaError_t run_as(const AttnArgs& a, cudaStream_t s) {
-    return a.yt == CQ_F32 ? run<D, 2, TILES>(a, s) : run<D, 1, TILES>(a, s);
+    if (a.yt == CQ_F32) return run<D, 2, TILES, true>(a, s);
+    return needs_windows(a) ? run<D, 1, TILES, true>(a, s) : run<D, 1, TILES, false>(a, s);
 }
 template <int D>
 cudaError_t run_d(const AttnArgs& a, cudaStream_t s) {

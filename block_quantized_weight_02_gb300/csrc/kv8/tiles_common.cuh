@@ -22,12 +22,15 @@ constexpr int HS = 4;                  // fp16 operand tiles in the ring (keys a
 // The tensor cores truncate what they add to an accumulator, a product of 16 tokens at a time: 0.4e-8 to 3.3e-8 of it each, the
 // most where the values have one sign, always towards zero (measured: 16 steps of two terms lost 8.8e-6).  So an accumulator
 // starts afresh every window<PT>() of a tile's steps, and what it held is added, rounded to nearest, to a sum in the workspace.
-// f32 outputs: 8 steps (16: 4 % faster, 4: 8 % slower for ragged prompts), and LOST a product is put back, the middle of what
+// f32 outputs: 8 steps (16: 5 % faster, 4: 9 % slower for ragged prompts), and LOST a product is put back, the middle of what
 // short windows lose: what is left is 2e-6 at most and a few 1e-7 mostly.  16-bit outputs (half the products): 128 steps, 7e-5
 // at most, under their own rounding.
 template <int PT>
 constexpr int window() { return PT == 2 ? 8 : 128; }
 constexpr float LOST = 1.1e-8f;
+// 16-bit outputs whose sequences have no room for more than a window are served without (WIN false): 24 sequences of 25 rows
+// 79.4 against 79.9 us (64 channels: 72.5 against 74), ragged prompts 258 against 270.
+inline bool needs_windows(const AttnArgs& a) { return a.yt == CQ_F32 || a.c.ldt * a.c.page > window<1>() * TN; }
 // From an accumulator that holds `steps` steps to O.
 template <int PT>
 __device__ __forceinline__ float acc_unit(int steps) { return PT == 2 ? fmaf((float)steps, LOST * (PT * TN / 16), 1.f) * 0x1p-10f : 0x1p-10f; }
