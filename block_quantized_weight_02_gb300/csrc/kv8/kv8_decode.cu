@@ -17,7 +17,7 @@
 //
 // Measured, calls in a chain: 4 rows of 8 heads of 128 channels, 32 sequences of 1000 to 32767 tokens, 178 us, 6.1 TB/s
 // (the shares are equal, but a third of the SMs draw 10 % less from memory and end last).  16 rows over 3 x 110000 tokens,
-// 4 heads: 86 us with f16 outputs, 3.9 TB/s, 105 with f32, bound by instructions (conversions, products, exponentials).
+// 4 heads: 86 us with f16 outputs, 3.9 TB/s, 106 with f32, bound by instructions (conversions, products, exponentials).
 // One row of 16 heads of 64 channels behind a window of 1024 tokens, 48 sequences: 38 us, 2.4 TB/s (35 out of a graph), of
 // which the list and the first load take 6 and the joins 8.  8 rows of 4 heads of one sequence of 777 tokens: 14 us of
 // latency.

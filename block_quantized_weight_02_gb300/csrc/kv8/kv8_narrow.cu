@@ -15,8 +15,8 @@
 // exponentials of neighbouring steps overlap), and whoever moves it rescales O^T in tensor memory.
 // Scales, weights and the list of work as in the kernel for many rows.
 //
-// Measured: 25 rows of 8 heads of 128 channels, 24 sequences of 300 to 9000 tokens: 80 us, 2.8 TB/s; f32 outputs 99 us.
-// 64 channels: 73 us.
+// Measured: 25 rows of 8 heads of 128 channels, 24 sequences of 300 to 9000 tokens: 80 us, 2.8 TB/s; f32 outputs 98 us.
+// 64 channels: 72 us.
 // Bound by a step's chain (scores, vote, weights to shared memory, product), two of which are under way at a time, and by
 // 10 us for the list and the joins.
 #include <cfloat>

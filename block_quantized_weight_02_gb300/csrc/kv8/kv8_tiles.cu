@@ -22,9 +22,9 @@
 // first small kernel lays the list out (only the device knows the lengths), a third joins the
 // row tiles that lie across shares, in share order.
 //
-// Measured, 128 channels, bf16 outputs: a 16384-token prompt of 32 heads over 8 KV heads 1790 us, 1230 TFLOP/s; prompts
-// of up to 2000 tokens behind up to 3000 267 us, 853; 2 x 1024 rows against 4500 to 5100 tokens, 24 heads, 139 us, 871.  f32
-// outputs: the ragged prompts 432 us; 64 channels: 221.  80 rows of 8 heads over 300 to 9000 tokens (TILES 1): 123 us.  A step of two tiles takes 1.85 us where its products alone would take 1.1: a tile's
+// Measured, 128 channels, bf16 outputs: a 16384-token prompt of 32 heads over 8 KV heads 1803 us, 1220 TFLOP/s; prompts
+// of up to 2000 tokens behind up to 3000 260 us, 876; 2 x 1024 rows against 4500 to 5100 tokens, 24 heads, 136 us, 889.  f32
+// outputs: the ragged prompts 435 us; 64 channels: 217.  80 rows of 8 heads over 300 to 9000 tokens (TILES 1): 123 us.  A step of two tiles takes 1.85 us where its products alone would take 1.1: a tile's
 // products wait for its exponentials (four cycles a warp and scheduler each) and each hand-over between the two costs a few
 // hundred cycles, which the other tile covers only in part.
 #include "tiles_common.cuh"
