@@ -15,9 +15,10 @@
  * than the others takes bits from them: attention over 4096 normal keys and values is
  * 2 % (norm) from that over the unrounded ones, 5 % if one key channel in 29 is 5 times
  * as large.  Values whose code rounds up past a type's largest one read as infinite in
- * it (above 65024 in fp16, above 127 * 2^121 in bf16 and f32).  A block that is given a value that is not finite gets the
- * scale NaN (its reading is NaN, not a plausible number) until it is written
- * again from its first token.
+ * it (above 65024 in fp16, above 127 * 2^121 in bf16 and f32).  A block that is given
+ * a value that is not finite gets the scale NaN (its reading is NaN, not a plausible
+ * number) until it is written again from its first token; lengths that go back leave a
+ * block its scale as well.
  * Rows past a sequence's length, and scales of blocks past it, are never used:
  * they may hold anything.
  *
@@ -53,9 +54,8 @@ typedef struct {
  * 1 <= B <= 65536.  Kq, Vq, Ks, Vs 16-byte aligned, table 4-byte aligned.
  * Device-detected (CQ_ERR_INDEX): a length outside [0, ldt * page] (attention: or
  * above 2^31 - 2048), a q_start that descends or leaves [0, T], a page number outside
- * [0, pages).  The rows of a
- * sequence with such an entry are unspecified, nothing outside the tensors is
- * touched. */
+ * [0, pages).  The rows of a sequence with such an entry are unspecified, nothing
+ * outside the tensors is touched. */
 
 /* ---------------------------------------------------------------------------
  * Write:  the rows of K and V become the last tokens of their sequences.
