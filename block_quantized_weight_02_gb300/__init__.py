@@ -18,6 +18,8 @@ INCLUDE = os.path.join(os.path.dirname(_HERE), "include", "cq.h")
 CQ_F16, CQ_BF16, CQ_F32 = 0, 1, 2
 CQ_OPT_SMALL_T_MAX, CQ_OPT_FORCE_PATH, CQ_OPT_WAIT_NS, CQ_OPT_TEST_STALL, CQ_OPT_TRACE, CQ_OPT_TC_BN, CQ_OPT_TC_KSPLIT, \
     CQ_OPT_TC_AMODE, CQ_OPT_TC_PAIR, CQ_OPT_STREAM_KERNEL = 0, 1, 2, 3, 4, 5, 6, 7, 8, 9
+CQ_ROPE_HALF, CQ_ROPE_PAIRS = 0, 1
+CQ_ROPE_PLAIN, CQ_ROPE_LINEAR, CQ_ROPE_BASE, CQ_ROPE_RAMP, CQ_ROPE_BANDS = 0, 1, 2, 3, 4
 STATUS = {0: "CQ_OK", 1: "CQ_ERR_NULL", 2: "CQ_ERR_DTYPE", 3: "CQ_ERR_SHAPE", 4: "CQ_ERR_ALIGN",
           5: "CQ_ERR_INDEX", 6: "CQ_ERR_WORKSPACE", 7: "CQ_ERR_CUDA", 8: "CQ_ERR_TIMEOUT", 9: "CQ_ERR_ARCH",
           10: "CQ_ERR_ARG"}
@@ -53,6 +55,13 @@ _SIGS = {
     "cq_attn_kv8_workspace_bytes": (_c_sz, [_c_i64] * 6),
     "cq_attn_kv8": (_c_int, [_c_p, _c_int, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_i64, ctypes.c_float, _c_int,
                              _c_i64, _c_p, _c_int, _c_i64, _c_p, _c_p, _c_sz, _c_p]),
+    "cq_rope": (_c_int, [_c_p, _c_int, _c_i64, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_int, _c_i64, _c_p]),
+    "cq_rope_freqs": (_c_int, [_c_i64, ctypes.c_double, _c_int] + [ctypes.c_double] * 4 + [_c_p, _c_p]),
+    "cq_kv8_write_rope": (_c_int, [_c_p, _c_p, _c_p, _c_int, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_p, _c_p]),
+    "cq_attn_kv8_tree": (_c_int, [_c_p, _c_int, _c_i64, _c_i64, _c_i64, _c_p, _c_p, _c_p, _c_i64, ctypes.c_float, _c_p,
+                                  _c_i64, _c_p, _c_int, _c_i64, _c_p, _c_p, _c_sz, _c_p]),
+    "cq_verify": (_c_int, [_c_p, _c_int, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_p, _c_p, _c_i64, _c_p, _c_i64, _c_i64,
+                           _c_p, _c_p, _c_p, _c_p, _c_i64, _c_p, _c_p]),
     "cq_dequant_q4": (_c_int, [_c_p, _c_p, _c_i64, _c_i64, _c_p, _c_p]),
     "cq_dequant_q8row": (_c_int, [_c_p, _c_p, _c_i64, _c_i64, _c_p, _c_p]),
     "cq_get_device_error": (_c_int, [_c_p]),
@@ -382,6 +391,165 @@ def cq_attn_kv8(Q, cache, q_start, lens, max_q, O, ws, scale=None, causal=True, 
                            cache._types.get(O.dtype, -1), ldo, None if lse is None else lse.data_ptr(),
                            None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(),
                            cache._stream(stream))
+    if raise_on_error:
+        _check(st)
+    return st
+
+
+# ---- a step of drafting (include/cq_draft.h) ----------------------------
+
+class _rope_desc(ctypes.Structure):
+    _fields_ = [("freq", _c_p), ("rot", _c_i64), ("layout", _c_int), ("mag", ctypes.c_float)]
+
+
+class cq_rope_spec:
+    """Rotary positions: freq f32 [rot / 2] radians per position on the device, the
+    layout of the pairs, a factor on the rotated channels.  Holds the tensor and
+    the C descriptor of the same name."""
+
+    def __init__(self, freq, layout=CQ_ROPE_HALF, mag=1.0):
+        import torch
+        if freq.dtype != torch.float32 or freq.dim() != 1 or not freq.is_contiguous():
+            raise ValueError(f"freq must be a dense f32 tensor [rot / 2], got {freq.dtype} {tuple(freq.shape)}")
+        self.freq = freq
+        self.desc = _rope_desc(freq.data_ptr(), 2 * freq.shape[0], layout, mag)
+        self._ref, self._device = ctypes.byref(self.desc), freq.get_device()
+
+    @staticmethod
+    def make(rot, base=10000.0, kind=CQ_ROPE_PLAIN, factor=1.0, low=1.0, high=32.0, trained=8192.0, layout=CQ_ROPE_HALF, device="cuda"):
+        """The spec of cq_rope_freqs' frequencies."""
+        freq, mag = cq_rope_freqs(rot, base, kind, factor, low, high, trained)
+        return cq_rope_spec(freq.to(device), layout, mag)
+
+
+def cq_rope_freqs(rot, base=10000.0, kind=CQ_ROPE_PLAIN, factor=1.0, low=1.0, high=32.0, trained=8192.0):
+    """(frequencies f32 [rot / 2] on the host, mag) of one of the kinds CQ_ROPE_PLAIN .. CQ_ROPE_BANDS."""
+    import torch
+    freq, mag = torch.empty(max(rot, 0) // 2, dtype=torch.float32), ctypes.c_float()
+    _check(lib().cq_rope_freqs(rot, base, kind, factor, low, high, trained, freq.data_ptr(), ctypes.byref(mag)))
+    return freq, mag.value
+
+
+def _here(*tensors):
+    """The current device's current stream, for tensors that all lie on that device (None: left out)."""
+    import torch
+    for t in tensors:
+        if t is not None and t.get_device() < 0:
+            raise ValueError("the tensors must be on a GPU")
+    dev = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor is on device {t.get_device()}, the current one is {dev}")
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _dense(t, what, dtype, shape):
+    """A dense tensor's address (None: NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a dense {dtype} tensor {list(shape)}, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _rows3(t, what):
+    """Row pitch of a [T][H][D] tensor whose rows are dense."""
+    sh, st = t.shape, t.stride()
+    if len(sh) != 3 or (sh[2] > 1 and st[2] != 1) or (sh[1] > 1 and st[1] != sh[2]):
+        raise ValueError(f"{what} must be [T][H][D] with dense rows, got shape {tuple(sh)}, strides {st}")
+    return st[0] if sh[0] > 1 else sh[1] * sh[2]
+
+
+def _mask(mask, T):
+    """(address, words a row) of a tree's mask [T][ldm], int32 or uint32, rows dense."""
+    import torch
+    if mask.dtype not in (torch.int32, torch.uint32) or mask.dim() != 2 or mask.shape[0] != T or (mask.shape[1] > 1 and mask.stride(1) != 1):
+        raise ValueError(f"mask must be int32 [{T}][words] with dense rows, got {mask.dtype} {tuple(mask.shape)}, strides {mask.stride()}")
+    return mask.data_ptr(), mask.shape[1], mask.stride(0) if T > 1 else mask.shape[1]
+
+
+def cq_rope(X, rope, pos, Y=None, stream=None, raise_on_error=True):
+    """Y (None: X itself) = the rows of X [T][H][D] (fp16/bf16/f32) at positions pos
+    (int32 [T]), their first rot channels rotated.  Y may have another type."""
+    import torch
+    Y = X if Y is None else Y
+    ldx, ldy = _rows3(X, "X"), _rows3(Y, "Y")
+    if Y.shape != X.shape:
+        raise ValueError("Y must have the shape of X")
+    T, H, D = X.shape
+    s = _here(X, Y, pos, rope.freq)
+    st = lib().cq_rope(X.data_ptr(), _xt(X), T, H, D, ldx, rope._ref, _dense(pos, "pos", torch.int32, (T,)), Y.data_ptr(), _xt(Y),
+                       ldy, s if stream is None else _stream(stream))
+    if raise_on_error:
+        _check(st)
+    return st
+
+
+def cq_kv8_write_rope(cache, K, V, q_start, lens, rope, pos=None, stream=None, raise_on_error=True):
+    """cq_kv8_write of keys that are rotated on the way: by pos (int32 [T]), or (None)
+    by their rows' places in their sequences."""
+    k, v, xt, T, ldk, ldv = cache._kv(K, V)
+    s = _here(K, V, q_start, lens, pos, rope.freq, cache.Kq)
+    st = lib().cq_kv8_write_rope(cache._ref, k, v, xt, T, ldk, ldv, cache._index(q_start, "q_start", cache.B + 1),
+                                 cache._index(lens, "lens", cache.B), rope._ref, _dense(pos, "pos", cache._int32, (T,)),
+                                 s if stream is None else _stream(stream))
+    if raise_on_error:
+        _check(st)
+    return st
+
+
+def cq_attn_kv8_tree(Q, cache, q_start, lens, max_q, mask, O, ws, scale=None, lse=None, stream=None, raise_on_error=True):
+    """cq_attn_kv8 for drafted trees: a row sees every token before its sequence's rows, and of
+    those the ones whose bits are set in its row of mask (int32 [T][words])."""
+    if Q.dim() != 3:
+        raise ValueError(f"Q must be [T][Hq][{cache.D}], got shape {tuple(Q.shape)}")
+    Hq = Q.shape[1]
+    T, ldq = cache._rows(Q, "Q", Hq)
+    T2, ldo = cache._rows(O, "O", Hq)
+    if T != T2:
+        raise ValueError("O must have the shape of Q")
+    bits, words, ldm = _mask(mask, T)
+    if 32 * words < min(max_q, T):
+        raise ValueError(f"mask rows of {words} words do not hold {max_q} bits")
+    l = _dense(lse, "lse", cache._float32, (T, Hq))
+    s = _here(Q, O, q_start, lens, mask, lse, ws, cache.Kq)
+    st = lib().cq_attn_kv8_tree(Q.data_ptr(), cache._types.get(Q.dtype, -1), T, Hq, ldq, cache._ref,
+                                cache._index(q_start, "q_start", cache.B + 1), cache._index(lens, "lens", cache.B), max_q,
+                                cache.D ** -0.5 if scale is None else scale, bits, ldm, O.data_ptr(),
+                                cache._types.get(O.dtype, -1), ldo, l, None if ws is None else ws.data_ptr(),
+                                0 if ws is None else ws.numel() * ws.element_size(), s if stream is None else _stream(stream))
+    if raise_on_error:
+        _check(st)
+    return st
+
+
+def cq_verify(P, tokens, q_start, max_q, u, u_last, out, path, count, Q=None, mask=None, stream=None, raise_on_error=True):
+    """Which of the drafted tokens stand against the target's probabilities P [T][V], and the
+    token after them.  tokens int32 [T], u f32 [T], u_last f32 [B]; Q [T][V]: the draft's
+    probabilities that the tokens were drawn from (None: chosen ones); mask: the
+    trees (None: chains).  out, path int32 [B][max_q or more], count int32 [B]."""
+    import torch
+    if P.dim() != 2 or (P.shape[1] > 1 and P.stride(1) != 1):
+        raise ValueError(f"P must be [T][V] with dense rows, got shape {tuple(P.shape)}, strides {P.stride()}")
+    T, V = P.shape
+    if Q is not None and (Q.shape != P.shape or Q.dtype != P.dtype or (V > 1 and Q.stride(1) != 1)):
+        raise ValueError(f"Q must have the type and shape of P and dense rows, got {Q.dtype} {tuple(Q.shape)}, strides {Q.stride()}")
+    B = u_last.shape[0]
+    pitch = lambda t: t.stride(0) if T > 1 else (V * t.element_size() + 15) // 16 * 16 // t.element_size()
+    for t, what in ((out, "out"), (path, "path")):
+        if t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] != B or t.shape[1] < max_q or (t.shape[1] > 1 and t.stride(1) != 1) \
+                or t.stride(0) != out.stride(0):
+            raise ValueError(f"{what} must be int32 [{B}][{max_q} or more] with dense rows of one pitch, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
+    bits, words, ldm = (None, 0, 0) if mask is None else _mask(mask, T)
+    if mask is not None and 32 * words < max_q:
+        raise ValueError(f"mask rows of {words} words do not hold {max_q} bits")
+    i32, f32 = torch.int32, torch.float32
+    s = _here(P, tokens, q_start, u, u_last, out, path, count, Q, mask)
+    st = lib().cq_verify(P.data_ptr(), _xt(P), T, V, pitch(P), None if Q is None else Q.data_ptr(), 0 if Q is None else pitch(Q),
+                         _dense(tokens, "tokens", i32, (T,)), bits, ldm, _dense(q_start, "q_start", i32, (B + 1,)), B, max_q,
+                         _dense(u, "u", f32, (T,)), _dense(u_last, "u_last", f32, (B,)), out.data_ptr(), path.data_ptr(),
+                         out.stride(0) if B > 1 else out.shape[1], _dense(count, "count", i32, (B,)),
+                         s if stream is None else _stream(stream))
     if raise_on_error:
         _check(st)
     return st

@@ -12,9 +12,11 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libcq.so")
 SOURCES = ["cq_api.cu", "k_aux.cu", "k_skinny.cu", "k_tc.cu", "k_tc_ffn.cu", "k_tc_q4a.cu", "k_tc_q8b.cu", "k_rows.cu", "cq_noalloc.cu",
-           "kv8/kv8_api.cu", "kv8/kv8_store.cu", "kv8/kv8_attn.cu", "kv8/kv8_decode.cu", "kv8/kv8_tiles.cu", "kv8/kv8_narrow.cu"]
+           "kv8/kv8_api.cu", "kv8/kv8_store.cu", "kv8/kv8_attn.cu", "kv8/kv8_decode.cu", "kv8/kv8_tiles.cu", "kv8/kv8_narrow.cu",
+           "kv8/kv8_decode_tree.cu", "kv8/kv8_tiles_tree.cu", "kv8/kv8_narrow_tree.cu", "draft/draft_api.cu", "draft/rope.cu", "draft/verify.cu"]
 HEADERS = ["cq_internal.h", "cq_ptx.cuh", "k_tc.cuh", "kv8/kv8.cuh", "kv8/attn_common.cuh",
-           "kv8/tiles_common.cuh"]
+           "kv8/tiles_common.cuh", "kv8/store_common.cuh", "kv8/kv8_checks.h", "kv8/kv8_decode.cuh", "kv8/kv8_tiles.cuh", "kv8/kv8_narrow.cuh",
+           "draft/draft.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-I", os.path.join(HERE, "..", "include")]
@@ -36,7 +38,7 @@ def _stale(target: str, deps) -> bool:
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     os.makedirs(OUT_DIR, exist_ok=True)
-    hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(HERE, "..", "include", h) for h in ("cq.h", "cq_kv8.h")]
+    hdrs = [os.path.join(CSRC, h) for h in HEADERS] + [os.path.join(HERE, "..", "include", h) for h in ("cq.h", "cq_kv8.h", "cq_draft.h")]
     procs = []
     objs = []
     for src in SOURCES:

@@ -1,0 +1,261 @@
+// Rotary positions of rows of heads, and the cache's write with rotated keys.
+//
+// Both are one pass over the data and bound by HBM: a (token, pair) angle costs about 80 instructions, so each
+// block of threads makes a table of its tokens' cosines and sines in shared memory once and every head takes
+// its factors from there.
+#include "../kv8/store_common.cuh"
+#include "draft.cuh"
+
+namespace cq {
+namespace draft {
+namespace {
+
+using kv8::In;
+
+// ---- rows ------------------------------------------------------------------------------------------------------------
+// A unit is 8 neighbouring channels of a head, together with their partners 8 channels rot/2 on in the half layout:
+// everything is moved 16 bytes at a time, and in place too, as a thread reads its units before it writes them.
+constexpr int THREADS = 256, EACH = 4;                   // units that a thread has under way
+
+template <class X>
+__device__ __forceinline__ void load8(const X* p, float (&f)[8]) {
+    if constexpr (sizeof(X) == 2) {
+        In<X>::get(__ldcs(reinterpret_cast<const uint4*>(p)), f);
+    } else {
+        const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    }
+}
+template <class Y>
+__device__ __forceinline__ void store8(Y* p, const float (&f)[8]) {
+    if constexpr (sizeof(Y) == 2) {
+        *reinterpret_cast<uint4*>(p) = In<Y>::put(f);
+    } else {
+        reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+}
+
+struct Rows {
+    const void* x;
+    void* y;
+    int64_t ldx, ldy;
+    int T, H, D, per;      // per: tokens of a block of threads
+};
+
+template <class X, class Y, int LAYOUT>
+__global__ void __launch_bounds__(THREADS) k_rope(const Rows a, const Rope rope) {
+    pdl_launch_dependents();
+    pdl_wait();
+    extern __shared__ float4 table4[];
+    float* cs = reinterpret_cast<float*>(table4);        // [per][half] cosines, then sines
+    float* sn = cs + a.per * rope.half;
+    const int64_t t0 = (int64_t)blockIdx.x * a.per;
+    const int n = (int)min((int64_t)a.per, a.T - t0);
+    for (int i = threadIdx.x; i < n * rope.half; i += THREADS) {
+        const int t = i / rope.half, k = i - t * rope.half;
+        cos_sin_at(turn_of(__ldcg(rope.freq + k)), __ldcg(rope.pos + t0 + t), rope.mag, cs[i], sn[i]);
+    }
+    __syncthreads();
+    const int turned = LAYOUT == CQ_ROPE_HALF ? rope.half / 8 : rope.half / 4;     // units of a head with pairs
+    const int units = turned + (a.D - 2 * rope.half) / 8, all = units * a.H * n;
+    const X* x = static_cast<const X*>(a.x) + t0 * a.ldx;
+    Y* y = static_cast<Y*>(a.y) + t0 * a.ldy;
+    for (int i0 = threadIdx.x; i0 < all; i0 += THREADS * EACH) {
+        float f[EACH][8], g[LAYOUT == CQ_ROPE_HALF ? EACH : 1][8];
+        int tok[EACH], unit[EACH];
+        int64_t at[EACH], to[EACH];
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+            const int i = i0 + e * THREADS;
+            const int h = i / units, u = i - h * units, t = h / a.H;
+            tok[e] = t;
+            unit[e] = u;
+            // (the half layout's channels past the rotated ones follow both halves)
+            const int ch = LAYOUT == CQ_ROPE_HALF && u >= turned ? 8 * u + rope.half : 8 * u;
+            at[e] = t * a.ldx + (int64_t)(h - t * a.H) * a.D + ch;
+            to[e] = t * a.ldy + (int64_t)(h - t * a.H) * a.D + ch;
+            if (i < all) {
+                load8(x + at[e], f[e]);
+                if (LAYOUT == CQ_ROPE_HALF && u < turned) load8(x + at[e] + rope.half, g[LAYOUT == CQ_ROPE_HALF ? e : 0]);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < EACH; ++e) {
+            if (i0 + e * THREADS >= all) break;
+            float(&a0)[8] = f[e], (&b0)[8] = g[LAYOUT == CQ_ROPE_HALF ? e : 0];
+            if (unit[e] < turned) {
+                constexpr int N = LAYOUT == CQ_ROPE_HALF ? 8 : 4;                  // pairs of a unit
+                float c[N], s[N];
+                const int k = tok[e] * rope.half + N * unit[e];
+#pragma unroll
+                for (int j = 0; j < N; j += 4) {
+                    const float4 p = *reinterpret_cast<const float4*>(cs + k + j), q = *reinterpret_cast<const float4*>(sn + k + j);
+                    c[j] = p.x, c[j + 1] = p.y, c[j + 2] = p.z, c[j + 3] = p.w;
+                    s[j] = q.x, s[j + 1] = q.y, s[j + 2] = q.z, s[j + 3] = q.w;
+                }
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    float& lo = LAYOUT == CQ_ROPE_HALF ? a0[j] : a0[2 * j & 7];
+                    float& hi = LAYOUT == CQ_ROPE_HALF ? b0[j] : a0[2 * j + 1 & 7];
+                    const float p = turn_first(lo, hi, c[j], s[j]), q = turn_second(lo, hi, c[j], s[j]);
+                    lo = p;
+                    hi = q;
+                }
+                if (LAYOUT == CQ_ROPE_HALF) store8(y + to[e] + rope.half, b0);
+            }
+            store8(y + to[e], a0);
+        }
+    }
+}
+
+template <class X, class Y>
+cudaError_t rope_as(Rows a, const Rope& rope, int layout, cudaStream_t s) {
+    // tokens of a block of threads: enough units for all threads, a table of at most 32 KB
+    const int units = a.D / 8 * a.H;
+    a.per = std::max(1, std::min({THREADS * EACH / units, 4096 / rope.half, a.T}));
+    const size_t smem = (size_t)a.per * rope.half * 8;
+    const dim3 grid((a.T + a.per - 1) / a.per);
+    if (layout == CQ_ROPE_HALF) return kv8::launch_pdl(k_rope<X, Y, CQ_ROPE_HALF>, grid, dim3(THREADS), smem, s, a, rope);
+    return kv8::launch_pdl(k_rope<X, Y, CQ_ROPE_PAIRS>, grid, dim3(THREADS), smem, s, a, rope);
+}
+template <class X>
+cudaError_t rope_from(const Rows& a, int yt, const Rope& rope, int layout, cudaStream_t s) {
+    if (yt == CQ_F16) return rope_as<X, __half>(a, rope, layout, s);
+    if (yt == CQ_BF16) return rope_as<X, __nv_bfloat16>(a, rope, layout, s);
+    return rope_as<X, float>(a, rope, layout, s);
+}
+
+// ---- keys and values to the cache -----------------------------------------------------------------------------------
+// One warp has one block of 32 tokens of one head, as in the write without rotation; the warps of a block of
+// threads have up to four heads of the keys and of the values of one block of tokens, and make its table together while
+// their rows are on the way.
+constexpr int HEADS = 4;
+
+template <class X, int D, int LAYOUT>
+__global__ void __launch_bounds__(2 * HEADS * 32) k_write_rope(const kv8::Cache c, const kv8::Batch b, const X* K, const X* V,
+                                                               int64_t ldk, int64_t ldv, const Rope rope, int groups) {
+    using namespace kv8;
+    pdl_launch_dependents();
+    pdl_wait();
+    constexpr int N = In<X>::N, LPR = D / N, RPI = 32 / LPR, IT = BLK / RPI;   // lanes a row, rows a step
+    __shared__ float4 cs4[BLK * D / 8], sn4[BLK * D / 8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int head = (int)(blockIdx.x % groups) * HEADS + (warp >> 1);
+    const Item it = find_item<true>(c, b, blockIdx.x / groups, warp & 1, head);
+    if (!it.ok) return;                                  // (the same for the whole block of threads)
+    const bool mine = head < c.Hkv;
+    const int sub = lane / LPR, col = (lane % LPR) * N;
+    const int64_t ld = it.kv ? ldv : ldk;
+    const X* src = (it.kv ? V : K) + it.row0 * ld + (int64_t)head * D + col;
+    uint4 u[IT];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int r = i * RPI + sub;
+        u[i] = make_uint4(0, 0, 0, 0);
+        if (mine && r >= it.lo && r < it.hi) u[i] = __ldcs(reinterpret_cast<const uint4*>(src + (r - it.lo) * ld));
+    }
+    float* cs = reinterpret_cast<float*>(cs4);
+    float* sn = reinterpret_cast<float*>(sn4);
+    // Factors in chunks of four pairs, rows of D / 8 chunks.  Half layout, 16-bit rows: a lane takes two neighbouring
+    // chunks; the even ones lie ahead of the odd ones, so that lanes read neighbouring chunks.
+    auto chunk = [&](int k) { return LAYOUT == CQ_ROPE_HALF && N == 8 ? (k >> 1) + (k & 1) * (D / 16) : k; };
+    for (int i = it.lo * rope.half + threadIdx.x; i < it.hi * rope.half; i += blockDim.x) {
+        const int r = i / rope.half, k = i - r * rope.half, at = r * (D / 2) + 4 * chunk(k >> 2) + (k & 3);
+        const int p = rope.pos ? __ldcg(rope.pos + it.row0 + (r - it.lo)) : it.tok0 + (r - it.lo);
+        cos_sin_at(turn_of(__ldcg(rope.freq + k)), p, rope.mag, cs[at], sn[at]);
+    }
+    __syncthreads();
+    if (!mine) return;
+    float f[IT][N];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) In<X>::get(u[i], f[i]);
+    if (!it.kv) {
+        const int h = rope.half;
+        if (LAYOUT == CQ_ROPE_HALF) {
+            const bool first = col < h, turns = col < 2 * h;
+            const int k = (first ? col : col - h) / 4;       // (channels past the rotated ones read row 0's and drop it)
+            const int from = turns ? first ? lane + h / N : lane - h / N : lane;
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                const int r = i * RPI + sub;
+                uint4 w;
+                w.x = __shfl_sync(0xffffffffu, u[i].x, from);
+                w.y = __shfl_sync(0xffffffffu, u[i].y, from);
+                w.z = __shfl_sync(0xffffffffu, u[i].z, from);
+                w.w = __shfl_sync(0xffffffffu, u[i].w, from);
+                float g[N];
+                In<X>::get(w, g);
+                if (turns && r >= it.lo && r < it.hi)
+#pragma unroll
+                    for (int j = 0; j < N; j += 4) {
+                        const float4 p = cs4[r * (D / 8) + chunk(k + j / 4)], q = sn4[r * (D / 8) + chunk(k + j / 4)];
+                        const float c4[4] = {p.x, p.y, p.z, p.w}, s4[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            f[i][j + e] = first ? turn_first(f[i][j + e], g[j + e], c4[e], s4[e]) : turn_second(g[j + e], f[i][j + e], c4[e], s4[e]);
+                    }
+            }
+        } else if (col < 2 * h) {
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                const int r = i * RPI + sub;
+                if (r < it.lo || r >= it.hi) continue;
+                float c4[N / 2], s4[N / 2];
+                if constexpr (N == 8) {
+                    const float4 p = cs4[r * (D / 8) + col / 8], q = sn4[r * (D / 8) + col / 8];
+                    c4[0] = p.x, c4[1] = p.y, c4[2] = p.z, c4[3] = p.w;
+                    s4[0] = q.x, s4[1] = q.y, s4[2] = q.z, s4[3] = q.w;
+                } else {
+                    const float2 p = *reinterpret_cast<const float2*>(cs + r * (D / 2) + col / 2), q = *reinterpret_cast<const float2*>(sn + r * (D / 2) + col / 2);
+                    c4[0] = p.x, c4[1] = p.y;
+                    s4[0] = q.x, s4[1] = q.y;
+                }
+#pragma unroll
+                for (int j = 0; j < N / 2; ++j) {
+                    const float p = turn_first(f[i][2 * j], f[i][2 * j + 1], c4[j], s4[j]), q = turn_second(f[i][2 * j], f[i][2 * j + 1], c4[j], s4[j]);
+                    f[i][2 * j] = p;
+                    f[i][2 * j + 1] = q;
+                }
+            }
+        }
+    }
+    store_block<D, N>(c, it, [&](int i, float (&v)[N]) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = f[i][j];
+    });
+}
+
+template <class X, int D>
+cudaError_t write_as(const kv8::Cache& c, const kv8::Batch& b, const void* K, const void* V, int64_t ldk, int64_t ldv, const Rope& rope,
+                     int layout, cudaStream_t s) {
+    const X *k = static_cast<const X*>(K), *v = static_cast<const X*>(V);
+    const int groups = (c.Hkv + HEADS - 1) / HEADS;
+    const dim3 grid((unsigned)(kv8::store_slots(c, b) * groups)), block(2 * std::min(c.Hkv, HEADS) * 32);
+    if (layout == CQ_ROPE_HALF) return kv8::launch_pdl(k_write_rope<X, D, CQ_ROPE_HALF>, grid, block, 0, s, c, b, k, v, ldk, ldv, rope, groups);
+    return kv8::launch_pdl(k_write_rope<X, D, CQ_ROPE_PAIRS>, grid, block, 0, s, c, b, k, v, ldk, ldv, rope, groups);
+}
+template <class X>
+cudaError_t write_from(const kv8::Cache& c, const kv8::Batch& b, int D, const void* K, const void* V, int64_t ldk, int64_t ldv,
+                       const Rope& rope, int layout, cudaStream_t s) {
+    return D == 128 ? write_as<X, 128>(c, b, K, V, ldk, ldv, rope, layout, s) : write_as<X, 64>(c, b, K, V, ldk, ldv, rope, layout, s);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const void* X, int xt, int T, int H, int D, int64_t ldx, const Rope& rope, int layout, void* Y, int yt,
+                        int64_t ldy, cudaStream_t s) {
+    const Rows a = {X, Y, ldx, ldy, T, H, D, 0};
+    if (xt == CQ_F16) return rope_from<__half>(a, yt, rope, layout, s);
+    if (xt == CQ_BF16) return rope_from<__nv_bfloat16>(a, yt, rope, layout, s);
+    return rope_from<float>(a, yt, rope, layout, s);
+}
+cudaError_t launch_write_rope(const kv8::Cache& c, const kv8::Batch& b, int D, const void* K, const void* V, int xt, int64_t ldk,
+                              int64_t ldv, const Rope& rope, int layout, cudaStream_t s) {
+    if (xt == CQ_F16) return write_from<__half>(c, b, D, K, V, ldk, ldv, rope, layout, s);
+    if (xt == CQ_BF16) return write_from<__nv_bfloat16>(c, b, D, K, V, ldk, ldv, rope, layout, s);
+    return write_from<float>(c, b, D, K, V, ldk, ldv, rope, layout, s);
+}
+
+}  // namespace draft
+}  // namespace cq

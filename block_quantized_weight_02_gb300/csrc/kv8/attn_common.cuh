@@ -108,18 +108,41 @@ __device__ __forceinline__ int first_seeing(const AttnArgs& a, int n, int L) {
 __device__ __forceinline__ float row_sum(float l, int f, int first) {
     return l == 0.f && f >= first ? __uint_as_float(0x7FC00000u) : l;
 }
+// With a mask (TREE) a row sees every token ahead of its sequence's n last ones, and of those the ones whose bits are set.
+// Token t is number t - (L - n) of them.
+__device__ __forceinline__ uint32_t mask_word(const AttnArgs& a, int row, int i, int n) {
+    return i >= 0 && i < (n + 31) / 32 ? __ldcg(a.mask + row * a.ldm + i) : 0u;
+}
+static __device__ __noinline__ bool tree_sees(const AttnArgs& a, int row, int n, int L) {
+    if (L > n) return true;
+    for (int i = 0; i < (n + 31) / 32; ++i) {
+        uint32_t w = mask_word(a, row, i, n);
+        const int lo = n - L - 32 * i, hi = n - 32 * i;              // tokens that are there: [n - L, n)
+        if (lo >= 32) continue;
+        if (lo > 0) w &= ~0u << lo;
+        if (hi < 32) w &= (1u << hi) - 1;
+        if (w) return true;
+    }
+    return false;
+}
+// The normaliser of the sequence's row f (q0: its first tensor row), as row_sum gives it.
+template <bool TREE>
+__device__ __forceinline__ float end_sum(const AttnArgs& a, float l, int f, int q0, int n, int L) {
+    if (!TREE) return row_sum(l, f, first_seeing(a, n, L));
+    return l == 0.f && tree_sees(a, q0 + f / (a.Hq / a.c.Hkv), n, L) ? __uint_as_float(0x7FC00000u) : l;
+}
 __device__ __forceinline__ float inv_sum(float l) { return l == 0.f ? 0.f : 1.0f / l; }
 __device__ __forceinline__ float lse_of(float m, float l) {
     return l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
 }
 
 // Joins the partials part(0) .. part(cnt - 1) of KV head h's row f (a (token, head) pair of the sequence whose first
-// tensor row is q0; rows from `first` on see a token), row r of the partials, NQ x 4 channels from d on: into `out`
+// tensor row is q0, with n rows and L tokens), row r of the partials, NQ x 4 channels from d on: into `out`
 // (nullable), else the output.  AT partials are read at a time; FAR ones come from other CTAs.
 template <bool FAR, class T>
 __device__ __forceinline__ T part_ld(const T* p) { return FAR ? __ldcg(p) : *p; }
-template <bool FAR, int D, int NQ, int AT, class P, class F>
-__device__ __forceinline__ void join(const AttnArgs& a, int q0, int first, int h, int f, int r, int d, int cnt, F part, P* out) {
+template <bool FAR, bool TREE, int D, int NQ, int AT, class P, class F>
+__device__ __forceinline__ void join(const AttnArgs& a, int q0, int n, int L, int h, int f, int r, int d, int cnt, F part, P* out) {
     float m = -INFINITY, l = 0.f;
     float4 o[NQ];
 #pragma unroll
@@ -178,7 +201,7 @@ __device__ __forceinline__ void join(const AttnArgs& a, int q0, int first, int h
     } else {
         const int G = a.Hq / a.c.Hkv, row = q0 + f / G, head = h * G + f % G;
         const int64_t at = row * a.ldo + (int64_t)head * D + d;
-        l = row_sum(l, f, first);
+        l = end_sum<TREE>(a, l, f, q0, n, L);
         const float inv = inv_sum(l);
 #pragma unroll
         for (int q = 0; q < NQ; ++q) store_out4(a.O, at + 4 * q, a.yt, o[q].x * inv, o[q].y * inv, o[q].z * inv, o[q].w * inv);

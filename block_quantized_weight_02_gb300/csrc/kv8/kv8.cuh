@@ -45,6 +45,8 @@ struct AttnArgs {
     float scale;
     void* ws;
     int stall;             // test only: copies are left out (few rows: all; else all but a CTA's first tile), so that a wait runs out
+    const uint32_t* mask;  // trees: which of a sequence's last tokens its rows see, ldm words a row (causal = 0 and no window then)
+    int64_t ldm;
 };
 
 cudaError_t launch_write(const Cache& c, const Batch& b, int D, const void* K, const void* V, int xt, int64_t ldk,
@@ -52,14 +54,18 @@ cudaError_t launch_write(const Cache& c, const Batch& b, int D, const void* K, c
 cudaError_t launch_read(const Cache& c, const Batch& b, int D, void* K, void* V, int yt, int64_t ldk, int64_t ldv,
                         cudaStream_t s);
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_attn_tree(const AttnArgs& a, cudaStream_t s);   // with a mask
 bool decode_serves(int64_t rows);                     // rows: query rows of a sequence that share a KV head
 size_t decode_workspace(int64_t D);
 cudaError_t launch_decode(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_decode_tree(const AttnArgs& a, cudaStream_t s);
 bool narrow_serves(int64_t rows);
 size_t narrow_workspace(int64_t T, int64_t G, int64_t D, int64_t B);
 cudaError_t launch_narrow(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_narrow_tree(const AttnArgs& a, cudaStream_t s);
 size_t tiles_workspace(int64_t T, int64_t G, int64_t D, int64_t B, int64_t max_q);
 cudaError_t launch_tiles(const AttnArgs& a, cudaStream_t s);
+cudaError_t launch_tiles_tree(const AttnArgs& a, cudaStream_t s);
 size_t attn_workspace(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q);        // of a call
 size_t attn_workspace_upto(int64_t T, int64_t Hq, int64_t Hkv, int64_t D, int64_t B, int64_t max_q);   // and of any smaller one
 

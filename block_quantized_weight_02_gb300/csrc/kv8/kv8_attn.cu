@@ -30,6 +30,11 @@ cudaError_t launch_attn(const AttnArgs& a, cudaStream_t s) {
     const int64_t rows = (int64_t)a.max_q * (a.Hq / a.c.Hkv);
     return decode_serves(rows) ? launch_decode(a, s) : narrow_serves(rows) ? launch_narrow(a, s) : launch_tiles(a, s);
 }
+// Trees of drafted tokens: the same kernels with a mask in the steps that reach the last tokens, by the same rule.
+cudaError_t launch_attn_tree(const AttnArgs& a, cudaStream_t s) {
+    const int64_t rows = (int64_t)a.max_q * (a.Hq / a.c.Hkv);
+    return decode_serves(rows) ? launch_decode_tree(a, s) : narrow_serves(rows) ? launch_narrow_tree(a, s) : launch_tiles_tree(a, s);
+}
 
 }  // namespace kv8
 }  // namespace cq
