@@ -1,8 +1,8 @@
 // Rotary positions of rows of heads, and the cache's write with rotated keys.
 //
 // Both are one pass over the data and bound by HBM: a (token, pair) angle costs about 80 instructions, so each
-// block of threads makes a table of its tokens' cosines and sines in shared memory once and every head takes
-// its factors from there.
+// block of threads makes a table of its tokens' cosines and sines in shared memory once, while its rows are on their way,
+// and every head takes its factors from there.
 #include "../kv8/store_common.cuh"
 #include "draft.cuh"
 
@@ -15,17 +15,29 @@ using kv8::In;
 // ---- rows ------------------------------------------------------------------------------------------------------------
 // A unit is 8 neighbouring channels of a head, together with their partners 8 channels rot/2 on in the half layout:
 // everything is moved 16 bytes at a time, and in place too, as a thread reads its units before it writes them.
-constexpr int THREADS = 256, EACH = 4;                   // units that a thread has under way
+constexpr int THREADS = 256;
+template <class X>
+constexpr int EACH = sizeof(X) == 2 ? 4 : 2;             // units that a thread has under way
 
 template <class X>
-__device__ __forceinline__ void load8(const X* p, float (&f)[8]) {
-    if constexpr (sizeof(X) == 2) {
-        In<X>::get(__ldcs(reinterpret_cast<const uint4*>(p)), f);
-    } else {
-        const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+struct Eight {                                           // 8 channels as they lie in memory
+    uint4 v[sizeof(X) / 2];
+    __device__ __forceinline__ void load(const X* p) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(X) / 2; ++i) v[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
     }
-}
+    __device__ __forceinline__ void get(float (&f)[8]) const {
+        if constexpr (sizeof(X) == 2) {
+            In<X>::get(v[0], f);
+        } else {
+            float a[4], b[4];
+            In<X>::get(v[0], a);
+            In<X>::get(v[1], b);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = a[i], f[4 + i] = b[i];
+        }
+    }
+};
 template <class Y>
 __device__ __forceinline__ void store8(Y* p, const float (&f)[8]) {
     if constexpr (sizeof(Y) == 2) {
@@ -45,6 +57,8 @@ struct Rows {
 
 template <class X, class Y, int LAYOUT>
 __global__ void __launch_bounds__(THREADS) k_rope(const Rows a, const Rope rope) {
+    constexpr bool HALVES = LAYOUT == CQ_ROPE_HALF;
+    constexpr int E = EACH<X>;
     pdl_launch_dependents();
     pdl_wait();
     extern __shared__ float4 table4[];
@@ -52,59 +66,58 @@ __global__ void __launch_bounds__(THREADS) k_rope(const Rows a, const Rope rope)
     float* sn = cs + a.per * rope.half;
     const int64_t t0 = (int64_t)blockIdx.x * a.per;
     const int n = (int)min((int64_t)a.per, a.T - t0);
-    for (int i = threadIdx.x; i < n * rope.half; i += THREADS) {
-        const int t = i / rope.half, k = i - t * rope.half;
-        cos_sin_at(turn_of(__ldcg(rope.freq + k)), __ldcg(rope.pos + t0 + t), rope.mag, cs[i], sn[i]);
-    }
-    __syncthreads();
-    const int turned = LAYOUT == CQ_ROPE_HALF ? rope.half / 8 : rope.half / 4;     // units of a head with pairs
+    const int turned = HALVES ? rope.half / 8 : rope.half / 4;                     // units of a head with pairs
     const int units = turned + (a.D - 2 * rope.half) / 8, all = units * a.H * n;
     const X* x = static_cast<const X*>(a.x) + t0 * a.ldx;
     Y* y = static_cast<Y*>(a.y) + t0 * a.ldy;
-    for (int i0 = threadIdx.x; i0 < all; i0 += THREADS * EACH) {
-        float f[EACH][8], g[LAYOUT == CQ_ROPE_HALF ? EACH : 1][8];
-        int tok[EACH], unit[EACH];
-        int64_t at[EACH], to[EACH];
+    for (int i0 = 0; i0 < all; i0 += THREADS * E) {
+        Eight<X> f[E], g[HALVES ? E : 1];
+        int tok[E], unit[E], ch[E];
 #pragma unroll
-        for (int e = 0; e < EACH; ++e) {
-            const int i = i0 + e * THREADS;
-            const int h = i / units, u = i - h * units, t = h / a.H;
-            tok[e] = t;
-            unit[e] = u;
+        for (int e = 0; e < E; ++e) {
+            const int i = i0 + e * THREADS + threadIdx.x, h = i / units, u = i - h * units, t = h / a.H;
             // (the half layout's channels past the rotated ones follow both halves)
-            const int ch = LAYOUT == CQ_ROPE_HALF && u >= turned ? 8 * u + rope.half : 8 * u;
-            at[e] = t * a.ldx + (int64_t)(h - t * a.H) * a.D + ch;
-            to[e] = t * a.ldy + (int64_t)(h - t * a.H) * a.D + ch;
+            tok[e] = t;
+            unit[e] = i < all ? u : -1;
+            ch[e] = (h - t * a.H) * a.D + (HALVES && u >= turned ? 8 * u + rope.half : 8 * u);
             if (i < all) {
-                load8(x + at[e], f[e]);
-                if (LAYOUT == CQ_ROPE_HALF && u < turned) load8(x + at[e] + rope.half, g[LAYOUT == CQ_ROPE_HALF ? e : 0]);
+                f[e].load(x + t * a.ldx + ch[e]);
+                if (HALVES && u < turned) g[HALVES ? e : 0].load(x + t * a.ldx + ch[e] + rope.half);
             }
         }
+        if (i0 == 0) {                                   // the table, while the first rows are on their way
+            for (int i = threadIdx.x; i < n * rope.half; i += THREADS) {
+                const int t = i / rope.half, k = i - t * rope.half;
+                cos_sin_at(turn_of(__ldcg(rope.freq + k)), __ldcg(rope.pos + t0 + t), rope.mag, cs[i], sn[i]);
+            }
+            __syncthreads();
+        }
 #pragma unroll
-        for (int e = 0; e < EACH; ++e) {
-            if (i0 + e * THREADS >= all) break;
-            float(&a0)[8] = f[e], (&b0)[8] = g[LAYOUT == CQ_ROPE_HALF ? e : 0];
+        for (int e = 0; e < E; ++e) {
+            if (unit[e] < 0) continue;
+            float lo[8], hi[8];
+            f[e].get(lo);
+            Y* to = y + tok[e] * a.ldy + ch[e];
             if (unit[e] < turned) {
-                constexpr int N = LAYOUT == CQ_ROPE_HALF ? 8 : 4;                  // pairs of a unit
-                float c[N], s[N];
+                constexpr int N = HALVES ? 8 : 4;        // pairs of a unit
+                if (HALVES) g[HALVES ? e : 0].get(hi);
                 const int k = tok[e] * rope.half + N * unit[e];
 #pragma unroll
                 for (int j = 0; j < N; j += 4) {
                     const float4 p = *reinterpret_cast<const float4*>(cs + k + j), q = *reinterpret_cast<const float4*>(sn + k + j);
-                    c[j] = p.x, c[j + 1] = p.y, c[j + 2] = p.z, c[j + 3] = p.w;
-                    s[j] = q.x, s[j + 1] = q.y, s[j + 2] = q.z, s[j + 3] = q.w;
-                }
+                    const float c[4] = {p.x, p.y, p.z, p.w}, s[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-                for (int j = 0; j < N; ++j) {
-                    float& lo = LAYOUT == CQ_ROPE_HALF ? a0[j] : a0[2 * j & 7];
-                    float& hi = LAYOUT == CQ_ROPE_HALF ? b0[j] : a0[2 * j + 1 & 7];
-                    const float p = turn_first(lo, hi, c[j], s[j]), q = turn_second(lo, hi, c[j], s[j]);
-                    lo = p;
-                    hi = q;
+                    for (int i = 0; i < 4; ++i) {
+                        float& a0 = HALVES ? lo[j + i] : lo[2 * i];
+                        float& b0 = HALVES ? hi[j + i] : lo[2 * i + 1];
+                        const float a1 = turn_first(a0, b0, c[i], s[i]), b1 = turn_second(a0, b0, c[i], s[i]);
+                        a0 = a1;
+                        b0 = b1;
+                    }
                 }
-                if (LAYOUT == CQ_ROPE_HALF) store8(y + to[e] + rope.half, b0);
+                if (HALVES) store8(to + rope.half, hi);
             }
-            store8(y + to[e], a0);
+            store8(to, lo);
         }
     }
 }
@@ -112,8 +125,8 @@ __global__ void __launch_bounds__(THREADS) k_rope(const Rows a, const Rope rope)
 template <class X, class Y>
 cudaError_t rope_as(Rows a, const Rope& rope, int layout, cudaStream_t s) {
     // tokens of a block of threads: enough units for all threads, a table of at most 32 KB
-    const int units = a.D / 8 * a.H;
-    a.per = std::max(1, std::min({THREADS * EACH / units, 4096 / rope.half, a.T}));
+    const int units = (rope.half / (layout == CQ_ROPE_HALF ? 8 : 4) + (a.D - 2 * rope.half) / 8) * a.H;
+    a.per = std::max(1, std::min({THREADS * EACH<X> / units, 4096 / rope.half, a.T}));
     const size_t smem = (size_t)a.per * rope.half * 8;
     const dim3 grid((a.T + a.per - 1) / a.per);
     if (layout == CQ_ROPE_HALF) return kv8::launch_pdl(k_rope<X, Y, CQ_ROPE_HALF>, grid, dim3(THREADS), smem, s, a, rope);
@@ -167,62 +180,53 @@ __global__ void __launch_bounds__(2 * HEADS * 32) k_write_rope(const kv8::Cache 
     }
     __syncthreads();
     if (!mine) return;
-    float f[IT][N];
+    // A key's channels are turned where they are needed, for the block's largest magnitude and again for the codes: kept in
+    // between, in f32, they would take twice the registers of the rows and leave half the warps.
+    const int h = rope.half;
+    const bool first = col < h, turns = !it.kv && col < 2 * h;
+    const int from = !turns ? lane : first ? lane + h / N : lane - h / N;    // half layout: the lane with the partners
+    const int at = LAYOUT == CQ_ROPE_HALF ? (first ? col : col - h) / 4 : col / 2;
+    store_block<D, N>(c, it, [&](int i, float (&f)[N]) {
+        In<X>::get(u[i], f);
+        if (it.kv) return;                               // (the same for the whole warp)
+        const int r = i * RPI + sub;
+        const bool turn = turns && r >= it.lo && r < it.hi;
+        if constexpr (LAYOUT == CQ_ROPE_HALF) {
+            uint4 w;
+            w.x = __shfl_sync(0xffffffffu, u[i].x, from);
+            w.y = __shfl_sync(0xffffffffu, u[i].y, from);
+            w.z = __shfl_sync(0xffffffffu, u[i].z, from);
+            w.w = __shfl_sync(0xffffffffu, u[i].w, from);
+            if (!turn) return;
+            float g[N];
+            In<X>::get(w, g);
 #pragma unroll
-    for (int i = 0; i < IT; ++i) In<X>::get(u[i], f[i]);
-    if (!it.kv) {
-        const int h = rope.half;
-        if (LAYOUT == CQ_ROPE_HALF) {
-            const bool first = col < h, turns = col < 2 * h;
-            const int k = (first ? col : col - h) / 4;       // (channels past the rotated ones read row 0's and drop it)
-            const int from = turns ? first ? lane + h / N : lane - h / N : lane;
+            for (int j = 0; j < N; j += 4) {
+                const float4 p = cs4[r * (D / 8) + chunk(at + j / 4)], q = sn4[r * (D / 8) + chunk(at + j / 4)];
+                const float c4[4] = {p.x, p.y, p.z, p.w}, s4[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                const int r = i * RPI + sub;
-                uint4 w;
-                w.x = __shfl_sync(0xffffffffu, u[i].x, from);
-                w.y = __shfl_sync(0xffffffffu, u[i].y, from);
-                w.z = __shfl_sync(0xffffffffu, u[i].z, from);
-                w.w = __shfl_sync(0xffffffffu, u[i].w, from);
-                float g[N];
-                In<X>::get(w, g);
-                if (turns && r >= it.lo && r < it.hi)
-#pragma unroll
-                    for (int j = 0; j < N; j += 4) {
-                        const float4 p = cs4[r * (D / 8) + chunk(k + j / 4)], q = sn4[r * (D / 8) + chunk(k + j / 4)];
-                        const float c4[4] = {p.x, p.y, p.z, p.w}, s4[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            f[i][j + e] = first ? turn_first(f[i][j + e], g[j + e], c4[e], s4[e]) : turn_second(g[j + e], f[i][j + e], c4[e], s4[e]);
-                    }
+                for (int e = 0; e < 4; ++e)
+                    f[j + e] = first ? turn_first(f[j + e], g[j + e], c4[e], s4[e]) : turn_second(g[j + e], f[j + e], c4[e], s4[e]);
             }
-        } else if (col < 2 * h) {
+        } else {
+            if (!turn) return;
+            float c4[N / 2], s4[N / 2];
+            if constexpr (N == 8) {
+                const float4 p = *reinterpret_cast<const float4*>(cs + r * (D / 2) + at), q = *reinterpret_cast<const float4*>(sn + r * (D / 2) + at);
+                c4[0] = p.x, c4[1] = p.y, c4[2] = p.z, c4[3] = p.w;
+                s4[0] = q.x, s4[1] = q.y, s4[2] = q.z, s4[3] = q.w;
+            } else {
+                const float2 p = *reinterpret_cast<const float2*>(cs + r * (D / 2) + at), q = *reinterpret_cast<const float2*>(sn + r * (D / 2) + at);
+                c4[0] = p.x, c4[1] = p.y;
+                s4[0] = q.x, s4[1] = q.y;
+            }
 #pragma unroll
-            for (int i = 0; i < IT; ++i) {
-                const int r = i * RPI + sub;
-                if (r < it.lo || r >= it.hi) continue;
-                float c4[N / 2], s4[N / 2];
-                if constexpr (N == 8) {
-                    const float4 p = cs4[r * (D / 8) + col / 8], q = sn4[r * (D / 8) + col / 8];
-                    c4[0] = p.x, c4[1] = p.y, c4[2] = p.z, c4[3] = p.w;
-                    s4[0] = q.x, s4[1] = q.y, s4[2] = q.z, s4[3] = q.w;
-                } else {
-                    const float2 p = *reinterpret_cast<const float2*>(cs + r * (D / 2) + col / 2), q = *reinterpret_cast<const float2*>(sn + r * (D / 2) + col / 2);
-                    c4[0] = p.x, c4[1] = p.y;
-                    s4[0] = q.x, s4[1] = q.y;
-                }
-#pragma unroll
-                for (int j = 0; j < N / 2; ++j) {
-                    const float p = turn_first(f[i][2 * j], f[i][2 * j + 1], c4[j], s4[j]), q = turn_second(f[i][2 * j], f[i][2 * j + 1], c4[j], s4[j]);
-                    f[i][2 * j] = p;
-                    f[i][2 * j + 1] = q;
-                }
+            for (int j = 0; j < N / 2; ++j) {
+                const float a0 = f[2 * j], b0 = f[2 * j + 1];
+                f[2 * j] = turn_first(a0, b0, c4[j], s4[j]);
+                f[2 * j + 1] = turn_second(a0, b0, c4[j], s4[j]);
             }
         }
-    }
-    store_block<D, N>(c, it, [&](int i, float (&v)[N]) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) v[j] = f[i][j];
     });
 }
 

@@ -11,17 +11,15 @@
 // so a pass needs A alone, however many were rejected.
 //
 // A border of the drawn number may lie anywhere, so sums carry 2^-40 and better: each term is the exact difference
-// in two floats, sums add the rounding errors that two floats lose (Knuth's two-sum), and the warps' sums are joined in 64
-// bits.  (Sums in 64 bits throughout would take one warp instruction in 16 cycles of an SM.)
-#include <cfloat>
-
+// in two floats, sums add the rounding errors that two floats lose (Knuth's two-sum), two elements an instruction.  64-bit
+// arithmetic, one warp instruction in 16 cycles of an SM, is left to the walk.
 #include "draft.cuh"
 
 namespace cq {
 namespace draft {
 namespace {
 
-constexpr int THREADS = 512, WARPS = THREADS / 32, MAX_CLUSTER = 16, MAX_ROWS = 1024;
+constexpr int THREADS = 256, WARPS = THREADS / 32, MAX_CLUSTER = 16, MAX_ROWS = 1024, UNROLL = 4;
 constexpr int SHARES = MAX_CLUSTER * WARPS;
 
 struct Row {
@@ -29,18 +27,32 @@ struct Row {
     float p, q, u;         // the target's and the draft's probability of the token after its parent
 };
 
+// A number in two floats, lo at most half a last place of hi.
+struct Two {
+    float hi, lo;
+};
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+    const float t = a.hi + b.hi, v = t - a.hi;
+    const float e = ((a.hi - (t - v)) + (b.hi - v)) + (a.lo + b.lo), h = t + e;
+    return {h, e - (h - t)};
+}
+__device__ __forceinline__ bool operator>(Two a, Two b) { return (a.hi - b.hi) + (a.lo - b.lo) > 0.f; }
+__device__ __forceinline__ Two times(Two a, float x) {
+    const float t = __fmul_rn(a.hi, x), e = fmaf(a.lo, x, fmaf(a.hi, x, -t)), h = t + e;
+    return {h, e - (h - t)};
+}
+__device__ __forceinline__ double wide(Two a) { return (double)a.hi + (double)a.lo; }
+
 struct Shared {
-    double sum[2][SHARES]; // the cluster's shares, of even and odd passes
-    double part[WARPS];    // of a look at one share
-    double total, mass, less;
-    int what, last, next, stand, fell, pass, share, bad;
+    Two sum[2][SHARES];    // the cluster's shares, of even and odd passes
+    Two part[WARPS];       // of a look at one share
+    Two aim;               // what the drawn number leaves within its share
+    double mass, less;
+    int what, last, next, stand, fell, pass, share;
     int path[MAX_ROWS];    // places of the rows that stand
     int gone[MAX_ROWS];    // rejected tokens that were not drawn
     Row row[MAX_ROWS];
 };
-
-// A positive finite number, or 0.
-__device__ __forceinline__ float weight(float x) { return __float_as_uint(x) - 1u < 0x7F7FFFFFu ? x : 0.f; }
 
 template <class X>
 constexpr int VEC = 16 / (int)sizeof(X);
@@ -50,93 +62,125 @@ __device__ __forceinline__ void widen(uint4 v, float (&f)[VEC<X>]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         if constexpr (sizeof(X) == 4) {
-            f[i] = weight(__uint_as_float(w[i]));
+            f[i] = __uint_as_float(w[i]);
         } else if constexpr (std::is_same<X, __half>::value) {
             const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-            f[2 * i] = weight(p.x);
-            f[2 * i + 1] = weight(p.y);
+            f[2 * i] = p.x;
+            f[2 * i + 1] = p.y;
         } else {
-            f[2 * i] = weight(__uint_as_float(w[i] << 16));
-            f[2 * i + 1] = weight(__uint_as_float(w[i] & 0xFFFF0000u));
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
         }
     }
 }
 template <class X>
 __device__ __forceinline__ float one(const X* p) {
-    if constexpr (sizeof(X) == 4) return weight(__ldcg(p));
-    else if constexpr (std::is_same<X, __half>::value) return weight(__half2float(__ldcg(p)));
-    else return weight(__bfloat162float(__ldcg(p)));
+    if constexpr (sizeof(X) == 4) return fmaxf(__ldcg(p), 0.f);
+    else if constexpr (std::is_same<X, __half>::value) return fmaxf(__half2float(__ldcg(p)), 0.f);
+    else return fmaxf(__bfloat162float(__ldcg(p)), 0.f);
 }
 
-struct Two {
-    float hi, lo;
-};
-// max(p - a q, 0), a in two floats, to 2^-46 of the larger term.
-__device__ __forceinline__ Two left_of(float p, float q, Two a) {
-    const float t = __fmul_rn(q, a.hi), tl = fmaf(q, a.lo, fmaf(q, a.hi, -t));
-    const float d = p - t, v = d - p;
-    const float e = ((p - (d - v)) - (t + v)) - tl;
-    const bool some = d + e > 0.f;
-    return {some ? d : 0.f, some ? e : 0.f};
-}
-__device__ __forceinline__ void add(Two& s, Two x) {
-    const float t = s.hi + x.hi, v = t - s.hi;
-    s.lo += ((s.hi - (t - v)) + (x.hi - v)) + x.lo;
-    s.hi = t;
-}
-
-// Terms of one vector of a row: elements from `at` on.  A row's last vector may be a part of one, of which nothing past
-// the row is read.
+// What is left at a row of P: max(P - a q, 0), a in two floats.  Negative entries and NaN count as 0 (the maxima drop them).
+enum { NOTHING_OFF = 0, Q_OFF = 1, MORE_OFF = 2 };       // a = 0; a = 1: one rejection; any a
 template <class X, bool DRAWN>
 struct Left {
+    static constexpr int N = VEC<X>;
     const X *p, *q;
     Two a;
-    bool less;             // a > 0
-    int V, ngone;
+    int off, V, ngone;
     const int* gone;
+    __device__ __forceinline__ Left(const VerifyArgs& v, const Shared& sm, int q0, bool whole) {
+        p = static_cast<const X*>(v.P) + (q0 + sm.last) * v.ldp;
+        q = DRAWN ? static_cast<const X*>(v.Q) + (q0 + sm.last) * v.ldq : nullptr;
+        const double less = whole ? 0.0 : sm.less;
+        a.hi = (float)less;
+        a.lo = (float)(less - (double)a.hi);
+        off = !DRAWN || less == 0.0 ? NOTHING_OFF : less == 1.0 ? Q_OFF : MORE_OFF;
+        V = v.V;
+        ngone = whole ? 0 : sm.fell;
+        gone = sm.gone;
+    }
+    // A row's last vector may be a part of one, of which nothing past the row is read.
     __device__ __forceinline__ uint4 load(const X* r, int at) const {
-        if (at + VEC<X> <= V) return __ldcg(reinterpret_cast<const uint4*>(r + at));
+        if (at + N <= V) return __ldcg(reinterpret_cast<const uint4*>(r + at));
         uint32_t w[4] = {0, 0, 0, 0};
         if (at < V)
 #pragma unroll
-            for (int i = 0; i < VEC<X>; ++i)
+            for (int i = 0; i < N; ++i)
                 if (at + i < V) {
                     if constexpr (sizeof(X) == 4) w[i] = __ldcg(reinterpret_cast<const uint32_t*>(r + at) + i);
                     else w[i / 2] |= (uint32_t)__ldcg(reinterpret_cast<const uint16_t*>(r + at) + i) << 16 * (i & 1);
                 }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    __device__ __forceinline__ void terms(uint4 pv, uint4 qv, int at, Two (&w)[VEC<X>]) const {
-        constexpr int N = VEC<X>;
-        float f[N], g[N];
+    __device__ __forceinline__ uint4 load_q(int at) const { return DRAWN && off ? load(q, at) : make_uint4(0, 0, 0, 0); }
+    // The vector's entries, with what was rejected as chosen taken out.
+    __device__ __forceinline__ void entries(uint4 pv, uint4 qv, int at, float (&f)[N], float (&g)[N]) const {
         widen<X>(pv, f);
-        if (DRAWN) widen<X>(qv, g);
+        widen<X>(qv, g);
 #pragma unroll
-        for (int i = 0; i < N; ++i) w[i] = DRAWN && less ? left_of(f[i], g[i], a) : Two{f[i], 0.f};
+        for (int i = 0; i < N; ++i) g[i] = DRAWN ? fmaxf(g[i], 0.f) : 0.f;
         if (!DRAWN)
             for (int k = 0; k < ngone; ++k)
 #pragma unroll
                 for (int i = 0; i < N; ++i)
-                    if (gone[k] == at + i) w[i] = {0.f, 0.f};
+                    if (gone[k] == at + i) f[i] = 0.f;
+    }
+    // One entry, to 2^-46 of the larger term.  With f >= t the difference's rounding error is (f - d) - t.
+    __device__ __forceinline__ Two term(float f, float g) const {
+        if (!DRAWN || off != MORE_OFF) {
+            const float h = fmaxf(f, g), d = h - g;
+            return {d, (h - d) - g};
+        }
+        const float t = __fmul_rn(g, a.hi), tl = fmaf(g, a.lo, fmaf(g, a.hi, -t));
+        const float h = fmaxf(f, t), d = h - t, e = ((h - d) - t) - tl;
+        return d + e > 0.f ? Two{d, e} : Two{0.f, 0.f};
+    }
+    // Adds a vector to running sums of the even and the odd entries.
+    __device__ __forceinline__ void add(uint4 pv, uint4 qv, int at, uint64_t& hi, uint64_t& lo) const {
+        float f[N], g[N];
+        entries(pv, qv, at, f, g);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+            uint64_t d, e = 0;
+            if (!DRAWN || off != MORE_OFF) {
+                const uint64_t h = pair(fmaxf(f[i], g[i]), fmaxf(f[i + 1], g[i + 1])), t = pair(g[i], g[i + 1]);
+                d = DRAWN ? sub2(h, t) : h;
+                if (DRAWN) e = sub2(sub2(h, d), t);
+            } else {
+                const Two x = term(f[i], g[i]), y = term(f[i + 1], g[i + 1]);
+                d = pair(x.hi, y.hi);
+                e = pair(x.lo, y.lo);
+            }
+            const uint64_t t = add2(hi, d), v = sub2(t, hi);
+            lo = add2(lo, add2(sub2(hi, sub2(t, v)), sub2(d, v)));
+            if (DRAWN) lo = add2(lo, e);
+            hi = t;
+        }
     }
 };
 
-__device__ __forceinline__ double warp_sum(double x) {
+__device__ __forceinline__ Two shuffle_up(Two x, int o) { return {__shfl_up_sync(0xffffffffu, x.hi, o), __shfl_up_sync(0xffffffffu, x.lo, o)}; }
+__device__ __forceinline__ Two shuffle(Two x, int l) { return {__shfl_sync(0xffffffffu, x.hi, l), __shfl_sync(0xffffffffu, x.lo, l)}; }
+__device__ __forceinline__ Two warp_sum(Two x) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    for (int o = 16; o; o >>= 1) x = x + Two{__shfl_xor_sync(0xffffffffu, x.hi, o), __shfl_xor_sync(0xffffffffu, x.lo, o)};
     return x;
 }
-__device__ __forceinline__ double warp_scan(double x) {
+// The sum of the lanes before this one; *all gets that of all.
+__device__ __forceinline__ Two warp_before(Two x, Two* all) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const double y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        const Two y = shuffle_up(x, o);
+        if (lane >= o) x = y + x;
     }
-    return x;
+    *all = shuffle(x, 31);
+    const Two y = shuffle_up(x, 1);
+    return lane ? y : Two{0.f, 0.f};
 }
-__device__ __forceinline__ void st_cluster_f64(uint32_t addr, double x) {
-    asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(addr), "d"(x) : "memory");
+__device__ __forceinline__ void st_cluster(uint32_t addr, Two x) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(x.hi), "f"(x.lo) : "memory");
 }
 
 template <class X, bool DRAWN>
@@ -264,32 +308,25 @@ __global__ void __launch_bounds__(THREADS) k_verify(const VerifyArgs a, int clus
         __syncthreads();
         // ---- a pass over what is left at the last row that stands
         const int turn = sm.pass & 1;
-        const double less = whole ? 0.0 : sm.less;
-        Left<X, DRAWN> left = {P + sm.last * a.ldp, DRAWN ? Q + sm.last * a.ldq : nullptr, {(float)less, (float)(less - (double)(float)less)},
-                               less > 0.0, a.V, whole ? 0 : sm.fell, sm.gone};
+        const Left<X, DRAWN> left(a, sm, q0, whole);
         const int mine = rank * WARPS + warp;
         const int v0 = min(mine * per, vecs), v1 = min(v0 + per, vecs);
-        Two s = {0.f, 0.f};
-        constexpr int UN = 4;
-        for (int v = v0 + lane; v < v1; v += 32 * UN) {
-            uint4 pv[UN], qv[UN];
+        uint64_t hi = 0, lo = 0;
+        for (int v = v0 + lane; v < v1; v += 32 * UNROLL) {
+            uint4 pv[UNROLL], qv[UNROLL];
 #pragma unroll
-            for (int i = 0; i < UN; ++i) {
+            for (int i = 0; i < UNROLL; ++i) {
                 const int at = v + 32 * i < v1 ? (v + 32 * i) * N : a.V;
                 pv[i] = left.load(left.p, at);
-                qv[i] = DRAWN && left.less ? left.load(left.q, at) : make_uint4(0, 0, 0, 0);
+                qv[i] = left.load_q(at);
             }
 #pragma unroll
-            for (int i = 0; i < UN; ++i) {
-                Two w[N];
-                left.terms(pv[i], qv[i], v + 32 * i < v1 ? (v + 32 * i) * N : a.V, w);
-#pragma unroll
-                for (int k = 0; k < N; ++k) add(s, w[k]);
-            }
+            for (int i = 0; i < UNROLL; ++i) left.add(pv[i], qv[i], (v + 32 * i) * N, hi, lo);
         }
-        const double sum = warp_sum((double)s.hi + (double)s.lo);
+        const float2 h = unpair(hi), l = unpair(lo);
+        const Two sum = warp_sum(Two{h.x, l.x} + Two{h.y, l.y});
         if (cluster > 1) {
-            if (lane < cluster) st_cluster_f64(mapa_shared(smem_u32(&sm.sum[turn][mine]), lane), sum);
+            if (lane < cluster) st_cluster(mapa_shared(smem_u32(&sm.sum[turn][mine]), lane), sum);
             cluster_sync_all();
         } else {
             if (lane == 0) sm.sum[turn][mine] = sum;
@@ -297,20 +334,18 @@ __global__ void __launch_bounds__(THREADS) k_verify(const VerifyArgs a, int clus
         }
         // ---- all shares' sums, and the share that holds the drawn number
         if (warp == 0) {
-            const int shares = cluster * WARPS;          // lane l has shares l k .. l k + k - 1
-            const int k = (shares + 31) / 32;
-            double own = 0.0;
+            const int shares = cluster * WARPS, k = (shares + 31) / 32;      // lane l has shares l k .. l k + k - 1
+            Two own = {0.f, 0.f}, total;
             for (int i = 0; i < k; ++i)
-                if (lane * k + i < shares) own += sm.sum[turn][lane * k + i];
-            const double upto = warp_scan(own), total = __shfl_sync(0xffffffffu, upto, 31);
-            const double aim = (double)__ldcg(a.u_last + b) * total;
-            double at = upto - own;
-            int found = -1, some = -1;
-            double before = 0.0, before_some = 0.0;
+                if (lane * k + i < shares) own = own + sm.sum[turn][lane * k + i];
+            Two at = warp_before(own, &total);
+            const Two aim = times(total, __ldcg(a.u_last + b));
+            int found = -1, some = -1;                   // the share; the last one that has anything
+            Two before = at, before_some = at;
             for (int i = 0; i < k; ++i)
                 if (lane * k + i < shares) {
-                    const double x = sm.sum[turn][lane * k + i];
-                    if (x > 0.0) {
+                    const Two x = sm.sum[turn][lane * k + i];
+                    if (x.hi > 0.f) {
                         some = lane * k + i;
                         before_some = at;
                         if (found < 0 && at + x > aim) {
@@ -318,16 +353,16 @@ __global__ void __launch_bounds__(THREADS) k_verify(const VerifyArgs a, int clus
                             before = at;
                         }
                     }
-                    at += x;
+                    at = at + x;
                 }
             const uint32_t who = __ballot_sync(0xffffffffu, found >= 0), any = __ballot_sync(0xffffffffu, some >= 0);
             const int src = who ? __ffs(who) - 1 : any ? 31 - __clz(any) : 0;
             const int share = __shfl_sync(0xffffffffu, who ? found : some, src);
-            const double base = __shfl_sync(0xffffffffu, who ? before : before_some, src);
+            const Two base = shuffle(who ? before : before_some, src);
             if (lane == 0) {
-                if (sm.what == 1) sm.mass = total;
+                if (sm.what == 1) sm.mass = wide(total);
                 sm.share = any ? share : -1;
-                sm.total = aim - base;                   // what is to be passed within the share
+                sm.aim = aim + Two{-base.hi, -base.lo};
                 ++sm.pass;
             }
         }
@@ -352,40 +387,39 @@ __global__ void __launch_bounds__(THREADS) k_verify(const VerifyArgs a, int clus
     }
     if (sm.share < 0 || sm.share / WARPS != rank) return;
     // The share again, a vector a thread: the first x whose running sum passes the aim, or the last one with a weight.
-    const double less = whole ? 0.0 : sm.less;
-    Left<X, DRAWN> left = {P + sm.last * a.ldp, DRAWN ? Q + sm.last * a.ldq : nullptr, {(float)less, (float)(less - (double)(float)less)},
-                           less > 0.0, a.V, whole ? 0 : sm.fell, sm.gone};
+    const Left<X, DRAWN> left(a, sm, q0, whole);
     const int v0 = sm.share * per, v1 = min(v0 + per, vecs);
-    double aim = sm.total;
+    const Two aim = sm.aim;
+    Two base = {0.f, 0.f};
     int newest = -1;                                     // the last x with a weight so far
     for (int c = v0; c < v1; c += THREADS) {
         const int v = c + tid, at = v < v1 ? v * N : a.V;
-        Two w[N];
-        left.terms(left.load(left.p, at), DRAWN && left.less ? left.load(left.q, at) : make_uint4(0, 0, 0, 0), at, w);
-        double own = 0.0;
-        int tail = -1;
+        float f[N], g[N];
+        left.entries(left.load(left.p, at), left.load_q(at), at, f, g);
+        Two own = {0.f, 0.f}, all;
+        int tail = -1, hit = INT32_MAX;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            own += (double)w[i].hi + (double)w[i].lo;
-            if (w[i].hi + w[i].lo > 0.f) tail = at + i;
+            const Two x = left.term(f[i], g[i]);
+            own = own + x;
+            if (x.hi > 0.f) tail = at + i;
         }
-        const double upto = warp_scan(own);
+        Two r = warp_before(own, &all);
         __syncthreads();                                 // (the look before is read)
-        if (lane == 31) sm.part[warp] = upto;
+        if (lane == 0) sm.part[warp] = all;
         if (tid == 0) sm.what = INT32_MAX, sm.next = -1;
         __syncthreads();
-        double run = upto - own, all = 0.0;
+        Two ahead = base;
         for (int i = 0; i < WARPS; ++i) {
-            if (i < warp) run += sm.part[i];
-            all += sm.part[i];
+            if (i == warp) r = ahead + r;
+            ahead = ahead + sm.part[i];
         }
-        int hit = INT32_MAX;
-        double r = run;
+        base = ahead;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const double x = (double)w[i].hi + (double)w[i].lo;
-            r += x;
-            if (hit == INT32_MAX && x > 0.0 && r > aim) hit = at + i;
+            const Two x = left.term(f[i], g[i]);
+            r = r + x;
+            if (hit == INT32_MAX && x.hi > 0.f && r > aim) hit = at + i;
         }
         if (hit != INT32_MAX) atomicMin(&sm.what, hit);
         if (tail >= 0) atomicMax(&sm.next, tail);
@@ -395,17 +429,16 @@ __global__ void __launch_bounds__(THREADS) k_verify(const VerifyArgs a, int clus
             newest = sm.what;
             break;
         }
-        aim -= all;
     }
     if (tid == 0) out[stand] = newest;
 }
 
 template <class X, bool DRAWN>
 cudaError_t run(const VerifyArgs& a, cudaStream_t s) {
-    // CTAs of a sequence: enough for every SM to have one, as long as a warp's share keeps 32 vectors
+    // CTAs of a sequence: enough for every SM to have two, as long as a warp's share keeps 16 vectors
     const int64_t vecs = (a.V + VEC<X> - 1) / VEC<X>;
     int cluster = 1;
-    while (cluster < MAX_CLUSTER && cluster * a.B < num_sms() && vecs >= (int64_t)cluster * 2 * WARPS * 32) cluster *= 2;
+    while (cluster < MAX_CLUSTER && cluster * a.B < 2 * num_sms() && vecs > (int64_t)cluster * WARPS * 32) cluster *= 2;
     if (cluster > 8) {
         const cudaError_t e = cudaFuncSetAttribute(k_verify<X, DRAWN>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;

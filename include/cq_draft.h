@@ -100,8 +100,8 @@ cq_status cq_attn_kv8_tree(const void* Q, int xt, int64_t T, int64_t Hq, int64_t
  * with w(0) + .. + w(x) > u_last[b] * (the sum of w), or the last x with w(x) > 0; if w is
  * nothing, from P[row], and if that is nothing as well the token is -1.  So every
  * token is distributed as the target's, if u and u_last are independent and uniform.
- * Entries of P and Q that are no positive finite numbers count as 0; rows of P are taken to
- * sum to 1 and are not normalised.
+ * Negative entries of P and Q and NaN count as 0; a row with an infinite entry leaves its
+ * sequence's outputs unspecified.  Rows of P are taken to sum to 1 and are not normalised.
  * out [B][ldo]: the tokens that stand, then the drawn one; path [B][ldo]: the rows that
  * stand, the first one included; the rest of a row's first max_q entries is -1.  count [B]: drafted tokens that
  * stand (a sequence without rows: 0, and -1 throughout).

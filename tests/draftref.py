@@ -91,7 +91,7 @@ def attend(cache, b, q, scale, bits, out):
 
 def verify(P, Q, tokens, parents, u, u_last):
     """(tokens that stand and the drawn one, places of the rows that stand) of one sequence; P, Q [n][V] f64."""
-    good = lambda x: np.where(np.isfinite(x) & (x > 0), x, 0.0)
+    good = lambda x: np.where(x > 0, x, 0.0)
     cur, out, path = 0, [], [0]
     while True:
         p, q = good(P[cur]), None if Q is None else good(Q[cur])

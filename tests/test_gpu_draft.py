@@ -495,10 +495,18 @@ def test_verify_edges():
             check_verify(z(2), None, i32([0, 9]), chain, [2], f(0.0, u), f(ul), tree=False)
     odd = z(2)
     odd[:, 9] = 1.0
-    odd[:, 0], odd[:, 1], odd[:, 2], odd[:, 3], odd[:, 60] = float("nan"), float("inf"), -1.0, -float("inf"), 0.25
+    odd[:, 0], odd[:, 2], odd[:, 3], odd[:, 60] = float("nan"), -1.0, -float("inf"), 0.25
     for ul in (0.0, 0.79, 0.81, 1.0):
         check_verify(odd, odd, i32([0, 60]), chain, [2], f(0.0, 0.9), f(ul), tree=False)
         check_verify(odd, None, i32([0, 0]), chain, [2], f(0.0, 0.0), f(ul), tree=False)
+    out, path, count = (torch.empty(s, dtype=torch.int32, device=DEV) for s in ((1, 2), (1, 2), (1,)))
+    for k in (0, 35, 69):                                                                       # an infinite entry: some token, no more
+        x = z(2)
+        x.copy_(odd)
+        x[:, k] = float("inf")
+        for Q in (x, odd, None):
+            cq.cq_verify(x, i32([0, 60]), i32([0, 2]), 2, f(0.0, 0.9), f(0.5), out, path, count, Q=Q)
+            assert cq.cq_get_device_error() == 0 and -1 <= out[0, count.item()].item() < V
     flat = z(1) + 1.0 / 64
     for k in range(V):                                                                          # borders met exactly
         check_verify(flat, None, i32([0]), [[-1]], [1], f(0.0), f(k / V), tree=False)
