@@ -16,8 +16,8 @@ using kv8::In;
 // A unit is 8 neighbouring channels of a head, together with their partners 8 channels rot/2 on in the half layout:
 // everything is moved 16 bytes at a time, and in place too, as a thread reads its units before it writes them.
 constexpr int THREADS = 256;
-template <class X>
-constexpr int EACH = sizeof(X) == 2 ? 4 : 2;             // units that a thread has under way
+template <class X, int LAYOUT>
+constexpr int EACH = sizeof(X) == 4 && LAYOUT == CQ_ROPE_HALF ? 2 : 4;   // units that a thread has under way
 
 template <class X>
 struct Eight {                                           // 8 channels as they lie in memory
@@ -58,7 +58,7 @@ struct Rows {
 template <class X, class Y, int LAYOUT>
 __global__ void __launch_bounds__(THREADS) k_rope(const Rows a, const Rope rope) {
     constexpr bool HALVES = LAYOUT == CQ_ROPE_HALF;
-    constexpr int E = EACH<X>;
+    constexpr int E = EACH<X, LAYOUT>;
     pdl_launch_dependents();
     pdl_wait();
     extern __shared__ float4 table4[];
@@ -126,7 +126,7 @@ template <class X, class Y>
 cudaError_t rope_as(Rows a, const Rope& rope, int layout, cudaStream_t s) {
     // tokens of a block of threads: enough units for all threads, a table of at most 32 KB
     const int units = (rope.half / (layout == CQ_ROPE_HALF ? 8 : 4) + (a.D - 2 * rope.half) / 8) * a.H;
-    a.per = std::max(1, std::min({THREADS * EACH<X> / units, 4096 / rope.half, a.T}));
+    a.per = std::max(1, std::min({THREADS * (layout == CQ_ROPE_HALF ? EACH<X, CQ_ROPE_HALF> : EACH<X, CQ_ROPE_PAIRS>) / units, 4096 / rope.half, a.T}));
     const size_t smem = (size_t)a.per * rope.half * 8;
     const dim3 grid((a.T + a.per - 1) / a.per);
     if (layout == CQ_ROPE_HALF) return kv8::launch_pdl(k_rope<X, Y, CQ_ROPE_HALF>, grid, dim3(THREADS), smem, s, a, rope);
@@ -140,102 +140,157 @@ cudaError_t rope_from(const Rows& a, int yt, const Rope& rope, int layout, cudaS
 }
 
 // ---- keys and values to the cache -----------------------------------------------------------------------------------
-// One warp has one block of 32 tokens of one head, as in the write without rotation; the warps of a block of
-// threads have up to four heads of the keys and of the values of one block of tokens, and make its table together while
-// their rows are on the way.
-constexpr int HEADS = 4;
+// A block of threads has one block of 32 tokens, and some or all of its heads: its table serves them all.  Two warps
+// have one head's keys or values, 16 tokens each, and exchange their largest magnitudes; a lane has 8 channels of a token,
+// in the half layout four and their partners, so that the turned values stay in registers between the magnitudes and the
+// codes (with a whole block to a warp they took 226, and turning twice instead cost more than the warps gained).
+// The next head's rows are on their way meanwhile.
+constexpr int WARPS = 8;
+
+// Four channels, as they lie in memory.
+template <class X>
+struct Four {
+    uint32_t v[sizeof(X)];
+    __device__ __forceinline__ void load(const X* p, bool in) {
+        if constexpr (sizeof(X) == 2) {
+            const uint2 u = in ? __ldcs(reinterpret_cast<const uint2*>(p)) : make_uint2(0, 0);
+            v[0] = u.x, v[1] = u.y;
+        } else {
+            const uint4 u = in ? __ldcs(reinterpret_cast<const uint4*>(p)) : make_uint4(0, 0, 0, 0);
+            v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
+        }
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(X) == 4) return __uint_as_float(v[i]);
+        else if constexpr (std::is_same<X, __half>::value) return __half2float(__ushort_as_half((unsigned short)(v[i / 2] >> 16 * (i & 1))));
+        else return __uint_as_float(i & 1 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16);
+    }
+};
+
+// The largest of three magnitudes; NaN if one is.
+__device__ __forceinline__ float max_abs(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 
 template <class X, int D, int LAYOUT>
-__global__ void __launch_bounds__(2 * HEADS * 32) k_write_rope(const kv8::Cache c, const kv8::Batch b, const X* K, const X* V,
-                                                               int64_t ldk, int64_t ldv, const Rope rope, int groups) {
+__global__ void __launch_bounds__(WARPS * 32, 2) k_write_rope(const kv8::Cache c, const kv8::Batch b, const X* K, const X* V,
+                                                              int64_t ldk, int64_t ldv, const Rope rope, int groups) {
     using namespace kv8;
+    constexpr int LPR = D / 8, RPI = 32 / LPR, IT = 16 / RPI;    // lanes a row, rows a step, steps
+    __shared__ float4 cs4[BLK * D / 8], sn4[BLK * D / 8];        // rows of D / 2 cosines and sines
+    __shared__ uint32_t tops[2][WARPS];
     pdl_launch_dependents();
     pdl_wait();
-    constexpr int N = In<X>::N, LPR = D / N, RPI = 32 / LPR, IT = BLK / RPI;   // lanes a row, rows a step
-    __shared__ float4 cs4[BLK * D / 8], sn4[BLK * D / 8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int head = (int)(blockIdx.x % groups) * HEADS + (warp >> 1);
-    const Item it = find_item<true>(c, b, blockIdx.x / groups, warp & 1, head);
+    const int kv = warp >> 1 & 1, row0 = 16 * (warp & 1) + lane / LPR, unit = lane % LPR;
+    const Item it = find_item<true>(c, b, blockIdx.x / groups, kv, 0);
     if (!it.ok) return;                                  // (the same for the whole block of threads)
-    const bool mine = head < c.Hkv;
-    const int sub = lane / LPR, col = (lane % LPR) * N;
-    const int64_t ld = it.kv ? ldv : ldk;
-    const X* src = (it.kv ? V : K) + it.row0 * ld + (int64_t)head * D + col;
-    uint4 u[IT];
+    const int h = rope.half, turned = LAYOUT == CQ_ROPE_HALF ? h / 4 : 2 * h / 8;
+    const bool turns = !kv && unit < turned;
+    const int ch = LAYOUT == CQ_ROPE_PAIRS ? 8 * unit : unit < turned ? 4 * unit : 8 * unit;
+    const int ch2 = LAYOUT == CQ_ROPE_HALF && unit < turned ? ch + h : ch + 4;
+    const int64_t ld = kv ? ldv : ldk;
+    const X* src = (kv ? V : K) + (it.row0 + row0 - it.lo) * ld;
+    Four<X> u[IT][2];
+    auto load = [&](int head) {
 #pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int r = i * RPI + sub;
-        u[i] = make_uint4(0, 0, 0, 0);
-        if (mine && r >= it.lo && r < it.hi) u[i] = __ldcs(reinterpret_cast<const uint4*>(src + (r - it.lo) * ld));
-    }
-    float* cs = reinterpret_cast<float*>(cs4);
-    float* sn = reinterpret_cast<float*>(sn4);
-    // Factors in chunks of four pairs, rows of D / 8 chunks.  Half layout, 16-bit rows: a lane takes two neighbouring
-    // chunks; the even ones lie ahead of the odd ones, so that lanes read neighbouring chunks.
-    auto chunk = [&](int k) { return LAYOUT == CQ_ROPE_HALF && N == 8 ? (k >> 1) + (k & 1) * (D / 16) : k; };
-    for (int i = it.lo * rope.half + threadIdx.x; i < it.hi * rope.half; i += blockDim.x) {
-        const int r = i / rope.half, k = i - r * rope.half, at = r * (D / 2) + 4 * chunk(k >> 2) + (k & 3);
-        const int p = rope.pos ? __ldcg(rope.pos + it.row0 + (r - it.lo)) : it.tok0 + (r - it.lo);
-        cos_sin_at(turn_of(__ldcg(rope.freq + k)), p, rope.mag, cs[at], sn[at]);
-    }
-    __syncthreads();
-    if (!mine) return;
-    // A key's channels are turned where they are needed, for the block's largest magnitude and again for the codes: kept in
-    // between, in f32, they would take twice the registers of the rows and leave half the warps.
-    const int h = rope.half;
-    const bool first = col < h, turns = !it.kv && col < 2 * h;
-    const int from = !turns ? lane : first ? lane + h / N : lane - h / N;    // half layout: the lane with the partners
-    const int at = LAYOUT == CQ_ROPE_HALF ? (first ? col : col - h) / 4 : col / 2;
-    store_block<D, N>(c, it, [&](int i, float (&f)[N]) {
-        In<X>::get(u[i], f);
-        if (it.kv) return;                               // (the same for the whole warp)
-        const int r = i * RPI + sub;
-        const bool turn = turns && r >= it.lo && r < it.hi;
-        if constexpr (LAYOUT == CQ_ROPE_HALF) {
-            uint4 w;
-            w.x = __shfl_sync(0xffffffffu, u[i].x, from);
-            w.y = __shfl_sync(0xffffffffu, u[i].y, from);
-            w.z = __shfl_sync(0xffffffffu, u[i].z, from);
-            w.w = __shfl_sync(0xffffffffu, u[i].w, from);
-            if (!turn) return;
-            float g[N];
-            In<X>::get(w, g);
-#pragma unroll
-            for (int j = 0; j < N; j += 4) {
-                const float4 p = cs4[r * (D / 8) + chunk(at + j / 4)], q = sn4[r * (D / 8) + chunk(at + j / 4)];
-                const float c4[4] = {p.x, p.y, p.z, p.w}, s4[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    f[j + e] = first ? turn_first(f[j + e], g[j + e], c4[e], s4[e]) : turn_second(g[j + e], f[j + e], c4[e], s4[e]);
-            }
-        } else {
-            if (!turn) return;
-            float c4[N / 2], s4[N / 2];
-            if constexpr (N == 8) {
-                const float4 p = *reinterpret_cast<const float4*>(cs + r * (D / 2) + at), q = *reinterpret_cast<const float4*>(sn + r * (D / 2) + at);
-                c4[0] = p.x, c4[1] = p.y, c4[2] = p.z, c4[3] = p.w;
-                s4[0] = q.x, s4[1] = q.y, s4[2] = q.z, s4[3] = q.w;
-            } else {
-                const float2 p = *reinterpret_cast<const float2*>(cs + r * (D / 2) + at), q = *reinterpret_cast<const float2*>(sn + r * (D / 2) + at);
-                c4[0] = p.x, c4[1] = p.y;
-                s4[0] = q.x, s4[1] = q.y;
-            }
-#pragma unroll
-            for (int j = 0; j < N / 2; ++j) {
-                const float a0 = f[2 * j], b0 = f[2 * j + 1];
-                f[2 * j] = turn_first(a0, b0, c4[j], s4[j]);
-                f[2 * j + 1] = turn_second(a0, b0, c4[j], s4[j]);
+        for (int i = 0; i < IT; ++i) {
+            const bool in = row0 + i * RPI >= it.lo && row0 + i * RPI < it.hi;
+            u[i][0].load(src + i * RPI * ld + head * D + ch, in);
+            u[i][1].load(src + i * RPI * ld + head * D + ch2, in);
+        }
+    };
+    int head = (int)(blockIdx.x % groups) * 2 + (warp >> 2);
+    if (head < c.Hkv) load(head);
+    {   // the table: a thread keeps to one pair
+        float* cs = reinterpret_cast<float*>(cs4);
+        float* sn = reinterpret_cast<float*>(sn4);
+        int wide = 8;
+        while (wide < h) wide *= 2;
+        const int k = threadIdx.x & (wide - 1);
+        if (k < h) {
+            const Turn f = turn_of(__ldcg(rope.freq + k));
+            for (int r = it.lo + threadIdx.x / wide; r < it.hi; r += WARPS * 32 / wide) {
+                const int p = rope.pos ? __ldcg(rope.pos + it.row0 + (r - it.lo)) : it.tok0 + (r - it.lo);
+                cos_sin_at(f, p, rope.mag, cs[r * (D / 2) + k], sn[r * (D / 2) + k]);
             }
         }
-    });
+    }
+    __syncthreads();
+    for (int n = 0; head < c.Hkv; head += 2 * groups, n ^= 1) {
+        float f[IT][8];
+#pragma unroll
+        for (int i = 0; i < IT; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[i][j] = u[i][j / 4].get(j & 3);
+        if (head + 2 * groups < c.Hkv) load(head + 2 * groups);
+        const int64_t block = it.block + (int64_t)head * (c.page / BLK);
+        float* sp = (kv ? c.s[1] : c.s[0]) + block;
+        const float s0 = it.lo > 0 ? *sp : 0.f;
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int r = row0 + i * RPI;
+            if (turns && r >= it.lo && r < it.hi) {
+                const float4 p = cs4[r * (D / 8) + unit], q = sn4[r * (D / 8) + unit];
+                const float c4[4] = {p.x, p.y, p.z, p.w}, s4[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    float& lo = f[i][LAYOUT == CQ_ROPE_HALF ? j : 2 * j];
+                    float& hi = f[i][LAYOUT == CQ_ROPE_HALF ? j + 4 : 2 * j + 1];
+                    const float a0 = lo, b0 = hi;
+                    lo = turn_first(a0, b0, c4[j], s4[j]);
+                    hi = turn_second(a0, b0, c4[j], s4[j]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) top = max_abs(top, f[i][j], f[i][j + 1]);
+        }
+        const uint32_t m0 = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+        if (lane == 0) tops[n][warp] = m0;
+        named_bar_sync(1 + (warp >> 1), 64);             // (both have the old scale, too)
+        const uint32_t m = max(m0, tops[n][warp ^ 1]);
+        const bool bad = m >= 0x7F800000u || s0 != s0;
+        const float s1 = bad ? __uint_as_float(0x7FC00000u) : fmaxf(s0, pow2(scale_exp(__uint_as_float(m))));
+        const float inv = bad ? 0.f : 1.0f / s1;         // exact: a power of two
+        int8_t* dst = (kv ? c.q[1] : c.q[0]) + block * (BLK * D);
+        if (it.lo > 0 && s1 > s0) {                      // the kept codes move to the larger scale
+            const float ratio = s0 * inv;
+            for (int r = row0; r < min(it.lo, (row0 & 16) + 16); r += RPI)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    uint32_t* p = reinterpret_cast<uint32_t*>(dst + r * D + (e ? ch2 : ch));
+                    const uint32_t w = *p;
+                    *p = pack4(code_of(byte_f(w, 0), ratio), code_of(byte_f(w, 1), ratio), code_of(byte_f(w, 2), ratio),
+                               code_of(byte_f(w, 3), ratio));
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < IT; ++i) {
+            const int r = row0 + i * RPI;
+            if (r < it.lo || r >= it.hi) continue;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float* g = f[i] + 4 * e;
+                *reinterpret_cast<uint32_t*>(dst + r * D + (e ? ch2 : ch)) =
+                    bad ? 0u : pack4(code_of(g[0], inv), code_of(g[1], inv), code_of(g[2], inv), code_of(g[3], inv));
+            }
+        }
+        if (lane == 0 && !(warp & 1)) *sp = s1;
+    }
 }
 
 template <class X, int D>
 cudaError_t write_as(const kv8::Cache& c, const kv8::Batch& b, const void* K, const void* V, int64_t ldk, int64_t ldv, const Rope& rope,
                      int layout, cudaStream_t s) {
     const X *k = static_cast<const X*>(K), *v = static_cast<const X*>(V);
-    const int groups = (c.Hkv + HEADS - 1) / HEADS;
-    const dim3 grid((unsigned)(kv8::store_slots(c, b) * groups)), block(2 * std::min(c.Hkv, HEADS) * 32);
+    // Blocks of threads of a block of tokens: one makes the table once, but goes through its heads two at a time; so more
+    // while they would not fill the GPU.
+    const int64_t slots = kv8::store_slots(c, b);
+    const int groups = (int)std::max<int64_t>(1, std::min<int64_t>((c.Hkv + 1) / 2, 4LL * num_sms() / slots));
+    const dim3 grid((unsigned)(slots * groups)), block(WARPS * 32);
     if (layout == CQ_ROPE_HALF) return kv8::launch_pdl(k_write_rope<X, D, CQ_ROPE_HALF>, grid, block, 0, s, c, b, k, v, ldk, ldv, rope, groups);
     return kv8::launch_pdl(k_write_rope<X, D, CQ_ROPE_PAIRS>, grid, block, 0, s, c, b, k, v, ldk, ldv, rope, groups);
 }
