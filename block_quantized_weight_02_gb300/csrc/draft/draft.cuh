@@ -61,11 +61,11 @@ __device__ __forceinline__ Turn turn_of(float freq) {
 // x in [-pi/4, pi/4] in two floats, and the series of sin x - x and cos x - 1 + x^2 / 2 (next terms below 2^-33) correct
 // leading parts that are exact.
 __device__ __forceinline__ void cos_sin(uint64_t t, float& c, float& s) {
-    constexpr float K = 0x1.921fb6p-62f, K2 = -0x1.777a5cp-87f;                  // 2 pi / 2^64
-    const uint32_t q = (uint32_t)((t + (1ull << 61)) >> 62);
-    const int64_t r = (int64_t)(t - ((uint64_t)q << 62));
-    const float rh = __ll2float_rn(r), rl = __ll2float_rn(r - (int64_t)rh);
-    const float x = __fmul_rn(rh, K), xl = fmaf(rh, K2, fmaf(rl, K, fmaf(rh, K, -x)));
+    constexpr float K = 0x1.921fb6p-30f, K2 = -0x1.777a5cp-55f, KL = 0x1.921fb6p-56f;   // 2 pi / 2^32, and / 2^58
+    const uint32_t top = (uint32_t)(t >> 32), low = (uint32_t)t, q = (top + (1u << 29)) >> 30;
+    const uint32_t r = top - (q << 30);                  // 30 bits and a sign; the upper 24 first, then the rest and `low`
+    const float rh = (float)(int)(r & ~63u), rl = (float)((r & 63u) << 26 | low >> 6);
+    const float x = __fmul_rn(rh, K), xl = fmaf(rl, KL, fmaf(rh, K2, fmaf(rh, K, -x)));
     const float z = __fmul_rn(x, x), zl = fmaf(2.f * x, xl, fmaf(x, x, -z));
     float p = fmaf(z, -1.f / 39916800.f, 1.f / 362880.f);
     p = fmaf(z, p, -1.f / 5040.f);
@@ -79,19 +79,26 @@ __device__ __forceinline__ void cos_sin(uint64_t t, float& c, float& s) {
     const float h = fmaf(-0.5f, z, 1.f), lost = fmaf(-0.5f, z, 1.f - h);
     const float cs = h + fmaf(z * z, p, fmaf(-0.5f, zl, lost));
     const float a = q & 1 ? sn : cs, b = q & 1 ? cs : sn;
-    c = (q + 1) & 2 ? -a : a;
-    s = q & 2 ? -b : b;
+    c = __uint_as_float(__float_as_uint(a) ^ ((q + 1) & 2) << 30);
+    s = __uint_as_float(__float_as_uint(b) ^ (q & 2) << 30);
 }
-// Of a pair at position p, times mag.
+// Of a pair at position p, times mag (NaN: a frequency that is no number).
+__device__ __forceinline__ float mag_of(const Turn& f, float mag) { return f.bad ? __uint_as_float(0x7FC00000u) : mag; }
 __device__ __forceinline__ void cos_sin_at(const Turn& f, int p, float mag, float& c, float& s) {
     cos_sin(f.f * (uint64_t)(int64_t)p, c, s);
-    c = f.bad ? __uint_as_float(0x7FC00000u) : c * mag;
-    s = f.bad ? __uint_as_float(0x7FC00000u) : s * mag;
+    c *= mag;
+    s *= mag;
 }
 
 // A pair turned: each product is rounded, then their sum, as the same steps in f32 anywhere else would.
 __device__ __forceinline__ float turn_first(float a, float b, float c, float s) { return __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s)); }
 __device__ __forceinline__ float turn_second(float a, float b, float c, float s) { return __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s)); }
+// Two pairs at once: a and b become what turn_first and turn_second give.
+__device__ __forceinline__ void turn2(uint64_t& a, uint64_t& b, uint64_t c, uint64_t s) {
+    const uint64_t p = sub2(mul2(a, c), mul2(b, s)), q = add2(mul2(b, c), mul2(a, s));
+    a = p;
+    b = q;
+}
 
 #endif  // __CUDACC__
 

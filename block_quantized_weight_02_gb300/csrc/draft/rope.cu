@@ -88,7 +88,8 @@ __global__ void __launch_bounds__(THREADS) k_rope(const Rows a, const Rope rope)
         if (i0 == 0) {                                   // the table, while the first rows are on their way
             for (int i = threadIdx.x; i < n * rope.half; i += THREADS) {
                 const int t = i / rope.half, k = i - t * rope.half;
-                cos_sin_at(turn_of(__ldcg(rope.freq + k)), __ldcg(rope.pos + t0 + t), rope.mag, cs[i], sn[i]);
+                const Turn w = turn_of(__ldcg(rope.freq + k));
+                cos_sin_at(w, __ldcg(rope.pos + t0 + t), mag_of(w, rope.mag), cs[i], sn[i]);
             }
             __syncthreads();
         }
@@ -144,7 +145,7 @@ cudaError_t rope_from(const Rows& a, int yt, const Rope& rope, int layout, cudaS
 // have one head's keys or values, 16 tokens each, and exchange their largest magnitudes; a lane has 8 channels of a token,
 // in the half layout four and their partners, so that the turned values stay in registers between the magnitudes and the
 // codes (with a whole block to a warp they took 226, and turning twice instead cost more than the warps gained).
-// The next head's rows are on their way meanwhile.
+// The next head's rows are on their way meanwhile (16-bit rows, or 64 channels).
 constexpr int WARPS = 8;
 
 // Four channels, as they lie in memory.
@@ -175,111 +176,147 @@ __device__ __forceinline__ float max_abs(float a, float b, float c) {
 }
 
 template <class X, int D, int LAYOUT>
-__global__ void __launch_bounds__(WARPS * 32, 2) k_write_rope(const kv8::Cache c, const kv8::Batch b, const X* K, const X* V,
-                                                              int64_t ldk, int64_t ldv, const Rope rope, int groups) {
-    using namespace kv8;
-    constexpr int LPR = D / 8, RPI = 32 / LPR, IT = 16 / RPI;    // lanes a row, rows a step, steps
-    __shared__ float4 cs4[BLK * D / 8], sn4[BLK * D / 8];        // rows of D / 2 cosines and sines
-    __shared__ uint32_t tops[2][WARPS];
-    pdl_launch_dependents();
-    pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int kv = warp >> 1 & 1, row0 = 16 * (warp & 1) + lane / LPR, unit = lane % LPR;
-    const Item it = find_item<true>(c, b, blockIdx.x / groups, kv, 0);
-    if (!it.ok) return;                                  // (the same for the whole block of threads)
-    const int h = rope.half, turned = LAYOUT == CQ_ROPE_HALF ? h / 4 : 2 * h / 8;
-    const bool turns = !kv && unit < turned;
-    const int ch = LAYOUT == CQ_ROPE_PAIRS ? 8 * unit : unit < turned ? 4 * unit : 8 * unit;
-    const int ch2 = LAYOUT == CQ_ROPE_HALF && unit < turned ? ch + h : ch + 4;
-    const int64_t ld = kv ? ldv : ldk;
-    const X* src = (kv ? V : K) + (it.row0 + row0 - it.lo) * ld;
-    Four<X> u[IT][2];
-    auto load = [&](int head) {
+struct Writer {
+    static constexpr int LPR = D / 8, RPI = 32 / LPR, IT = 16 / RPI;     // lanes a row, rows a step, steps
+    static constexpr bool AHEAD = sizeof(X) * D <= 256;  // two heads' rows at once fit the registers
+    const kv8::Cache& c;
+    const kv8::Item& it;
+    const float4 *cs4, *sn4;                             // rows of D / 2 cosines and sines
+    uint32_t (*tops)[WARPS];
+    int half;                                            // rot / 2
+
+    // The block's rows out of `src` (row it.lo's), FULL: all 32.
+    template <bool FULL>
+    __device__ __forceinline__ void run(const X* src, int64_t ld, int head, int step, int* place, const Rope& rope) {
+        using namespace kv8;
+        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kv = warp >> 1 & 1;
+        const int row0 = 16 * (warp & 1) + lane / LPR, unit = lane % LPR;
+        const int turned = half / 4;                     // units of a row with pairs
+        const bool turns = !kv && unit < turned;
+        const int ch = LAYOUT == CQ_ROPE_PAIRS ? 8 * unit : unit < turned ? 4 * unit : 8 * unit;
+        const int ch2 = LAYOUT == CQ_ROPE_HALF && unit < turned ? ch + half : ch + 4;
+        auto in = [&](int i) { return FULL || (row0 + i * RPI >= it.lo && row0 + i * RPI < it.hi); };
+        const X* from = src + (row0 - it.lo) * ld + ch;
+        Four<X> u[IT][2];
+        auto load = [&](int head) {
+            const X* p = from + head * D;
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const bool in = row0 + i * RPI >= it.lo && row0 + i * RPI < it.hi;
-            u[i][0].load(src + i * RPI * ld + head * D + ch, in);
-            u[i][1].load(src + i * RPI * ld + head * D + ch2, in);
-        }
-    };
-    int head = (int)(blockIdx.x % groups) * 2 + (warp >> 2);
-    if (head < c.Hkv) load(head);
-    {   // the table: a thread keeps to one pair
-        float* cs = reinterpret_cast<float*>(cs4);
-        float* sn = reinterpret_cast<float*>(sn4);
-        int wide = 8;
-        while (wide < h) wide *= 2;
-        const int k = threadIdx.x & (wide - 1);
-        if (k < h) {
-            const Turn f = turn_of(__ldcg(rope.freq + k));
-            for (int r = it.lo + threadIdx.x / wide; r < it.hi; r += WARPS * 32 / wide) {
-                const int p = rope.pos ? __ldcg(rope.pos + it.row0 + (r - it.lo)) : it.tok0 + (r - it.lo);
-                cos_sin_at(f, p, rope.mag, cs[r * (D / 2) + k], sn[r * (D / 2) + k]);
+            for (int i = 0; i < IT; ++i, p += RPI * ld) {
+                u[i][0].load(p, in(i));
+                u[i][1].load(p + (ch2 - ch), in(i));
             }
-        }
-    }
-    __syncthreads();
-    for (int n = 0; head < c.Hkv; head += 2 * groups, n ^= 1) {
-        float f[IT][8];
+        };
+        if (head < c.Hkv) load(head);
+        table(place, rope);
+        __syncthreads();
+        float* sp = (kv ? c.s[1] : c.s[0]) + it.block;
+        int8_t* dst = (kv ? c.q[1] : c.q[0]) + it.block * (BLK * D) + row0 * D + ch;
+        const int blocks = c.page / BLK;                 // from a head's blocks to the next one's
+        for (int n = 0; head < c.Hkv; head += step, n ^= 1) {
+            uint64_t f[IT][4];                           // a row's channels in pairs: ch .., ch2 ..
 #pragma unroll
-        for (int i = 0; i < IT; ++i)
+            for (int i = 0; i < IT; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[i][j] = u[i][j / 4].get(j & 3);
-        if (head + 2 * groups < c.Hkv) load(head + 2 * groups);
-        const int64_t block = it.block + (int64_t)head * (c.page / BLK);
-        float* sp = (kv ? c.s[1] : c.s[0]) + block;
-        const float s0 = it.lo > 0 ? *sp : 0.f;
-        float top = 0.f;
+                for (int j = 0; j < 4; ++j) f[i][j] = pair(u[i][j / 2].get(2 * (j & 1)), u[i][j / 2].get(2 * (j & 1) + 1));
+            if (AHEAD && head + step < c.Hkv) load(head + step);
+            float* sph = sp + (int64_t)head * blocks;
+            int8_t* to = dst + (int64_t)head * blocks * (BLK * D);
+            const float s0 = !FULL && it.lo > 0 ? *sph : 0.f;
+            float top = 0.f;
 #pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int r = row0 + i * RPI;
-            if (turns && r >= it.lo && r < it.hi) {
-                const float4 p = cs4[r * (D / 8) + unit], q = sn4[r * (D / 8) + unit];
-                const float c4[4] = {p.x, p.y, p.z, p.w}, s4[4] = {q.x, q.y, q.z, q.w};
+            for (int i = 0; i < IT; ++i) {
+                if (turns && in(i)) {
+                    const float4 p = cs4[(row0 + i * RPI) * (D / 8) + unit], q = sn4[(row0 + i * RPI) * (D / 8) + unit];
+                    if (LAYOUT == CQ_ROPE_HALF) {
+                        turn2(f[i][0], f[i][2], pair(p.x, p.y), pair(q.x, q.y));
+                        turn2(f[i][1], f[i][3], pair(p.z, p.w), pair(q.z, q.w));
+                    } else {                             // (a, b) (a, b) of two pairs at a time
+                        const float c4[4] = {p.x, p.y, p.z, p.w}, s4[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 v = unpair(f[i][j]);
+                            f[i][j] = pair(turn_first(v.x, v.y, c4[j], s4[j]), turn_second(v.x, v.y, c4[j], s4[j]));
+                        }
+                    }
+                }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    float& lo = f[i][LAYOUT == CQ_ROPE_HALF ? j : 2 * j];
-                    float& hi = f[i][LAYOUT == CQ_ROPE_HALF ? j + 4 : 2 * j + 1];
-                    const float a0 = lo, b0 = hi;
-                    lo = turn_first(a0, b0, c4[j], s4[j]);
-                    hi = turn_second(a0, b0, c4[j], s4[j]);
+                    const float2 v = unpair(f[i][j]);
+                    top = max_abs(top, v.x, v.y);
                 }
             }
+            const uint32_t m0 = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+            if (lane == 0) tops[n][warp] = m0;
+            named_bar_sync(1 + (warp >> 1), 64);         // (both have the old scale, too)
+            const uint32_t m = max(m0, tops[n][warp ^ 1]);
+            const bool bad = m >= 0x7F800000u || s0 != s0;
+            const float s1 = bad ? __uint_as_float(0x7FC00000u) : fmaxf(s0, pow2(scale_exp(__uint_as_float(m))));
+            const float inv = bad ? 0.f : 1.0f / s1;     // exact: a power of two
+            if (!FULL && it.lo > 0 && s1 > s0) {         // the kept codes move to the larger scale
+                const float ratio = s0 * inv;
+                for (int i = 0; i < IT && row0 + i * RPI < it.lo; ++i)
 #pragma unroll
-            for (int j = 0; j < 8; j += 2) top = max_abs(top, f[i][j], f[i][j + 1]);
-        }
-        const uint32_t m0 = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
-        if (lane == 0) tops[n][warp] = m0;
-        named_bar_sync(1 + (warp >> 1), 64);             // (both have the old scale, too)
-        const uint32_t m = max(m0, tops[n][warp ^ 1]);
-        const bool bad = m >= 0x7F800000u || s0 != s0;
-        const float s1 = bad ? __uint_as_float(0x7FC00000u) : fmaxf(s0, pow2(scale_exp(__uint_as_float(m))));
-        const float inv = bad ? 0.f : 1.0f / s1;         // exact: a power of two
-        int8_t* dst = (kv ? c.q[1] : c.q[0]) + block * (BLK * D);
-        if (it.lo > 0 && s1 > s0) {                      // the kept codes move to the larger scale
-            const float ratio = s0 * inv;
-            for (int r = row0; r < min(it.lo, (row0 & 16) + 16); r += RPI)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    uint32_t* p = reinterpret_cast<uint32_t*>(dst + r * D + (e ? ch2 : ch));
-                    const uint32_t w = *p;
-                    *p = pack4(code_of(byte_f(w, 0), ratio), code_of(byte_f(w, 1), ratio), code_of(byte_f(w, 2), ratio),
-                               code_of(byte_f(w, 3), ratio));
-                }
-        }
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int r = row0 + i * RPI;
-            if (r < it.lo || r >= it.hi) continue;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float* g = f[i] + 4 * e;
-                *reinterpret_cast<uint32_t*>(dst + r * D + (e ? ch2 : ch)) =
-                    bad ? 0u : pack4(code_of(g[0], inv), code_of(g[1], inv), code_of(g[2], inv), code_of(g[3], inv));
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t* p = reinterpret_cast<uint32_t*>(to + i * RPI * D + (e ? ch2 - ch : 0));
+                        const uint32_t w = *p;
+                        *p = pack4(code_of(byte_f(w, 0), ratio), code_of(byte_f(w, 1), ratio), code_of(byte_f(w, 2), ratio),
+                                   code_of(byte_f(w, 3), ratio));
+                    }
             }
+            if (bad) {                                   // (a spoilt block's codes are 0)
+#pragma unroll
+                for (int i = 0; i < IT; ++i) f[i][0] = f[i][1] = f[i][2] = f[i][3] = 0;
+            }
+            const uint64_t by = pair(inv, inv), one = pair(12582912.0f, 12582912.0f);
+#pragma unroll
+            for (int i = 0; i < IT; ++i) {
+                if (!in(i)) continue;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {            // the codes are the sums' low bytes, as in code_of
+                    const uint64_t a = fma2(f[i][2 * e], by, one), b = fma2(f[i][2 * e + 1], by, one);
+                    *reinterpret_cast<uint32_t*>(to + i * RPI * D + (e ? ch2 - ch : 0)) =
+                        pack4((uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32));
+                }
+            }
+            if (lane == 0 && !(warp & 1)) *sph = s1;
+            if (!AHEAD && head + step < c.Hkv) load(head + step);
         }
-        if (lane == 0 && !(warp & 1)) *sp = s1;
     }
+
+    // Cosines and sines of the block's rows; a thread keeps to one pair.
+    __device__ __forceinline__ void table(int* place, const Rope& rope) const {
+        float* cs = reinterpret_cast<float*>(const_cast<float4*>(cs4));
+        float* sn = reinterpret_cast<float*>(const_cast<float4*>(sn4));
+        if (threadIdx.x < it.hi - it.lo) place[it.lo + threadIdx.x] = rope.pos ? __ldcg(rope.pos + it.row0 + threadIdx.x) : it.tok0 + (int)threadIdx.x;
+        int wide = 8;
+        while (wide < half) wide *= 2;
+        const int k = threadIdx.x & (wide - 1);
+        const Turn f = turn_of(k < half ? __ldcg(rope.freq + k) : 0.f);
+        const float mag = mag_of(f, rope.mag);
+        __syncthreads();
+        if (k < half)
+            for (int r = it.lo + threadIdx.x / wide; r < it.hi; r += WARPS * 32 / wide)
+                cos_sin_at(f, place[r], mag, cs[r * (D / 2) + k], sn[r * (D / 2) + k]);
+    }
+};
+
+template <class X, int D, int LAYOUT>
+__global__ void __launch_bounds__(WARPS * 32, 2) k_write_rope(const kv8::Cache c, const kv8::Batch b, const X* K, const X* V,
+                                                              int64_t ldk, int64_t ldv, const Rope rope, int groups) {
+    __shared__ float4 cs4[kv8::BLK * D / 8], sn4[kv8::BLK * D / 8];
+    __shared__ uint32_t tops[2][WARPS];
+    __shared__ int place[kv8::BLK];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, kv = warp >> 1 & 1;
+    const kv8::Item it = kv8::find_item<true>(c, b, blockIdx.x / groups, kv, 0);
+    if (!it.ok) return;                                  // (the same for the whole block of threads)
+    Writer<X, D, LAYOUT> w = {c, it, cs4, sn4, tops, rope.half};
+    const int64_t ld = kv ? ldv : ldk;
+    const X* src = (kv ? V : K) + it.row0 * ld;
+    const int head = (int)(blockIdx.x % groups) * 2 + (warp >> 2), step = 2 * groups;
+    if (it.hi - it.lo == kv8::BLK) w.template run<true>(src, ld, head, step, place, rope);
+    else w.template run<false>(src, ld, head, step, place, rope);
 }
 
 template <class X, int D>
