@@ -430,56 +430,77 @@ def cq_rope_freqs(rot, base=10000.0, kind=CQ_ROPE_PLAIN, factor=1.0, low=1.0, hi
     return freq, mag.value
 
 
-def _here(*tensors):
+_T = None
+
+
+def _types():
+    """{torch type: CQ_F16 ..}, and torch's int32, f32, uint32 and its raw stream calls (looked up once: a call's time counts)."""
+    global _T
+    if _T is None:
+        import torch
+        _T = ({torch.float16: CQ_F16, torch.bfloat16: CQ_BF16, torch.float32: CQ_F32}, torch.int32, torch.float32, torch.uint32, torch._C)
+    return _T
+
+
+def _here(first, *rest):
     """The current device's current stream, for tensors that all lie on that device (None: left out)."""
-    import torch
-    for t in tensors:
+    d = first.get_device()
+    if d >= 0:
+        C = (_T or _types())[4]
+        dev = C._cuda_getDevice()
+        for t in rest:
+            if t is not None and t.get_device() != d:
+                break
+        else:
+            if d == dev:
+                return C._cuda_getCurrentRawStream(dev)
+    for t in (first, *rest):
         if t is not None and t.get_device() < 0:
             raise ValueError("the tensors must be on a GPU")
-    dev = torch._C._cuda_getDevice()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"a tensor is on device {t.get_device()}, the current one is {dev}")
-    return torch._C._cuda_getCurrentRawStream(dev)
+    raise ValueError("the tensors must be on the current device")
 
 
-def _dense(t, what, dtype, shape):
-    """A dense tensor's address (None: NULL)."""
+def _dense(t, what, dtype, n):
+    """The address of a dense tensor of n entries (None: NULL)."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{what} must be a dense {dtype} tensor {list(shape)}, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
+    if t.dtype is not dtype or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be a dense {dtype} tensor of {n} entries, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
     return t.data_ptr()
 
 
-def _rows3(t, what):
+def _rows3(sh, st, what):
     """Row pitch of a [T][H][D] tensor whose rows are dense."""
-    sh, st = t.shape, t.stride()
     if len(sh) != 3 or (sh[2] > 1 and st[2] != 1) or (sh[1] > 1 and st[1] != sh[2]):
         raise ValueError(f"{what} must be [T][H][D] with dense rows, got shape {tuple(sh)}, strides {st}")
     return st[0] if sh[0] > 1 else sh[1] * sh[2]
 
 
-def _mask(mask, T):
-    """(address, words a row) of a tree's mask [T][ldm], int32 or uint32, rows dense."""
-    import torch
-    if mask.dtype not in (torch.int32, torch.uint32) or mask.dim() != 2 or mask.shape[0] != T or (mask.shape[1] > 1 and mask.stride(1) != 1):
-        raise ValueError(f"mask must be int32 [{T}][words] with dense rows, got {mask.dtype} {tuple(mask.shape)}, strides {mask.stride()}")
-    return mask.data_ptr(), mask.shape[1], mask.stride(0) if T > 1 else mask.shape[1]
+def _mask(mask, T, bits):
+    """(address, row pitch) of a tree's mask [T][words], int32 or uint32, rows dense and of so many bits at least."""
+    sh, st, dt = mask.shape, mask.stride(), mask.dtype
+    ty = _T or _types()
+    if (dt is not ty[1] and dt is not ty[3]) or len(sh) != 2 or sh[0] != T or (sh[1] > 1 and st[1] != 1) or 32 * sh[1] < bits:
+        raise ValueError(f"mask must be int32 [{T}][words] with dense rows of {bits} bits, got {dt} {tuple(sh)}, strides {st}")
+    return mask.data_ptr(), st[0] if T > 1 else sh[1]
 
 
 def cq_rope(X, rope, pos, Y=None, stream=None, raise_on_error=True):
     """Y (None: X itself) = the rows of X [T][H][D] (fp16/bf16/f32) at positions pos
     (int32 [T]), their first rot channels rotated.  Y may have another type."""
-    import torch
-    Y = X if Y is None else Y
-    ldx, ldy = _rows3(X, "X"), _rows3(Y, "Y")
-    if Y.shape != X.shape:
-        raise ValueError("Y must have the shape of X")
-    T, H, D = X.shape
+    types, i32, _, _, _ = _T or _types()
+    sh = X.shape
+    ldx = ldy = _rows3(sh, X.stride(), "X")
+    if Y is None:
+        Y = X
+    elif Y is not X:
+        if Y.shape != sh:
+            raise ValueError("Y must have the shape of X")
+        ldy = _rows3(sh, Y.stride(), "Y")
+    T, H, D = sh
     s = _here(X, Y, pos, rope.freq)
-    st = lib().cq_rope(X.data_ptr(), _xt(X), T, H, D, ldx, rope._ref, _dense(pos, "pos", torch.int32, (T,)), Y.data_ptr(), _xt(Y),
-                       ldy, s if stream is None else _stream(stream))
+    st = lib().cq_rope(X.data_ptr(), types.get(X.dtype, -1), T, H, D, ldx, rope._ref, _dense(pos, "pos", i32, T), Y.data_ptr(),
+                       types.get(Y.dtype, -1), ldy, s if stream is None else _stream(stream))
     if raise_on_error:
         _check(st)
     return st
@@ -491,7 +512,7 @@ def cq_kv8_write_rope(cache, K, V, q_start, lens, rope, pos=None, stream=None, r
     k, v, xt, T, ldk, ldv = cache._kv(K, V)
     s = _here(K, V, q_start, lens, pos, rope.freq, cache.Kq)
     st = lib().cq_kv8_write_rope(cache._ref, k, v, xt, T, ldk, ldv, cache._index(q_start, "q_start", cache.B + 1),
-                                 cache._index(lens, "lens", cache.B), rope._ref, _dense(pos, "pos", cache._int32, (T,)),
+                                 cache._index(lens, "lens", cache.B), rope._ref, _dense(pos, "pos", cache._int32, T),
                                  s if stream is None else _stream(stream))
     if raise_on_error:
         _check(st)
@@ -508,10 +529,8 @@ def cq_attn_kv8_tree(Q, cache, q_start, lens, max_q, mask, O, ws, scale=None, ls
     T2, ldo = cache._rows(O, "O", Hq)
     if T != T2:
         raise ValueError("O must have the shape of Q")
-    bits, words, ldm = _mask(mask, T)
-    if 32 * words < min(max_q, T):
-        raise ValueError(f"mask rows of {words} words do not hold {max_q} bits")
-    l = _dense(lse, "lse", cache._float32, (T, Hq))
+    bits, ldm = _mask(mask, T, min(max_q, T))
+    l = _dense(lse, "lse", cache._float32, T * Hq)
     s = _here(Q, O, q_start, lens, mask, lse, ws, cache.Kq)
     st = lib().cq_attn_kv8_tree(Q.data_ptr(), cache._types.get(Q.dtype, -1), T, Hq, ldq, cache._ref,
                                 cache._index(q_start, "q_start", cache.B + 1), cache._index(lens, "lens", cache.B), max_q,
@@ -528,27 +547,31 @@ def cq_verify(P, tokens, q_start, max_q, u, u_last, out, path, count, Q=None, ma
     token after them.  tokens int32 [T], u f32 [T], u_last f32 [B]; Q [T][V]: the draft's
     probabilities that the tokens were drawn from (None: chosen ones); mask: the
     trees (None: chains).  out, path int32 [B][max_q or more], count int32 [B]."""
-    import torch
-    if P.dim() != 2 or (P.shape[1] > 1 and P.stride(1) != 1):
-        raise ValueError(f"P must be [T][V] with dense rows, got shape {tuple(P.shape)}, strides {P.stride()}")
-    T, V = P.shape
-    if Q is not None and (Q.shape != P.shape or Q.dtype != P.dtype or (V > 1 and Q.stride(1) != 1)):
-        raise ValueError(f"Q must have the type and shape of P and dense rows, got {Q.dtype} {tuple(Q.shape)}, strides {Q.stride()}")
-    B = u_last.shape[0]
-    pitch = lambda t: t.stride(0) if T > 1 else (V * t.element_size() + 15) // 16 * 16 // t.element_size()
-    for t, what in ((out, "out"), (path, "path")):
-        if t.dtype is not torch.int32 or t.dim() != 2 or t.shape[0] != B or t.shape[1] < max_q or (t.shape[1] > 1 and t.stride(1) != 1) \
-                or t.stride(0) != out.stride(0):
-            raise ValueError(f"{what} must be int32 [{B}][{max_q} or more] with dense rows of one pitch, got {t.dtype} {tuple(t.shape)}, strides {t.stride()}")
-    bits, words, ldm = (None, 0, 0) if mask is None else _mask(mask, T)
-    if mask is not None and 32 * words < max_q:
-        raise ValueError(f"mask rows of {words} words do not hold {max_q} bits")
-    i32, f32 = torch.int32, torch.float32
+    types, i32, f32, _, _ = _T or _types()
+    sh, st, dt = P.shape, P.stride(), P.dtype
+    if len(sh) != 2 or (sh[1] > 1 and st[1] != 1):
+        raise ValueError(f"P must be [T][V] with dense rows, got shape {tuple(sh)}, strides {st}")
+    T, V = sh
+    ldp = ldq = st[0] if T > 1 else (V + 7) // 8 * 8             # (of one row any pitch will do)
+    q = None
+    if Q is not None:
+        sq = Q.stride()
+        if Q.shape != sh or Q.dtype is not dt or (V > 1 and sq[1] != 1):
+            raise ValueError(f"Q must have the type and shape of P and dense rows, got {Q.dtype} {tuple(Q.shape)}, strides {sq}")
+        q = Q.data_ptr()
+        if T > 1:
+            ldq = sq[0]
+    B = u_last.numel()
+    so, st = out.shape, out.stride()
+    if out.dtype is not i32 or path.dtype is not i32 or len(so) != 2 or so[0] != B or so[1] < max_q or (so[1] > 1 and st[1] != 1) \
+            or path.shape != so or path.stride() != st:
+        raise ValueError(f"out and path must be int32 [{B}][{max_q} or more] with dense rows of one pitch, got {out.dtype} {tuple(so)}, strides {st}, "
+                         f"and {path.dtype} {tuple(path.shape)}, strides {path.stride()}")
+    bits, ldm = (None, 0) if mask is None else _mask(mask, T, max_q)
     s = _here(P, tokens, q_start, u, u_last, out, path, count, Q, mask)
-    st = lib().cq_verify(P.data_ptr(), _xt(P), T, V, pitch(P), None if Q is None else Q.data_ptr(), 0 if Q is None else pitch(Q),
-                         _dense(tokens, "tokens", i32, (T,)), bits, ldm, _dense(q_start, "q_start", i32, (B + 1,)), B, max_q,
-                         _dense(u, "u", f32, (T,)), _dense(u_last, "u_last", f32, (B,)), out.data_ptr(), path.data_ptr(),
-                         out.stride(0) if B > 1 else out.shape[1], _dense(count, "count", i32, (B,)),
+    st = lib().cq_verify(P.data_ptr(), types.get(dt, -1), T, V, ldp, q, ldq, _dense(tokens, "tokens", i32, T), bits, ldm,
+                         _dense(q_start, "q_start", i32, B + 1), B, max_q, _dense(u, "u", f32, T), _dense(u_last, "u_last", f32, B),
+                         out.data_ptr(), path.data_ptr(), st[0] if B > 1 else so[1], _dense(count, "count", i32, B),
                          s if stream is None else _stream(stream))
     if raise_on_error:
         _check(st)

@@ -19,7 +19,7 @@ namespace cq {
 namespace draft {
 namespace {
 
-constexpr int THREADS = 256, WARPS = THREADS / 32, MAX_CLUSTER = 16, MAX_ROWS = 1024, UNROLL = 4;
+constexpr int THREADS = 256, WARPS = THREADS / 32, MAX_CLUSTER = 8, MAX_ROWS = 1024, UNROLL = 4, LOOK = 2;
 constexpr int SHARES = MAX_CLUSTER * WARPS;
 
 struct Row {
@@ -184,7 +184,7 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, Two x) {
 }
 
 template <class X, bool DRAWN>
-__global__ void __launch_bounds__(THREADS) k_verify(const VerifyArgs a, int cluster) {
+__global__ void __launch_bounds__(THREADS, 4) k_verify(const VerifyArgs a, int cluster) {
     constexpr int N = VEC<X>;
     __shared__ Shared sm;
     pdl_launch_dependents();
@@ -242,8 +242,8 @@ __global__ void __launch_bounds__(THREADS) k_verify(const VerifyArgs a, int clus
     if (__syncthreads_or(bad)) {
         if (tid == 0) kv8::set_err(a.err, DEV_INDEX);
     }
-    // every CTA of the cluster has begun before another writes to it
-    if (cluster > 1) cluster_sync_all();
+    // (every CTA of the cluster has begun before another writes to it: waited for before the first sums go out)
+    if (cluster > 1) cluster_arrive_relaxed();
 
     const int vecs = (a.V + N - 1) / N, per = (vecs + cluster * WARPS - 1) / (cluster * WARPS);   // vectors of a share
     bool whole = false;                                  // nothing was left: P as it is
@@ -264,7 +264,18 @@ __global__ void __launch_bounds__(THREADS) k_verify(const VerifyArgs a, int clus
                 const Row r = sm.row[j];
                 const double p = r.p, q = r.q;
                 bool stands;
-                if (DRAWN) {
+                if (mass == 1.0 && less == 0.0 && fell == 0) {
+                    // nothing rejected yet: u q < p, exactly, in 32 bits (t < p leaves no room for a rounding in between)
+                    const float g = DRAWN ? r.q : 1.f, t = __fmul_rn(r.u, g);
+                    stands = t < r.p || (t == r.p && fmaf(r.u, g, -t) < 0.f);
+                    if (!stands && DRAWN) less = 1.0;
+                    if (!stands && !DRAWN) {
+                        mass -= p;
+                        if (lane == 0) sm.gone[0] = r.token;
+                        __syncwarp();
+                        fell = 1;
+                    }
+                } else if (DRAWN) {
                     if (less > 0.0 && !waits) {          // a sibling was rejected: what is left of the mass?
                         what = 1;
                         break;
@@ -326,6 +337,7 @@ __global__ void __launch_bounds__(THREADS) k_verify(const VerifyArgs a, int clus
         const float2 h = unpair(hi), l = unpair(lo);
         const Two sum = warp_sum(Two{h.x, l.x} + Two{h.y, l.y});
         if (cluster > 1) {
+            if (sm.pass == 0) cluster_wait_acquire();
             if (lane < cluster) st_cluster(mapa_shared(smem_u32(&sm.sum[turn][mine]), lane), sum);
             cluster_sync_all();
         } else {
@@ -386,23 +398,33 @@ __global__ void __launch_bounds__(THREADS) k_verify(const VerifyArgs a, int clus
         }
     }
     if (sm.share < 0 || sm.share / WARPS != rank) return;
-    // The share again, a vector a thread: the first x whose running sum passes the aim, or the last one with a weight.
+    // The share again, neighbouring vectors a thread: the first x whose running sum passes the aim, or the last one with a weight.
     const Left<X, DRAWN> left(a, sm, q0, whole);
     const int v0 = sm.share * per, v1 = min(v0 + per, vecs);
     const Two aim = sm.aim;
     Two base = {0.f, 0.f};
     int newest = -1;                                     // the last x with a weight so far
-    for (int c = v0; c < v1; c += THREADS) {
-        const int v = c + tid, at = v < v1 ? v * N : a.V;
-        float f[N], g[N];
-        left.entries(left.load(left.p, at), left.load_q(at), at, f, g);
+    for (int c = v0; c < v1; c += THREADS * LOOK) {
+        const int v = c + tid * LOOK;
+        uint4 pv[LOOK], qv[LOOK];
+#pragma unroll
+        for (int k = 0; k < LOOK; ++k) {
+            const int at = v + k < v1 ? (v + k) * N : a.V;
+            pv[k] = left.load(left.p, at);
+            qv[k] = left.load_q(at);
+        }
         Two own = {0.f, 0.f}, all;
         int tail = -1, hit = INT32_MAX;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const Two x = left.term(f[i], g[i]);
-            own = own + x;
-            if (x.hi > 0.f) tail = at + i;
+        for (int k = 0; k < LOOK; ++k) {
+            float f[N], g[N];
+            left.entries(pv[k], qv[k], (v + k) * N, f, g);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const Two x = left.term(f[i], g[i]);
+                own = own + x;
+                if (x.hi > 0.f) tail = (v + k) * N + i;
+            }
         }
         Two r = warp_before(own, &all);
         __syncthreads();                                 // (the look before is read)
@@ -415,11 +437,18 @@ __global__ void __launch_bounds__(THREADS) k_verify(const VerifyArgs a, int clus
             ahead = ahead + sm.part[i];
         }
         base = ahead;
+        if (r + own > aim || c + THREADS * LOOK >= v1) { // (its number may lie here)
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const Two x = left.term(f[i], g[i]);
-            r = r + x;
-            if (hit == INT32_MAX && x.hi > 0.f && r > aim) hit = at + i;
+            for (int k = 0; k < LOOK; ++k) {
+                float f[N], g[N];
+                left.entries(pv[k], qv[k], (v + k) * N, f, g);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    const Two x = left.term(f[i], g[i]);
+                    r = r + x;
+                    if (hit == INT32_MAX && x.hi > 0.f && r > aim) hit = (v + k) * N + i;
+                }
+            }
         }
         if (hit != INT32_MAX) atomicMin(&sm.what, hit);
         if (tail >= 0) atomicMax(&sm.next, tail);
@@ -435,14 +464,12 @@ __global__ void __launch_bounds__(THREADS) k_verify(const VerifyArgs a, int clus
 
 template <class X, bool DRAWN>
 cudaError_t run(const VerifyArgs& a, cudaStream_t s) {
-    // CTAs of a sequence: enough for every SM to have two, as long as a warp's share keeps 16 vectors
+    // CTAs of a sequence: as many as the SMs hold at once, four each (another wave of them would begin with its latencies
+    // again), as long as a warp's share keeps 16 vectors.  Up to 8: 64 chains over 152001 tokens take 20 us with 8 CTAs each, 25
+    // with 4, 32 with 16; one chain over 32000 7.9, 8.3 and 8.3; 16 trees over 131072 11.9, 13.2 and 12.2.
     const int64_t vecs = (a.V + VEC<X> - 1) / VEC<X>;
     int cluster = 1;
-    while (cluster < MAX_CLUSTER && cluster * a.B < 2 * num_sms() && vecs > (int64_t)cluster * WARPS * 32) cluster *= 2;
-    if (cluster > 8) {
-        const cudaError_t e = cudaFuncSetAttribute(k_verify<X, DRAWN>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-    }
+    while (cluster < MAX_CLUSTER && 2 * cluster * a.B <= 4 * num_sms() && vecs > (int64_t)cluster * WARPS * 32) cluster *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.B * cluster));
     cfg.blockDim = dim3(THREADS);
