@@ -113,10 +113,10 @@ __device__ __forceinline__ float row_sum(float l, int f, int first) {
 __device__ __forceinline__ uint32_t mask_word(const AttnArgs& a, int row, int i, int n) {
     return i >= 0 && i < (n + 31) / 32 ? __ldcg(a.mask + row * a.ldm + i) : 0u;
 }
-static __device__ __noinline__ bool tree_sees(const AttnArgs& a, int row, int n, int L) {
+static __device__ __noinline__ bool tree_sees(const uint32_t* mask, int n, int L) {
     if (L > n) return true;
     for (int i = 0; i < (n + 31) / 32; ++i) {
-        uint32_t w = mask_word(a, row, i, n);
+        uint32_t w = __ldcg(mask + i);
         const int lo = n - L - 32 * i, hi = n - 32 * i;              // tokens that are there: [n - L, n)
         if (lo >= 32) continue;
         if (lo > 0) w &= ~0u << lo;
@@ -129,7 +129,7 @@ static __device__ __noinline__ bool tree_sees(const AttnArgs& a, int row, int n,
 template <bool TREE>
 __device__ __forceinline__ float end_sum(const AttnArgs& a, float l, int f, int q0, int n, int L) {
     if (!TREE) return row_sum(l, f, first_seeing(a, n, L));
-    return l == 0.f && tree_sees(a, q0 + f / (a.Hq / a.c.Hkv), n, L) ? __uint_as_float(0x7FC00000u) : l;
+    return l == 0.f && tree_sees(a.mask + (q0 + f / (a.Hq / a.c.Hkv)) * a.ldm, n, L) ? __uint_as_float(0x7FC00000u) : l;
 }
 __device__ __forceinline__ float inv_sum(float l) { return l == 0.f ? 0.f : 1.0f / l; }
 __device__ __forceinline__ float lse_of(float m, float l) {
