@@ -145,8 +145,8 @@ cudaError_t rope_from(const Rows& a, int yt, const Rope& rope, int layout, cudaS
 // have one head's keys or values, 16 tokens each, and exchange their largest magnitudes; a lane has 8 channels of a token,
 // in the half layout four and their partners, so that the turned values stay in registers between the magnitudes and the
 // codes (with a whole block to a warp they took 226, and turning twice instead cost more than the warps gained).
-// The next head's rows are on their way meanwhile (16-bit rows, or 64 channels).
-constexpr int WARPS = 8;
+// The next head's rows are on their way meanwhile (16-bit rows, or 64 channels).  W warps: 8, two heads at a time; 4 where
+// there is one head, so that an SM has more blocks.
 
 // Four channels, as they lie in memory.
 template <class X>
@@ -175,19 +175,19 @@ __device__ __forceinline__ float max_abs(float a, float b, float c) {
     return r;
 }
 
-template <class X, int D, int LAYOUT>
+template <class X, int D, int LAYOUT, int W>
 struct Writer {
     static constexpr int LPR = D / 8, RPI = 32 / LPR, IT = 16 / RPI;     // lanes a row, rows a step, steps
     static constexpr bool AHEAD = sizeof(X) * D <= 256;  // two heads' rows at once fit the registers
     const kv8::Cache& c;
     const kv8::Item& it;
     const float4 *cs4, *sn4;                             // rows of D / 2 cosines and sines
-    uint32_t (*tops)[WARPS];
+    uint32_t (*tops)[W];
     int half;                                            // rot / 2
 
     // The block's rows out of `src` (row it.lo's), FULL: all 32.
     template <bool FULL>
-    __device__ __forceinline__ void run(const X* src, int64_t ld, int head, int step, int* place, const Rope& rope) {
+    __device__ __forceinline__ void run(const X* src, int64_t ld, int head, int step, const Rope& rope, float freq, int k, int wide) {
         using namespace kv8;
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, kv = warp >> 1 & 1;
         const int row0 = 16 * (warp & 1) + lane / LPR, unit = lane % LPR;
@@ -207,7 +207,7 @@ struct Writer {
             }
         };
         if (head < c.Hkv) load(head);
-        table(place, rope);
+        table(rope, freq, k, wide);
         __syncthreads();
         float* sp = (kv ? c.s[1] : c.s[0]) + it.block;
         int8_t* dst = (kv ? c.q[1] : c.q[0]) + it.block * (BLK * D) + row0 * D + ch;
@@ -283,40 +283,49 @@ struct Writer {
         }
     }
 
-    // Cosines and sines of the block's rows; a thread keeps to one pair.
-    __device__ __forceinline__ void table(int* place, const Rope& rope) const {
+    // Cosines and sines of the block's rows; a thread keeps to one pair (k of `wide`, a power of two).
+    __device__ __forceinline__ void table(const Rope& rope, float freq, int k, int wide) const {
         float* cs = reinterpret_cast<float*>(const_cast<float4*>(cs4));
         float* sn = reinterpret_cast<float*>(const_cast<float4*>(sn4));
-        if (threadIdx.x < it.hi - it.lo) place[it.lo + threadIdx.x] = rope.pos ? __ldcg(rope.pos + it.row0 + threadIdx.x) : it.tok0 + (int)threadIdx.x;
-        int wide = 8;
-        while (wide < half) wide *= 2;
-        const int k = threadIdx.x & (wide - 1);
-        const Turn f = turn_of(k < half ? __ldcg(rope.freq + k) : 0.f);
+        constexpr int PASSES = D / (2 * W);              // of 32 W / wide rows, at most
+        const int step = W * 32 / wide, r0 = it.lo + threadIdx.x / wide;
+        int p[PASSES];
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+            const int at = r0 - it.lo + i * step;
+            p[i] = rope.pos && at < it.hi - it.lo ? __ldcg(rope.pos + it.row0 + at) : it.tok0 + at;
+        }
+        const Turn f = turn_of(freq);
         const float mag = mag_of(f, rope.mag);
-        __syncthreads();
         if (k < half)
-            for (int r = it.lo + threadIdx.x / wide; r < it.hi; r += WARPS * 32 / wide)
-                cos_sin_at(f, place[r], mag, cs[r * (D / 2) + k], sn[r * (D / 2) + k]);
+#pragma unroll
+            for (int i = 0; i < PASSES; ++i) {
+                const int r = r0 + i * step;
+                if (r < it.hi) cos_sin_at(f, p[i], mag, cs[r * (D / 2) + k], sn[r * (D / 2) + k]);
+            }
     }
 };
 
-template <class X, int D, int LAYOUT>
-__global__ void __launch_bounds__(WARPS * 32, 2) k_write_rope(const kv8::Cache c, const kv8::Batch b, const X* K, const X* V,
+template <class X, int D, int LAYOUT, int W>
+__global__ void __launch_bounds__(W * 32, (sizeof(X) * D == 128 ? 3 : 2) * 8 / W) k_write_rope(const kv8::Cache c, const kv8::Batch b, const X* K, const X* V,
                                                               int64_t ldk, int64_t ldv, const Rope rope, int groups) {
     __shared__ float4 cs4[kv8::BLK * D / 8], sn4[kv8::BLK * D / 8];
-    __shared__ uint32_t tops[2][WARPS];
-    __shared__ int place[kv8::BLK];
+    __shared__ uint32_t tops[2][W];
     pdl_launch_dependents();
     pdl_wait();
     const int warp = threadIdx.x >> 5, kv = warp >> 1 & 1;
+    int wide = 8;
+    while (wide < rope.half) wide *= 2;
+    const int k = threadIdx.x & (wide - 1);
+    const float freq = k < rope.half ? __ldcg(rope.freq + k) : 0.f;
     const kv8::Item it = kv8::find_item<true>(c, b, blockIdx.x / groups, kv, 0);
     if (!it.ok) return;                                  // (the same for the whole block of threads)
-    Writer<X, D, LAYOUT> w = {c, it, cs4, sn4, tops, rope.half};
+    Writer<X, D, LAYOUT, W> w = {c, it, cs4, sn4, tops, rope.half};
     const int64_t ld = kv ? ldv : ldk;
     const X* src = (kv ? V : K) + it.row0 * ld;
-    const int head = (int)(blockIdx.x % groups) * 2 + (warp >> 2), step = 2 * groups;
-    if (it.hi - it.lo == kv8::BLK) w.template run<true>(src, ld, head, step, place, rope);
-    else w.template run<false>(src, ld, head, step, place, rope);
+    const int head = (int)(blockIdx.x % groups) * (W / 4) + (warp >> 2), step = W / 4 * groups;
+    if (it.hi - it.lo == kv8::BLK) w.template run<true>(src, ld, head, step, rope, freq, k, wide);
+    else w.template run<false>(src, ld, head, step, rope, freq, k, wide);
 }
 
 template <class X, int D>
@@ -327,9 +336,10 @@ cudaError_t write_as(const kv8::Cache& c, const kv8::Batch& b, const void* K, co
     // while they would not fill the GPU.
     const int64_t slots = kv8::store_slots(c, b);
     const int groups = (int)std::max<int64_t>(1, std::min<int64_t>((c.Hkv + 1) / 2, 4LL * num_sms() / slots));
-    const dim3 grid((unsigned)(slots * groups)), block(WARPS * 32);
-    if (layout == CQ_ROPE_HALF) return kv8::launch_pdl(k_write_rope<X, D, CQ_ROPE_HALF>, grid, block, 0, s, c, b, k, v, ldk, ldv, rope, groups);
-    return kv8::launch_pdl(k_write_rope<X, D, CQ_ROPE_PAIRS>, grid, block, 0, s, c, b, k, v, ldk, ldv, rope, groups);
+    const dim3 grid((unsigned)(slots * groups));
+    auto run = [&](auto kernel, int warps) { return kv8::launch_pdl(kernel, grid, dim3(warps * 32), 0, s, c, b, k, v, ldk, ldv, rope, groups); };
+    if (layout == CQ_ROPE_HALF) return c.Hkv == 1 ? run(k_write_rope<X, D, CQ_ROPE_HALF, 4>, 4) : run(k_write_rope<X, D, CQ_ROPE_HALF, 8>, 8);
+    return c.Hkv == 1 ? run(k_write_rope<X, D, CQ_ROPE_PAIRS, 4>, 4) : run(k_write_rope<X, D, CQ_ROPE_PAIRS, 8>, 8);
 }
 template <class X>
 cudaError_t write_from(const kv8::Cache& c, const kv8::Batch& b, int D, const void* K, const void* V, int64_t ldk, int64_t ldv,

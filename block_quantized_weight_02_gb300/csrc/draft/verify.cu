@@ -333,6 +333,9 @@ __global__ void __launch_bounds__(THREADS, 4) k_verify(const VerifyArgs a, int c
             }
 #pragma unroll
             for (int i = 0; i < UNROLL; ++i) left.add(pv[i], qv[i], (v + 32 * i) * N, hi, lo);
+            const uint64_t h = add2(hi, lo);             // (lo stays below a last place of hi, however many there are)
+            lo = sub2(lo, sub2(h, hi));
+            hi = h;
         }
         const float2 h = unpair(hi), l = unpair(lo);
         const Two sum = warp_sum(Two{h.x, l.x} + Two{h.y, l.y});
