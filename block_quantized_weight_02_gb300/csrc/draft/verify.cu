@@ -19,7 +19,7 @@ namespace cq {
 namespace draft {
 namespace {
 
-constexpr int THREADS = 256, WARPS = THREADS / 32, MAX_CLUSTER = 8, MAX_ROWS = 1024, UNROLL = 4, LOOK = 2;
+constexpr int THREADS = 256, WARPS = THREADS / 32, MAX_CLUSTER = 8, MAX_ROWS = 1024, UNROLL = 4;
 constexpr int SHARES = MAX_CLUSTER * WARPS;
 
 struct Row {
@@ -99,6 +99,13 @@ struct Left {
         V = v.V;
         ngone = whole ? 0 : sm.fell;
         gone = sm.gone;
+    }
+    // The warp's entries will be those in [lo, hi): most have none of the rejected tokens.
+    __device__ __forceinline__ void narrow(int lo, int hi) {
+        if (DRAWN || ngone == 0) return;
+        bool mine = false;
+        for (int k = threadIdx.x & 31; k < ngone; k += 32) mine |= gone[k] >= lo && gone[k] < hi;
+        if (!__any_sync(0xffffffffu, mine)) ngone = 0;
     }
     // A row's last vector may be a part of one, of which nothing past the row is read.
     __device__ __forceinline__ uint4 load(const X* r, int at) const {
@@ -185,13 +192,14 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, Two x) {
 
 template <class X, bool DRAWN>
 __global__ void __launch_bounds__(THREADS, 4) k_verify(const VerifyArgs a, int cluster) {
-    constexpr int N = VEC<X>;
+    constexpr int N = VEC<X>, LOOK = 8 / N;              // LOOK: vectors of a thread that looks at a share again
     __shared__ Shared sm;
     pdl_launch_dependents();
     pdl_wait();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int b = blockIdx.x / cluster, rank = blockIdx.x % cluster;
     const int q0 = __ldcg(a.q_start + b), n = __ldcg(a.q_start + b + 1) - q0;
+    const float u_last = __ldcg(a.u_last + b);
     int32_t* out = a.out + b * a.ldo;
     int32_t* path = a.path + b * a.ldo;
     const bool ok = kv8::rows_ok(q0, q0 + n, a.T, a.max_q);
@@ -319,9 +327,10 @@ __global__ void __launch_bounds__(THREADS, 4) k_verify(const VerifyArgs a, int c
         __syncthreads();
         // ---- a pass over what is left at the last row that stands
         const int turn = sm.pass & 1;
-        const Left<X, DRAWN> left(a, sm, q0, whole);
+        Left<X, DRAWN> left(a, sm, q0, whole);
         const int mine = rank * WARPS + warp;
         const int v0 = min(mine * per, vecs), v1 = min(v0 + per, vecs);
+        left.narrow(v0 * N, v1 * N);
         uint64_t hi = 0, lo = 0;
         for (int v = v0 + lane; v < v1; v += 32 * UNROLL) {
             uint4 pv[UNROLL], qv[UNROLL];
@@ -354,7 +363,7 @@ __global__ void __launch_bounds__(THREADS, 4) k_verify(const VerifyArgs a, int c
             for (int i = 0; i < k; ++i)
                 if (lane * k + i < shares) own = own + sm.sum[turn][lane * k + i];
             Two at = warp_before(own, &total);
-            const Two aim = times(total, __ldcg(a.u_last + b));
+            const Two aim = times(total, u_last);
             int found = -1, some = -1;                   // the share; the last one that has anything
             Two before = at, before_some = at;
             for (int i = 0; i < k; ++i)
@@ -402,8 +411,9 @@ __global__ void __launch_bounds__(THREADS, 4) k_verify(const VerifyArgs a, int c
     }
     if (sm.share < 0 || sm.share / WARPS != rank) return;
     // The share again, neighbouring vectors a thread: the first x whose running sum passes the aim, or the last one with a weight.
-    const Left<X, DRAWN> left(a, sm, q0, whole);
+    Left<X, DRAWN> left(a, sm, q0, whole);
     const int v0 = sm.share * per, v1 = min(v0 + per, vecs);
+    left.narrow(v0 * N, v1 * N);
     const Two aim = sm.aim;
     Two base = {0.f, 0.f};
     int newest = -1;                                     // the last x with a weight so far
@@ -416,7 +426,7 @@ __global__ void __launch_bounds__(THREADS, 4) k_verify(const VerifyArgs a, int c
             pv[k] = left.load(left.p, at);
             qv[k] = left.load_q(at);
         }
-        Two own = {0.f, 0.f}, all;
+        Two all, t[LOOK * N];
         int tail = -1, hit = INT32_MAX;
 #pragma unroll
         for (int k = 0; k < LOOK; ++k) {
@@ -424,11 +434,15 @@ __global__ void __launch_bounds__(THREADS, 4) k_verify(const VerifyArgs a, int c
             left.entries(pv[k], qv[k], (v + k) * N, f, g);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const Two x = left.term(f[i], g[i]);
-                own = own + x;
-                if (x.hi > 0.f) tail = (v + k) * N + i;
+                t[k * N + i] = left.term(f[i], g[i]);
+                if (t[k * N + i].hi > 0.f) tail = (v + k) * N + i;
             }
         }
+#pragma unroll
+        for (int o = 1; o < LOOK * N; o *= 2)            // (in pairs: a chain of sums takes 50 cycles each)
+#pragma unroll
+            for (int i = 0; i < LOOK * N; i += 2 * o) t[i] = t[i] + t[i + o];
+        const Two own = t[0];
         Two r = warp_before(own, &all);
         __syncthreads();                                 // (the look before is read)
         if (lane == 0) sm.part[warp] = all;

@@ -154,17 +154,18 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
         return (int64_t)nq * G - it.f0 > x * TM ? n : 0;
     };
     constexpr int EACH = TILES == 1 ? 2 : 1;      // tile x takes steps x0, x0 + EACH, ..
+    constexpr bool LATE = TILES == 1 && D == 128; // a step's values are loaded and converted after the next step's keys
 
     if (warp >= CONV_WARP) {
         regs_down<REGS_CONV>();
         // ---- codes -> fp16: thread = token; keys and values of a step alternate
         const int tok = threadIdx.x & 127;
         uint32_t k = 0;                          // tiles so far
-        if constexpr (TILES == 1) {
+        if constexpr (LATE) {
             // The conversion sets the pace here.  A step's values come after the next step's keys (as they are loaded): their
             // place is only free once the weights of two steps before are used, and keys that waited behind them came late.
             // The next tile's codes are on their way to registers while the place for its operands is waited for.  (26 rows of
-            // 32 trees 212 us, 248 with neither; TILES 2 measured 4 to 7 % slower with registers ahead.)
+            // 32 trees 208 us, 248 with neither; 64 channels 97 against 85, and TILES 2 measured 2 to 7 % slower.)
             uint4 v[D / 16];
             auto fetch = [&]() {
                 if (!wait_warp(raw_full + 8 * (k % M::RS), k / M::RS & 1)) return;
@@ -697,7 +698,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
             }
             __syncwarp();
         } else if (warp == LOAD_WARP) {
-            load_codes<D, M::RS, TILES == 1>(a, list, w, maps, sb + M::R, raw_full, raw_empty, scales, sc_full, wait_warp, alive);
+            load_codes<D, M::RS, LATE>(a, list, w, maps, sb + M::R, raw_full, raw_empty, scales, sc_full, wait_warp, alive);
             if (!alive) {      // copies in flight land in memory that must still be this CTA's
                 for (int i = 0; i < M::RS; ++i)
                     for (uint32_t par = 0; par < 2; ++par) wait_bar(raw_full + 8 * i, par, 10000000, never);
