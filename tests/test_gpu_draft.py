@@ -711,3 +711,140 @@ def test_tree_wait_timeout_reports_status_and_the_next_call_is_right(n, group):
     assert cq.cq_get_device_error() == 0
     want, _, e, _ = draftref.attend(s.ref, 0, f64(q), 0.125, bits[0], "f32")
     assert np.all(np.abs(f64(o) - want) <= e)
+
+
+# ---- calls that no list of sizes makes ------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("n,group", [(3, 2), (6, 4), (20, 4), (40, 8)])
+def test_rows_behind_the_last_sequence(n, group):
+    """Rows past q_start[B] belong to nobody: outputs, lse and the cache's other pages stay as they were."""
+    held = [50, 10]
+    s = Setup(91, [120, 80], 2, 64, 32)
+    s.write(held, "bf16")
+    r = cq.cq_rope_spec(freqs(64))
+    T, real = 2 * n + 5, 2 * n
+    k, v = s.rows(T, 2, "bf16"), s.rows(T, 2, "bf16")
+    pools = [t.clone() for t in (s.cache.Kq, s.cache.Ks, s.cache.Vq, s.cache.Vs)]
+    s.len = [h + n for h in held]
+    kr = torch.empty(k.shape, device=DEV)
+    place = i32([p for h in held for p in range(h, h + n)] + [0] * 5)
+    cq.cq_rope(k, r, place, kr)
+    cq.cq_kv8_write_rope(s.cache, k, v, starts([n, n]), i32(s.len), r, place)
+    for b in range(2):
+        s.ref.write(b, f64(kr[b * n:b * n + n]), f64(v[b * n:b * n + n]))
+    same(s)
+    used = set(s.table.flatten().tolist())
+    for t, old in zip((s.cache.Kq, s.cache.Ks, s.cache.Vq, s.cache.Vs), pools):
+        rest = [p for p in range(t.shape[0]) if p not in used]
+        assert rest and torch.equal(t[rest].view(torch.uint8), old[rest].view(torch.uint8))
+    bits = trees_of(np.random.default_rng(n), [n, n])
+    q = s.rows(T, 2 * group, "bf16", 0.2)
+    o, l = torch.full((T, 2 * group, 64), 7.0, device=DEV), torch.full((T, 2 * group), 8.0, device=DEV)
+    ws = torch.empty(cq.cq_attn_kv8_workspace_bytes(T, 2 * group, 2, 64, 2, n), dtype=torch.uint8, device=DEV)
+    mask = torch.from_numpy(draftref.words([x for b in bits for x in b] + [(1 << n) - 1] * 5, 2)).to(DEV)
+    cq.cq_attn_kv8_tree(q, s.cache, starts([n, n]), i32(s.len), n, mask, o, ws, lse=l)
+    assert cq.cq_get_device_error() == 0
+    assert (o[real:] == 7.0).all() and (l[real:] == 8.0).all()
+    for b in range(2):
+        want, _, e, _ = draftref.attend(s.ref, b, f64(q[b * n:b * n + n]), 0.125, bits[b], "f32")
+        assert np.all(np.abs(f64(o[b * n:b * n + n]) - want) <= e)
+
+
+def test_mask_and_keys_past_32_bits():
+    """Masks and keys whose last rows lie past 2^31 elements."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    n, B, pitch = 7, 300, 1 << 20
+    T = n * B
+    s = Setup(92, [n + 3] * B, 1, 64, 32)
+    s.write([3] * B, "bf16")
+    wide = torch.zeros(T * pitch, dtype=torch.float16, device=DEV)
+    k = wide.as_strided((T, 1, 64), (pitch, 64, 1))
+    k.copy_(s.rows(T, 1, "f16", 0.3))
+    v = s.rows(T, 1, "f16", 0.3)
+    r = cq.cq_rope_spec(freqs(32))
+    rotated(s, k, v, [n] * B, r, "half")
+    back = s.read("f32", [0] * (B - 1) + [0], [0] * (B - 1) + [n + 3])[0]
+    np.testing.assert_array_equal(f64(back), s.ref.values(0, B - 1))
+    del wide, k
+    bits = trees_of(np.random.default_rng(2), [n] * B)
+    words = torch.zeros(T * pitch, dtype=torch.int32, device=DEV)
+    mask = words.as_strided((T, 1), (pitch, 1))
+    mask.copy_(torch.from_numpy(draftref.words([x for b in bits for x in b], 1)).to(DEV))
+    q, o = s.rows(T, 2, "f16", 0.3), torch.empty(T, 2, 64, device=DEV)
+    ws = torch.empty(cq.cq_attn_kv8_workspace_bytes(T, 2, 1, 64, B, n), dtype=torch.uint8, device=DEV)
+    cq.cq_attn_kv8_tree(q, s.cache, starts([n] * B), i32(s.len), n, mask, o, ws)
+    assert cq.cq_get_device_error() == 0
+    for b in (0, B // 2, B - 1):
+        want, _, e, _ = draftref.attend(s.ref, b, f64(q[b * n:b * n + n]), 0.125, bits[b], "f32")
+        assert np.all(np.abs(f64(o[b * n:b * n + n]) - want) <= e)
+
+
+def test_verify_many_sequences():
+    """As many sequences as the call takes, most of them without rows."""
+    g, B, V = gen(93), 65536, 24
+    counts = [0] * B
+    for b in range(0, B, 997):
+        counts[b] = 1 + b % 3
+    T = sum(counts)
+    P = probabilities(g, T, V, "f32", 1.0)
+    Q = probabilities(g, T, V, "f32", 1.0)
+    parents = [list(range(-1, c - 1)) for c in counts]
+    u, ul = torch.rand(T, generator=g, device=DEV), torch.rand(B, generator=g, device=DEV)
+    out, path = torch.empty(B, 3, dtype=torch.int32, device=DEV), torch.empty(B, 3, dtype=torch.int32, device=DEV)
+    count = torch.empty(B, dtype=torch.int32, device=DEV)
+    tokens = drafted(g, Q, [p for p in parents if p], [c for c in counts if c], V)
+    cq.cq_verify(P, tokens, starts(counts), 3, u, ul, out, path, count, Q=Q)
+    assert cq.cq_get_device_error() == 0
+    out, path, count = out.tolist(), path.tolist(), count.tolist()
+    at = 0
+    for b, n in enumerate(counts):
+        if n == 0:
+            assert out[b] == path[b] == [-1] * 3 and count[b] == 0
+            continue
+        want, rows = draftref.verify(f64(P[at:at + n]), f64(Q[at:at + n]), tokens.tolist()[at:at + n], parents[b], f64(u[at:at + n]), f64(ul)[b])
+        assert out[b] == want + [-1] * (3 - len(want)) and path[b] == [at + i for i in rows] + [-1] * (3 - len(rows)) and count[b] == len(rows) - 1
+        at += n
+
+
+def test_calls_on_two_streams_at_once():
+    """The same calls with their own buffers on two streams, many times over: the bits of a call alone."""
+    rng, n, B = np.random.default_rng(94), 20, 3
+    sets = []
+    for seed in (94, 95):
+        s = Setup(seed, [400] * B, 2, 64, 32)
+        s.write([300, 100, 7], "bf16")
+        s.write([n] * B, "bf16")
+        q = s.rows(n * B, 8, "bf16", 0.2)
+        g = gen(seed)
+        P = probabilities(g, n * B, 9000, "bf16", 2.0)
+        parents = [draftref.tree(rng, n) for _ in range(B)]
+        sets.append({"s": s, "q": q, "r": cq.cq_rope_spec(freqs(64)), "pos": torch.arange(n * B, device=DEV).int(), "y": torch.empty_like(q),
+                     "mask": torch.from_numpy(draftref.words([x for p in parents for x in draftref.bits_of(p)], 1)).to(DEV),
+                     "o": torch.empty(n * B, 8, 64, device=DEV), "P": P, "tokens": drafted(g, P, parents, [n] * B, 9000),
+                     "ws": torch.empty(cq.cq_attn_kv8_workspace_bytes(n * B, 8, 2, 64, B, n), dtype=torch.uint8, device=DEV),
+                     "u": torch.rand(n * B, generator=g, device=DEV), "ul": torch.rand(B, generator=g, device=DEV), "qs": starts([n] * B), "lens": i32(s.len),
+                     "out": torch.empty(B, n, dtype=torch.int32, device=DEV), "path": torch.empty(B, n, dtype=torch.int32, device=DEV),
+                     "count": torch.empty(B, dtype=torch.int32, device=DEV)})
+
+    def call(x):
+        cq.cq_rope(x["q"], x["r"], x["pos"], x["y"])
+        cq.cq_attn_kv8_tree(x["y"], x["s"].cache, x["qs"], x["lens"], n, x["mask"], x["o"], x["ws"])
+        cq.cq_verify(x["P"], x["tokens"], x["qs"], n, x["u"], x["ul"], x["out"], x["path"], x["count"], Q=x["P"], mask=x["mask"])
+
+    names = ("y", "o", "out", "path", "count")
+    alone = []
+    for x in sets:
+        call(x)
+        alone.append([x[k].clone() for k in names])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    for _ in range(20):
+        for x, stream in zip(sets, streams):
+            with torch.cuda.stream(stream):
+                call(x)
+    torch.cuda.synchronize()
+    for x, want, stream in zip(sets, alone, streams):
+        assert cq.cq_get_device_error(stream) == 0
+        for k, w in zip(names, want):
+            assert torch.equal(x[k], w), k
