@@ -22,9 +22,12 @@
 // first small kernel lays the list out (only the device knows the lengths), a third joins the
 // row tiles that lie across shares, in share order.
 //
+// TREE: in steps that reach a sequence's last tokens a row's mask words, shifted to the step's tokens, tell what it sees.
+//
 // Measured, 128 channels, bf16 outputs: a 16384-token prompt of 32 heads over 8 KV heads 1803 us, 1220 TFLOP/s; prompts
 // of up to 2000 tokens behind up to 3000 260 us, 876; 2 x 1024 rows against 4500 to 5100 tokens, 24 heads, 136 us, 889.  f32
-// outputs: the ragged prompts 435 us; 64 channels: 217.  80 rows of 8 heads over 300 to 9000 tokens (TILES 1): 123 us.  A step of two tiles takes 1.85 us where its products alone would take 1.1: a tile's
+// outputs: the ragged prompts 435 us; 64 channels: 217.  80 rows of 8 heads over 300 to 9000 tokens (TILES 1): 119 us; 26 rows
+// of 4 heads of a group of 32 trees (TILES 1 with a mask) over 1000 to 16000 tokens 208 us, 2.8 TB/s.  A step of two tiles takes 1.85 us where its products alone would take 1.1: a tile's
 // products wait for its exponentials (four cycles a warp and scheduler each) and each hand-over between the two costs a few
 // hundred cycles, which the other tile covers only in part.
 #pragma once
@@ -77,6 +80,7 @@ __device__ __forceinline__ void weights(float y0, float y1, uint64_t& sum, uint3
         p2 = pack_f16(y0 - h.x, y1 - h.y);
     }
 }
+// TREE: with a mask.
 template <int D, int PT, int TILES, bool WIN, bool TREE>
 __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Maps maps, const AttnArgs a, uint64_t wait_ns) {
     using M = Smem<D, TILES>;
