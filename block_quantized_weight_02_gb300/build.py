@@ -15,7 +15,7 @@ SOURCES = ["cq_api.cu", "k_aux.cu", "k_skinny.cu", "k_tc.cu", "k_tc_ffn.cu", "k_
            "kv8/kv8_api.cu", "kv8/kv8_store.cu", "kv8/kv8_attn.cu", "kv8/kv8_decode.cu", "kv8/kv8_tiles.cu", "kv8/kv8_narrow.cu",
            "kv8/kv8_decode_tree.cu", "kv8/kv8_tiles_tree.cu", "kv8/kv8_narrow_tree.cu", "draft/draft_api.cu", "draft/rope.cu", "draft/verify.cu"]
 HEADERS = ["cq_internal.h", "cq_ptx.cuh", "k_tc.cuh", "kv8/kv8.cuh", "kv8/attn_common.cuh",
-           "kv8/tiles_common.cuh", "kv8/store_common.cuh", "kv8/kv8_checks.h", "kv8/kv8_decode.cuh", "kv8/kv8_tiles.cuh", "kv8/kv8_narrow.cuh",
+           "kv8/tiles_common.cuh", "kv8/f32x2.cuh", "kv8/store_common.cuh", "kv8/kv8_checks.h", "kv8/kv8_decode.cuh", "kv8/kv8_tiles.cuh", "kv8/kv8_narrow.cuh",
            "draft/draft.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",

@@ -10,6 +10,7 @@
 #include "../../../include/cq_kv8.h"
 #include "../cq_internal.h"
 #include "../cq_ptx.cuh"
+#include "f32x2.cuh"
 
 namespace cq {
 namespace kv8 {
