@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(THREADS, 4) k_verify(const VerifyArgs a, int c
         if (j > 0) {
             r.token = __ldcg(a.tokens + q0 + j);
             r.u = __ldcg(a.u + q0 + j);
+            if (r.u < 0.f) r.u = 0.f;                    // (what has no probability must not stand; NaN rejects)
             if (a.mask) {
                 r.parent = -1;
                 const uint32_t* m = a.mask + (q0 + j) * a.ldm;
@@ -254,6 +255,7 @@ __global__ void __launch_bounds__(THREADS, 4) k_verify(const VerifyArgs a, int c
         if (tid == 0) kv8::set_err(a.err, DEV_INDEX);
     }
     // (every CTA of the cluster has begun before another writes to it: waited for before the first sums go out)
+    __syncwarp();
     if (cluster > 1) cluster_arrive_relaxed();
 
     const int vecs = (a.V + N - 1) / N, per = (vecs + cluster * WARPS - 1) / (cluster * WARPS);   // vectors of a share
@@ -298,7 +300,7 @@ __global__ void __launch_bounds__(THREADS, 4) k_verify(const VerifyArgs a, int c
                     bool again = false;
                     for (int k = lane; k < fell; k += 32) again |= sm.gone[k] == r.token;
                     const double w = __any_sync(0xffffffffu, again) ? 0.0 : p;
-                    stands = r.u * mass < w;
+                    stands = r.u * fmax(mass, 0.0) < w;  // (numbers above 1 may have taken more than there was)
                     if (!stands) {
                         mass -= w;
                         if (lane == 0) sm.gone[fell] = r.token;
@@ -354,6 +356,7 @@ __global__ void __launch_bounds__(THREADS, 4) k_verify(const VerifyArgs a, int c
         if (cluster > 1) {
             if (sm.pass == 0) cluster_wait_acquire();
             if (lane < cluster) st_cluster(mapa_shared(smem_u32(&sm.sum[turn][mine]), lane), sum);
+            __syncwarp();
             cluster_sync_all();
         } else {
             if (lane == 0) sm.sum[turn][mine] = sum;

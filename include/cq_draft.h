@@ -87,7 +87,8 @@ cq_status cq_attn_kv8_tree(const void* Q, int xt, int64_t T, int64_t Hq, int64_t
 
 /* ---------------------------------------------------------------------------
  * Check of drafted tokens.  P[r] are the target's probabilities of what follows row r,
- * tokens[r] is row r's token (a first row's is not read), u[r] its random number in [0, 1).
+ * tokens[r] is row r's token (a first row's is not read), u[r] its random number in [0, 1)
+ * (less counts as 0; with 1 or more, or NaN, it falls).
  * A row's parent is the last row before it that its mask names (rows without one are
  * left out); mask NULL: a chain, each row after the one before it.
  * The walk begins at the first row, and at each row goes through its children in order:
@@ -95,7 +96,7 @@ cq_status cq_attn_kv8_tree(const void* Q, int xt, int64_t T, int64_t Hq, int64_t
  *     u[c] * Q[row][x] * m < w(x)         (Q: tokens drawn from the draft's Q[row])
  *     u[c] * m < w(x)                     (Q NULL: tokens chosen, not drawn),
  *   and the walk goes on from c; else w becomes max(w - m Q[row], 0) and m its sum
- *   (Q NULL: w(x) becomes 0 and m is lessened by what it was).
+ *   (Q NULL: w(x) becomes 0 and m is lessened by what it was, down to 0).
  * Where no child stands the next token is drawn from what w has become: the smallest x
  * with w(0) + .. + w(x) > u_last[b] * (the sum of w), or the last x with w(x) > 0; if w is
  * nothing, from P[row], and if that is nothing as well the token is -1.  So every
@@ -107,7 +108,8 @@ cq_status cq_attn_kv8_tree(const void* Q, int xt, int64_t T, int64_t Hq, int64_t
  * stand (a sequence without rows: 0, and -1 throughout).
  * P, Q: pt fp16, bf16 or f32 [T][V], row pitches ldp, ldq elements (multiples of 16
  * bytes, >= V), 16-byte aligned.  All else int32 or f32, 4-byte aligned.
- * Arithmetic: as exact as 64-bit floating point to 2^-40 of a sum, whatever the type.
+ * Arithmetic: differences and comparisons as in 64 bits, sums to 2^-40 of themselves, whatever
+ * the type; the same call gives the same bits.
  * Shape rules: T >= 1, 1 <= V < 2^30, 1 <= B <= 65536, 1 <= max_q <= 1024, ldo >= max_q;
  * no sequence has more than max_q rows.  One launch, no workspace.
  * Device-detected (CQ_ERR_INDEX): a q_start that descends or leaves [0, T], more than

@@ -100,7 +100,9 @@ def verify(P, Q, tokens, parents, u, u_last):
             if parents[c] != cur:
                 continue
             x = tokens[c]
-            if u[c] * (1.0 if Q is None else q[x]) * m < w[x]:
+            r = 0.0 if u[c] < 0 else u[c]
+            if r * (1.0 if Q is None else q[x]) * max(m, 0.0) < w[x]:
+                assert w[x] > 0
                 go = c
                 break
             if Q is None:

@@ -514,6 +514,20 @@ def test_verify_edges():
     check_verify(tiny, None, i32([0]), [[-1]], [1], f(0.0), f(0.5), tree=False)
 
 
+@pytest.mark.parametrize("drawn", [False, True])
+def test_verify_numbers_out_of_range(drawn):
+    """Random numbers of 1 and more, negative ones and NaN: nothing without a probability stands or is drawn."""
+    g, V, n = gen(14), 40, 12
+    P, Q = probabilities(g, n, V, "f32", 1.0), probabilities(g, n, V, "f32", 1.0)
+    P[:, ::3] = 0.0
+    nan = float("nan")
+    for i, u in enumerate(([1.0] * n, [1.5] * n, [3.0] * n, [-1.0] * n, [nan] * n, [nan, 2.0, 0.5] * 4)):
+        for ul in (1.0, 7.0, -2.0, nan):
+            for parents in ([-1] + [0] * (n - 1), list(range(-1, n - 1))):
+                tokens = torch.randint(0, V, (n,), generator=g, device=DEV).int()
+                check_verify(P, Q if drawn else None, tokens, [parents], [n], torch.tensor(u, device=DEV), torch.tensor([ul], device=DEV))
+
+
 def test_verify_next_to_borders():
     """Draws as near to a border as f32 numbers come, over a vocabulary whose running sums 32 bits cannot hold."""
     g, V = gen(8), 120000
