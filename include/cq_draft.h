@@ -88,7 +88,7 @@ cq_status cq_attn_kv8_tree(const void* Q, int xt, int64_t T, int64_t Hq, int64_t
 /* ---------------------------------------------------------------------------
  * Check of drafted tokens.  P[r] are the target's probabilities of what follows row r,
  * tokens[r] is row r's token (a first row's is not read), u[r] its random number in [0, 1)
- * (less counts as 0; with 1 or more, or NaN, it falls).
+ * (less counts as 0, NaN falls).
  * A row's parent is the last row before it that its mask names (rows without one are
  * left out); mask NULL: a chain, each row after the one before it.
  * The walk begins at the first row, and at each row goes through its children in order:
