@@ -94,6 +94,7 @@ __device__ __forceinline__ float across(const float (&v)[NR]) {
 template <int D, int PT, bool WIN, bool TREE>
 __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ Maps maps, const AttnArgs a, uint64_t wait_ns) {
     using M = Smem<D, PT>;
+    constexpr int WINDOW = window<PT, D, TREE>();
     extern __shared__ __align__(1024) uint8_t raw[];
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     const uint32_t sb = smem_u32(smem), raw_full = sb + M::BARS, raw_empty = raw_full + 8 * M::RS,
@@ -259,14 +260,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                 }
             };
             bool gone = false;
-            for (int j0 = 0; j0 < n && !gone; j0 += WIN ? window<PT>() : n) {
+            for (int j0 = 0; j0 < n && !gone; j0 += WIN ? WINDOW : n) {
                 if (WIN && __builtin_expect(j0 > 0 && x == 0, PT == 2)) {    // the next window: what the last one holds goes to the sum
                     // (the window's first scores come after all products but the last, whose phase follows on theirs)
                     wait_warp(s_full, steps & 1);
                     follow();
                     wait_warp(pv_done, (done0 + j0 - 1) & 1);
                     tc_fence_after();
-                    const float un = acc_unit<PT>(window<PT>());
+                    const float un = acc_unit<PT, TREE>(WINDOW);
 #pragma unroll 1
                     for (int c = 0; c < NR / 16; ++c) {
                         uint32_t y[16];
@@ -277,14 +278,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                             for (int e = 0; e < 16; ++e) {
                                 const int r = 16 * c + e;
                                 float* o = &part->o[r][tid];
-                                const float z = j0 > window<PT>() ? *o * since(rows->m_sum[r], -rows->rc[r].y) : 0.f;
+                                const float z = j0 > WINDOW ? *o * since(rows->m_sum[r], -rows->rc[r].y) : 0.f;
                                 *o = fmaf(__uint_as_float(y[e]), un, z);
                             }
                     }
                     any_of(false, 1 + x, 128);               // all have read the old maxima
                     if (quarter == 0) rows->m_sum[lane] = -rows->rc[lane].y;
                 }
-                for (int j = j0 + x; j < (WIN ? min(j0 + window<PT>(), n) : n); j += 2, ++steps) {
+                for (int j = j0 + x; j < (WIN ? min(j0 + WINDOW, n) : n); j += 2, ++steps) {
                     const uint32_t tile = tile0 + j;
                     wait_warp(sc_full + 8 * (tile % SS), tile / SS & 1);
                     const Block blk = scales[tile % SS * NB + quarter];   // this warp's 32 tokens are one block
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
             tc_fence_after();
             // O^T: thread = channel; this group's half of the rows
             const bool whole = w.from == 0 && w.until == w.it.steps;
-            const float un = acc_unit<PT>((n - 1) % window<PT>() + 1);
+            const float un = acc_unit<PT, TREE>((n - 1) % WINDOW + 1);
             // (a loop: what runs once a part should not push the loops of every step out of the instruction cache)
 #pragma unroll 1
             for (int r = 16 * x; r < min(16 * x + 16, nrows); ++r) {
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                 sum *= pow2i(-(int)W_EXP);
                 const float m = -rows->rc[r].y;
                 float o = __uint_as_float(y) * un;
-                if (WIN && n > window<PT>() && tid < D) o = fmaf(part->o[r][tid], since(rows->m_sum[r], m), o);
+                if (WIN && n > WINDOW && tid < D) o = fmaf(part->o[r][tid], since(rows->m_sum[r], m), o);
                 if (whole) {
                     sum = end_sum<TREE>(a, sum, f, q0, nq, L);
                     const int64_t row = q0 + f / G, head = w.at.h * G + f % G;
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                     // (D 64: the tile's upper 64 channels are the lower ones again, and unused)
                     const uint32_t va = uniform(desc_outer(sb + M::H + (vt % HS) * M::HT, D == 128 ? TN * 128 : 0));
                     const uint32_t pb = uniform(desc_outer(sb + M::P + (M::PBUF == 1 ? 0 : x) * PT * M::PT_BYTES, 0));
-                    const uint32_t acc = WIN ? j % window<PT>() != 0 : j > 0;
+                    const uint32_t acc = WIN ? j % WINDOW != 0 : j > 0;
                     if (elect_one()) {
 #pragma unroll
                         for (int z = 0; z < PT; ++z)

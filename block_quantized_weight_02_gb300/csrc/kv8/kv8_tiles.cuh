@@ -84,6 +84,7 @@ __device__ __forceinline__ void weights(float y0, float y1, uint64_t& sum, uint3
 template <int D, int PT, int TILES, bool WIN, bool TREE>
 __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Maps maps, const AttnArgs a, uint64_t wait_ns) {
     using M = Smem<D, TILES>;
+    constexpr int WINDOW = window<PT, D, TREE>();
     extern __shared__ __align__(1024) uint8_t raw[];
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     const uint32_t sb = smem_u32(smem), raw_full = sb + M::MISC, raw_empty = raw_full + 8 * M::RS,
@@ -309,13 +310,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
             Part<D, TILES>* part = TILES == 1 && x == 1 ? &sp->odd[blockIdx.x] : &sp->cta[blockIdx.x][w.from == 0 ? 1 : 0];
             float m_sum = -INFINITY;
             bool summed = false;
-            for (int j0 = 0; j0 < mine; j0 += WIN ? window<PT>() : mine) {
+            for (int j0 = 0; j0 < mine; j0 += WIN ? WINDOW : mine) {
                 // A part's first scores are waited for before its first scales: a tile that takes no part in some items
                 // does not see every phase of the scales' barriers, and these scores come after all phases but the last.
                 if (!wait_warp(s_full + 8 * x, steps & 1)) break;
                 if (WIN && j0 > 0 && u0.wf <= u0.wl) {  // the next window: its scores came after all products so far
                     tc_fence_after();
-                    const float un = acc_unit<PT>(window<PT>()), keep = since(m_sum, m);
+                    const float un = acc_unit<PT, TREE>(WINDOW), keep = since(m_sum, m);
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t y[32];
@@ -335,7 +336,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                     m_sum = m;
                     summed = true;
                 }
-                for (int j = j0; j < (WIN ? min(j0 + window<PT>(), mine) : mine); ++j, ++steps) {
+                for (int j = j0; j < (WIN ? min(j0 + WINDOW, mine) : mine); ++j, ++steps) {
                     const uint32_t tile = tile0 + j * EACH + (TILES == 1 ? x : 0);
                     if (!wait_warp(sc_full + 8 * (tile % SS), tile / SS & 1)) break;
                     const int t0 = w.it.tok0 + (w.from + (int)(tile - tile0)) * TN;
@@ -509,7 +510,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
             ++parts;
             tc_fence_after();
             const bool begins = cur.from == 0, ends = cur.until == cur.it.steps, whole = begins && ends;
-            const float un = acc_unit<PT>((mine - 1) % window<PT>() + 1);
+            const float un = acc_unit<PT, TREE>((mine - 1) % WINDOW + 1);
             l *= pow2i(-(int)W_EXP);
             // TILES 1: the odd steps' result goes to the even steps' threads
             Part<D, TILES>* odd = &sp->odd[TILES == 1 ? blockIdx.x : 0];
@@ -679,7 +680,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                         const uint32_t next = kt + 2 * EACH;
                         if (!h_wait(kt + 1) || (j + 1 < mine && !h_wait(next)) || !take(both)) break;
                         if (!wait_warp(p_ready + 8 * x, steps++ & 1)) break;
-                        pv(kt + 1, WIN ? j % window<PT>() != 0 : j > 0);
+                        pv(kt + 1, WIN ? j % WINDOW != 0 : j > 0);
                         if (j + 1 < mine) {
                             qk(next, both);
                             if (elect_one()) {

@@ -25,15 +25,19 @@ constexpr int HS = 4;                  // fp16 operand tiles in the ring (keys a
 // f32 outputs: 8 steps (16: 5 % faster, 4: 9 % slower for ragged prompts), and LOST a product is put back, the middle of what
 // short windows lose: what is left is 2e-6 at most and a few 1e-7 mostly.  16-bit outputs (half the products): 128 steps, 7e-5
 // at most, under their own rounding.
-template <int PT>
-constexpr int window() { return PT == 2 ? 8 : 128; }
-constexpr float LOST = 1.1e-8f;
+// With a mask (TREE), f32 outputs: 64 channels 4 steps, and LOST 1.6e-8, what values of both signs lose in drawn cases of 1000 to
+// 30000 tokens (their errors: 1.1e-6 of the norm to 6e-7 at 64 channels; 128 channels keep the 8 steps, 4 would take 285 us for 260 for trees of
+// 64 rows over 70000 and 100000 tokens).
+template <int PT, int D, bool TREE>
+constexpr int window() { return PT == 2 ? TREE && D == 64 ? 4 : 8 : 128; }
+template <bool TREE>
+constexpr float LOST = TREE ? 1.6e-8f : 1.1e-8f;
 // 16-bit outputs whose sequences have no room for more than a window are served without (WIN false): 24 sequences of 25 rows
 // 79.4 against 79.9 us (64 channels: 72.5 against 74), ragged prompts 258 against 270.
-inline bool needs_windows(const AttnArgs& a) { return a.yt == CQ_F32 || a.c.ldt * a.c.page > window<1>() * TN; }
+inline bool needs_windows(const AttnArgs& a) { return a.yt == CQ_F32 || a.c.ldt * a.c.page > window<1, 128, false>() * TN; }
 // From an accumulator that holds `steps` steps to O.
-template <int PT>
-__device__ __forceinline__ float acc_unit(int steps) { return PT == 2 ? fmaf((float)steps, LOST * (PT * TN / 16), 1.f) * 0x1p-10f : 0x1p-10f; }
+template <int PT, bool TREE>
+__device__ __forceinline__ float acc_unit(int steps) { return PT == 2 ? fmaf((float)steps, LOST<TREE> * (PT * TN / 16), 1.f) * 0x1p-10f : 0x1p-10f; }
 constexpr float W_EXP = 10.f, GROW = 5.f;   // weights carry 2^10 (acc_unit takes it off) and grow by 2^5 before the maximum moves
 
 // What the softmax needs of a block (written by the loading warp, which has the time).

@@ -862,3 +862,34 @@ def test_calls_on_two_streams_at_once():
         assert cq.cq_get_device_error(stream) == 0
         for k, w in zip(names, want):
             assert torch.equal(x[k], w), k
+
+
+@pytest.mark.parametrize("n,group", [(1, 4), (5, 5), (16, 4), (150, 1)])
+@pytest.mark.parametrize("out", ["f32", "f16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("sign", [False, True])
+def test_long_sums_of_trees(n, group, out, D, sign):
+    """Sums over 40960 tokens that one SM takes in turn, of one sign (truncation shrinks them all alike) and of both: the
+    results' projection on the exact ones.  f32 outputs put back 1.6e-8 a product of a window of 128 (64 channels: 64),
+    which loses 0.4e-8 to 4.3e-8: 3.5e-6 at most; 16-bit ones lose up to 6.6e-8 of each of 1024: 7e-5."""
+    B, Hkv, L, page = 32, 16, 40960, 1024
+    s = Setup(65, [L], Hkv, D, page, spare=0)
+    s.len = [L]
+    k, v = s.rows(L, Hkv, "bf16", 0.3), s.rows(L, Hkv, "bf16", 0.3)
+    v = v.abs() if sign else v
+    cq.cq_kv8_write(s.cache, k, v, starts([L]), i32([L]))
+    k, v = (x.double().transpose(0, 1) for x in s.read("f32"))
+    s.cache = cq.cq_kv8_cache(s.cache.Kq, s.cache.Ks, s.cache.Vq, s.cache.Vs, s.table.repeat(B, 1))   # all over the same pages
+    q = s.rows(B * n, Hkv * group, "f16", 0.3)
+    o = torch.empty(B * n, Hkv * group, D, dtype=TORCH[out], device=DEV)
+    ws = torch.empty(cq.cq_attn_kv8_workspace_bytes(B * n, Hkv * group, Hkv, D, B, n), dtype=torch.uint8, device=DEV)
+    mask = torch.full((B * n, (n + 31) // 32), -1, dtype=torch.int32, device=DEV)
+    cq.cq_attn_kv8_tree(q, s.cache, starts([n] * B), i32([L] * B), n, mask, o, ws)
+    assert cq.cq_get_device_error() == 0
+    for b in (0, B - 1):
+        x = q[b * n:b * n + n].double().view(n, Hkv, group, D).permute(1, 0, 2, 3).reshape(Hkv, n * group, D)
+        w = torch.softmax(x @ k.transpose(1, 2) * D ** -0.5, 2)
+        ref = (w @ v).view(Hkv, n, group, D).transpose(0, 1).reshape(n, Hkv * group, D)
+        err = o[b * n:b * n + n].double() - ref
+        along = float((err * ref).sum() / (ref * ref).sum())
+        assert abs(along) <= (3.5e-6 if out == "f32" else 7e-5), along
