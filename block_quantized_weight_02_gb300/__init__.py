@@ -309,6 +309,7 @@ class cq_kv8_cache:
         self.Hkv, self.D, self.B, self._ref = Hkv, D, table.shape[0], ctypes.byref(self.desc)
         self._types = {torch.float16: CQ_F16, torch.bfloat16: CQ_BF16, torch.float32: CQ_F32}
         self._int32, self._float32, self._cuda = torch.int32, torch.float32, torch._C
+        self._device = Kq.get_device()
 
     Kq, Ks, Vq, Vs, table = map(_described, ("Kq", "Ks", "Vq", "Vs", "table"))
 
@@ -442,21 +443,18 @@ def _types():
     return _T
 
 
-def _here(first, *rest):
-    """The current device's current stream, for tensors that all lie on that device (None: left out)."""
-    d = first.get_device()
+def _here(d, *tensors):
+    """The current device's current stream, for tensors that all lie on that device, d (None: left out)."""
     if d >= 0:
         C = (_T or _types())[4]
-        dev = C._cuda_getDevice()
-        for t in rest:
+        for t in tensors:
             if t is not None and t.get_device() != d:
                 break
         else:
-            if d == dev:
-                return C._cuda_getCurrentRawStream(dev)
-    for t in (first, *rest):
-        if t is not None and t.get_device() < 0:
-            raise ValueError("the tensors must be on a GPU")
+            if d == C._cuda_getDevice():
+                return C._cuda_getCurrentRawStream(d)
+    if d < 0 or any(t is not None and t.get_device() < 0 for t in tensors):
+        raise ValueError("the tensors must be on a GPU")
     raise ValueError("the tensors must be on the current device")
 
 
@@ -498,7 +496,7 @@ def cq_rope(X, rope, pos, Y=None, stream=None, raise_on_error=True):
             raise ValueError("Y must have the shape of X")
         ldy = _rows3(sh, Y.stride(), "Y")
     T, H, D = sh
-    s = _here(X, Y, pos, rope.freq)
+    s = _here(rope._device, X, Y, pos)
     st = lib().cq_rope(X.data_ptr(), types.get(X.dtype, -1), T, H, D, ldx, rope._ref, _dense(pos, "pos", i32, T), Y.data_ptr(),
                        types.get(Y.dtype, -1), ldy, s if stream is None else _stream(stream))
     if raise_on_error:
@@ -510,7 +508,7 @@ def cq_kv8_write_rope(cache, K, V, q_start, lens, rope, pos=None, stream=None, r
     """cq_kv8_write of keys that are rotated on the way: by pos (int32 [T]), or (None)
     by their rows' places in their sequences."""
     k, v, xt, T, ldk, ldv = cache._kv(K, V)
-    s = _here(K, V, q_start, lens, pos, rope.freq, cache.Kq)
+    s = _here(cache._device, K, V, q_start, lens, pos, rope.freq)
     st = lib().cq_kv8_write_rope(cache._ref, k, v, xt, T, ldk, ldv, cache._index(q_start, "q_start", cache.B + 1),
                                  cache._index(lens, "lens", cache.B), rope._ref, _dense(pos, "pos", cache._int32, T),
                                  s if stream is None else _stream(stream))
@@ -531,7 +529,7 @@ def cq_attn_kv8_tree(Q, cache, q_start, lens, max_q, mask, O, ws, scale=None, ls
         raise ValueError("O must have the shape of Q")
     bits, ldm = _mask(mask, T, min(max_q, T))
     l = _dense(lse, "lse", cache._float32, T * Hq)
-    s = _here(Q, O, q_start, lens, mask, lse, ws, cache.Kq)
+    s = _here(cache._device, Q, O, q_start, lens, mask, lse, ws)
     st = lib().cq_attn_kv8_tree(Q.data_ptr(), cache._types.get(Q.dtype, -1), T, Hq, ldq, cache._ref,
                                 cache._index(q_start, "q_start", cache.B + 1), cache._index(lens, "lens", cache.B), max_q,
                                 cache.D ** -0.5 if scale is None else scale, bits, ldm, O.data_ptr(),
@@ -568,7 +566,7 @@ def cq_verify(P, tokens, q_start, max_q, u, u_last, out, path, count, Q=None, ma
         raise ValueError(f"out and path must be int32 [{B}][{max_q} or more] with dense rows of one pitch, got {out.dtype} {tuple(so)}, strides {st}, "
                          f"and {path.dtype} {tuple(path.shape)}, strides {path.stride()}")
     bits, ldm = (None, 0) if mask is None else _mask(mask, T, max_q)
-    s = _here(P, tokens, q_start, u, u_last, out, path, count, Q, mask)
+    s = _here(P.get_device(), tokens, q_start, u, u_last, out, path, count, Q, mask)
     st = lib().cq_verify(P.data_ptr(), types.get(dt, -1), T, V, ldp, q, ldq, _dense(tokens, "tokens", i32, T), bits, ldm,
                          _dense(q_start, "q_start", i32, B + 1), B, max_q, _dense(u, "u", f32, T), _dense(u_last, "u_last", f32, B),
                          out.data_ptr(), path.data_ptr(), st[0] if B > 1 else so[1], _dense(count, "count", i32, B),
