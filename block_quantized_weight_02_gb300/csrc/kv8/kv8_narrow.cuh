@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
             }
             __syncwarp();
         } else if (warp == LOAD_WARP) {
-            load_codes<D, M::RS, false>(a, list, w, maps, sb + M::R, raw_full, raw_empty, scales, sc_full, wait_warp, alive);
+            load_codes<D, M::RS>(a, list, w, maps, sb + M::R, raw_full, raw_empty, scales, sc_full, wait_warp, alive);
             if (!alive) {      // copies in flight land in memory that must still be this CTA's
                 for (int i = 0; i < M::RS; ++i)
                     for (uint32_t par = 0; par < 2; ++par) wait_bar(raw_full + 8 * i, par, 10000000, never);

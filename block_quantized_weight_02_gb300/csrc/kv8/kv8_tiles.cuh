@@ -26,8 +26,8 @@
 //
 // Measured, 128 channels, bf16 outputs: a 16384-token prompt of 32 heads over 8 KV heads 1803 us, 1220 TFLOP/s; prompts
 // of up to 2000 tokens behind up to 3000 260 us, 876; 2 x 1024 rows against 4500 to 5100 tokens, 24 heads, 136 us, 889.  f32
-// outputs: the ragged prompts 435 us; 64 channels: 217.  80 rows of 8 heads over 300 to 9000 tokens (TILES 1): 119 us; 26 rows
-// of 4 heads of a group of 32 trees (TILES 1 with a mask) over 1000 to 16000 tokens 208 us, 2.8 TB/s.  A step of two tiles takes 1.85 us where its products alone would take 1.1: a tile's
+// outputs: the ragged prompts 435 us; 64 channels: 217.  80 rows of 8 heads over 300 to 9000 tokens (TILES 1): 110 us; 26 rows
+// of 4 heads of a group of 32 trees (TILES 1 with a mask) over 1000 to 16000 tokens 180 us, 3.2 TB/s.  A step of two tiles takes 1.85 us where its products alone would take 1.1: a tile's
 // products wait for its exponentials (four cycles a warp and scheduler each) and each hand-over between the two costs a few
 // hundred cycles, which the other tile covers only in part.
 #pragma once
@@ -80,8 +80,8 @@ __device__ __forceinline__ void weights(float y0, float y1, uint64_t& sum, uint3
         p2 = pack_f16(y0 - h.x, y1 - h.y);
     }
 }
-// TREE: with a mask.
-template <int D, int PT, int TILES, bool WIN, bool TREE>
+// TREE: with a mask.  AHEAD: codes a tile ahead in the converters' registers.
+template <int D, int PT, int TILES, bool WIN, bool TREE, bool AHEAD>
 __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Maps maps, const AttnArgs a, uint64_t wait_ns) {
     using M = Smem<D, TILES>;
     constexpr int WINDOW = window<PT, D, TREE>();
@@ -159,46 +159,34 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
         return (int64_t)nq * G - it.f0 > x * TM ? n : 0;
     };
     constexpr int EACH = TILES == 1 ? 2 : 1;      // tile x takes steps x0, x0 + EACH, ..
-    constexpr bool LATE = TILES == 1 && D == 128; // a step's values are loaded and converted after the next step's keys
 
     if (warp >= CONV_WARP) {
         regs_down<REGS_CONV>();
         // ---- codes -> fp16: thread = token; keys and values of a step alternate
         const int tok = threadIdx.x & 127;
-        uint32_t k = 0;                          // tiles so far
-        if constexpr (LATE) {
-            // The conversion sets the pace here.  A step's values come after the next step's keys (as they are loaded): their
-            // place is only free once the weights of two steps before are used, and keys that waited behind them came late.
-            // The next tile's codes are on their way to registers while the place for its operands is waited for.  (26 rows of
-            // 32 trees 208 us, 248 with neither; 64 channels 97 against 85, and TILES 2 measured 2 to 7 % slower.)
-            uint4 v[D / 16];
-            auto fetch = [&]() {
-                if (!wait_warp(raw_full + 8 * (k % M::RS), k / M::RS & 1)) return;
+        uint32_t k = 0;                          // operand tiles so far
+        uint4 v[AHEAD ? D / 16 : 1];
+        auto arrived = [&]() { return wait_warp(raw_full + 8 * (k % M::RS), k / M::RS & 1); };
+        auto fetch = [&]() {
+            if (arrived())
 #pragma unroll
-                for (int c = 0; c < D / 16; ++c) v[c] = fetch_chunk<D>(smem + M::R + k % M::RS * M::RT + tok * D, tok, c);
-            };
-            for (bool first = true; alive && w.next(a, list, first); first = false) {
-                const uint32_t k0 = k, n = w.until - w.from;
-                fetch();
-                while (alive && k < k0 + 2 * n) {
-                    const uint32_t t = k - k0, kt = k0 + late_tile(t, n), rs = k % M::RS, hs = kt % HS;
-                    if (!wait_warp(h_empty + 8 * hs, (kt / HS & 1) ^ 1)) break;
+                for (int c = 0; c < (AHEAD ? D / 16 : 0); ++c) v[c] = fetch_chunk<D>(smem + M::R + k % M::RS * M::RT + tok * D, tok, c);
+        };
+        for (bool first = true; alive && w.next(a, list, first); first = false) {
+            const uint32_t end = k + 2 * (w.until - w.from);
+            if (AHEAD) fetch();
+            while (k < end && alive) {
+                const uint32_t rs = k % M::RS, hs = k % HS;
+                if ((!AHEAD && !arrived()) || !wait_warp(h_empty + 8 * hs, (k / HS & 1) ^ 1)) break;
+                if constexpr (AHEAD) {
 #pragma unroll
                     for (int c = 0; c < D / 16; ++c) convert_chunk(v[c], smem + M::H + hs * M::HT + tok * 128, tok, c);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(raw_empty + 8 * rs);
                     fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(raw_empty + 8 * rs);
-                        mbar_arrive(h_full + 8 * hs);
-                    }
-                    if (++k < k0 + 2 * n) fetch();
-                }
-            }
-        } else {
-            for (bool first = true; alive && w.next(a, list, first); first = false) {
-                for (int j = 0; j < 2 * (w.until - w.from) && alive; ++j, ++k) {
-                    const uint32_t rs = k % M::RS, hs = k % HS;
-                    if (!wait_warp(raw_full + 8 * rs, k / M::RS & 1) || !wait_warp(h_empty + 8 * hs, (k / HS & 1) ^ 1)) break;
+                    if (lane == 0) mbar_arrive(h_full + 8 * hs);
+                } else {
                     convert_tile<D>(smem + M::R + rs * M::RT, smem + M::H + hs * M::HT, tok);
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -207,6 +195,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                         mbar_arrive(h_full + 8 * hs);
                     }
                 }
+                ++k;
+                if (AHEAD && k < end) fetch();
             }
         }
     } else if (warp >= SOFT_WARP) {
@@ -675,18 +665,20 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                     qk(kt, both);
                     if (elect_one()) release(kt);
                     for (int j = 0; j < mine; ++j, kt += 2 * EACH) {
-                        // what is mostly there already is waited for first: each such wait takes 100 cycles, which
-                        // would come between the weights and their product
+                        // the values are mostly there already and waited for first: each such wait takes 100 cycles, which
+                        // would come between the weights and their product.  The next keys often are not, and the
+                        // conversion that brings them may wait for the place of these values: their product goes first, and
+                        // hands it back by itself (one row tile of 80 rows 123 us to 110, 1024-row blocks 135.3 to 133.7)
                         const uint32_t next = kt + 2 * EACH;
-                        if (!h_wait(kt + 1) || (j + 1 < mine && !h_wait(next)) || !take(both)) break;
+                        if (!h_wait(kt + 1) || !take(both)) break;
                         if (!wait_warp(p_ready + 8 * x, steps++ & 1)) break;
                         pv(kt + 1, WIN ? j % WINDOW != 0 : j > 0);
                         if (j + 1 < mine) {
+                            if (elect_one()) release(kt + 1);
+                            __syncwarp();
+                            if (!h_wait(next)) break;
                             qk(next, both);
-                            if (elect_one()) {
-                                release(kt + 1);
-                                release(next);
-                            }
+                            if (elect_one()) release(next);
                         } else if (elect_one()) {
                             tc_commit(o_full + 8 * x);
                             pass(both, x == 1);
@@ -703,7 +695,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
             }
             __syncwarp();
         } else if (warp == LOAD_WARP) {
-            load_codes<D, M::RS, LATE>(a, list, w, maps, sb + M::R, raw_full, raw_empty, scales, sc_full, wait_warp, alive);
+            load_codes<D, M::RS>(a, list, w, maps, sb + M::R, raw_full, raw_empty, scales, sc_full, wait_warp, alive);
             if (!alive) {      // copies in flight land in memory that must still be this CTA's
                 for (int i = 0; i < M::RS; ++i)
                     for (uint32_t par = 0; par < 2; ++par) wait_bar(raw_full + 8 * i, par, 10000000, never);
@@ -734,27 +726,35 @@ __global__ void __launch_bounds__(256) k_tiles_join(const AttnArgs a, int ctas) 
                                  [&](int j) { return j == 0 ? &sp->cta[i][1] : &sp->cta[i + j][0]; }, (Part<D, TILES>*)nullptr);
 }
 
-template <int D, int PT, int TILES, bool WIN, bool TREE>
+template <int D, int PT, int TILES, bool WIN, bool TREE, bool AHEAD>
 cudaError_t run(const AttnArgs& a, cudaStream_t s) {
     Maps maps;
     if (!make_maps(a, maps)) return cudaErrorInvalidValue;
     constexpr size_t smem = Smem<D, TILES>::END + 1024;
     static_assert(smem <= 232448, "shared memory");
-    cudaError_t e = cudaFuncSetAttribute(k_tiles<D, PT, TILES, WIN, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(k_tiles<D, PT, TILES, WIN, TREE, AHEAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int ctas = std::min(num_sms(), MAX_CTAS), G = a.Hq / a.c.Hkv, rows = TILES * TM;
     e = launch_pdl(k_tiles_plan<TILES * TM>, dim3(1), dim3(PLAN_THREADS), 0, s, a, &static_cast<Space<D, TILES>*>(a.ws)->list, (int)slots_of(a.b.T, G, a.c.B, rows), ctas);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(k_tiles<D, PT, TILES, WIN, TREE>, dim3(ctas), dim3(THREADS), smem, s, maps, a, (uint64_t)options().wait_ns.load());
+    e = launch_pdl(k_tiles<D, PT, TILES, WIN, TREE, AHEAD>, dim3(ctas), dim3(THREADS), smem, s, maps, a, (uint64_t)options().wait_ns.load());
     if (e != cudaSuccess) return e;
     const unsigned y = (unsigned)((std::min<int64_t>(rows, (int64_t)a.max_q * G) + 31) / 32);
     return launch_pdl(k_tiles_join<D, TILES, TREE>, dim3(ctas, y), dim3(256), 0, s, a, ctas);
 }
 
+// AHEAD shortens a step and lengthens an item's begin: trees of one row tile take it at 64 channels (26 rows of 32 trees of up
+// to 2000 tokens 46.9 us against 47.7, up to 16000 136.5 against 147.2) and, at 128, where sequences have room for more than 12288 tokens (up to
+// 2000 tokens 65.2 against 61.7, 8000 117.8 against 116.3, 11000 142.5 against 144.6, 16000 180.1 against 193.0; bf16 queries 134.2 against 127.6 at
+// 8000, 161.5 against 159.1, 195.9 against 201.5), or f32 outputs (257 against 266).  Without a mask 80 rows over 300 to 9000 tokens take
+// 115 us so and 110 without, two row tiles 2 % more.
 template <int D, int TILES, bool TREE>
 cudaError_t run_as(const AttnArgs& a, cudaStream_t s) {
-    if (a.yt == CQ_F32) return run<D, 2, TILES, true, TREE>(a, s);
-    return needs_windows(a) ? run<D, 1, TILES, true, TREE>(a, s) : run<D, 1, TILES, false, TREE>(a, s);
+    constexpr bool CAN = TREE && TILES == 1;
+    if (a.yt == CQ_F32) return run<D, 2, TILES, true, TREE, CAN>(a, s);
+    if (needs_windows(a)) return run<D, 1, TILES, true, TREE, CAN>(a, s);
+    if constexpr (CAN && D == 128) return a.c.ldt * a.c.page > 12288 ? run<D, 1, TILES, false, TREE, true>(a, s) : run<D, 1, TILES, false, TREE, false>(a, s);
+    else return run<D, 1, TILES, false, TREE, CAN>(a, s);
 }
 template <int D, bool TREE>
 cudaError_t run_d(const AttnArgs& a, cudaStream_t s) {

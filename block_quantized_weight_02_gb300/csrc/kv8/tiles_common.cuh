@@ -230,8 +230,8 @@ struct Walk {
 };
 
 // ---- loads by one warp: lane NB i + c has block c of step i of a batch of LB steps.  RS code tiles in the ring, keys
-// and values in turn, LATE: a step's values after the next step's keys; `wait` is a bounded wait with one answer for the warp.
-template <int D, int RS, bool LATE, class W>
+// and values in turn; `wait` is a bounded wait with one answer for the warp.
+template <int D, int RS, class W>
 __device__ __forceinline__ void load_codes(const AttnArgs& a, const List* list, Walk w, const Maps& maps, uint32_t ring,
                                            uint32_t raw_full, uint32_t raw_empty, Block* scales, uint32_t sc_full, W wait,
                                            const bool& alive) {
@@ -255,30 +255,24 @@ __device__ __forceinline__ void load_codes(const AttnArgs& a, const List* list, 
                 s1 = make_float2(__ldcg(a.c.s[0] + row1 / BLK), __ldcg(a.c.s[1] + row1 / BLK));
             }
         };
-        // The keys (z 0) or values of step i of the batch whose rows are `row`.
-        auto load = [&](int z, int row, int i) {
-            const bool have = lane / NB == i && row >= 0;
-            const uint32_t blocks = __popc(__ballot_sync(0xffffffffu, have)), rs = k % RS, bar = raw_full + 8 * rs;
-            if (!alive || !wait(raw_empty + 8 * rs, (k / RS & 1) ^ 1)) return;
-            const bool issue = !a.stall || k == 0;
-            if (lane == 0 && issue) mbar_arrive_expect_tx(bar, blocks * BLK * D);
-            __syncwarp();
-            if (have && issue) tma_load_2d(ring + rs * (TN * D) + lane % NB * BLK * D, &maps.t[z], bar, 0, row);
-            ++k;
-        };
         look_up(w.from);
         int hi = -64;                     // largest value exponent of the part up to this batch
-        int row0 = -1;                    // rows of the batch before
         for (int j0 = w.from; j0 < w.until && alive; j0 += LB) {
-            const int row = row1, steps = min(LB, w.until - j0);
+            const int row = row1;
             const float2 s = s1;
             Block blk;
             if (j0 + LB < w.until) look_up(j0 + LB);
-            for (int i = 0; i < steps && alive; ++i, ++tile) {
-                load(0, row, i);
-                if (!LATE) load(1, row, i);
-                else if (i > 0) load(1, row, i - 1);
-                else if (j0 > w.from) load(1, row0, LB - 1);
+            for (int i = 0; i < min(LB, w.until - j0) && alive; ++i, ++tile) {
+                const bool me = lane / NB == i, have = me && row >= 0;
+                const uint32_t blocks = __popc(__ballot_sync(0xffffffffu, have));
+                for (int z = 0; z < 2 && alive; ++z, ++k) {
+                    const uint32_t rs = k % RS, bar = raw_full + 8 * rs;
+                    if (!wait(raw_empty + 8 * rs, (k / RS & 1) ^ 1)) break;
+                    const bool issue = !a.stall || k == 0;
+                    if (lane == 0 && issue) mbar_arrive_expect_tx(bar, blocks * BLK * D);
+                    __syncwarp();
+                    if (have && issue) tma_load_2d(ring + rs * (TN * D) + lane % NB * BLK * D, &maps.t[z], bar, 0, row);
+                }
                 if (!alive) break;
                 if (i == 0) {                       // of the whole batch (now that the first copies are on their way)
                     const int lv = value_exp(s.y);
@@ -286,17 +280,13 @@ __device__ __forceinline__ void load_codes(const AttnArgs& a, const List* list, 
                     const bool far = row >= 0 && lv < hi - APART;
                     blk = {s.y == s.y ? s.x : s.y, (float)lv, far ? 0.f : pow2i(-lv), far};
                 }
-                if (lane / NB == i) scales[tile % SS * NB + lane % NB] = blk;
+                if (me) scales[tile % SS * NB + lane % NB] = blk;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(sc_full + 8 * (tile % SS));
             }
-            if (LATE && alive && j0 + LB >= w.until) load(1, row, steps - 1);
-            row0 = row;
         }
     }
 }
-// The operand tile (2 step: keys, 2 step + 1: values) that tile t of a part of n steps is, as LATE loads them.
-__device__ __forceinline__ uint32_t late_tile(uint32_t t, uint32_t n) { return t == 0 || t == 2 * n - 1 ? t : t & 1 ? t + 1 : t - 1; }
 
 // ---- a tile of codes [128 tokens][D] -> fp16 (exactly), chunks of 64 channels [128][128 B], swizzled; one token a thread
 template <int D>
