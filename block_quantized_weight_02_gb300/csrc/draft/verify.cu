@@ -13,7 +13,7 @@
 // Measured: 64 chains over 152001 entries, f32, 20 us (78 MB if every chain ends early: 3.9 TB/s, of which 8 us are
 // latency); one chain over 32000 7.6 us; 16 trees of 26 rows over 131072 bf16 entries 10.0 us.
 //
-// A border of the drawn number may lie anywhere, so sums carry 2^-40 and better: each term is the exact difference
+// A border of the drawn number may lie anywhere, so sums carry 2^-40 and better: each term is the difference
 // in two floats, sums add the rounding errors that two floats lose (Knuth's two-sum), two elements an instruction.  64-bit
 // arithmetic, one warp instruction in 16 cycles of an SM, is left to the walk.
 #include "draft.cuh"
@@ -136,15 +136,18 @@ struct Left {
                 for (int i = 0; i < N; ++i)
                     if (gone[k] == at + i) f[i] = 0.f;
     }
-    // One entry, to 2^-46 of the larger term.  With f >= t the difference's rounding error is (f - d) - t.
+    // One entry: exact for a up to 1 (with f >= g the difference's rounding error is (f - d) - g), else to 2^-45 of the larger term.
+    // The float f may lie next to the product's own float, on either side, and the two rests decide: so the difference is
+    // taken with both (Knuth's two-sum, twice), and its first float is positive where the entry is.
     __device__ __forceinline__ Two term(float f, float g) const {
         if (!DRAWN || off != MORE_OFF) {
             const float h = fmaxf(f, g), d = h - g;
             return {d, (h - d) - g};
         }
         const float t = __fmul_rn(g, a.hi), tl = fmaf(g, a.lo, fmaf(g, a.hi, -t));
-        const float h = fmaxf(f, t), d = h - t, e = ((h - d) - t) - tl;
-        return d + e > 0.f ? Two{d, e} : Two{0.f, 0.f};
+        const float d = f - t, b = d - f, e = ((f - (d - b)) - (t + b)) - tl;
+        const float h = d + e, c = h - d;
+        return h > 0.f ? Two{h, (d - (h - c)) + (e - c)} : Two{0.f, 0.f};
     }
     // Adds a vector to running sums of the even and the odd entries.
     __device__ __forceinline__ void add(uint4 pv, uint4 qv, int at, uint64_t& hi, uint64_t& lo) const {

@@ -1,6 +1,10 @@
 """GPU parity of a drafting step against the 64-bit references of draftref: rotary positions
 and masked attention within bounds that follow from their roundings, the cache's codes as
 those of rotated keys, the check of drafted tokens exactly."""
+import bisect
+import itertools
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -893,3 +897,126 @@ def test_long_sums_of_trees(n, group, out, D, sign):
         err = o[b * n:b * n + n].double() - ref
         along = float((err * ref).sum() / (ref * ref).sum())
         assert abs(along) <= (3.5e-6 if out == "f32" else 7e-5), along
+
+
+# ---- what is left after several rejected siblings -------------------------------------------------------------------
+
+class Left:
+    """max(P - A q, 0) after `fell` rejected children drawn from q, in rational arithmetic."""
+
+    def __init__(self, p, q, fell):
+        P, Q = ([int(x) for x in np.ldexp(np.where(r > 0, r, 0.0), 149)] for r in (f64(p), f64(q)))
+        a, bits, m = 0, 0, 1                                    # A and the mass in 2^-bits
+        for _ in range(fell):
+            a += m
+            w = [max((x << bits) - a * y, 0) for x, y in zip(P, Q)]
+            bits, a, m = bits + 149, a << 149, sum(w)           # entries are whole numbers of 2^-149
+        self.sums, self.at = list(itertools.accumulate(w)), [x for x, y in enumerate(w) if y]
+        self.whole, self.mass = m, float(Fraction(m, 1 << bits))
+
+    def drawn(self, ul):
+        """The token that a number draws, and how far from it the nearest border of another one lies."""
+        u = Fraction(float(ul))
+        x = bisect.bisect_right(self.sums, u.numerator * self.whole // u.denominator)
+        if x >= len(self.sums):
+            return self.at[-1], self.mass                       # (nothing after the last one can be drawn)
+        below, aim = self.sums[x - 1] if x else 0, u * self.whole
+        near = [self.sums[x] - aim] if x < self.at[-1] else [self.whole]
+        near += [aim - below] if x > self.at[0] else []
+        return x, float(min(near) / self.whole) * self.mass
+
+    def border(self, x):
+        return np.float32(float(Fraction(self.sums[x], self.whole)))
+
+
+def siblings_fall(P, Q, fell, ul):
+    """The token that cq_verify draws for a row whose `fell` children all fall (their numbers are NaN)."""
+    n = fell + 1
+    tokens, u = torch.zeros(n, dtype=torch.int32, device=DEV), torch.full((n,), float("nan"), device=DEV)
+    mask = torch.from_numpy(draftref.words(draftref.bits_of([-1] + [0] * fell), 1)).to(DEV)
+    out, path, count = (torch.full(s, 777, dtype=torch.int32, device=DEV) for s in ((1, n), (1, n), (1,)))
+    cq.cq_verify(P, tokens, i32([0, n]), n, u, torch.tensor([float(ul)], device=DEV), out, path, count, Q=Q, mask=mask)
+    assert cq.cq_get_device_error() == 0 and count.item() == 0 and path[0].tolist() == [0] + [-1] * fell
+    return out[0, 0].item()
+
+
+def first_row(row, n, dtype="f32"):
+    """[n][V] with this first row, rows on 16 bytes."""
+    x = torch.zeros(n, (len(row) + 7) // 8 * 8, dtype=TORCH[dtype], device=DEV)[:, :len(row)]
+    x[0] = torch.as_tensor(row)
+    return x
+
+
+@pytest.mark.parametrize("fell", [1, 2, 3, 6])
+@pytest.mark.parametrize("V,dtype", [(300, "f32"), (32000, "f32"), (32000, "bf16"), (150001, "f32"), (150001, "f16")])
+def test_verify_siblings_next_to_borders(fell, V, dtype):
+    """Draws as near to the borders of max(P - A q, 0) as f32 numbers come.  Entries are within 2^-45 of the larger of P and A q and
+    sums within 2^-40; A is a sum of up to 6 of them, whose errors do not grow (a larger A leaves less): with rows that sum to 1,
+    borders lie within 7 2^-45 + 7 2^-40 < 2^-37 of where they belong."""
+    g = gen(V + fell)
+    logits = 2.0 * torch.randn(V, generator=g, device=DEV)
+    P = first_row(torch.softmax(logits, 0), fell + 1, dtype)
+    Q = first_row(torch.softmax(logits + 0.5 * torch.randn(V, generator=g, device=DEV), 0), fell + 1, dtype)
+    left, tried = Left(P[0], Q[0], fell), 0
+    for x in np.random.default_rng(V + fell).choice(left.at, 12):
+        u = left.border(x)
+        for ul in (np.nextafter(u, np.float32(0)), u, np.nextafter(u, np.float32(1))):
+            want, margin = left.drawn(ul)
+            if margin > 2.0 ** -37:
+                tried += 1
+                assert siblings_fall(P, Q, fell, ul) == want, (x, ul, margin)
+    assert tried > 12
+
+
+@pytest.mark.parametrize("fell", [1, 2, 3, 5])
+@pytest.mark.parametrize("V,dtype", [(32000, "f32"), (100000, "bf16")])
+def test_verify_siblings_leave_few_tokens(fell, V, dtype):
+    """Whatever is left lies in the first tokens, though every other one has a probability: none of those is drawn, and there is
+    always a token."""
+    g = gen(fell)
+    q = torch.softmax(0.5 * torch.randn(V, generator=g, device=DEV), 0)
+    p = 0.98 * q
+    p[:200] = 4.0 * fell * q[:200]
+    P, Q = first_row(p, fell + 1, dtype), first_row(q, fell + 1, dtype)
+    left = Left(P[0], Q[0], fell)
+    assert 0 < left.mass and left.at[-1] < 200
+    for ul in (0.0, 0.3, 0.7, 0.99, 1.0 - 2.0 ** -24, 1.0, 2.0):
+        want, margin = left.drawn(np.float32(ul))
+        assert margin > 2.0 ** -37
+        assert siblings_fall(P, Q, fell, ul) == want
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_verify_siblings_leave_roundings(dtype):
+    """P is A q as the type rounds it, so that what is left are those roundings, 2^-9 or 2^-25 of an entry (bf16, f32) in half of
+    them, and no other entry is drawn.  A is 5/4 and a little, of which sums lose 2^-42, and entries are within 2^-45 of
+    5/4 q: as Q sums to 1, borders lie within 2^-41 of where they belong."""
+    V, fell = 1000, 2
+    r = np.random.default_rng(4).integers(1 << 22, 1 << 23, V) * 2 + 1           # 24 bits, odd: 5/4 of it is no f32 number
+    if dtype == "bf16":
+        r = r >> 16 << 16 | 1 << 16
+    q = np.ldexp(r.astype(np.float64), -35)
+    rest = 1.0 - q.sum()
+    # the last entries make the sum 1, in numbers of the type
+    parts = []
+    while rest > 0:
+        m, e = np.frexp(rest)
+        x = np.ldexp(np.floor(np.ldexp(m, 8)), e - 8)
+        parts.append(x)
+        rest -= x
+    q = np.concatenate([q, parts])
+    assert q.sum() == 1.0
+    Q = first_row(q, fell + 1, dtype)
+    assert np.array_equal(f64(Q[0]), q)
+    P = first_row(1.25 * q, fell + 1, dtype)
+    left = Left(P[0], Q[0], fell)
+    some = 0
+    for x in np.random.default_rng(5).choice(left.at, 60):
+        for part in (0.3, 0.5, 0.7):
+            below = left.sums[x - 1] if x else 0
+            ul = np.float32(float(Fraction(below + int((left.sums[x] - below) * part), left.whole)))
+            want, margin = left.drawn(ul)
+            if margin > 2.0 ** -41:
+                some += 1
+                assert siblings_fall(P, Q, fell, ul) == want
+    assert some > 30
