@@ -281,9 +281,10 @@ __global__ void __launch_bounds__(THREADS, 4) k_verify(const VerifyArgs a, int c
                 const double p = r.p, q = r.q;
                 bool stands;
                 if (mass == 1.0 && less == 0.0 && fell == 0) {
-                    // nothing rejected yet: u q < p, exactly, in 32 bits (t < p leaves no room for a rounding in between)
+                    // nothing rejected yet: u q < p, exactly: in 32 bits (t < p leaves no room for a rounding in between) unless the
+                    // product's rounding error may be none of their numbers
                     const float g = DRAWN ? r.q : 1.f, t = __fmul_rn(r.u, g);
-                    stands = t < r.p || (t == r.p && fmaf(r.u, g, -t) < 0.f);
+                    stands = t >= 0x1p-100f ? t < r.p || (t == r.p && fmaf(r.u, g, -t) < 0.f) : r.u * (double)g < p;
                     if (!stands && DRAWN) less = 1.0;
                     if (!stands && !DRAWN) {
                         mass -= p;

@@ -1020,3 +1020,20 @@ def test_verify_siblings_leave_roundings(dtype):
                 some += 1
                 assert siblings_fall(P, Q, fell, ul) == want
     assert some > 30
+
+
+def test_verify_tiny_numbers():
+    """Products of numbers below f32's normal ones: u q < p as real numbers have it."""
+    cases = [(u, q, p) for u in (0.25, 0.5, 0.625, 0.75, 0.9375) for q in range(1, 8) for p in range(8)]
+    B, V = len(cases), 8
+    P, Q = torch.zeros(2 * B, V), torch.zeros(2 * B, V)
+    P[:, 5] = Q[:, 5] = 0.5
+    P[0::2, 3] = torch.tensor([np.ldexp(float(p), -149) for _, _, p in cases])
+    Q[0::2, 3] = torch.tensor([np.ldexp(float(q), -149) for _, q, _ in cases])
+    u = torch.tensor([x for x, _, _ in cases], device=DEV).repeat_interleave(2)
+    out, path = (torch.empty(B, 2, dtype=torch.int32, device=DEV) for _ in range(2))
+    count = torch.empty(B, dtype=torch.int32, device=DEV)
+    cq.cq_verify(P.to(DEV), torch.full((2 * B,), 3, dtype=torch.int32, device=DEV), starts([2] * B), 2, u, torch.full((B,), 0.5, device=DEV),
+                 out, path, count, Q=Q.to(DEV))
+    assert cq.cq_get_device_error() == 0
+    assert count.tolist() == [int(x * q < p) for x, q, p in cases]
