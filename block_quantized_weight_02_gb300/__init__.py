@@ -406,15 +406,21 @@ class _rope_desc(ctypes.Structure):
 class cq_rope_spec:
     """Rotary positions: freq f32 [rot / 2] radians per position on the device, the
     layout of the pairs, a factor on the rotated channels.  Holds the tensor and
-    the C descriptor of the same name."""
+    the C descriptor of the same name.  What is assigned to one of the three names
+    is checked like the first ones and takes its place in the descriptor."""
 
     def __init__(self, freq, layout=CQ_ROPE_HALF, mag=1.0):
+        self._describe(freq, layout, mag)
+
+    def _describe(self, freq, layout, mag):
         import torch
         if freq.dtype != torch.float32 or freq.dim() != 1 or not freq.is_contiguous():
             raise ValueError(f"freq must be a dense f32 tensor [rot / 2], got {freq.dtype} {tuple(freq.shape)}")
-        self.freq = freq
         self.desc = _rope_desc(freq.data_ptr(), 2 * freq.shape[0], layout, mag)
+        self._held = {"freq": freq, "layout": layout, "mag": mag}
         self._ref, self._device = ctypes.byref(self.desc), freq.get_device()
+
+    freq, layout, mag = map(_described, ("freq", "layout", "mag"))
 
     @staticmethod
     def make(rot, base=10000.0, kind=CQ_ROPE_PLAIN, factor=1.0, low=1.0, high=32.0, trained=8192.0, layout=CQ_ROPE_HALF, device="cuda"):

@@ -167,6 +167,26 @@ def test_binding_refuses_wrong_tensors():
         cq.cq_verify(**good)
 
 
+def test_what_is_assigned_to_positions_reaches_the_descriptor():
+    """The descriptor holds addresses: it must follow the tensor, whose old one is given up."""
+    a, b = torch.zeros(32), torch.ones(16)
+    r = cq.cq_rope_spec(a, cq.CQ_ROPE_PAIRS, 1.25)
+    assert (r.freq is a, r.layout, r.mag) == (True, cq.CQ_ROPE_PAIRS, 1.25)
+    r.freq = b
+    assert r.freq is b and (r.desc.freq, r.desc.rot, r.desc.layout, r.desc.mag) == (b.data_ptr(), 32, cq.CQ_ROPE_PAIRS, 1.25)
+    assert r._device == b.get_device()
+    r.mag, r.layout = 2.0, cq.CQ_ROPE_HALF
+    assert (r.desc.freq, r.desc.layout, r.desc.mag) == (b.data_ptr(), cq.CQ_ROPE_HALF, 2.0)
+    assert ctypes.cast(r._ref, ctypes.POINTER(cq._rope_desc)).contents.mag == 2.0     # what calls hand over
+    for bad in (b.double(), b.view(2, 8), torch.zeros(32)[::2]):
+        with pytest.raises(ValueError):
+            r.freq = bad
+    for name, bad in (("layout", "half"), ("mag", "large")):
+        with pytest.raises(TypeError):
+            setattr(r, name, bad)
+    assert r.freq is b and (r.desc.freq, r.desc.layout, r.desc.mag) == (b.data_ptr(), cq.CQ_ROPE_HALF, 2.0) and (r.layout, r.mag) == (0, 2.0)
+
+
 # ---- frequencies ----------------------------------------------------------------------------------------------------
 
 def test_frequencies():
