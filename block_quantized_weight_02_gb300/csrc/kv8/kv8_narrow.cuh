@@ -94,7 +94,7 @@ __device__ __forceinline__ float across(const float (&v)[NR]) {
 template <int D, int PT, bool WIN, bool TREE>
 __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ Maps maps, const AttnArgs a, uint64_t wait_ns) {
     using M = Smem<D, PT>;
-    constexpr int WINDOW = window<PT, D, TREE>();
+    constexpr int WINDOW = window<PT>();
     extern __shared__ __align__(1024) uint8_t raw[];
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     const uint32_t sb = smem_u32(smem), raw_full = sb + M::BARS, raw_empty = raw_full + 8 * M::RS,
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
                     follow();
                     wait_warp(pv_done, (done0 + j0 - 1) & 1);
                     tc_fence_after();
-                    const float un = acc_unit<PT, TREE>(WINDOW);
+                    const float un = acc_unit<PT>(WINDOW);
 #pragma unroll 1
                     for (int c = 0; c < NR / 16; ++c) {
                         uint32_t y[16];
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_narrow(const __grid_constant__ M
             tc_fence_after();
             // O^T: thread = channel; this group's half of the rows
             const bool whole = w.from == 0 && w.until == w.it.steps;
-            const float un = acc_unit<PT, TREE>((n - 1) % WINDOW + 1);
+            const float un = acc_unit<PT>((n - 1) % WINDOW + 1);
             // (a loop: what runs once a part should not push the loops of every step out of the instruction cache)
 #pragma unroll 1
             for (int r = 16 * x; r < min(16 * x + 16, nrows); ++r) {

@@ -84,7 +84,7 @@ __device__ __forceinline__ void weights(float y0, float y1, uint64_t& sum, uint3
 template <int D, int PT, int TILES, bool WIN, bool TREE, bool AHEAD>
 __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Maps maps, const AttnArgs a, uint64_t wait_ns) {
     using M = Smem<D, TILES>;
-    constexpr int WINDOW = window<PT, D, TREE>();
+    constexpr int WINDOW = window<PT>();
     extern __shared__ __align__(1024) uint8_t raw[];
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     const uint32_t sb = smem_u32(smem), raw_full = sb + M::MISC, raw_empty = raw_full + 8 * M::RS,
@@ -306,7 +306,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                 if (!wait_warp(s_full + 8 * x, steps & 1)) break;
                 if (WIN && j0 > 0 && u0.wf <= u0.wl) {  // the next window: its scores came after all products so far
                     tc_fence_after();
-                    const float un = acc_unit<PT, TREE>(WINDOW), keep = since(m_sum, m);
+                    const float un = acc_unit<PT>(WINDOW), keep = since(m_sum, m);
 #pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t y[32];
@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
             ++parts;
             tc_fence_after();
             const bool begins = cur.from == 0, ends = cur.until == cur.it.steps, whole = begins && ends;
-            const float un = acc_unit<PT, TREE>((mine - 1) % WINDOW + 1);
+            const float un = acc_unit<PT>((mine - 1) % WINDOW + 1);
             l *= pow2i(-(int)W_EXP);
             // TILES 1: the odd steps' result goes to the even steps' threads
             Part<D, TILES>* odd = &sp->odd[TILES == 1 ? blockIdx.x : 0];

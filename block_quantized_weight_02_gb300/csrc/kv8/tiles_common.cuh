@@ -19,25 +19,23 @@ constexpr int ITEM_COST = 7;
 constexpr int SS = 8;                  // steps whose scales are kept
 constexpr int LB = 32 / NB;            // steps that the loading warp looks up at a time
 constexpr int HS = 4;                  // fp16 operand tiles in the ring (keys and values alternate)
-// The tensor cores truncate what they add to an accumulator, a product of 16 tokens at a time: 0.4e-8 to 3.3e-8 of it each, the
-// most where the values have one sign, always towards zero (measured: 16 steps of two terms lost 8.8e-6).  So an accumulator
-// starts afresh every window<PT>() of a tile's steps, and what it held is added, rounded to nearest, to a sum in the workspace.
-// f32 outputs: 8 steps (16: 5 % faster, 4: 9 % slower for ragged prompts), and LOST a product is put back, the middle of what
-// short windows lose: what is left is 2e-6 at most and a few 1e-7 mostly.  16-bit outputs (half the products): 128 steps, 7e-5
-// at most, under their own rounding.
-// With a mask (TREE), f32 outputs: 64 channels 4 steps, and LOST 1.6e-8, what values of both signs lose in drawn cases of 1000 to
-// 30000 tokens (their errors: 1.1e-6 of the norm to 6e-7 at 64 channels; 128 channels keep the 8 steps, 4 would take 285 us for 260 for trees of
-// 64 rows over 70000 and 100000 tokens).
-template <int PT, int D, bool TREE>
-constexpr int window() { return PT == 2 ? TREE && D == 64 ? 4 : 8 : 128; }
-template <bool TREE>
-constexpr float LOST = TREE ? 1.6e-8f : 1.1e-8f;
+// The tensor cores truncate what they add to an accumulator, a product of 16 tokens at a time, towards zero: what is lost goes with
+// what the accumulator holds already.  So it is nothing where a weight or two make the sum, and on average 2.3e-8 of the whole
+// a product where it grows evenly (values of one sign; half of it where they have both): measured, f32 outputs over 40960
+// tokens, 3.0e-6 with windows of 8 steps, 1.4e-6 with 4, 0.7e-6 with 2.  Hence windows: an accumulator starts afresh every window<PT>()
+// of a tile's steps, and what it held is added, rounded to nearest, to a sum in the workspace.
+// f32 outputs: 8 steps (trees of 64 rows over 70000 and 100000 tokens 255 us; 281 with 4, 338 with 2), and LOST a product is put
+// back, the middle between nothing and 2.3e-8, so that 1.6e-6 is left on either side; the same with a mask and without.
+// 16-bit outputs (half the products): 128 steps, 7e-5 at most, under their own rounding.
+template <int PT>
+constexpr int window() { return PT == 2 ? 8 : 128; }
+constexpr float LOST = 1.1e-8f;
 // 16-bit outputs whose sequences have no room for more than a window are served without (WIN false): 24 sequences of 25 rows
 // 79.4 against 79.9 us (64 channels: 72.5 against 74), ragged prompts 258 against 270.
-inline bool needs_windows(const AttnArgs& a) { return a.yt == CQ_F32 || a.c.ldt * a.c.page > window<1, 128, false>() * TN; }
+inline bool needs_windows(const AttnArgs& a) { return a.yt == CQ_F32 || a.c.ldt * a.c.page > window<1>() * TN; }
 // From an accumulator that holds `steps` steps to O.
-template <int PT, bool TREE>
-__device__ __forceinline__ float acc_unit(int steps) { return PT == 2 ? fmaf((float)steps, LOST<TREE> * (PT * TN / 16), 1.f) * 0x1p-10f : 0x1p-10f; }
+template <int PT>
+__device__ __forceinline__ float acc_unit(int steps) { return PT == 2 ? fmaf((float)steps, LOST * (PT * TN / 16), 1.f) * 0x1p-10f : 0x1p-10f; }
 constexpr float W_EXP = 10.f, GROW = 5.f;   // weights carry 2^10 (acc_unit takes it off) and grow by 2^5 before the maximum moves
 
 // What the softmax needs of a block (written by the loading warp, which has the time).

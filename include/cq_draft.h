@@ -79,8 +79,7 @@ cq_status cq_kv8_write_rope(const cq_kv8_cache* cache, const void* K, const void
  * tokens) sees every token before lens[b] - n_b and, of the last n_b tokens, those i
  * whose bit is set in mask row r (bits of tokens that are not there count for nothing).
  * A row that sees nothing gets O = 0 and lse = -inf.  Types, shape rules, workspace and
- * arithmetic are those of cq_attn_kv8 (of what sums lose in the tensor cores, f32 outputs get
- * back a little more here).
+ * arithmetic are those of cq_attn_kv8.
  * ------------------------------------------------------------------------- */
 cq_status cq_attn_kv8_tree(const void* Q, int xt, int64_t T, int64_t Hq, int64_t ldq, const cq_kv8_cache* cache,
                            const int32_t* q_start, const int32_t* lens, int64_t max_q, float scale, const uint32_t* mask,

@@ -1037,3 +1037,58 @@ def test_verify_tiny_numbers():
                  out, path, count, Q=Q.to(DEV))
     assert cq.cq_get_device_error() == 0
     assert count.tolist() == [int(x * q < p) for x, q, p in cases]
+
+
+# ---- what f32 outputs put back of truncated sums ---------------------------------------------------------------------
+
+def few_tokens_decide(n, group, D, out, L, at, B=32, Hkv=16):
+    """(outputs, exact ones) of rows whose weights all lie on the tokens `at`, evenly: their scores are 90 above the others', whose
+    weights are below 2^-128."""
+    s = Setup(66, [L], Hkv, D, 1024, spare=0)
+    s.len = [L]
+    k, v = torch.zeros(L, Hkv, D, device=DEV), s.rows(L, Hkv, "f32", 0.3)
+    k[at] = 90.0 * D ** -0.5
+    cq.cq_kv8_write(s.cache, k, v, starts([L]), i32([L]))
+    k, v = (f64(x) for x in s.read("f32"))
+    assert np.all(np.abs(k[at] * D ** 0.5 - 90.0) < 1.0) and not np.delete(k, at, 0).any()
+    s.cache = cq.cq_kv8_cache(s.cache.Kq, s.cache.Ks, s.cache.Vq, s.cache.Vs, s.table.repeat(B, 1))       # all over the same pages
+    q, o = torch.ones(B * n, Hkv * group, D, dtype=torch.bfloat16, device=DEV), torch.empty(B * n, Hkv * group, D, dtype=TORCH[out], device=DEV)
+    ws = torch.empty(cq.cq_attn_kv8_workspace_bytes(B * n, Hkv * group, Hkv, D, B, n), dtype=torch.uint8, device=DEV)
+    mask = torch.full((B * n, (n + 31) // 32), -1, dtype=torch.int32, device=DEV)
+    cq.cq_attn_kv8_tree(q, s.cache, starts([n] * B), i32([L] * B), n, mask, o, ws)
+    assert cq.cq_get_device_error() == 0
+    return f64(o).reshape(B * n, Hkv, group, D), np.broadcast_to(v[at].mean(0)[None, :, None], (B * n, Hkv, group, D))
+
+
+@pytest.mark.parametrize("n,group", [(1, 4), (4, 4), (5, 5), (16, 4), (32, 8)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_one_token_decides(n, group, D):
+    """A row that gives all weight to one token loses nothing to truncation, wherever in a window the token lies.  What is put back for a
+    product of 16 tokens and term, 1.1e-8, is then too much: 16 in each of up to 8 steps, 1.41e-6, and three roundings of
+    2^-24 (its factor, and two products).  The others' weights come to 4500 2^-128 of values up to 2^6: less than 2^-109."""
+    for L, at in ((40, 0), (1024, 3), (1024, 1023), (1152, 500), (4500, 4200)):
+        o, want = few_tokens_decide(n, group, D, "f32", L, [at])
+        steps = min(-(-L // 128), 8)
+        assert np.all(np.abs(o - want) <= np.abs(want) * (steps * 16 * 1.1e-8 + 3 * 2.0 ** -24) + 2.0 ** -109), (L, at)
+
+
+@pytest.mark.parametrize("counts,group", [([3, 4], 2), ([4, 3], 4), ([6, 4], 5), ([26, 20], 4), ([32, 25], 8)])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [64, 128])
+def test_chain_has_the_bits_of_the_causal_call(counts, group, out, D):
+    """The same arithmetic with a mask as without, whichever kernel: one item a KV head, so that both have the same shares."""
+    held = [300, 9000]
+    s = Setup(67, [n + h for n, h in zip(counts, held)], 2, D, 64)
+    s.len = [n + h for n, h in zip(counts, held)]
+    T, Hq, most = sum(counts), 2 * group, max(counts)
+    k, v = s.rows(sum(s.len), 2, "bf16", 0.3), s.rows(sum(s.len), 2, "bf16", 0.3)
+    cq.cq_kv8_write(s.cache, k, v, starts(s.len), i32(s.len))
+    q = s.rows(T, Hq, "bf16", 0.3)
+    ws = torch.empty(cq.cq_attn_kv8_workspace_bytes(T, Hq, 2, D, 2, most), dtype=torch.uint8, device=DEV)
+    a, b = (torch.empty(T, Hq, D, dtype=TORCH[out], device=DEV) for _ in range(2))
+    la, lb = (torch.empty(T, Hq, device=DEV) for _ in range(2))
+    mask = torch.from_numpy(draftref.words([(2 << i) - 1 for n in counts for i in range(n)], (most + 31) // 32)).to(DEV)
+    cq.cq_attn_kv8(q, s.cache, starts(counts), i32(s.len), most, a, ws, lse=la)
+    cq.cq_attn_kv8_tree(q, s.cache, starts(counts), i32(s.len), most, mask, b, ws, lse=lb)
+    assert cq.cq_get_device_error() == 0
+    assert torch.equal(a, b) and torch.equal(la, lb)
