@@ -80,10 +80,16 @@ __device__ __forceinline__ void weights(float y0, float y1, uint64_t& sum, uint3
         p2 = pack_f16(y0 - h.x, y1 - h.y);
     }
 }
-// TREE: with a mask.  AHEAD: codes a tile ahead in the converters' registers.
-template <int D, int PT, int TILES, bool WIN, bool TREE, bool AHEAD>
+// TREE: with a mask.
+// AHEAD: codes a tile ahead in the converters' registers, which shortens a step and lengthens an item's begin.  Trees of one row
+// tile (140 shapes of 1 to 48 sequences, 500 to 40000 tokens, both sides): 64 channels 0 to 8 % faster, 128 with f32
+// outputs 0 to 4 %, with fp16 ones 3 % slower (32 trees of up to 2000 tokens, 57.5 us to 59.1) to 10 % faster (up to 40000, 403 to 361),
+// with bf16 ones 4 % slower (5000, 106 to 111; 12000, 75.1 to 78.3) to 9 % faster (40000, 438 to 397).  Without a mask 80 rows over 300 to 9000 tokens take
+// 115 us so and 110 without, two row tiles 2 % more.
+template <int D, int PT, int TILES, bool WIN, bool TREE>
 __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Maps maps, const AttnArgs a, uint64_t wait_ns) {
     using M = Smem<D, TILES>;
+    constexpr bool AHEAD = TREE && TILES == 1;
     constexpr int WINDOW = window<PT>();
     extern __shared__ __align__(1024) uint8_t raw[];
     uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -726,35 +732,27 @@ __global__ void __launch_bounds__(256) k_tiles_join(const AttnArgs a, int ctas) 
                                  [&](int j) { return j == 0 ? &sp->cta[i][1] : &sp->cta[i + j][0]; }, (Part<D, TILES>*)nullptr);
 }
 
-template <int D, int PT, int TILES, bool WIN, bool TREE, bool AHEAD>
+template <int D, int PT, int TILES, bool WIN, bool TREE>
 cudaError_t run(const AttnArgs& a, cudaStream_t s) {
     Maps maps;
     if (!make_maps(a, maps)) return cudaErrorInvalidValue;
     constexpr size_t smem = Smem<D, TILES>::END + 1024;
     static_assert(smem <= 232448, "shared memory");
-    cudaError_t e = cudaFuncSetAttribute(k_tiles<D, PT, TILES, WIN, TREE, AHEAD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = cudaFuncSetAttribute(k_tiles<D, PT, TILES, WIN, TREE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int ctas = std::min(num_sms(), MAX_CTAS), G = a.Hq / a.c.Hkv, rows = TILES * TM;
     e = launch_pdl(k_tiles_plan<TILES * TM>, dim3(1), dim3(PLAN_THREADS), 0, s, a, &static_cast<Space<D, TILES>*>(a.ws)->list, (int)slots_of(a.b.T, G, a.c.B, rows), ctas);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(k_tiles<D, PT, TILES, WIN, TREE, AHEAD>, dim3(ctas), dim3(THREADS), smem, s, maps, a, (uint64_t)options().wait_ns.load());
+    e = launch_pdl(k_tiles<D, PT, TILES, WIN, TREE>, dim3(ctas), dim3(THREADS), smem, s, maps, a, (uint64_t)options().wait_ns.load());
     if (e != cudaSuccess) return e;
     const unsigned y = (unsigned)((std::min<int64_t>(rows, (int64_t)a.max_q * G) + 31) / 32);
     return launch_pdl(k_tiles_join<D, TILES, TREE>, dim3(ctas, y), dim3(256), 0, s, a, ctas);
 }
 
-// AHEAD shortens a step and lengthens an item's begin: trees of one row tile take it at 64 channels (26 rows of 32 trees of up
-// to 2000 tokens 46.9 us against 47.7, up to 16000 136.5 against 147.2) and, at 128, where sequences have room for more than 12288 tokens (up to
-// 2000 tokens 65.2 against 61.7, 8000 117.8 against 116.3, 11000 142.5 against 144.6, 16000 180.1 against 193.0; bf16 queries 134.2 against 127.6 at
-// 8000, 161.5 against 159.1, 195.9 against 201.5), or f32 outputs (257 against 266).  Without a mask 80 rows over 300 to 9000 tokens take
-// 115 us so and 110 without, two row tiles 2 % more.
 template <int D, int TILES, bool TREE>
 cudaError_t run_as(const AttnArgs& a, cudaStream_t s) {
-    constexpr bool CAN = TREE && TILES == 1;
-    if (a.yt == CQ_F32) return run<D, 2, TILES, true, TREE, CAN>(a, s);
-    if (needs_windows(a)) return run<D, 1, TILES, true, TREE, CAN>(a, s);
-    if constexpr (CAN && D == 128) return a.c.ldt * a.c.page > 12288 ? run<D, 1, TILES, false, TREE, true>(a, s) : run<D, 1, TILES, false, TREE, false>(a, s);
-    else return run<D, 1, TILES, false, TREE, CAN>(a, s);
+    if (a.yt == CQ_F32) return run<D, 2, TILES, true, TREE>(a, s);
+    return needs_windows(a) ? run<D, 1, TILES, true, TREE>(a, s) : run<D, 1, TILES, false, TREE>(a, s);
 }
 template <int D, bool TREE>
 cudaError_t run_d(const AttnArgs& a, cudaStream_t s) {
