@@ -45,7 +45,55 @@ __global__ void __launch_bounds__(WARPS * 32) k_kv8_write(const Cache c, const B
         u[i] = make_uint4(0, 0, 0, 0);
         if (r >= it.lo && r < it.hi) u[i] = __ldcs(reinterpret_cast<const uint4*>(src + (r - it.lo) * ld));
     }
-    store_block<D, N>(c, it, [&](int i, float (&f)[N]) { In<X>::get(u[i], f); });
+    float* sp = c.s[it.kv] + it.block;
+    const float s0 = it.lo > 0 ? *sp : 0.f;
+    // largest magnitude, as bits: an infinity or NaN is larger than every finite value
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        float f[N];
+        In<X>::get(u[i], f);
+#pragma unroll
+        for (int j = 0; j < N; ++j) m = max(m, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    const bool bad = m >= 0x7F800000u || s0 != s0;
+    const float s1 = bad ? __uint_as_float(0x7FC00000u) : fmaxf(s0, pow2(scale_exp(__uint_as_float(m))));
+    const float inv = bad ? 0.f : 1.0f / s1;      // exact: a power of two
+    int8_t* dst = c.q[it.kv] + it.block * (BLK * D) + col;
+    if (it.lo > 0 && s1 > s0) {                   // the kept codes move to the larger scale
+        const float ratio = s0 * inv;
+        for (int i = 0; i < IT; ++i) {
+            const int r = i * RPI + sub;
+            if (r < it.lo) {
+                uint32_t* p = reinterpret_cast<uint32_t*>(dst + r * D);
+#pragma unroll
+                for (int j = 0; j < N / 4; ++j) {
+                    const uint32_t w = p[j];
+                    p[j] = pack4(code_of(byte_f(w, 0), ratio), code_of(byte_f(w, 1), ratio),
+                                 code_of(byte_f(w, 2), ratio), code_of(byte_f(w, 3), ratio));
+                }
+            }
+        }
+    }
+    __syncwarp();   // every lane has read the old scale
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int r = i * RPI + sub;
+        float f[N];
+        In<X>::get(u[i], f);
+        uint32_t w[N / 4];
+#pragma unroll
+        for (int j = 0; j < N / 4; ++j)
+            w[j] = bad ? 0u
+                       : pack4(code_of(f[4 * j], inv), code_of(f[4 * j + 1], inv), code_of(f[4 * j + 2], inv),
+                               code_of(f[4 * j + 3], inv));
+        if (r >= it.lo && r < it.hi) {
+            if constexpr (N == 8) *reinterpret_cast<uint2*>(dst + r * D) = make_uint2(w[0], w[1]);
+            else *reinterpret_cast<uint32_t*>(dst + r * D) = w[0];
+        }
+    }
+    if (lane == 0) *sp = s1;
 }
 
 template <class Y, int D>
