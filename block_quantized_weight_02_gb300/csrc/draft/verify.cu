@@ -491,12 +491,15 @@ __global__ void __launch_bounds__(THREADS, 4) k_verify(const VerifyArgs a, int c
 
 template <class X, bool DRAWN>
 cudaError_t run(const VerifyArgs& a, cudaStream_t s) {
-    // CTAs of a sequence: as many as the SMs hold at once, four each (another wave of them would begin with its latencies
-    // again), as long as a warp's share keeps 16 vectors.  Up to 8: 64 chains over 152001 tokens take 20 us with 8 CTAs each, 25
-    // with 4, 32 with 16; one chain over 32000 7.9, 8.3 and 8.3; 16 trees over 131072 11.9, 13.2 and 12.2.
+    // CTAs of a sequence: twice as many, as long as the SMs hold them all at once, four each (but not four on every one, which clusters
+    // do not fill: another wave of them would begin with its latencies again), and a warp's share keeps 64 vectors, or 128
+    // where SMs have more than one.  Of 216 shapes (1 to 300 sequences over 2000 to 152064 entries) within 0.4 % of the best of 1,
+    // 2, 4 and 8 CTAs on average, 14 % at worst (76 sequences over 32000 f32 entries 12.2 us with 4, 10.7 with 2): 64 chains over 152064
+    // f32 entries 19.5 us with 8, 24.9 with 4; 152 over 8000 bf16 entries 8.0 with one, 15.1 with 4; one over 32000 7.4 with 8, 11.5 with one.
     const int64_t vecs = (a.V + VEC<X> - 1) / VEC<X>;
     int cluster = 1;
-    while (cluster < MAX_CLUSTER && 2 * cluster * a.B <= 4 * num_sms() && vecs > (int64_t)cluster * WARPS * 32) cluster *= 2;
+    for (int64_t ctas = 2LL * a.B; cluster < MAX_CLUSTER && ctas < 4 * num_sms() && vecs > (int64_t)cluster * WARPS * (ctas <= num_sms() ? 128 : 256); ctas *= 2)
+        cluster *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.B * cluster));
     cfg.blockDim = dim3(THREADS);
