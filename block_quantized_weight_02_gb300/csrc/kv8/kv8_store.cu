@@ -26,25 +26,13 @@ __device__ __forceinline__ Item my_item(const Cache& c, const Batch& b) {
     return find_item<WRITE>(c, b, w >> 1, (int)(w & 1), head);
 }
 
+// A warp stores block `it` and its scale: u holds this lane's channels of rows i RPI + lane / LPR, 0 in rows that are not the call's.
+// (A function of its own takes 3 to 24 registers less than the same lines in the kernel, which wrote four prompts of 16000 to
+// 16384 tokens, 8 heads of 128 channels, in 90 us for 79 (fp16), 75 for 73 (bf16).)
 template <class X, int D>
-__global__ void __launch_bounds__(WARPS * 32) k_kv8_write(const Cache c, const Batch b, const X* K, const X* V,
-                                                          int64_t ldk, int64_t ldv) {
-    pdl_launch_dependents();
-    pdl_wait();
-    const Item it = my_item<true>(c, b);
-    if (!it.ok) return;
+__device__ __forceinline__ void store_block(const Cache& c, const Item& it, const uint4 (&u)[BLK * D / In<X>::N / 32]) {
     constexpr int N = In<X>::N, LPR = D / N, RPI = 32 / LPR, IT = BLK / RPI;   // lanes a row, rows a step
-    const int lane = threadIdx.x & 31;
-    const int sub = lane / LPR, col = (lane % LPR) * N;
-    const int64_t ld = it.kv ? ldv : ldk;
-    const X* src = (it.kv ? V : K) + it.row0 * ld + (int64_t)it.head * D + col;
-    uint4 u[IT];
-#pragma unroll
-    for (int i = 0; i < IT; ++i) {
-        const int r = i * RPI + sub;
-        u[i] = make_uint4(0, 0, 0, 0);
-        if (r >= it.lo && r < it.hi) u[i] = __ldcs(reinterpret_cast<const uint4*>(src + (r - it.lo) * ld));
-    }
+    const int lane = threadIdx.x & 31, sub = lane / LPR, col = (lane % LPR) * N;
     float* sp = c.s[it.kv] + it.block;
     const float s0 = it.lo > 0 ? *sp : 0.f;
     // largest magnitude, as bits: an infinity or NaN is larger than every finite value
@@ -94,6 +82,28 @@ __global__ void __launch_bounds__(WARPS * 32) k_kv8_write(const Cache c, const B
         }
     }
     if (lane == 0) *sp = s1;
+}
+
+template <class X, int D>
+__global__ void __launch_bounds__(WARPS * 32) k_kv8_write(const Cache c, const Batch b, const X* K, const X* V,
+                                                          int64_t ldk, int64_t ldv) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const Item it = my_item<true>(c, b);
+    if (!it.ok) return;
+    constexpr int N = In<X>::N, LPR = D / N, RPI = 32 / LPR, IT = BLK / RPI;   // lanes a row, rows a step
+    const int lane = threadIdx.x & 31;
+    const int sub = lane / LPR, col = (lane % LPR) * N;
+    const int64_t ld = it.kv ? ldv : ldk;
+    const X* src = (it.kv ? V : K) + it.row0 * ld + (int64_t)it.head * D + col;
+    uint4 u[IT];
+#pragma unroll
+    for (int i = 0; i < IT; ++i) {
+        const int r = i * RPI + sub;
+        u[i] = make_uint4(0, 0, 0, 0);
+        if (r >= it.lo && r < it.hi) u[i] = __ldcs(reinterpret_cast<const uint4*>(src + (r - it.lo) * ld));
+    }
+    store_block<X, D>(c, it, u);
 }
 
 template <class Y, int D>
