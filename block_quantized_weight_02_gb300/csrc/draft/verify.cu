@@ -10,8 +10,9 @@
 //   w_{k+1} = max(w_k - m_k q, 0) = max(P - (A_k + m_k) q, 0),
 // so a pass needs A alone, however many were rejected.
 //
-// Measured: 64 chains over 152001 entries, f32, 20 us (78 MB if every chain ends early: 3.9 TB/s, of which 8 us are
-// latency); one chain over 32000 7.6 us; 16 trees of 26 rows over 131072 bf16 entries 10.0 us.
+// Measured: 64 chains over 152001 entries, f32, 19.5 us (78 MB if every chain ends early: 4.0 TB/s, of which 8 us are
+// latency); one chain over 32000 7.4 us; 16 trees of 26 chosen tokens over 131072 bf16 entries 10.5 us.  A pass after a
+// rejection, of one tree and of 16: over 32000 f32 entries 4.1 and 4.9 us, over 128000 7.5 and 10.
 //
 // A border of the drawn number may lie anywhere, so sums carry 2^-40 and better: each term is the difference
 // in two floats, sums add the rounding errors that two floats lose (Knuth's two-sum), two elements an instruction.  64-bit

@@ -674,7 +674,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_tiles(const __grid_constant__ Ma
                         // the values are mostly there already and waited for first: each such wait takes 100 cycles, which
                         // would come between the weights and their product.  The next keys often are not, and the
                         // conversion that brings them may wait for the place of these values: their product goes first, and
-                        // hands it back by itself (one row tile of 80 rows 123 us to 110, 1024-row blocks 135.3 to 133.7)
+                        // hands it back by itself (one row tile of 80 rows 123 us to 110, 1024-row blocks 137.4 to 136.3)
                         const uint32_t next = kt + 2 * EACH;
                         if (!h_wait(kt + 1) || !take(both)) break;
                         if (!wait_warp(p_ready + 8 * x, steps++ & 1)) break;
