@@ -109,8 +109,8 @@ cq_status cq_attn_kv8_tree(const void* Q, int xt, int64_t T, int64_t Hq, int64_t
  * P, Q: pt fp16, bf16 or f32 [T][V], row pitches ldp, ldq elements (multiples of 16
  * bytes, >= V), 16-byte aligned.  All else int32 or f32, 4-byte aligned.
  * Arithmetic, whatever the type: comparisons as in 64 bits, entries of w exactly after one
- * rejection and to 2^-45 of the larger of P and what was taken off after more, sums to 2^-40
- * of themselves; what has no weight is never drawn.  The same call gives the same bits.
+ * rejection and to 2^-45 of the larger of P and what was taken off after more, sums of them
+ * to 2^-40.  The same call gives the same bits.
  * Shape rules: T >= 1, 1 <= V < 2^30, 1 <= B <= 65536, 1 <= max_q <= 1024, ldo >= max_q;
  * no sequence has more than max_q rows.  One launch, no workspace.
  * Device-detected (CQ_ERR_INDEX): a q_start that descends or leaves [0, T], more than
